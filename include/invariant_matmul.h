@@ -423,6 +423,67 @@ gemm_status ozaki_run(ozaki_plan_t plan, const double* A, const double* B, doubl
 
 void ozaki_plan_destroy(ozaki_plan_t plan);
 
+/* ---------------------------------------------------------------------------
+ * Root-mean-square norm of rows, with the residual's addition, and fp8 rows
+ * with a scale each: what stands in front of a linear layer.  x is
+ * [rows, cols] row-major and contiguous, fp16 or bf16; cols a multiple of 8
+ * (16 for fp8 outputs, the K rule of the fp8 product) and at most 32768.
+ *   h = round(x + residual), the residual stream in its own type (h = x
+ *       without a residual);
+ *   rstd = 1 / sqrt(sum_k h_k^2 / cols + eps), t_k = (h_k rstd) weight_k, fp32;
+ *   out = round(t) in the input's type, or, with an fp8 output,
+ *   row_scale = max(max_k |t_k| / FMAX, 2^-120), FMAX = 448 (e4m3) or 57344
+ *       (e5m2), and out = round8(t / row_scale): the row is out * row_scale.
+ * Row i of every output is a bitwise function of row i of the inputs, the
+ * weight, cols and eps.  A row that holds a NaN or an infinity is NaN where
+ * the formula is (a 16-bit output), or NaN throughout (an fp8 output, whose
+ * row_scale is then infinite or NaN); other rows are unaffected.
+ * No passage of the pages defines these calls.
+ * ------------------------------------------------------------------------- */
+typedef struct rms_norm_plan_s* rms_norm_plan_t;
+
+/* Plan a norm.  in: GEMM_F16 or GEMM_BF16; out: the same type, GEMM_F8_E4M3 or
+ * GEMM_F8_E5M2; eps finite and >= 0.  GEMM_ERR_INVALID_VALUE for a negative
+ * size or a NULL handle, GEMM_ERR_UNSUPPORTED for other types, cols or eps. */
+gemm_status rms_norm_plan(int64_t rows, int64_t cols, gemm_dtype in, gemm_dtype out, float eps,
+                          rms_norm_plan_t* plan);
+
+/* The norm, on `stream`.  residual and residual_out: [rows, cols] in the input's
+ * type, both NULL or both given (residual_out receives h and may be x or
+ * residual itself; no other operands may overlap).  weight: [cols] in the
+ * input's type, or NULL for ones.  row_scale: fp32 [rows], for fp8 outputs
+ * (NULL otherwise).  rstd: fp32 [rows] for the backward pass, or NULL.
+ * Matrices and weight are 16-byte aligned, row_scale and rstd 4-byte. */
+gemm_status rms_norm_run(rms_norm_plan_t plan, const void* x, const void* residual,
+                         const void* weight, void* out, float* row_scale, void* residual_out,
+                         float* rstd, void* stream);
+
+/* Bytes of workspace rms_norm_backward needs for the weight's gradient (the
+ * fp32 sums of row groups).  0 for a NULL plan. */
+size_t rms_norm_workspace_size(rms_norm_plan_t plan);
+
+/* Gradients of the norm (plans with a 16-bit output).  dy: the gradient of out;
+ * h: the residual stream the norm read (residual_out, or x without a
+ * residual); rstd: as rms_norm_run left it; dh: the gradient that reaches h from
+ * elsewhere, or NULL.  With n = h rstd and g = weight dy:
+ *   dx = round(rstd (g - n sum_j(g_j n_j) / cols) + dh),
+ * the gradient of x and of the residual alike, and
+ *   dweight = round(sum over rows of dy n), [cols] in the input's type, or NULL
+ * (then no workspace is needed).  dx may be dy or dh itself.  dweight sums the
+ * rows in an order that (rows, cols) fix, without atomics; dx is a function of
+ * its row alone. */
+gemm_status rms_norm_backward(rms_norm_plan_t plan, const void* dy, const void* h,
+                              const void* weight, const float* rstd, const void* dh, void* dx,
+                              void* dweight, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+void rms_norm_plan_destroy(rms_norm_plan_t plan);
+
+/* The fp8 rows of x [rows, cols] alone: t = x in the formula above (activations
+ * that no norm precedes, or a weight [N, K] with a scale per output). */
+gemm_status quantize_rows(int64_t rows, int64_t cols, gemm_dtype in, gemm_dtype out, const void* x,
+                          void* q, float* row_scale, void* stream);
+
 /* Name of a status ("GEMM_OK", ...); a static string.  Housekeeping. */
 const char* gemm_status_string(gemm_status status);
 

@@ -29,6 +29,8 @@ __all__ = [
     "PLAN_TILE_BY_M", "PLAN_FP8_FP32_ACCUM",
     "OzakiPlan", "ozaki_plan", "ozaki_plan_info", "ozaki_workspace_size", "ozaki_split",
     "ozaki_multiply", "ozaki_run", "ozaki_mm",
+    "LAYER_SYMBOLS", "RmsNormPlan", "rms_norm_plan", "rms_norm_run", "rms_norm_workspace_size",
+    "rms_norm_backward", "quantize_rows",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libinvariant_matmul.so")
@@ -50,6 +52,11 @@ EXPORTED_SYMBOLS = (
     "gemm_plan_destroy", "gemm_status_string", "gemm_last_hip_error", "gemm_splitk_run_noalloc",
     "ozaki_plan", "ozaki_plan_info", "ozaki_workspace_size", "ozaki_split", "ozaki_multiply",
     "ozaki_run", "ozaki_plan_destroy",
+)
+# The calls around a linear layer: the row norm and fp8 rows.
+LAYER_SYMBOLS = (
+    "rms_norm_plan", "rms_norm_run", "rms_norm_workspace_size", "rms_norm_backward",
+    "rms_norm_plan_destroy", "quantize_rows",
 )
 
 
@@ -143,7 +150,16 @@ def lib() -> ctypes.CDLL:
         L.ozaki_run.argtypes = [vp, vp, vp, vp, vp, sz, vp]
         L.ozaki_plan_destroy.argtypes = [vp]
         L.ozaki_plan_destroy.restype = None
-        for f in ("gemm_plan", "gemm_plan_ex", "gemm_plan_ex2", "gemm_plan_info",
+        L.rms_norm_plan.argtypes = [i64, i64, i32, i32, f32, pp]
+        L.rms_norm_run.argtypes = [vp] * 9
+        L.rms_norm_workspace_size.argtypes = [vp]
+        L.rms_norm_workspace_size.restype = sz
+        L.rms_norm_backward.argtypes = [vp] * 9 + [sz, vp]
+        L.rms_norm_plan_destroy.argtypes = [vp]
+        L.rms_norm_plan_destroy.restype = None
+        L.quantize_rows.argtypes = [i64, i64, i32, i32, vp, vp, vp, vp]
+        for f in ("rms_norm_plan", "rms_norm_run", "rms_norm_backward", "quantize_rows",
+                  "gemm_plan", "gemm_plan_ex", "gemm_plan_ex2", "gemm_plan_info",
                   "gemm_plan_tile_of", "gemm_run", "gemm_run_bias", "gemm_splitk_run",
                   "gemm_splitk_run_bias", "gemm_splitk_run_noalloc", "gemm_last_hip_error", "ozaki_plan", "ozaki_plan_info",
                   "ozaki_split", "ozaki_multiply", "ozaki_run"):
@@ -152,15 +168,19 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
+_TORCH_DTYPE: dict = {}  # torch dtype -> code, filled on first use
+
+
 def _dtype_code(dt) -> int:
     if isinstance(dt, int):
         return dt
     if isinstance(dt, str):
         return DTYPE[dt]
-    import torch
-    m = {torch.float16: 0, torch.bfloat16: 1, torch.float8_e4m3fn: 2, torch.float8_e5m2: 3,
-         torch.float32: 4}
-    return m[dt]
+    if not _TORCH_DTYPE:
+        import torch
+        _TORCH_DTYPE.update({torch.float16: 0, torch.bfloat16: 1, torch.float8_e4m3fn: 2,
+                             torch.float8_e5m2: 3, torch.float32: 4})
+    return _TORCH_DTYPE[dt]
 
 
 class Plan:
@@ -479,3 +499,83 @@ def ozaki_mm(A, B, type2="bf16", slices: int = 0, d: int = 0, chunk: int = 0, st
     C = torch.empty((M, N), dtype=torch.float64, device=A.device)
     ozaki_run(plan, A.contiguous(), B.contiguous(), C, ws, stream)
     return C
+
+
+# ---- Row norm and fp8 rows ------------------------------------------------------
+
+class RmsNormPlan:
+    """Owns an rms_norm_plan_t; destroyed with the object."""
+
+    def __init__(self, handle: int, rows: int, cols: int, in_dtype: int, out_dtype: int):
+        self.handle = handle
+        self.rows, self.cols = rows, cols
+        self.in_dtype, self.out_dtype = in_dtype, out_dtype
+        self._lib = lib()
+
+    def __del__(self):
+        h, self.handle = getattr(self, "handle", None), None
+        if h:
+            self._lib.rms_norm_plan_destroy(h)
+
+    @property
+    def workspace_bytes(self) -> int:
+        return rms_norm_workspace_size(self)
+
+
+def rms_norm_plan(rows: int, cols: int, dtype, out_dtype=None, eps: float = 1e-6) -> RmsNormPlan:
+    """Plan the norm of [rows, cols]; out_dtype: dtype (the default), "e4m3" or "e5m2"."""
+    i = _dtype_code(dtype)
+    o = i if out_dtype is None else _dtype_code(out_dtype)
+    h = ctypes.c_void_p()
+    _check(lib().rms_norm_plan(rows, cols, i, o, eps, ctypes.byref(h)), "rms_norm_plan")
+    return RmsNormPlan(h.value, rows, cols, i, o)
+
+
+def rms_norm_run(plan: RmsNormPlan, x, out, weight=None, residual=None, residual_out=None,
+                 row_scale=None, rstd=None, stream=None) -> None:
+    """out = the norm of x (+ residual, whose sum goes to residual_out)."""
+    n, f32 = plan.rows * plan.cols, DTYPE["f32"]
+    _check_tensor(x, "x", plan.in_dtype, n)
+    _check_tensor(residual, "residual", plan.in_dtype, n)
+    _check_tensor(weight, "weight", plan.in_dtype, plan.cols)
+    _check_tensor(out, "out", plan.out_dtype, n)
+    _check_tensor(row_scale, "row_scale", f32, plan.rows)
+    _check_tensor(residual_out, "residual_out", plan.in_dtype, n)
+    _check_tensor(rstd, "rstd", f32, plan.rows)
+    _check(lib().rms_norm_run(plan.handle, _addr(x), _addr(residual), _addr(weight), _addr(out),
+                              _addr(row_scale), _addr(residual_out), _addr(rstd),
+                              _stream(stream, x, out)), "rms_norm_run")
+
+
+def rms_norm_workspace_size(plan: RmsNormPlan) -> int:
+    return int(lib().rms_norm_workspace_size(plan.handle))
+
+
+def rms_norm_backward(plan: RmsNormPlan, dy, h, rstd, dx, weight=None, dh=None, dweight=None,
+                      workspace=None, stream=None, workspace_bytes=None) -> None:
+    """dx (and dweight, with a workspace) from dy, the stream h, rstd and dh."""
+    n = plan.rows * plan.cols
+    for t, name, numel in ((dy, "dy", n), (h, "h", n), (weight, "weight", plan.cols),
+                           (dh, "dh", n), (dx, "dx", n), (dweight, "dweight", plan.cols)):
+        _check_tensor(t, name, plan.in_dtype, numel)
+    _check_tensor(rstd, "rstd", DTYPE["f32"], plan.rows)
+    _check_ws_device(workspace)
+    _check(lib().rms_norm_backward(plan.handle, _addr(dy), _addr(h), _addr(weight), _addr(rstd),
+                                   _addr(dh), _addr(dx), _addr(dweight), _addr(workspace),
+                                   _ws_bytes(workspace, workspace_bytes), _stream(stream, dy, dx)),
+           "rms_norm_backward")
+
+
+def quantize_rows(x, q, row_scale, rows=None, cols=None, dtype=None, out_dtype=None,
+                  stream=None) -> None:
+    """fp8 rows q of the 16-bit matrix x [rows, cols] with a scale each; the
+    sizes and types come from the tensors (give them for raw addresses)."""
+    if rows is None:
+        rows, cols = x.shape
+    i = _dtype_code(x.dtype if dtype is None else dtype)
+    o = _dtype_code(q.dtype if out_dtype is None else out_dtype)
+    _check_tensor(x, "x", i, rows * cols)
+    _check_tensor(q, "q", o, rows * cols)
+    _check_tensor(row_scale, "row_scale", DTYPE["f32"], rows)
+    _check(lib().quantize_rows(rows, cols, i, o, _addr(x), _addr(q), _addr(row_scale),
+                               _stream(stream, x, q)), "quantize_rows")

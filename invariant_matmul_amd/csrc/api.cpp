@@ -252,12 +252,6 @@ hipError_t device_ready() {
   return n > 0 ? hipSuccess : hipErrorNoDevice;
 }
 
-// One operand of a call: its first byte and the bytes the kernels touch.
-struct Span {
-  const void* p;
-  size_t bytes;
-};
-
 // True if the span lies in device memory that kernels on device `dev` may
 // access: inside one allocation made on that device, or in managed memory.
 // A pointer the runtime does not know (pageable host memory), host memory,
@@ -361,6 +355,12 @@ int oz_exact_bits(int64_t k, int m3) {
 namespace imm {
 
 gemm_status record_hip_error(hipError_t e) { return hip_fail(e); }
+
+gemm_status check_device_operands(std::initializer_list<Span> spans) {
+  const hipError_t e = device_ready();
+  if (e != hipSuccess) return hip_fail(e);
+  return check_device_spans(spans);
+}
 
 gemm_status check_run_args(const gemm_plan_s* p, const void* A, const void* B, const void* C,
                            const float* bias) {

@@ -3,11 +3,21 @@
 
 #include <hip/hip_runtime.h>
 
+#include <initializer_list>
+
 #include "imm_internal.h"
 
 namespace imm {
 
 // Host-side helpers of the C ABI (api.cpp).
+// One operand of a call: its first byte and the bytes the kernels touch.
+struct Span {
+  const void* p;
+  size_t bytes;
+};
+// A usable device, and every span with a non-null pointer inside one device
+// allocation of the current device (GEMM_ERR_HIP, GEMM_ERR_INVALID_VALUE).
+gemm_status check_device_operands(std::initializer_list<Span> spans);
 // Records a HIP error as the thread's last error; returns GEMM_ERR_HIP.
 gemm_status record_hip_error(hipError_t e);
 // The checks of a run call that need no runtime: plan, NULL and alignment.

@@ -1,0 +1,138 @@
+// Host side of the calls around a linear layer: the row norm, fp8 rows.
+// Validation and launches only; the plans hold sizes and types.
+#include <hip/hip_runtime.h>
+
+#include <climits>
+#include <cmath>
+#include <new>
+
+#include "host_internal.h"
+
+using namespace imm;
+
+struct rms_norm_plan_s {
+  int64_t rows, cols;
+  int in, out;
+  float eps;
+};
+
+namespace {
+
+bool is_f8(int dt) { return dt == GEMM_F8_E4M3 || dt == GEMM_F8_E5M2; }
+bool is_16bit(int dt) { return dt == GEMM_F16 || dt == GEMM_BF16; }
+bool aligned(const void* p, unsigned bytes) {
+  return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0;
+}
+// A required operand: present and aligned.
+bool good(const void* p, unsigned bytes) { return p && aligned(p, bytes); }
+
+gemm_status status_of(hipError_t e) { return e == hipSuccess ? GEMM_OK : record_hip_error(e); }
+
+gemm_status check_rows(int64_t rows, int64_t cols, int in, int out) {
+  if (rows < 0 || cols < 0) return GEMM_ERR_INVALID_VALUE;
+  if (!is_16bit(in) || (out != in && !is_f8(out))) return GEMM_ERR_UNSUPPORTED;
+  if (rows > INT_MAX || cols > kMaxRowCols || cols % (is_f8(out) ? 16 : 8) != 0)
+    return GEMM_ERR_UNSUPPORTED;
+  return GEMM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+gemm_status rms_norm_plan(int64_t rows, int64_t cols, gemm_dtype in, gemm_dtype out, float eps,
+                          rms_norm_plan_t* plan) {
+  if (!plan) return GEMM_ERR_INVALID_VALUE;
+  *plan = nullptr;
+  const gemm_status st = check_rows(rows, cols, in, out);
+  if (st != GEMM_OK) return st;
+  if (!std::isfinite(eps) || eps < 0.0f) return GEMM_ERR_UNSUPPORTED;
+  rms_norm_plan_s* p = new (std::nothrow) rms_norm_plan_s{rows, cols, in, out, eps};
+  if (!p) return GEMM_ERR_INVALID_VALUE;
+  *plan = p;
+  return GEMM_OK;
+}
+
+gemm_status rms_norm_run(rms_norm_plan_t p, const void* x, const void* residual,
+                         const void* weight, void* out, float* row_scale, void* residual_out,
+                         float* rstd, void* stream) {
+  if (!p) return GEMM_ERR_INVALID_VALUE;
+  if (p->rows == 0 || p->cols == 0) return GEMM_OK;
+  const bool f8 = is_f8(p->out);
+  if (!good(x, 16) || !good(out, 16) || !aligned(weight, 16) || !aligned(rstd, 4))
+    return GEMM_ERR_INVALID_VALUE;
+  if (!residual != !residual_out || !aligned(residual, 16) || !aligned(residual_out, 16))
+    return GEMM_ERR_INVALID_VALUE;
+  if (f8 ? !good(row_scale, 4) : row_scale != nullptr) return GEMM_ERR_INVALID_VALUE;
+  const size_t n = (size_t)p->rows * (size_t)p->cols;
+  const size_t per_row = (size_t)p->rows * sizeof(float);
+  const gemm_status st = check_device_operands({{x, 2 * n},
+                                                {residual, 2 * n},
+                                                {weight, 2 * (size_t)p->cols},
+                                                {out, f8 ? n : 2 * n},
+                                                {row_scale, per_row},
+                                                {residual_out, 2 * n},
+                                                {rstd, per_row}});
+  if (st != GEMM_OK) return st;
+  const RmsNormArgs a{x,    residual, weight,  out,     row_scale, residual_out,
+                      rstd, p->rows,  p->cols, p->eps};
+  return status_of(launch_rms_norm(p->in, p->out, true, a, static_cast<hipStream_t>(stream)));
+}
+
+size_t rms_norm_workspace_size(rms_norm_plan_t p) {
+  if (!p || is_f8(p->out)) return 0;
+  return (size_t)rms_norm_backward_parts(p->rows, p->cols) * (size_t)p->cols * sizeof(float);
+}
+
+gemm_status rms_norm_backward(rms_norm_plan_t p, const void* dy, const void* h,
+                              const void* weight, const float* rstd, const void* dh, void* dx,
+                              void* dweight, void* workspace, size_t workspace_bytes,
+                              void* stream) {
+  if (!p) return GEMM_ERR_INVALID_VALUE;
+  if (is_f8(p->out)) return GEMM_ERR_UNSUPPORTED;
+  if (p->cols == 0 || (p->rows == 0 && !dweight)) return GEMM_OK;
+  if (!aligned(dweight, 16)) return GEMM_ERR_INVALID_VALUE;
+  const size_t n = (size_t)p->rows * (size_t)p->cols, need = rms_norm_workspace_size(p);
+  if (p->rows > 0) {
+    if (!good(dy, 16) || !good(h, 16) || !aligned(weight, 16) || !good(rstd, 4) ||
+        !aligned(dh, 16) || !good(dx, 16))
+      return GEMM_ERR_INVALID_VALUE;
+    if (dweight) {
+      if (!workspace || workspace_bytes < need) return GEMM_ERR_WORKSPACE;
+      if (!aligned(workspace, 16)) return GEMM_ERR_INVALID_VALUE;
+    }
+  }
+  const bool any = p->rows > 0;
+  const gemm_status st = check_device_operands({{any ? dy : nullptr, 2 * n},
+                                                {any ? h : nullptr, 2 * n},
+                                                {any ? weight : nullptr, 2 * (size_t)p->cols},
+                                                {any ? rstd : nullptr, (size_t)p->rows * 4},
+                                                {any ? dh : nullptr, 2 * n},
+                                                {any ? dx : nullptr, 2 * n},
+                                                {dweight, 2 * (size_t)p->cols},
+                                                {any && dweight ? workspace : nullptr, need}});
+  if (st != GEMM_OK) return st;
+  const RmsNormBwdArgs a{dy, h,  weight, rstd,
+                         dh, dx, any && dweight ? static_cast<float*>(workspace) : nullptr,
+                         p->rows, p->cols};
+  return status_of(launch_rms_norm_backward(p->in, a, dweight, static_cast<hipStream_t>(stream)));
+}
+
+void rms_norm_plan_destroy(rms_norm_plan_t p) { delete p; }
+
+gemm_status quantize_rows(int64_t rows, int64_t cols, gemm_dtype in, gemm_dtype out, const void* x,
+                          void* q, float* row_scale, void* stream) {
+  if (!is_f8(out)) return GEMM_ERR_UNSUPPORTED;
+  gemm_status st = check_rows(rows, cols, in, out);
+  if (st != GEMM_OK) return st;
+  if (rows == 0 || cols == 0) return GEMM_OK;
+  if (!good(x, 16) || !good(q, 16) || !good(row_scale, 4)) return GEMM_ERR_INVALID_VALUE;
+  const size_t n = (size_t)rows * (size_t)cols;
+  st = check_device_operands({{x, 2 * n}, {q, n}, {row_scale, (size_t)rows * sizeof(float)}});
+  if (st != GEMM_OK) return st;
+  const RmsNormArgs a{x,       nullptr, nullptr, q,   row_scale, nullptr,
+                      nullptr, rows,    cols,    0.0f};
+  return status_of(launch_rms_norm(in, out, false, a, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"
