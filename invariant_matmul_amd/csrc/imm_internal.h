@@ -189,37 +189,4 @@ hipError_t launch_oz_split(int type2, bool per_row, const double* x, int64_t R, 
                            int64_t Ro, int64_t Co, const int32_t* e, int slices, int rho, int delta,
                            void* out, hipStream_t s);
 
-// Row kernels (rms_norm.hip).  cols is a multiple of 8, at most kMaxRowCols;
-// every pointer is 16-byte aligned (row_scale, rstd: 4).
-constexpr int64_t kMaxRowCols = 32768;  // 1024 threads of four 8-element vectors
-// Workgroups of the backward pass (each leaves its parts of dw): two per
-// compute unit of a 256-CU MI355X.
-constexpr int64_t kRmsNormBwdGroups = 512;
-struct RmsNormArgs {
-  const void* x;
-  const void* residual;  // or null
-  const void* weight;    // or null: ones
-  void* out;
-  float* row_scale;      // fp8 outputs
-  void* residual_out;    // with residual
-  float* rstd;           // or null
-  int64_t rows, cols;
-  float eps;
-};
-struct RmsNormBwdArgs {
-  const void* dy;
-  const void* h;
-  const void* weight;    // or null: ones
-  const float* rstd;
-  const void* dh;        // or null
-  void* dx;
-  float* parts;          // [rms_norm_backward_parts, cols], or null: no dw
-  int64_t rows, cols;
-};
-// norm = false: the plain quantisation of rows (out is an fp8 type).
-hipError_t launch_rms_norm(int in, int out, bool norm, const RmsNormArgs& a, hipStream_t s);
-hipError_t launch_rms_norm_backward(int in, const RmsNormBwdArgs& a, void* dweight, hipStream_t s);
-int64_t rms_norm_backward_groups(int64_t rows, int64_t cols);
-int64_t rms_norm_backward_parts(int64_t rows, int64_t cols);
-
 }  // namespace imm

@@ -7,6 +7,7 @@
 #include <new>
 
 #include "host_internal.h"
+#include "layer_internal.h"
 
 using namespace imm;
 

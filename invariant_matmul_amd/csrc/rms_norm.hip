@@ -24,6 +24,7 @@
 // the addition followed by the norm, and the backward pass recomputes from the
 // stored stream exactly what the forward pass normalised.
 #include "kernel_common.h"
+#include "layer_internal.h"
 
 namespace imm {
 namespace {
