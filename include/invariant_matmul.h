@@ -301,6 +301,17 @@ gemm_status gemm_splitk_run_bias(gemm_plan_t plan, const void* A, const void* B,
                                  const float* bias, void* C, void* workspace,
                                  size_t workspace_bytes, void* stream);
 
+/* As gemm_run_bias with one scale per row of A and one per column of B, the
+ * product of fp8 rows that carry their scales (activations
+ * from rms_norm_run or quantize_rows, weights [N, K] with a scale per output):
+ *   C[i, j] = convert(((scale sum_ij) row_scale[i]) col_scale[j] + bias[j]),
+ * each product and the sum rounded in fp32.  row_scale: device fp32 [M],
+ * col_scale: device fp32 [N], 4-byte aligned, both required.  Plans with fp8
+ * inputs and GEMM_PLAN_B_TRANSPOSED only (GEMM_ERR_UNSUPPORTED otherwise);
+ * GEMM_PLAN_PERSISTENT is ignored.  No passage of the pages defines them. */
+gemm_status gemm_run_scaled(gemm_plan_t plan, const void* A, const void* B, const float* row_scale,
+                            const float* col_scale, const float* bias, void* C, void* stream);
+
 /* Frees a host plan (NULL is ignored).  Housekeeping: no passage. */
 void gemm_plan_destroy(gemm_plan_t plan);
 
@@ -435,7 +446,8 @@ void ozaki_plan_destroy(ozaki_plan_t plan);
  *   row_scale = max(max_k |t_k| / FMAX, 2^-120), FMAX = 448 (e4m3) or 57344
  *       (e5m2), and out = round8(t / row_scale): the row is out * row_scale.
  * Row i of every output is a bitwise function of row i of the inputs, the
- * weight, cols and eps.  A row that holds a NaN or an infinity is NaN where
+ * weight, cols and eps.  The sum of squares is fp32: a row with magnitudes above
+ * 2^63 overflows it (rstd = 0).  A row that holds a NaN or an infinity is NaN where
  * the formula is (a 16-bit output), or NaN throughout (an fp8 output, whose
  * row_scale is then infinite or NaN); other rows are unaffected.
  * No passage of the pages defines these calls.
@@ -483,6 +495,45 @@ void rms_norm_plan_destroy(rms_norm_plan_t plan);
  * that no norm precedes, or a weight [N, K] with a scale per output). */
 gemm_status quantize_rows(int64_t rows, int64_t cols, gemm_dtype in, gemm_dtype out, const void* x,
                           void* q, float* row_scale, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Linear layer with 4-bit weights and group scales: y = x W^T + bias with
+ *   W[n, k] = scale[n, g] (q[n, k] - zero[n, g]), g = k / group,
+ * q in 0..15.  x [M, K] and y [M, N] are fp16 or bf16, row-major, contiguous;
+ * N a multiple of 8, K a multiple of group, group 32, 64 or 128.  The sums of
+ * a group run over x and the integers q on the matrix cores in fp32:
+ *   P = sum_k x q, X = sum_k x;  acc = fma(scale, fma(-zero, X, P), acc)
+ * with the groups in ascending order, and y = round(acc + bias): no weight is
+ * rounded.  Row i of y is a bitwise function of row i of x, of the weights and
+ * bias, N, K and group.  A row of x that holds a NaN or an infinity has no
+ * finite element in y.  No passage of the pages defines these calls.
+ * ------------------------------------------------------------------------- */
+typedef struct w4_plan_s* w4_plan_t;
+
+/* Plan y[M, N] = x[M, K] W^T.  dtype: GEMM_F16 or GEMM_BF16 (of x, the scales
+ * and y).  GEMM_ERR_INVALID_VALUE for a negative size or a NULL handle,
+ * GEMM_ERR_UNSUPPORTED for other types, groups or sizes (M up to 2^31 - 1; N
+ * and K below 2^31, and at most 2^31 workgroups). */
+gemm_status w4_plan(int64_t M, int64_t N, int64_t K, gemm_dtype dtype, int group, w4_plan_t* plan);
+
+/* Bytes of the packed weight, which (N, K, group) alone fix: any plan with
+ * the same N, K, dtype and group reads it, whatever its M.  0 for a NULL plan. */
+size_t w4_packed_size(w4_plan_t plan);
+
+/* Lays a weight out for w4_run, once.  q: [N, K / 2] bytes, byte j of a row
+ * holding element 2 j in its low and 2 j + 1 in its high half; scales:
+ * [N, K / group] of the plan's dtype; zeros: [N, K / group] bytes, or NULL for 8
+ * (symmetric weights).  packed: w4_packed_size(plan) bytes, 16-byte aligned
+ * (scales 2-byte). */
+gemm_status w4_pack(w4_plan_t plan, const void* q, const void* scales, const void* zeros,
+                    void* packed, void* stream);
+
+/* y = x W^T + bias on `stream`.  x, packed and y 16-byte aligned; bias: fp32
+ * [N], 4-byte aligned, or NULL. */
+gemm_status w4_run(w4_plan_t plan, const void* x, const void* packed, const float* bias, void* y,
+                   void* stream);
+
+void w4_plan_destroy(w4_plan_t plan);
 
 /* Name of a status ("GEMM_OK", ...); a static string.  Housekeeping. */
 const char* gemm_status_string(gemm_status status);

@@ -17,12 +17,13 @@ is no fallback: if the shared library is missing, importing it raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 __all__ = [
     "GemmError", "Plan", "PlanInfo", "gemm_plan", "gemm_plan_ex", "gemm_plan_ex2",
     "gemm_plan_info", "gemm_workspace_size", "gemm_plan_tile_of", "gemm_run", "gemm_splitk_run",
-    "gemm_splitk_run_noalloc", "NOALLOC_WORKSPACE_BYTES",
+    "gemm_splitk_run_noalloc", "NOALLOC_WORKSPACE_BYTES", "gemm_run_scaled",
     "gemm_plan_destroy", "gemm_status_string", "gemm_last_hip_error", "mm", "out_torch_dtype",
     "lib", "LIB_PATH",
     "DTYPE", "TILE", "STATUS", "EXPORTED_SYMBOLS", "PLAN_B_TRANSPOSED", "PLAN_PERSISTENT",
@@ -30,7 +31,7 @@ __all__ = [
     "OzakiPlan", "ozaki_plan", "ozaki_plan_info", "ozaki_workspace_size", "ozaki_split",
     "ozaki_multiply", "ozaki_run", "ozaki_mm",
     "LAYER_SYMBOLS", "RmsNormPlan", "rms_norm_plan", "rms_norm_run", "rms_norm_workspace_size",
-    "rms_norm_backward", "quantize_rows",
+    "rms_norm_backward", "quantize_rows", "W4Plan", "w4_plan", "w4_packed_size", "w4_pack", "w4_run",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libinvariant_matmul.so")
@@ -50,13 +51,15 @@ EXPORTED_SYMBOLS = (
     "gemm_plan", "gemm_plan_ex", "gemm_plan_ex2", "gemm_plan_info", "gemm_workspace_size",
     "gemm_plan_tile_of", "gemm_run", "gemm_run_bias", "gemm_splitk_run", "gemm_splitk_run_bias",
     "gemm_plan_destroy", "gemm_status_string", "gemm_last_hip_error", "gemm_splitk_run_noalloc",
+    "gemm_run_scaled",
     "ozaki_plan", "ozaki_plan_info", "ozaki_workspace_size", "ozaki_split", "ozaki_multiply",
     "ozaki_run", "ozaki_plan_destroy",
 )
-# The calls around a linear layer: the row norm and fp8 rows.
+# The calls around a linear layer: the row norm, fp8 rows and 4-bit weights.
 LAYER_SYMBOLS = (
     "rms_norm_plan", "rms_norm_run", "rms_norm_workspace_size", "rms_norm_backward",
-    "rms_norm_plan_destroy", "quantize_rows",
+    "rms_norm_plan_destroy", "quantize_rows", "w4_plan", "w4_packed_size", "w4_pack", "w4_run",
+    "w4_plan_destroy",
 )
 
 
@@ -135,6 +138,7 @@ def lib() -> ctypes.CDLL:
         L.gemm_splitk_run.argtypes = [vp, vp, vp, vp, vp, ctypes.c_size_t, vp]
         L.gemm_splitk_run_bias.argtypes = [vp, vp, vp, vp, vp, vp, ctypes.c_size_t, vp]
         L.gemm_splitk_run_noalloc.argtypes = [vp, vp, vp, vp, vp]
+        L.gemm_run_scaled.argtypes = [vp] * 8
         L.gemm_plan_destroy.argtypes = [vp]
         L.gemm_plan_destroy.restype = None
         L.gemm_status_string.argtypes = [i32]
@@ -158,8 +162,15 @@ def lib() -> ctypes.CDLL:
         L.rms_norm_plan_destroy.argtypes = [vp]
         L.rms_norm_plan_destroy.restype = None
         L.quantize_rows.argtypes = [i64, i64, i32, i32, vp, vp, vp, vp]
-        for f in ("rms_norm_plan", "rms_norm_run", "rms_norm_backward", "quantize_rows",
-                  "gemm_plan", "gemm_plan_ex", "gemm_plan_ex2", "gemm_plan_info",
+        L.w4_plan.argtypes = [i64, i64, i64, i32, i32, pp]
+        L.w4_packed_size.argtypes = [vp]
+        L.w4_packed_size.restype = sz
+        L.w4_pack.argtypes = [vp] * 6
+        L.w4_run.argtypes = [vp] * 6
+        L.w4_plan_destroy.argtypes = [vp]
+        L.w4_plan_destroy.restype = None
+        for f in ("gemm_run_scaled", "rms_norm_plan", "rms_norm_run", "rms_norm_backward",
+                  "quantize_rows", "w4_plan", "w4_pack", "w4_run", "gemm_plan", "gemm_plan_ex", "gemm_plan_ex2", "gemm_plan_info",
                   "gemm_plan_tile_of", "gemm_run", "gemm_run_bias", "gemm_splitk_run",
                   "gemm_splitk_run_bias", "gemm_splitk_run_noalloc", "gemm_last_hip_error", "ozaki_plan", "ozaki_plan_info",
                   "ozaki_split", "ozaki_multiply", "ozaki_run"):
@@ -197,6 +208,11 @@ class Plan:
 
     @property
     def info(self) -> dict:
+        return gemm_plan_info(self)
+
+    @functools.cached_property
+    def fixed(self) -> dict:
+        """The plan's information, read once (a plan never changes)."""
         return gemm_plan_info(self)
 
     @property
@@ -342,6 +358,21 @@ def gemm_splitk_run_noalloc(plan: Plan, A, B, C, stream=None) -> None:
                            f"bytes, more than the library's {NOALLOC_WORKSPACE_BYTES}")
     _check(lib().gemm_splitk_run_noalloc(plan.handle, _addr(A), _addr(B), _addr(C),
                                          _stream(stream, A, B, C)), "gemm_splitk_run_noalloc")
+
+
+def gemm_run_scaled(plan: Plan, A, B, row_scale, col_scale, C, stream=None, bias=None) -> None:
+    """C = (A @ B) * row_scale[:, None] * col_scale (+ bias) in one pass (fp8
+    inputs, B transposed)."""
+    i = plan.fixed
+    _check_tensor(A, "A", i["in_dtype"], i["M"] * i["K"])
+    _check_tensor(B, "B", i["in_dtype"], i["K"] * i["N"])
+    _check_tensor(C, "C", i["out_dtype"], i["M"] * i["N"])
+    _check_tensor(bias, "bias", DTYPE["f32"], i["N"])
+    _check_tensor(row_scale, "row_scale", DTYPE["f32"], i["M"])
+    _check_tensor(col_scale, "col_scale", DTYPE["f32"], i["N"])
+    _check(lib().gemm_run_scaled(plan.handle, _addr(A), _addr(B), _addr(row_scale),
+                                 _addr(col_scale), _addr(bias), _addr(C), _stream(stream, A, B, C)),
+           "gemm_run_scaled")
 
 
 def gemm_plan_destroy(plan: Plan) -> None:
@@ -579,3 +610,61 @@ def quantize_rows(x, q, row_scale, rows=None, cols=None, dtype=None, out_dtype=N
     _check_tensor(row_scale, "row_scale", DTYPE["f32"], rows)
     _check(lib().quantize_rows(rows, cols, i, o, _addr(x), _addr(q), _addr(row_scale),
                                _stream(stream, x, q)), "quantize_rows")
+
+
+# ---- 4-bit weights ----------------------------------------------------------------
+
+class W4Plan:
+    """Owns a w4_plan_t; destroyed with the object."""
+
+    def __init__(self, handle: int, M: int, N: int, K: int, dtype: int, group: int):
+        self.handle = handle
+        self.M, self.N, self.K = M, N, K
+        self.dtype, self.group = dtype, group
+        self._lib = lib()
+
+    def __del__(self):
+        h, self.handle = getattr(self, "handle", None), None
+        if h:
+            self._lib.w4_plan_destroy(h)
+
+
+def w4_plan(M: int, N: int, K: int, dtype, group: int = 128) -> W4Plan:
+    """Plan y [M, N] = x [M, K] @ W^T with 4-bit weights in groups of 32, 64 or 128."""
+    d = _dtype_code(dtype)
+    h = ctypes.c_void_p()
+    _check(lib().w4_plan(M, N, K, d, group, ctypes.byref(h)), "w4_plan")
+    return W4Plan(h.value, M, N, K, d, group)
+
+
+def w4_packed_size(plan: W4Plan) -> int:
+    return int(lib().w4_packed_size(plan.handle))
+
+
+def _check_bytes(t, name, nbytes):
+    if t is None or isinstance(t, int):
+        return
+    if not t.is_contiguous() or t.element_size() != 1 or t.numel() != nbytes:
+        raise ValueError(f"{name} must be a contiguous tensor of {nbytes} bytes")
+    _check_device(t, name)
+
+
+def w4_pack(plan: W4Plan, q, scales, packed, zeros=None, stream=None) -> None:
+    """Lay out q [N, K / 2] bytes, scales and zeros [N, K / group] into packed."""
+    pairs = plan.N * (plan.K // plan.group)
+    _check_bytes(q, "q", plan.N * plan.K // 2)
+    _check_tensor(scales, "scales", plan.dtype, pairs)
+    _check_bytes(zeros, "zeros", pairs)
+    _check_bytes(packed, "packed", w4_packed_size(plan))
+    _check(lib().w4_pack(plan.handle, _addr(q), _addr(scales), _addr(zeros), _addr(packed),
+                         _stream(stream, q, packed)), "w4_pack")
+
+
+def w4_run(plan: W4Plan, x, packed, y, bias=None, stream=None) -> None:
+    """y = x @ W^T (+ bias, an fp32 vector of N) from the packed weight."""
+    _check_tensor(x, "x", plan.dtype, plan.M * plan.K)
+    _check_bytes(packed, "packed", w4_packed_size(plan))
+    _check_tensor(y, "y", plan.dtype, plan.M * plan.N)
+    _check_tensor(bias, "bias", DTYPE["f32"], plan.N)
+    _check(lib().w4_run(plan.handle, _addr(x), _addr(packed), _addr(bias), _addr(y),
+                        _stream(stream, x, y)), "w4_run")

@@ -618,6 +618,27 @@ gemm_status gemm_splitk_run_bias(gemm_plan_t p, const void* A, const void* B, co
                          static_cast<hipStream_t>(stream));
 }
 
+gemm_status gemm_run_scaled(gemm_plan_t p, const void* A, const void* B, const float* row_scale,
+                            const float* col_scale, const float* bias, void* C, void* stream) {
+  gemm_status st = check_run_args(p, A, B, C, bias);
+  if (st != GEMM_OK) return st;
+  if (elem_bytes(p->in) != 1 || !p->b_trans) return GEMM_ERR_UNSUPPORTED;
+  if (p->M == 0 || p->N == 0) return GEMM_OK;
+  if (!row_scale || !col_scale || !aligned4(row_scale) || !aligned4(col_scale))
+    return GEMM_ERR_INVALID_VALUE;
+  st = check_device_operands({{row_scale, (size_t)p->M * sizeof(float)},
+                              {col_scale, (size_t)p->N * sizeof(float)}});
+  if (st == GEMM_OK) st = check_gemm_spans(p, A, B, C, bias, nullptr, 0);
+  if (st != GEMM_OK) return st;
+  ScaledArgs a;
+  static_cast<GemmArgs&>(a) = make_args(p, A, B, C, false);
+  a.bias = bias;
+  a.row_scale = row_scale;
+  a.col_scale = col_scale;
+  const hipError_t e = launch_gemm_scaled(*p, p->run_tile, a, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? GEMM_OK : hip_fail(e);
+}
+
 void gemm_plan_destroy(gemm_plan_t p) { delete p; }
 
 gemm_status ozaki_plan(int64_t M, int64_t N, int64_t K, gemm_dtype type2, int slices, int d,

@@ -345,6 +345,8 @@ __global__ __launch_bounds__(WM * WN * 64, (waves_per_simd<TBM, TBN, WM, WN, NS>
   // 16x16x32 fp16 step over the fp8 LDS layout, 8 bytes of K per lane
   constexpr bool W16 = T::W16;
   static_assert(!W16 || MODE != MODE_OZAKI, "widened fp8 in an Ozaki pass");
+  // row and column scales in the epilogue (MODE_STORE of fp8 inputs)
+  constexpr bool SCALED = std::is_base_of<ScaledArgs, ARGS>::value;
   constexpr bool F8S = EB == 1 && !T::I8 && !W16 && MODE != MODE_OZAKI;
   constexpr bool B16 = M16 || F8S || W16;    // 16 x 16 output blocks
   constexpr int BLK = B16 ? 16 : 32;         // MFMA output block edge
@@ -815,10 +817,13 @@ __global__ __launch_bounds__(WM * WN * 64, (waves_per_simd<TBM, TBN, WM, WN, NS>
         const unsigned loff = (unsigned)(lrow * (int)g.N + lcol) * OB;
         auto body = [&](auto plain) {
 #pragma clang fp contract(off)
-          float bv[FN];
+          float bv[FN], cs[FN];
           if constexpr (!decltype(plain)::value) {
 #pragma unroll
-            for (int j = 0; j < FN; ++j) bv[j] = g.bias ? g.bias[tn0 + lcol + j * BLK] : 0.0f;
+            for (int j = 0; j < FN; ++j) {
+              bv[j] = g.bias ? g.bias[tn0 + lcol + j * BLK] : 0.0f;
+              if constexpr (SCALED) cs[j] = g.col_scale[tn0 + lcol + j * BLK];
+            }
           }
 #pragma unroll
           for (int i = 0; i < FM; ++i) {
@@ -826,11 +831,14 @@ __global__ __launch_bounds__(WM * WN * 64, (waves_per_simd<TBM, TBN, WM, WN, NS>
             for (int r = 0; r < NACC; ++r) {
               const int rr = i * BLK + (B16 ? r : 8 * (r >> 2) + (r & 3));
               char* const rb = base + (int64_t)rr * g.N * OB;
+              float rs = 1.0f;
+              if constexpr (SCALED) rs = g.row_scale[tm0 + lrow + rr];
 #pragma unroll
               for (int j = 0; j < FN; ++j) {
                 float v = acc[i][j][r];
                 if constexpr (!decltype(plain)::value) {
                   v = g.scale == 1.0f ? v : v * g.scale;
+                  if constexpr (SCALED) v = (v * rs) * cs[j];
                   if (g.bias) v = v + bv[j];
                 }
                 char* const p = rb + j * BLK * OB + loff;
@@ -842,7 +850,7 @@ __global__ __launch_bounds__(WM * WN * 64, (waves_per_simd<TBM, TBN, WM, WN, NS>
             }
           }
         };
-        if (MODE == MODE_SLICE || (g.scale == 1.0f && !g.bias))
+        if (MODE == MODE_SLICE || (!SCALED && g.scale == 1.0f && !g.bias))
           body(std::true_type{});
         else if constexpr (MODE != MODE_SLICE)
           body(std::false_type{});
@@ -871,6 +879,11 @@ __global__ __launch_bounds__(WM * WN * 64, (waves_per_simd<TBM, TBN, WM, WN, NS>
             const float v = acc[i][j][r];
             if constexpr (MODE == MODE_SLICE) {
               static_cast<float*>(g.C)[(ksl * g.M + row) * g.N + col] = v;
+            } else if constexpr (SCALED) {
+#pragma clang fp contract(off)
+              float s = g.scale == 1.0f ? v : v * g.scale;
+              s = (s * g.row_scale[row]) * g.col_scale[col];
+              store_final<OUT>(g.C, row * g.N + col, s, 1.0f, g.bias, col);
             } else {
               store_final<OUT>(g.C, row * g.N + col, v, g.scale, g.bias, col);
             }
@@ -1235,6 +1248,33 @@ hipError_t launch_cfg(const gemm_plan_s& p, const GemmArgs& a, bool slice, hipSt
   return hipGetLastError();
 }
 
+// The single pass with row and column scales: fp8 inputs, B transposed.
+template <int IN, int TBM, int WM, int NS>
+hipError_t launch_scaled_cfg(const gemm_plan_s& p, const ScaledArgs& a, hipStream_t s) {
+  const dim3 grid((unsigned)a.grid), block(WM * 4 * 64);
+  if (p.out == GEMM_F32)
+    hipLaunchKernelGGL((gemm_dma_kernel<IN, GEMM_F32, MODE_STORE, TBM, WIDE_TBN, WM, 4, NS, true,
+                                        ScaledArgs>), grid, block, 0, s, a);
+  else if (p.out == GEMM_F16)
+    hipLaunchKernelGGL((gemm_dma_kernel<IN, GEMM_F16, MODE_STORE, TBM, WIDE_TBN, WM, 4, NS, true,
+                                        ScaledArgs>), grid, block, 0, s, a);
+  else
+    hipLaunchKernelGGL((gemm_dma_kernel<IN, GEMM_BF16, MODE_STORE, TBM, WIDE_TBN, WM, 4, NS, true,
+                                        ScaledArgs>), grid, block, 0, s, a);
+  return hipGetLastError();
+}
+
+template <int IN>
+hipError_t launch_scaled_in(const gemm_plan_s& p, int tile, const ScaledArgs& a, hipStream_t s) {
+  switch (tile) {
+    case GEMM_TILE_256x256: return launch_scaled_cfg<IN, 256, 2, 2>(p, a, s);
+    case GEMM_TILE_128x256: return launch_scaled_cfg<IN, 128, 2, 3>(p, a, s);
+    case GEMM_TILE_64x256: return launch_scaled_cfg<IN, 64, 1, 4>(p, a, s);
+    case GEMM_TILE_32x256: return launch_scaled_cfg<IN, 32, 1, 4>(p, a, s);
+    default: return hipErrorInvalidValue;
+  }
+}
+
 // Persistent single pass on the 256 x 256 tile.
 template <int IN, bool BT>
 hipError_t launch_persist_in(const gemm_plan_s& p, const PersistArgs& a, hipStream_t s) {
@@ -1306,6 +1346,18 @@ hipError_t launch_ozaki_gemm(int type2, const OzGemmArgs& a, hipStream_t s) {
   else
     return hipErrorInvalidValue;
   return hipGetLastError();
+}
+
+hipError_t launch_gemm_scaled(const gemm_plan_s& p, int tile, const ScaledArgs& a, hipStream_t s) {
+  switch (p.in) {
+    case GEMM_F8_E4M3:
+      return p.f8_fp32 ? launch_scaled_in<kInE4M3W>(p, tile, a, s)
+                       : launch_scaled_in<GEMM_F8_E4M3>(p, tile, a, s);
+    case GEMM_F8_E5M2:
+      return p.f8_fp32 ? launch_scaled_in<kInE5M2W>(p, tile, a, s)
+                       : launch_scaled_in<GEMM_F8_E5M2>(p, tile, a, s);
+    default: return hipErrorInvalidValue;
+  }
 }
 
 hipError_t launch_gemm_persist(const gemm_plan_s& p, const PersistArgs& a, hipStream_t s) {

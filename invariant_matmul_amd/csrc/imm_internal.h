@@ -146,6 +146,13 @@ struct PersistArgs : GemmArgs {
   int64_t wgs;
 };
 
+// A product whose epilogue also multiplies by one scale per row of A and one per
+// column of B (fp8 rows with scales): C = ((scale sum) row_scale) col_scale + bias.
+struct ScaledArgs : GemmArgs {
+  const float* row_scale;  // fp32 [M]
+  const float* col_scale;  // fp32 [N]
+};
+
 struct ReduceArgs {
   const float* ws;
   void* C;
@@ -165,6 +172,9 @@ hipError_t launch_reduce(const gemm_plan_s& p, const ReduceArgs& a, hipStream_t 
 // The DMA-fed kernels (gemm_dma.hip); launch_gemm forwards the DMA tiles to it.
 hipError_t launch_gemm_dma(const gemm_plan_s& p, int tile, const GemmArgs& a, bool slice_mode,
                            hipStream_t s);
+// The single pass of fp8 inputs, B transposed, with row and column scales
+// (gemm_dma.hip).
+hipError_t launch_gemm_scaled(const gemm_plan_s& p, int tile, const ScaledArgs& a, hipStream_t s);
 // The persistent single pass on the 256 x 256 DMA tile (gemm_dma.hip).
 hipError_t launch_gemm_persist(const gemm_plan_s& p, const PersistArgs& a, hipStream_t s);
 // The Ozaki slice-pair product on the DMA kernel (gemm_dma.hip); type2 is

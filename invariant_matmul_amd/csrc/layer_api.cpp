@@ -1,4 +1,5 @@
-// Host side of the calls around a linear layer: the row norm, fp8 rows.
+// Host side of the calls around a linear layer: the row norm, fp8 rows, 4-bit
+// weights.
 // Validation and launches only; the plans hold sizes and types.
 #include <hip/hip_runtime.h>
 
@@ -15,6 +16,12 @@ struct rms_norm_plan_s {
   int64_t rows, cols;
   int in, out;
   float eps;
+};
+
+struct w4_plan_s {
+  int64_t M, N, K;
+  int dtype, group;
+  int64_t nblocks, kblocks, groups;  // of 16 outputs, of 128 K, of `group` K
 };
 
 namespace {
@@ -135,5 +142,67 @@ gemm_status quantize_rows(int64_t rows, int64_t cols, gemm_dtype in, gemm_dtype 
                       nullptr, rows,    cols,    0.0f};
   return status_of(launch_rms_norm(in, out, false, a, static_cast<hipStream_t>(stream)));
 }
+
+gemm_status w4_plan(int64_t M, int64_t N, int64_t K, gemm_dtype dtype, int group, w4_plan_t* plan) {
+  if (!plan) return GEMM_ERR_INVALID_VALUE;
+  *plan = nullptr;
+  if (M < 0 || N < 0 || K < 0) return GEMM_ERR_INVALID_VALUE;
+  if (!is_16bit(dtype) || (group != 32 && group != 64 && group != 128)) return GEMM_ERR_UNSUPPORTED;
+  if (M > INT_MAX || N > INT_MAX || K > INT_MAX || N % 8 != 0 || K % group != 0)
+    return GEMM_ERR_UNSUPPORTED;
+  const int64_t nblocks = (N + 15) / 16, kblocks = (K + 127) / 128, groups = K / group;
+  // one workgroup per 16 x 16 outputs at most, one packing thread per dword
+  if (nblocks * ((M + 15) / 16) > INT_MAX || nblocks * kblocks > INT_MAX ||
+      nblocks * groups > INT_MAX)
+    return GEMM_ERR_UNSUPPORTED;
+  w4_plan_s* p = new (std::nothrow) w4_plan_s{M, N, K, dtype, group, nblocks, kblocks, groups};
+  if (!p) return GEMM_ERR_INVALID_VALUE;
+  *plan = p;
+  return GEMM_OK;
+}
+
+size_t w4_packed_size(w4_plan_t p) {
+  if (!p) return 0;
+  return (size_t)p->nblocks * ((size_t)p->kblocks * 1024 + (size_t)p->groups * 64);
+}
+
+gemm_status w4_pack(w4_plan_t p, const void* q, const void* scales, const void* zeros,
+                    void* packed, void* stream) {
+  if (!p) return GEMM_ERR_INVALID_VALUE;
+  if (p->N == 0 || p->K == 0) return GEMM_OK;
+  if (!q || !good(scales, 2) || !good(packed, 16)) return GEMM_ERR_INVALID_VALUE;
+  const size_t pairs = (size_t)p->N * (size_t)p->groups;
+  const gemm_status st = check_device_operands({{q, (size_t)p->N * (size_t)p->K / 2},
+                                                {scales, 2 * pairs},
+                                                {zeros, pairs},
+                                                {packed, w4_packed_size(p)}});
+  if (st != GEMM_OK) return st;
+  return status_of(launch_w4_pack(p->N, p->K, p->group, q, scales, zeros, packed,
+                                  static_cast<hipStream_t>(stream)));
+}
+
+gemm_status w4_run(w4_plan_t p, const void* x, const void* packed, const float* bias, void* y,
+                   void* stream) {
+  if (!p) return GEMM_ERR_INVALID_VALUE;
+  if (p->M == 0 || p->N == 0) return GEMM_OK;
+  if (!good(y, 16) || !aligned(bias, 4)) return GEMM_ERR_INVALID_VALUE;
+  const bool any = p->K > 0;
+  if (any && (!good(x, 16) || !good(packed, 16))) return GEMM_ERR_INVALID_VALUE;
+  const size_t M = (size_t)p->M, N = (size_t)p->N, K = (size_t)p->K;
+  const gemm_status st = check_device_operands({{any ? x : nullptr, 2 * M * K},
+                                                {any ? packed : nullptr, w4_packed_size(p)},
+                                                {bias, N * sizeof(float)},
+                                                {y, 2 * M * N}});
+  if (st != GEMM_OK) return st;
+  const char* const sz = static_cast<const char*>(packed) + p->nblocks * p->kblocks * 1024;
+  const W4Args a{x,    packed, reinterpret_cast<const unsigned*>(any ? sz : nullptr),
+                 bias, y,      p->M,
+                 p->N, p->K,   p->nblocks,
+                 p->kblocks,   p->groups,
+                 p->group};
+  return status_of(launch_w4(p->dtype, a, static_cast<hipStream_t>(stream)));
+}
+
+void w4_plan_destroy(w4_plan_t p) { delete p; }
 
 }  // extern "C"

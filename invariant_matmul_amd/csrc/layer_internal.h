@@ -39,4 +39,20 @@ hipError_t launch_rms_norm_backward(int in, const RmsNormBwdArgs& a, void* dweig
 int64_t rms_norm_backward_groups(int64_t rows, int64_t cols);
 int64_t rms_norm_backward_parts(int64_t rows, int64_t cols);
 
+// 4-bit weights (w4.hip).  packed: nblocks x kblocks blocks of 16 outputs x 128 K
+// (1 KB each), followed by sz [groups, 16 nblocks].
+struct W4Args {
+  const void* x;         // [M, K]
+  const void* packed;
+  const unsigned* sz;
+  const float* bias;     // fp32 [N] or null
+  void* y;               // [M, N]
+  int64_t M, N, K;
+  int64_t nblocks, kblocks, groups;
+  int group;
+};
+hipError_t launch_w4_pack(int64_t N, int64_t K, int group, const void* q, const void* scales,
+                          const void* zeros, void* packed, hipStream_t s);
+hipError_t launch_w4(int in, const W4Args& a, hipStream_t s);
+
 }  // namespace imm

@@ -46,8 +46,13 @@ The operators around a linear layer keep the same promise, row by row:
     q, s, h = torch_ops.rms_norm_quant(x, w, residual=r)  # fp8 rows and their scales
 
 rms_norm takes part in autograd (its backward pass is a kernel of the library;
-the weight's gradient is the one result that sums over rows).  The fp8 form
-and quantize_rows are for serving: they refuse inputs that require a gradient.
+the weight's gradient is the one result that sums over rows).  The others are
+for serving and refuse inputs that require a gradient:
+
+    wq, ws = torch_ops.quantize_rows(W)                # once
+    y = torch_ops.linear_f8(q, s, wq, ws)              # fp8 rows and their scales
+    w4 = torch_ops.pack_w4(q4, scales, zeros)          # once
+    y = torch_ops.linear_w4(x, w4, bias)               # 4-bit weights
 """
 from __future__ import annotations
 
@@ -58,14 +63,13 @@ import warnings
 
 import torch
 
-from . import (PLAN_B_TRANSPOSED, PLAN_TILE_BY_M, gemm_plan_ex2, gemm_run, gemm_splitk_run,
-               gemm_workspace_size, ozaki_plan, ozaki_run, ozaki_workspace_size, rms_norm_plan)
-from . import quantize_rows as _quantize_rows
-from . import rms_norm_backward as _rms_norm_backward
-from . import rms_norm_run as _rms_norm_run
+from . import (PLAN_B_TRANSPOSED, PLAN_FP8_FP32_ACCUM, PLAN_TILE_BY_M, GemmError, _dtype_code,
+               gemm_plan_ex2, gemm_run, gemm_splitk_run, gemm_workspace_size, lib, ozaki_plan,
+               ozaki_run, ozaki_workspace_size, rms_norm_plan, w4_packed_size, w4_plan)
 
 __all__ = ["mm", "addmm", "linear", "matmul", "batch_invariant_mode", "supported",
-           "rms_norm", "rms_norm_forward", "rms_norm_backward", "rms_norm_quant", "quantize_rows"]
+           "rms_norm", "rms_norm_forward", "rms_norm_backward", "rms_norm_quant", "quantize_rows",
+           "linear_f8", "W4Weight", "pack_w4", "linear_w4"]
 
 _DT = {torch.float16: "f16", torch.bfloat16: "bf16"}
 
@@ -211,7 +215,12 @@ def _mode_addmm(bias, a, b, *, beta=1, alpha=1):
     return r + (bias if beta == 1 else bias * beta)
 
 
-# ---- Row norm and fp8 rows ------------------------------------------------------
+# ---- Row norm, fp8 rows, 4-bit weights --------------------------------------------
+#
+# These operators check their tensors here and hand addresses straight to the
+# C ABI (which checks the memory behind them): a decode step calls them with a
+# few microseconds of GPU work each, where a second round of checks would cost
+# more than the kernel.
 
 _F8 = (torch.float8_e4m3fn, torch.float8_e5m2)
 
@@ -221,11 +230,46 @@ def _norm_plan(rows: int, cols: int, dtype, out_dtype, eps: float):
     return rms_norm_plan(rows, cols, dtype, out_dtype, eps)
 
 
+@functools.lru_cache(maxsize=512)
+def _f8_plan(M: int, N: int, K: int, dtype, out_dtype, flags: int):
+    # one pass, never a split of K: its bits are those of every M, and a split
+    # workspace [split, M, N] would cost a long batch more than the product
+    return gemm_plan_ex2(M, N, K, dtype, out_dtype, split_k=1, flags=flags)
+
+
+@functools.lru_cache(maxsize=512)
+def _w4_plan(M: int, N: int, K: int, dtype, group: int):
+    return w4_plan(M, N, K, dtype, group)
+
+
 def _dense(t: torch.Tensor) -> torch.Tensor:
     """t itself if the kernels can read it in place (contiguous, 16-byte
     aligned), else a copy."""
     t = t.contiguous()
     return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
+def _ptr(t) -> int:
+    return 0 if t is None else t.data_ptr()
+
+
+def _stream_of(where: str, device) -> int:
+    """The current stream of the current device, which must be the tensors'."""
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"{where}: the tensors are on {device}, but the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _done(status: int, where: str):
+    if status:
+        raise GemmError(status, where)
+
+
+def _refuse_grad(where: str, *tensors):
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        raise ValueError(f"{where} has no backward pass: call it under torch.no_grad() or with "
+                         "detached tensors")
 
 
 def _check_norm(where: str, x, weight, residual):
@@ -240,32 +284,34 @@ def _check_norm(where: str, x, weight, residual):
         raise ValueError(f"{where}: residual must have the shape, type and device of x")
 
 
-def _refuse_grad(where: str, *tensors):
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
-        raise ValueError(f"{where} has no backward pass: call it under torch.no_grad() or with "
-                         "detached tensors")
+def _check_f8_rows(where: str, x, dtype):
+    if dtype not in _F8 or x.shape[-1] % 16 != 0:
+        raise ValueError(f"{where}: dtype must be float8_e4m3fn or float8_e5m2 and the last size a "
+                         "multiple of 16")
 
 
-def _norm(x, weight, eps, residual, out_dtype, want_rstd):
+def _norm(where, x, weight, eps, residual, out_dtype, want_rstd):
     """(out, stream, row_scale or None, rstd or None), the outputs new tensors."""
+    stream = _stream_of(where, x.device)
     cols = x.shape[-1]
     rows = x.numel() // cols if cols else 0
-    out = torch.empty(x.shape, dtype=out_dtype, device=x.device)
-    h = x if residual is None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    lead = x.shape[:-1]
+    plan = _norm_plan(rows, cols, x.dtype, out_dtype, eps)
+    x = _dense(x)
+    out = torch.empty_like(x, dtype=out_dtype)
+    h = x if residual is None else torch.empty_like(x)
     scale = rstd = None
     if out_dtype in _F8:
-        scale = torch.empty(lead, dtype=torch.float32, device=x.device)
+        scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
     if want_rstd:
-        rstd = torch.empty(lead, dtype=torch.float32, device=x.device)
-    plan = _norm_plan(rows, cols, x.dtype, out_dtype, float(eps))
+        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
     if rows:
-        x = _dense(x)
-        if residual is None:
-            h = x
-        _rms_norm_run(plan, x, out, None if weight is None else _dense(weight),
-                      None if residual is None else _dense(residual),
-                      None if residual is None else h, scale, rstd)
+        if weight is not None:
+            weight = _dense(weight)
+        if residual is not None:
+            residual = _dense(residual)
+        _done(lib().rms_norm_run(plan.handle, x.data_ptr(), _ptr(residual), _ptr(weight),
+                                 out.data_ptr(), _ptr(scale), 0 if residual is None else h.data_ptr(),
+                                 _ptr(rstd), stream), where)
     return out, h, scale, rstd
 
 
@@ -274,7 +320,7 @@ def rms_norm_forward(x: torch.Tensor, weight=None, eps: float = 1e-6, residual=N
     and the fp32 reciprocal root mean square of each row of h, which
     rms_norm_backward takes.  No autograd: rms_norm is the differentiable form."""
     _check_norm("rms_norm_forward", x, weight, residual)
-    y, h, _, rstd = _norm(x, weight, eps, residual, x.dtype, True)
+    y, h, _, rstd = _norm("rms_norm_forward", x, weight, eps, residual, x.dtype, True)
     return y, h, rstd
 
 
@@ -283,30 +329,38 @@ def rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight, rstd: torch.Ten
     """(dx, dweight) of rms_norm_forward: dy is the gradient of y, dh the gradient
     of h from its other uses (or None).  dx is the gradient of x and of the
     residual alike; dweight is None without a weight or with weight_grad=False."""
-    _check_norm("rms_norm_backward", h, weight, dy)
+    where = "rms_norm_backward"
+    _check_norm(where, h, weight, dy)
     if dh is not None:
-        _check_norm("rms_norm_backward", h, None, dh)
+        _check_norm(where, h, None, dh)
     if rstd.dtype != torch.float32 or rstd.shape != h.shape[:-1] or rstd.device != h.device:
         raise ValueError("rms_norm_backward: rstd must hold one float32 value per row of h")
+    stream = _stream_of(where, h.device)
     cols = h.shape[-1]
     rows = h.numel() // cols if cols else 0
-    dx = torch.empty(h.shape, dtype=h.dtype, device=h.device)
-    dw = ws = None
     plan = _norm_plan(rows, cols, h.dtype, h.dtype, 0.0)  # eps acts through rstd alone
-    if weight is not None and weight_grad:
-        dw = torch.empty(cols, dtype=h.dtype, device=h.device)
-        if rows:
-            ws = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device=h.device)
-    _rms_norm_backward(plan, _dense(dy), _dense(h), rstd.contiguous(), dx,
-                       None if weight is None else _dense(weight),
-                       None if dh is None else _dense(dh), dw, ws)
+    dy, h, rstd = _dense(dy), _dense(h), rstd.contiguous()
+    dx = torch.empty_like(h)
+    dw = ws = None
+    nws = 0
+    if weight is not None:
+        weight = _dense(weight)
+        if weight_grad:
+            dw = torch.empty_like(weight)
+            nws = plan.workspace_bytes
+            ws = torch.empty(nws, dtype=torch.uint8, device=h.device)
+    if dh is not None:
+        dh = _dense(dh)
+    _done(lib().rms_norm_backward(plan.handle, dy.data_ptr(), h.data_ptr(), _ptr(weight),
+                                  rstd.data_ptr(), _ptr(dh), dx.data_ptr(), _ptr(dw), _ptr(ws), nws,
+                                  stream), where)
     return dx, dw
 
 
 class _RmsNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, residual, eps):
-        y, h, _, rstd = _norm(x, weight, eps, residual, x.dtype, True)
+        y, h, _, rstd = _norm("rms_norm", x, weight, eps, residual, x.dtype, True)
         ctx.save_for_backward(h, weight, rstd)
         ctx.set_materialize_grads(False)
         return (y, h) if residual is not None else y
@@ -330,10 +384,10 @@ def rms_norm(x: torch.Tensor, weight=None, eps: float = 1e-6, residual=None):
     size a multiple of 8 and at most 32768; statistics are fp32.  Row i of the
     result depends on row i alone.  Differentiable."""
     _check_norm("rms_norm", x, weight, residual)
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad
-                                       for t in (x, weight, residual)):
+    if torch.is_grad_enabled() and (x.requires_grad or (weight is not None and weight.requires_grad)
+                                    or (residual is not None and residual.requires_grad)):
         return _RmsNorm.apply(x, weight, residual, eps)
-    y, h, _, _ = _norm(x, weight, eps, residual, x.dtype, False)
+    y, h, _, _ = _norm("rms_norm", x, weight, eps, residual, x.dtype, False)
     return (y, h) if residual is not None else y
 
 
@@ -343,30 +397,159 @@ def rms_norm_quant(x: torch.Tensor, weight=None, eps: float = 1e-6, residual=Non
     rounding, as fp8 (e4m3fn or e5m2) rows with an fp32 scale each (the row is
     q * scale; the largest magnitude of a row becomes the type's largest
     value).  The last size is a multiple of 16."""
-    _check_norm("rms_norm_quant", x, weight, residual)
-    if dtype not in _F8 or x.shape[-1] % 16 != 0:
-        raise ValueError("rms_norm_quant: dtype must be float8_e4m3fn or float8_e5m2 and the last "
-                         "size a multiple of 16")
-    _refuse_grad("rms_norm_quant", x, weight, residual)
-    q, h, scale, _ = _norm(x, weight, eps, residual, dtype, False)
+    where = "rms_norm_quant"
+    _check_norm(where, x, weight, residual)
+    _check_f8_rows(where, x, dtype)
+    _refuse_grad(where, x, weight, residual)
+    q, h, scale, _ = _norm(where, x, weight, eps, residual, dtype, False)
     return (q, scale, h) if residual is not None else (q, scale)
 
 
 def quantize_rows(x: torch.Tensor, dtype=torch.float8_e4m3fn):
     """(q, scale): the rows of x (its last dimension) as fp8 with an fp32 scale
     each, for activations that no norm precedes and for weights [N, K]."""
-    _check_norm("quantize_rows", x, None, None)
-    if dtype not in _F8 or x.shape[-1] % 16 != 0:
-        raise ValueError("quantize_rows: dtype must be float8_e4m3fn or float8_e5m2 and the last "
-                         "size a multiple of 16")
-    _refuse_grad("quantize_rows", x)
-    cols = x.shape[-1]
-    q = torch.empty(x.shape, dtype=dtype, device=x.device)
+    where = "quantize_rows"
+    _check_norm(where, x, None, None)
+    _check_f8_rows(where, x, dtype)
+    _refuse_grad(where, x)
+    stream = _stream_of(where, x.device)
+    x = _dense(x)
+    q = torch.empty_like(x, dtype=dtype)
     scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    cols = x.shape[-1]
     if x.numel():
-        x2 = _dense(x).reshape(-1, cols)
-        _quantize_rows(x2, q.reshape(-1, cols), scale.reshape(-1))
+        _done(lib().quantize_rows(x.numel() // cols, cols, _dtype_code(x.dtype), _dtype_code(dtype),
+                                  x.data_ptr(), q.data_ptr(), scale.data_ptr(), stream), where)
     return q, scale
+
+
+def _bias32(where: str, bias, N: int, device):
+    if bias is None:
+        return None
+    if bias.numel() != N or bias.device != device:
+        raise ValueError(f"{where}: the bias must hold {N} values on {device}")
+    return bias.reshape(N).to(torch.float32).contiguous()
+
+
+def linear_f8(x: torch.Tensor, x_scale: torch.Tensor, weight: torch.Tensor,
+              weight_scale: torch.Tensor, bias=None, out_dtype=torch.bfloat16,
+              fp32_accum: bool = False) -> torch.Tensor:
+    """y = (x x_scale) @ (weight weight_scale)^T + bias for fp8 rows with scales.
+
+    x [..., K] and weight [N, K] are float8_e4m3fn or float8_e5m2 (both the
+    same; K and N multiples of 16), x_scale fp32 [...] (one per row) and
+    weight_scale fp32 [N], as rms_norm_quant and quantize_rows leave them.
+    The products are summed on the fp8 matrix step, scaled by row and by
+    column in fp32, the bias added in fp32, and the result rounded once to
+    out_dtype (bf16, fp16 or fp32).  fp32_accum=True sums on the fp16 step
+    instead (half the matrix rate, the fp32 error bound for every K).  Row i of
+    y depends on row i of x, its scale and the weight alone."""
+    where = "linear_f8"
+    dev = x.device
+    if not (x.is_cuda and x.dtype in _F8 and x.dim() >= 1 and weight.dim() == 2
+            and weight.dtype == x.dtype and weight.device == dev
+            and weight.shape[1] == x.shape[-1]
+            and weight.shape[0] % 16 == 0 and weight.shape[1] % 16 == 0):
+        raise ValueError(
+            "linear_f8: needs fp8 CUDA tensors of one type, x [..., K] and weight [N, K] with K and "
+            f"N multiples of 16; got {tuple(x.shape)} {x.dtype} on {x.device} and "
+            f"{tuple(weight.shape)} {weight.dtype} on {weight.device}")
+    if out_dtype not in (torch.bfloat16, torch.float16, torch.float32):
+        raise ValueError("linear_f8: out_dtype must be bfloat16, float16 or float32")
+    N, K = weight.shape
+    lead = x.shape[:-1]
+    if not (x_scale.dtype == weight_scale.dtype == torch.float32 and x_scale.shape == lead
+            and weight_scale.shape == (N,) and x_scale.device == weight_scale.device == dev):
+        raise ValueError(
+            f"linear_f8: x_scale must be float32 {tuple(lead)} and weight_scale float32 {(N,)} on "
+            f"{dev}; got {x_scale.dtype} {tuple(x_scale.shape)} on {x_scale.device} and "
+            f"{weight_scale.dtype} {tuple(weight_scale.shape)} on {weight_scale.device}")
+    bias = _bias32(where, bias, N, dev)
+    _refuse_grad(where, x, x_scale, weight, weight_scale, bias)
+    stream = _stream_of(where, dev)
+    M = x_scale.numel()
+    out = torch.empty((*lead, N), dtype=out_dtype, device=dev)
+    if M == 0 or N == 0:
+        return out
+    x, weight = _dense(x), _dense(weight)
+    x_scale, weight_scale = x_scale.contiguous(), weight_scale.contiguous()
+    flags = PLAN_TILE_BY_M | PLAN_B_TRANSPOSED | (PLAN_FP8_FP32_ACCUM if fp32_accum else 0)
+    plan = _f8_plan(M, N, K, x.dtype, out_dtype, flags)
+    _done(lib().gemm_run_scaled(plan.handle, x.data_ptr(), weight.data_ptr(), x_scale.data_ptr(),
+                                weight_scale.data_ptr(), _ptr(bias), out.data_ptr(), stream), where)
+    return out
+
+
+class W4Weight:
+    """A 4-bit weight [N, K] as linear_w4 reads it (made by pack_w4)."""
+
+    __slots__ = ("packed", "N", "K", "group", "dtype")
+
+    def __init__(self, packed: torch.Tensor, N: int, K: int, group: int, dtype: torch.dtype):
+        self.packed, self.N, self.K, self.group, self.dtype = packed, N, K, group, dtype
+
+    def to(self, device) -> "W4Weight":
+        return W4Weight(self.packed.to(device), self.N, self.K, self.group, self.dtype)
+
+
+def pack_w4(q: torch.Tensor, scales: torch.Tensor, zeros=None) -> W4Weight:
+    """Lay out a 4-bit weight once, for linear_w4.
+
+    q: uint8 [N, K / 2], byte j of a row holding element 2 j in its low and
+    2 j + 1 in its high half; scales [N, K / group], fp16 or bf16 (the type of
+    the activations), group 32, 64 or 128; zeros: uint8 [N, K / group], or None
+    for 8.  The weight is scales (q - zeros).  N is a multiple of 8."""
+    where = "pack_w4"
+    if not (q.is_cuda and q.dtype == torch.uint8 and q.dim() == 2 and scales.dim() == 2
+            and scales.dtype in _DT and scales.device == q.device and scales.shape[0] == q.shape[0]):
+        raise ValueError("pack_w4: needs uint8 q [N, K / 2] and fp16/bf16 scales [N, K / group] on one "
+                         f"CUDA device; got {tuple(q.shape)} {q.dtype} on {q.device} and "
+                         f"{tuple(scales.shape)} {scales.dtype} on {scales.device}")
+    N, K = q.shape[0], 2 * q.shape[1]
+    groups = scales.shape[1]
+    group = K // groups if groups else 0
+    if N % 8 != 0 or group not in (32, 64, 128) or groups * group != K:
+        raise ValueError(f"pack_w4: N = {N} must be a multiple of 8 and K = {K} hold {groups} groups "
+                         "of 32, 64 or 128")
+    if zeros is not None and (zeros.dtype != torch.uint8 or zeros.shape != scales.shape
+                              or zeros.device != q.device):
+        raise ValueError("pack_w4: zeros must be uint8 of the shape and device of scales")
+    _refuse_grad(where, scales)
+    stream = _stream_of(where, q.device)
+    plan = _w4_plan(1, N, K, scales.dtype, group)
+    packed = torch.empty(w4_packed_size(plan), dtype=torch.uint8, device=q.device)
+    q, scales = q.contiguous(), scales.contiguous()
+    if zeros is not None:
+        zeros = zeros.contiguous()
+    if packed.numel():
+        _done(lib().w4_pack(plan.handle, q.data_ptr(), scales.data_ptr(), _ptr(zeros),
+                            packed.data_ptr(), stream), where)
+    return W4Weight(packed, N, K, group, scales.dtype)
+
+
+def linear_w4(x: torch.Tensor, weight: W4Weight, bias=None) -> torch.Tensor:
+    """y = x @ W^T + bias for a packed 4-bit weight W [N, K] and x [..., K] of the
+    type of its scales.  Sums are fp32 over the exact integers, scales applied
+    per group in fp32, one rounding at the end.  Row i of y depends on row i
+    of x and the weight alone, for every number of rows."""
+    where = "linear_w4"
+    dev = x.device
+    if not (x.is_cuda and x.dtype == weight.dtype and x.dim() >= 1 and x.shape[-1] == weight.K
+            and weight.packed.device == dev):
+        raise ValueError(f"linear_w4: needs a {weight.dtype} CUDA tensor [..., {weight.K}] on "
+                         f"{weight.packed.device}, got {tuple(x.shape)} {x.dtype} on {x.device}")
+    N = weight.N
+    bias = _bias32(where, bias, N, dev)
+    _refuse_grad(where, x, bias)
+    stream = _stream_of(where, dev)
+    x = _dense(x)
+    y = torch.empty((*x.shape[:-1], N), dtype=x.dtype, device=dev)
+    M = x.numel() // weight.K
+    if M:
+        plan = _w4_plan(M, N, weight.K, x.dtype, weight.group)
+        _done(lib().w4_run(plan.handle, x.data_ptr(), weight.packed.data_ptr(), _ptr(bias),
+                           y.data_ptr(), stream), where)
+    return y
 
 
 _mode_lock = threading.Lock()

@@ -1,0 +1,228 @@
+"""Linear layers with 4-bit weights and group scales (linear_w4, w4_run).
+
+Oracles.  In 64 bits: y = sum_g s (sum x (q - z)) + b, with a bound from the
+arithmetic: a group's two fp32 chains are off by at most group 2^-24 of their
+magnitudes, the groups' sum by (groups + 1) 2^-24, so y by
+  (group + groups + 4) 2^-24 sum |s| |x| (q + z) + |b| 2^-24
+before the rounding to the output type (half a step).  Bitwise: for integer x a
+group's sums are exact, so the documented chain of fused multiply-adds can be
+replayed in 64 bits, rounding to fp32 after each.
+"""
+import pytest
+import torch
+
+import invariant_matmul_amd as imm
+from invariant_matmul_amd import torch_ops
+from tests.helpers import dev
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f16": torch.float16, "bf16": torch.bfloat16}
+TINY = {"f16": 2.0 ** -25, "bf16": 2.0 ** -134}
+
+
+def make(M, N, K, group, dt, seed, integers=False):
+    g = torch.Generator().manual_seed(seed)
+    s = {"q": torch.randint(0, 256, (N, K // 2), generator=g, dtype=torch.uint8),
+         "s": ((torch.rand(N, K // group, generator=g) + 0.5) * 0.2 * max(1, K) ** -0.5).to(DT[dt]),
+         "z": torch.randint(0, 16, (N, K // group), generator=g, dtype=torch.uint8),
+         "b": torch.randn(N, generator=g)}
+    s["x"] = (torch.randint(-8, 9, (M, K), generator=g).to(DT[dt]) if integers
+              else torch.randn(M, K, generator=g).to(DT[dt]))
+    return {k: v.to(dev()) for k, v in s.items()}
+
+
+def unpacked(s):
+    q = torch.empty(s["q"].shape[0], 2 * s["q"].shape[1], device=dev(), dtype=torch.float64)
+    q[:, 0::2] = (s["q"] & 15).double()
+    q[:, 1::2] = (s["q"] >> 4).double()
+    return q
+
+
+def oracle(s, group, zeros, bias):
+    q, sc = unpacked(s), s["s"].double().repeat_interleave(group, 1)
+    z = s["z"].double().repeat_interleave(group, 1) if zeros else torch.full_like(q, 8.0)
+    x = s["x"].double()
+    y = x @ (sc * (q - z)).t()
+    mag = x.abs() @ (sc.abs() * (q + z)).t()
+    if bias:
+        y = y + s["b"].double()
+    return y, mag
+
+
+def check(y, s, group, zeros, bias, dt):
+    want, mag = oracle(s, group, zeros, bias)
+    groups = s["s"].shape[1]
+    tol = mag * (group + groups + 4) * 2.0 ** -24 + want.abs() * (torch.finfo(DT[dt]).eps / 2) * (1 + 2.0 ** -20)
+    tol = tol + TINY[dt] + (s["b"].double().abs() * 2.0 ** -23 if bias else 0)
+    err = (y.double() - want).abs()
+    assert (err <= tol).all(), float((err / tol).max())
+
+
+SHAPES = [(1, 8, 128), (1, 4096, 4096), (3, 264, 256), (16, 1024, 1152), (17, 40, 640), (31, 520, 2048),
+          (64, 256, 14336), (65, 1032, 384), (129, 136, 1024), (300, 512, 512), (1030, 264, 896)]
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_against_64_bits(shape, group, dt):
+    s = make(*shape, group, dt, sum(shape) + group)
+    w = torch_ops.pack_w4(s["q"], s["s"], s["z"])
+    y = torch_ops.linear_w4(s["x"], w, bias=s["b"])
+    assert y.dtype == DT[dt] and y.shape == shape[:2]
+    check(y, s, group, True, True, dt)
+    y = torch_ops.linear_w4(s["x"], torch_ops.pack_w4(s["q"], s["s"]))
+    check(y, s, group, False, False, dt)
+
+
+@pytest.mark.parametrize("K,group", [(32, 32), (96, 32), (160, 32), (4128, 32), (64, 64), (192, 64), (4160, 64)])
+@pytest.mark.parametrize("M", [1, 20, 90, 400])
+def test_groups_that_end_inside_a_block(K, group, M):
+    s = make(M, 56, K, group, "bf16", K + M)
+    y = torch_ops.linear_w4(s["x"], torch_ops.pack_w4(s["q"], s["s"], s["z"]), bias=s["b"])
+    check(y, s, group, True, True, "bf16")
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("M", [1, 16, 40, 100, 260, 700])
+def test_bits_of_the_documented_chain(M, group, dt):
+    N, K = 72, 2176
+    s = make(M, N, K, group, dt, 61, integers=True)
+    y = torch_ops.linear_w4(s["x"], torch_ops.pack_w4(s["q"], s["s"], s["z"]), bias=s["b"])
+    q, x = unpacked(s), s["x"].double()
+    acc = torch.zeros(M, N, dtype=torch.float64, device=dev())
+    for g in range(K // group):
+        k = slice(g * group, (g + 1) * group)
+        v = x[:, k] @ (q[:, k] - s["z"][:, g].double()[:, None]).t()  # exact integers
+        acc = (acc + v * s["s"][:, g].double()).float().double()
+    want = (acc.float() + s["b"]).to(DT[dt])
+    assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("N,K,group", [(4096, 2048, 128), (1032, 4096, 64), (264, 14336, 32)])
+def test_rows_do_not_depend_on_the_batch(N, K, group):
+    s = make(600, N, K, group, "bf16", 67)
+    w = torch_ops.pack_w4(s["q"], s["s"], s["z"])
+    y = torch_ops.linear_w4(s["x"], w, bias=s["b"])
+    for lo, hi in ((0, 1), (599, 600), (5, 13), (3, 19), (9, 26), (0, 48), (7, 71), (100, 228), (11, 300)):
+        assert torch.equal(torch_ops.linear_w4(s["x"][lo:hi], w, bias=s["b"]), y[lo:hi]), (lo, hi)
+
+
+def test_every_code_and_zero_point():
+    """All 16 codes against all 256 zero points: one column and group per pair."""
+    K, group = 64, 32
+    q = torch.arange(16).repeat_interleave(256)
+    z = torch.arange(256).repeat(16)
+    N = 4096
+    s = {"q": (q | (q << 4)).to(torch.uint8)[:, None].expand(N, K // 2).contiguous().to(dev()),
+         "s": torch.full((N, 2), 0.25, dtype=torch.float16, device=dev()),
+         "z": torch.stack((z, z), 1).to(torch.uint8).to(dev())}
+    x = torch.zeros(2, K, dtype=torch.float16, device=dev())
+    x[0, 3], x[1, 40] = 1.0, -2.0
+    y = torch_ops.linear_w4(x, torch_ops.pack_w4(s["q"], s["s"], s["z"]))
+    v = 0.25 * (q - z).double().to(dev())
+    assert torch.equal(y.double(), torch.stack((v, -2 * v)))
+
+
+@pytest.mark.parametrize("M", [12, 80, 300])
+def test_bad_rows_and_scales_stay_alone(M):
+    s = make(M, 136, 512, 64, "bf16", 71)
+    y = torch_ops.linear_w4(s["x"], torch_ops.pack_w4(s["q"], s["s"], s["z"]))
+    x, sc = s["x"].clone(), s["s"].clone()
+    x[3, 100], x[M - 1, 511], x[5] = float("nan"), float("inf"), 0
+    sc[7, 2], sc[9] = float("nan"), 0
+    z = torch_ops.linear_w4(x, torch_ops.pack_w4(s["q"], sc, s["z"]))
+    rows = [i for i in range(M) if i not in (3, 5, M - 1)]
+    cols = [j for j in range(136) if j not in (7, 9)]
+    assert torch.equal(z[rows][:, cols], y[rows][:, cols])
+    assert not torch.isfinite(z[3]).any() and not torch.isfinite(z[M - 1][cols]).any()
+    assert z[:, 7].isnan().all() and (z[rows, 9] == 0).all() and (z[5, cols] == 0).all()
+
+
+def test_views_shapes_and_empty():
+    s = make(24, 72, 256, 64, "f16", 73)
+    w = torch_ops.pack_w4(s["q"], s["s"], s["z"])
+    y = torch_ops.linear_w4(s["x"], w)
+    z = torch_ops.linear_w4(s["x"].view(2, 3, 4, 256), w)
+    assert z.shape == (2, 3, 4, 72) and torch.equal(z.view(24, 72), y)
+    assert torch.equal(torch_ops.linear_w4(s["x"][5], w), y[5])
+    wide = torch.zeros(24, 301, dtype=torch.float16, device=dev())
+    wide[:, 1:257] = s["x"]
+    assert torch.equal(torch_ops.linear_w4(wide[:, 1:257], w), y)
+    flat = torch.zeros(24 * 256 + 4, dtype=torch.float16, device=dev())
+    flat[4:] = s["x"].reshape(-1)
+    assert torch.equal(torch_ops.linear_w4(flat[4:].view(24, 256), w), y)
+    qt, st, zt = (t.t().contiguous().t() for t in (s["q"], s["s"], s["z"]))
+    w2 = torch_ops.pack_w4(qt, st, zt)
+    assert torch.equal(w2.packed, w.packed)
+    assert torch_ops.linear_w4(s["x"][:0], w).shape == (0, 72)
+    assert torch.equal(torch_ops.linear_w4(s["x"], w.to(dev())), y)
+
+
+@pytest.mark.parametrize("M", [1, 24, 200])
+def test_streams_graphs_and_rows_behind(M):
+    s = make(M, 1032, 1024, 128, "bf16", 79)
+    w = torch_ops.pack_w4(s["q"], s["s"], s["z"])
+    want = torch_ops.linear_w4(s["x"], w, bias=s["b"])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = torch_ops.linear_w4(s["x"], w, bias=s["b"])
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = torch_ops.linear_w4(s["x"], w, bias=s["b"])
+    for _ in range(4):
+        out.fill_(0)
+        torch_ops.linear_w4(s["x"] * 2, w)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    buf = torch.full((M + 2, 1032), 7.0, dtype=torch.bfloat16, device=dev())
+    imm.w4_run(imm.w4_plan(M, 1032, 1024, "bf16", 128), s["x"], w.packed, buf[:M], bias=s["b"])
+    assert torch.equal(buf[:M], want) and (buf[M:] == 7).all()
+
+
+def test_norm_then_product():
+    """What a serving layer runs: norm with the residual, then the 4-bit product."""
+    s = make(33, 520, 1024, 128, "bf16", 83)
+    g = torch.Generator().manual_seed(84)
+    r = torch.randn(33, 1024, generator=g).bfloat16().to(dev())
+    nw = (1 + 0.1 * torch.randn(1024, generator=g)).bfloat16().to(dev())
+    w = torch_ops.pack_w4(s["q"], s["s"], s["z"])
+    h, stream = torch_ops.rms_norm(s["x"], nw, 1e-6, residual=r)
+    y = torch_ops.linear_w4(h, w, bias=s["b"])
+    check(y, {**s, "x": h}, 128, True, True, "bf16")
+    for i in (0, 20, 32):
+        h1, _ = torch_ops.rms_norm(s["x"][i:i + 1], nw, 1e-6, residual=r[i:i + 1])
+        assert torch.equal(torch_ops.linear_w4(h1, w, bias=s["b"])[0], y[i])
+
+
+def test_refusals_on_the_gpu():
+    s = make(4, 64, 256, 64, "f16", 89)
+    w = torch_ops.pack_w4(s["q"], s["s"], s["z"])
+    for call in (lambda: torch_ops.linear_w4(s["x"].bfloat16(), w),
+                 lambda: torch_ops.linear_w4(s["x"][:, :128], w),
+                 lambda: torch_ops.linear_w4(s["x"].cpu(), w),
+                 lambda: torch_ops.linear_w4(s["x"], w.to("cpu")),
+                 lambda: torch_ops.linear_w4(s["x"], w, bias=s["b"][:3]),
+                 lambda: torch_ops.linear_w4(s["x"].clone().requires_grad_(), w),
+                 lambda: torch_ops.pack_w4(s["q"].to(torch.int8), s["s"]),
+                 lambda: torch_ops.pack_w4(s["q"], s["s"].float()),
+                 lambda: torch_ops.pack_w4(s["q"], s["s"][:, :3]),
+                 lambda: torch_ops.pack_w4(s["q"], s["s"][:, :1]),
+                 lambda: torch_ops.pack_w4(s["q"], s["s"], s["z"][:, :2]),
+                 lambda: torch_ops.pack_w4(s["q"], s["s"], s["z"].half()),
+                 lambda: torch_ops.pack_w4(s["q"][:60], s["s"][:60])):
+        with pytest.raises(ValueError):
+            call()
+    L, p = imm.lib(), imm.w4_plan(4, 64, 256, "f16", 64)
+    y = torch.empty(4, 64, dtype=torch.float16, device=dev())
+    pinned = torch.zeros(4, 256, dtype=torch.float16).pin_memory()
+    assert L.w4_run(p.handle, pinned.data_ptr(), w.packed.data_ptr(), None, y.data_ptr(), None) == 1
+    big = imm.w4_plan(1 << 24, 64, 256, "f16", 64)  # rows far past these operands
+    assert L.w4_run(big.handle, s["x"].data_ptr(), w.packed.data_ptr(), None, y.data_ptr(), None) == 1

@@ -98,12 +98,73 @@ def test_quantize_rows_arguments():
     assert run(rows=0, x=0, q=0, s=0) == OK
 
 
+def test_scaled_product_arguments():
+    L = imm.lib()
+    plan = imm.gemm_plan_ex2(4, 64, 128, "e4m3", "bf16", flags=imm.PLAN_B_TRANSPOSED)
+
+    def run(p=plan, a=P, b=P, rs=P, cs=P, bias=0, c=P):
+        h = p.handle if p else None
+        return L.gemm_run_scaled(h, a, b, rs, cs, bias, c, None)
+
+    assert run(None) == INVALID
+    for bad in ({"a": 0}, {"b": 0}, {"c": 0}, {"rs": 0}, {"cs": 0}, {"a": P + 8}, {"b": P + 4}, {"c": P + 2},
+                {"rs": P + 2}, {"cs": P + 1}, {"bias": P + 2}):
+        assert run(**bad) == INVALID, bad
+    for other in (imm.gemm_plan_ex2(4, 64, 128, "e4m3", "bf16"),
+                  imm.gemm_plan_ex2(4, 64, 128, "f16", "f16", flags=imm.PLAN_B_TRANSPOSED)):
+        assert run(other) == UNSUPPORTED
+    empty = imm.gemm_plan_ex2(0, 64, 128, "e4m3", "bf16", flags=imm.PLAN_B_TRANSPOSED)
+    assert run(empty, a=0, b=0, rs=0, cs=0, c=0) == OK
+
+
+@pytest.mark.parametrize("args,want", [
+    ((4, 64, 256, "bf16", 128), OK), ((0, 64, 256, "f16", 64), OK), ((4, 0, 256, "f16", 32), OK),
+    ((4, 64, 0, "f16", 32), OK), ((4, 8, 96, "f16", 32), OK), ((-1, 64, 256, "f16", 128), INVALID),
+    ((4, -8, 256, "f16", 128), INVALID), ((4, 64, -128, "f16", 128), INVALID),
+    ((4, 60, 256, "f16", 128), UNSUPPORTED), ((4, 64, 192, "f16", 128), UNSUPPORTED),
+    ((4, 64, 256, "f16", 16), UNSUPPORTED), ((4, 64, 256, "f16", 256), UNSUPPORTED),
+    ((4, 64, 256, "f16", 0), UNSUPPORTED), ((4, 64, 256, "f16", -32), UNSUPPORTED),
+    ((4, 64, 256, "f32", 128), UNSUPPORTED), ((4, 64, 256, "e4m3", 128), UNSUPPORTED),
+    ((1 << 31, 64, 256, "f16", 128), UNSUPPORTED), ((1 << 30, 1 << 20, 256, "f16", 128), UNSUPPORTED),
+    ((4, 1 << 30, 1 << 20, "f16", 128), UNSUPPORTED),
+])
+def test_w4_plan_arguments(args, want):
+    assert status(imm.w4_plan, *args) == want
+
+
+def test_w4_arguments():
+    L = imm.lib()
+    assert L.w4_plan(4, 64, 256, 0, 128, None) == INVALID
+    assert L.w4_packed_size(None) == 0
+    # 4 column blocks x 2 K blocks of 1 KB, and 4 groups x 64 scale words
+    p = imm.w4_plan(4, 56, 256, "f16", 64)
+    assert imm.w4_packed_size(p) == 4 * 2 * 1024 + 4 * 64 * 4
+    assert imm.w4_packed_size(imm.w4_plan(9999, 56, 256, "f16", 64)) == imm.w4_packed_size(p)
+
+    def pack(plan=p, q=P, s=P, z=0, packed=P):
+        return L.w4_pack(plan.handle if plan else None, q, s, z, packed, None)
+
+    def run(plan=p, x=P, packed=P, b=0, y=P):
+        return L.w4_run(plan.handle if plan else None, x, packed, b, y, None)
+
+    assert pack(None) == pack(q=0) == pack(s=0) == pack(packed=0) == pack(s=P + 1) == pack(packed=P + 8) == INVALID
+    assert run(None) == run(x=0) == run(packed=0) == run(y=0) == INVALID
+    assert run(x=P + 8) == run(packed=P + 4) == run(y=P + 2) == run(b=P + 2) == INVALID
+    assert run(imm.w4_plan(0, 64, 128, "f16"), x=0, packed=0, y=0) == OK
+    assert run(imm.w4_plan(4, 0, 128, "f16"), x=0, packed=0, y=0) == OK
+    assert pack(imm.w4_plan(4, 64, 0, "f16"), q=0, s=0, packed=0) == OK
+
+
 def test_operators_refuse_host_tensors_and_wrong_shapes():
     x = torch.zeros(4, 64, dtype=torch.bfloat16)
     w = torch.ones(64, dtype=torch.bfloat16)
     for call in (lambda: torch_ops.rms_norm(x, w), lambda: torch_ops.rms_norm_quant(x, w),
                  lambda: torch_ops.quantize_rows(x), lambda: torch_ops.rms_norm_forward(x, w),
-                 lambda: torch_ops.rms_norm_backward(x, x, w, torch.zeros(4))):
+                 lambda: torch_ops.rms_norm_backward(x, x, w, torch.zeros(4)),
+                 lambda: torch_ops.linear_f8(x.to(torch.float8_e4m3fn), torch.ones(4),
+                                             x.to(torch.float8_e4m3fn), torch.ones(4)),
+                 lambda: torch_ops.pack_w4(torch.zeros(8, 64, dtype=torch.uint8),
+                                           torch.ones(8, 1).half())):
         with pytest.raises(ValueError):
             call()
     p = imm.rms_norm_plan(4, 64, "bf16")
