@@ -528,10 +528,15 @@ size_t w4_packed_size(w4_plan_t plan);
 gemm_status w4_pack(w4_plan_t plan, const void* q, const void* scales, const void* zeros,
                     void* packed, void* stream);
 
+/* Bytes of workspace w4_run needs (the sums of x per group, for many rows; 0
+ * for few rows or a NULL plan). */
+size_t w4_workspace_size(w4_plan_t plan);
+
 /* y = x W^T + bias on `stream`.  x, packed and y 16-byte aligned; bias: fp32
- * [N], 4-byte aligned, or NULL. */
+ * [N], 4-byte aligned, or NULL; workspace: w4_workspace_size(plan) bytes,
+ * 16-byte aligned (NULL where that is 0). */
 gemm_status w4_run(w4_plan_t plan, const void* x, const void* packed, const float* bias, void* y,
-                   void* stream);
+                   void* workspace, size_t workspace_bytes, void* stream);
 
 void w4_plan_destroy(w4_plan_t plan);
 

@@ -31,7 +31,8 @@ __all__ = [
     "OzakiPlan", "ozaki_plan", "ozaki_plan_info", "ozaki_workspace_size", "ozaki_split",
     "ozaki_multiply", "ozaki_run", "ozaki_mm",
     "LAYER_SYMBOLS", "RmsNormPlan", "rms_norm_plan", "rms_norm_run", "rms_norm_workspace_size",
-    "rms_norm_backward", "quantize_rows", "W4Plan", "w4_plan", "w4_packed_size", "w4_pack", "w4_run",
+    "rms_norm_backward", "quantize_rows", "W4Plan", "w4_plan", "w4_packed_size", "w4_pack",
+    "w4_workspace_size", "w4_run",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libinvariant_matmul.so")
@@ -58,8 +59,8 @@ EXPORTED_SYMBOLS = (
 # The calls around a linear layer: the row norm, fp8 rows and 4-bit weights.
 LAYER_SYMBOLS = (
     "rms_norm_plan", "rms_norm_run", "rms_norm_workspace_size", "rms_norm_backward",
-    "rms_norm_plan_destroy", "quantize_rows", "w4_plan", "w4_packed_size", "w4_pack", "w4_run",
-    "w4_plan_destroy",
+    "rms_norm_plan_destroy", "quantize_rows", "w4_plan", "w4_packed_size", "w4_pack",
+    "w4_workspace_size", "w4_run", "w4_plan_destroy",
 )
 
 
@@ -166,7 +167,9 @@ def lib() -> ctypes.CDLL:
         L.w4_packed_size.argtypes = [vp]
         L.w4_packed_size.restype = sz
         L.w4_pack.argtypes = [vp] * 6
-        L.w4_run.argtypes = [vp] * 6
+        L.w4_workspace_size.argtypes = [vp]
+        L.w4_workspace_size.restype = sz
+        L.w4_run.argtypes = [vp] * 6 + [sz, vp]
         L.w4_plan_destroy.argtypes = [vp]
         L.w4_plan_destroy.restype = None
         for f in ("gemm_run_scaled", "rms_norm_plan", "rms_norm_run", "rms_norm_backward",
@@ -622,6 +625,7 @@ class W4Plan:
         self.M, self.N, self.K = M, N, K
         self.dtype, self.group = dtype, group
         self._lib = lib()
+        self.workspace_bytes = int(self._lib.w4_workspace_size(handle))
 
     def __del__(self):
         h, self.handle = getattr(self, "handle", None), None
@@ -660,11 +664,18 @@ def w4_pack(plan: W4Plan, q, scales, packed, zeros=None, stream=None) -> None:
                          _stream(stream, q, packed)), "w4_pack")
 
 
-def w4_run(plan: W4Plan, x, packed, y, bias=None, stream=None) -> None:
+def w4_workspace_size(plan: W4Plan) -> int:
+    return int(lib().w4_workspace_size(plan.handle))
+
+
+def w4_run(plan: W4Plan, x, packed, y, bias=None, workspace=None, stream=None,
+           workspace_bytes=None) -> None:
     """y = x @ W^T (+ bias, an fp32 vector of N) from the packed weight."""
     _check_tensor(x, "x", plan.dtype, plan.M * plan.K)
     _check_bytes(packed, "packed", w4_packed_size(plan))
     _check_tensor(y, "y", plan.dtype, plan.M * plan.N)
     _check_tensor(bias, "bias", DTYPE["f32"], plan.N)
+    _check_ws_device(workspace)
     _check(lib().w4_run(plan.handle, _addr(x), _addr(packed), _addr(bias), _addr(y),
+                        _addr(workspace), _ws_bytes(workspace, workspace_bytes),
                         _stream(stream, x, y)), "w4_run")

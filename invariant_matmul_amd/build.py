@@ -55,6 +55,7 @@ def _compile(src: str, verbose: bool) -> str:
 # check in it that no instruction touches a register an inline-assembly LDS
 # read (whose completion the compiler does not track) will still write.
 DMA_ASM = os.path.join(BUILD_DIR, "gemm_dma.gfx950.s")
+W4_ASM = os.path.join(BUILD_DIR, "w4.gfx950.s")
 
 
 def _device_asm(src: str, out: str, verbose: bool) -> str:
@@ -85,10 +86,12 @@ def build(verbose: bool = False) -> str:
     probe library); returns the GEMM library's path."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     srcs = SOURCES + PROBE_SOURCES
-    with concurrent.futures.ThreadPoolExecutor(max_workers=len(srcs) + 1) as ex:
-        asm = ex.submit(_device_asm, "gemm_dma.hip", DMA_ASM, verbose)
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(srcs) + 2) as ex:
+        asm = [ex.submit(_device_asm, "gemm_dma.hip", DMA_ASM, verbose),
+               ex.submit(_device_asm, "w4.hip", W4_ASM, verbose)]
         objs = dict(zip(srcs, ex.map(lambda s: _compile(s, verbose), srcs)))
-        asm.result()
+        for a in asm:
+            a.result()
     _link([objs[s] for s in SOURCES], LIB, verbose)
     _link([objs[s] for s in PROBE_SOURCES], PROBE_LIB, verbose)
     return LIB

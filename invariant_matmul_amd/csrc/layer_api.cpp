@@ -181,25 +181,38 @@ gemm_status w4_pack(w4_plan_t p, const void* q, const void* scales, const void* 
                                   static_cast<hipStream_t>(stream)));
 }
 
+size_t w4_workspace_size(w4_plan_t p) {
+  if (!p || p->N == 0 || !w4_uses_tiles(p->M, p->K)) return 0;
+  return (size_t)p->groups * (size_t)((p->M + kW4RowPad - 1) / kW4RowPad * kW4RowPad) * sizeof(float);
+}
+
 gemm_status w4_run(w4_plan_t p, const void* x, const void* packed, const float* bias, void* y,
-                   void* stream) {
+                   void* workspace, size_t workspace_bytes, void* stream) {
   if (!p) return GEMM_ERR_INVALID_VALUE;
   if (p->M == 0 || p->N == 0) return GEMM_OK;
   if (!good(y, 16) || !aligned(bias, 4)) return GEMM_ERR_INVALID_VALUE;
   const bool any = p->K > 0;
   if (any && (!good(x, 16) || !good(packed, 16))) return GEMM_ERR_INVALID_VALUE;
+  const size_t need = w4_workspace_size(p);
+  if (need) {
+    if (!workspace || workspace_bytes < need) return GEMM_ERR_WORKSPACE;
+    if (!aligned(workspace, 16)) return GEMM_ERR_INVALID_VALUE;
+  }
   const size_t M = (size_t)p->M, N = (size_t)p->N, K = (size_t)p->K;
   const gemm_status st = check_device_operands({{any ? x : nullptr, 2 * M * K},
                                                 {any ? packed : nullptr, w4_packed_size(p)},
                                                 {bias, N * sizeof(float)},
-                                                {y, 2 * M * N}});
+                                                {y, 2 * M * N},
+                                                {need ? workspace : nullptr, need}});
   if (st != GEMM_OK) return st;
   const char* const sz = static_cast<const char*>(packed) + p->nblocks * p->kblocks * 1024;
   const W4Args a{x,    packed, reinterpret_cast<const unsigned*>(any ? sz : nullptr),
                  bias, y,      p->M,
                  p->N, p->K,   p->nblocks,
                  p->kblocks,   p->groups,
-                 p->group};
+                 p->group,     need ? static_cast<float*>(workspace) : nullptr,
+                 (p->M + kW4RowPad - 1) / kW4RowPad * kW4RowPad,
+                 0,            0,      0};
   return status_of(launch_w4(p->dtype, a, static_cast<hipStream_t>(stream)));
 }
 

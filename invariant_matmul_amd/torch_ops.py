@@ -547,8 +547,10 @@ def linear_w4(x: torch.Tensor, weight: W4Weight, bias=None) -> torch.Tensor:
     M = x.numel() // weight.K
     if M:
         plan = _w4_plan(M, N, weight.K, x.dtype, weight.group)
+        nws = plan.workspace_bytes
+        ws = torch.empty(nws, dtype=torch.uint8, device=dev) if nws else None
         _done(lib().w4_run(plan.handle, x.data_ptr(), weight.packed.data_ptr(), _ptr(bias),
-                           y.data_ptr(), stream), where)
+                           y.data_ptr(), _ptr(ws), nws, stream), where)
     return y
 
 

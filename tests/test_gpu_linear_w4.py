@@ -183,7 +183,9 @@ def test_streams_graphs_and_rows_behind(M):
         torch.cuda.synchronize()
         assert torch.equal(out, want)
     buf = torch.full((M + 2, 1032), 7.0, dtype=torch.bfloat16, device=dev())
-    imm.w4_run(imm.w4_plan(M, 1032, 1024, "bf16", 128), s["x"], w.packed, buf[:M], bias=s["b"])
+    plan = imm.w4_plan(M, 1032, 1024, "bf16", 128)
+    ws = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device=dev())
+    imm.w4_run(plan, s["x"], w.packed, buf[:M], bias=s["b"], workspace=ws)
     assert torch.equal(buf[:M], want) and (buf[M:] == 7).all()
 
 
@@ -223,6 +225,8 @@ def test_refusals_on_the_gpu():
     L, p = imm.lib(), imm.w4_plan(4, 64, 256, "f16", 64)
     y = torch.empty(4, 64, dtype=torch.float16, device=dev())
     pinned = torch.zeros(4, 256, dtype=torch.float16).pin_memory()
-    assert L.w4_run(p.handle, pinned.data_ptr(), w.packed.data_ptr(), None, y.data_ptr(), None) == 1
-    big = imm.w4_plan(1 << 24, 64, 256, "f16", 64)  # rows far past these operands
-    assert L.w4_run(big.handle, s["x"].data_ptr(), w.packed.data_ptr(), None, y.data_ptr(), None) == 1
+    assert L.w4_run(p.handle, pinned.data_ptr(), w.packed.data_ptr(), None, y.data_ptr(),
+                    None, 0, None) == 1
+    big = imm.w4_plan(1 << 24, 64, 256, "f16", 64)  # rows past any allocation here
+    assert L.w4_run(big.handle, s["x"].data_ptr(), w.packed.data_ptr(), None, y.data_ptr(),
+                    w.packed.data_ptr(), big.workspace_bytes, None) == 1

@@ -7,12 +7,28 @@ import pytest
 import torch
 
 import invariant_matmul_amd as imm
-from invariant_matmul_amd import torch_ops
+from invariant_matmul_amd import build, torch_ops
+from tests.lds_read_check import file_hazards
 
 HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include",
                       "invariant_matmul.h")
 OK, INVALID, UNSUPPORTED, WORKSPACE = 0, 1, 2, 3
 P = 4096  # an aligned address that no check reads
+
+
+def test_tile_kernels_have_no_in_flight_read_hazard():
+    """The 4-bit tile kernels issue LDS reads the compiler does not track (see
+    tests/lds_read_check.py)."""
+    if not os.path.exists(build.W4_ASM):
+        pytest.skip("device assembly not built (run invariant_matmul_amd.build)")
+    with open(build.W4_ASM) as f:
+        text = f.read()
+    hazards, n = file_hazards(text, "w4_tile_kernel")
+    assert n >= 6, n
+    assert not hazards, {k[:90]: list(v.items())[:3] for k, v in list(hazards.items())[:5]}
+    # a spilled register would be stored before its read has landed
+    spills = re.findall(r"\.vgpr_spill_count:\s+(\d+)", text)
+    assert len(spills) >= n and set(spills) == {"0"}, spills
 
 
 def status(call, *args, **kw):
@@ -144,8 +160,8 @@ def test_w4_arguments():
     def pack(plan=p, q=P, s=P, z=0, packed=P):
         return L.w4_pack(plan.handle if plan else None, q, s, z, packed, None)
 
-    def run(plan=p, x=P, packed=P, b=0, y=P):
-        return L.w4_run(plan.handle if plan else None, x, packed, b, y, None)
+    def run(plan=p, x=P, packed=P, b=0, y=P, ws=0, n=0):
+        return L.w4_run(plan.handle if plan else None, x, packed, b, y, ws, n, None)
 
     assert pack(None) == pack(q=0) == pack(s=0) == pack(packed=0) == pack(s=P + 1) == pack(packed=P + 8) == INVALID
     assert run(None) == run(x=0) == run(packed=0) == run(y=0) == INVALID
@@ -153,6 +169,12 @@ def test_w4_arguments():
     assert run(imm.w4_plan(0, 64, 128, "f16"), x=0, packed=0, y=0) == OK
     assert run(imm.w4_plan(4, 0, 128, "f16"), x=0, packed=0, y=0) == OK
     assert pack(imm.w4_plan(4, 64, 0, "f16"), q=0, s=0, packed=0) == OK
+    # many rows: the sums of x per group, rows rounded up to 128
+    many = imm.w4_plan(300, 64, 256, "f16", 64)
+    assert many.workspace_bytes == imm.w4_workspace_size(many) == 4 * 384 * 4
+    assert imm.w4_workspace_size(p) == L.w4_workspace_size(None) == 0
+    assert run(many) == run(many, ws=P, n=4 * 384 * 4 - 1) == WORKSPACE
+    assert run(many, ws=P + 8, n=1 << 20) == INVALID
 
 
 def test_operators_refuse_host_tensors_and_wrong_shapes():
