@@ -502,7 +502,7 @@ gemm_status quantize_rows(int64_t rows, int64_t cols, gemm_dtype in, gemm_dtype 
  * q in 0..15.  x [M, K] and y [M, N] are fp16 or bf16, row-major, contiguous;
  * N a multiple of 8, K a multiple of group, group 32, 64 or 128.  The sums of
  * a group run over x and the integers q on the matrix cores in fp32:
- *   P = sum_k x q, X = sum_k x;  acc = fma(scale, fma(-zero, X, P), acc)
+ *   X = sum_k x;  P = -zero X + sum_k x q;  acc = fma(scale, P, acc)
  * with the groups in ascending order, and y = round(acc + bias): no weight is
  * rounded.  Row i of y is a bitwise function of row i of x, of the weights and
  * bias, N, K and group.  A row of x that holds a NaN or an infinity has no

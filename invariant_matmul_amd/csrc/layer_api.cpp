@@ -182,8 +182,8 @@ gemm_status w4_pack(w4_plan_t p, const void* q, const void* scales, const void* 
 }
 
 size_t w4_workspace_size(w4_plan_t p) {
-  if (!p || p->N == 0 || !w4_uses_tiles(p->M, p->K)) return 0;
-  return (size_t)p->groups * (size_t)((p->M + kW4RowPad - 1) / kW4RowPad * kW4RowPad) * sizeof(float);
+  if (!p || p->N == 0 || !w4_uses_tiles(p->M, p->N, p->K, p->group)) return 0;
+  return (size_t)p->groups * (size_t)((p->M + kW4RowPad - 1) / kW4RowPad * kW4RowPad) * 8;
 }
 
 gemm_status w4_run(w4_plan_t p, const void* x, const void* packed, const float* bias, void* y,
@@ -210,7 +210,7 @@ gemm_status w4_run(w4_plan_t p, const void* x, const void* packed, const float* 
                  bias, y,      p->M,
                  p->N, p->K,   p->nblocks,
                  p->kblocks,   p->groups,
-                 p->group,     need ? static_cast<float*>(workspace) : nullptr,
+                 p->group,     need ? workspace : nullptr,
                  (p->M + kW4RowPad - 1) / kW4RowPad * kW4RowPad,
                  0,            0,      0};
   return status_of(launch_w4(p->dtype, a, static_cast<hipStream_t>(stream)));

@@ -50,15 +50,16 @@ struct W4Args {
   int64_t M, N, K;
   int64_t nblocks, kblocks, groups;
   int group;
-  // the tile kernel: sums of x per group, fp32 [groups, m_pad] (workspace; null
-  // selects the few-rows kernel), and its grid
-  float* sums;
+  // the tile kernel: sums of x per group as three bf16 pieces, 8 bytes each,
+  // [groups, m_pad] (workspace; null selects the few-rows kernel), and its grid
+  void* sums;
   int64_t m_pad;
   int64_t tiles_m, tiles_n, grid;
 };
 // Whether a product of M rows runs on the tile kernel (and needs the sums).
-bool w4_uses_tiles(int64_t M, int64_t K);
-constexpr int64_t kW4RowPad = 128;  // m_pad: M rounded up to a multiple of it
+bool w4_uses_tiles(int64_t M, int64_t N, int64_t K, int group);
+constexpr int64_t kMaxOffset = ((int64_t)1 << 31) - (1 << 16);
+constexpr int64_t kW4RowPad = 128;  // rows of the largest tile; m_pad: M rounded up to it
 hipError_t launch_w4_pack(int64_t N, int64_t K, int group, const void* q, const void* scales,
                           const void* zeros, void* packed, hipStream_t s);
 hipError_t launch_w4(int in, const W4Args& a, hipStream_t s);

@@ -5,15 +5,18 @@
 // q in 0..15, groups of 32, 64 or 128 consecutive K, one scale (the type of x)
 // and one zero point per output and group.
 //
-// The sum of a group is taken on the matrix cores over the integers q, which
-// fp16 and bf16 hold exactly: P = sum x q and X = sum x (the same step with a
-// right operand of ones), both fp32 chains of the 16x16x32 step in ascending K
-// from +0.  Then, in fp32,
-//   acc = fma(s, fma(-z, X, P), acc), groups in ascending order from +0,
+// The sum of a group is taken on the matrix cores.  X = sum x comes first (the
+// 16x16x32 step with an operand of ones), and is split into three bf16 pieces
+// that add up to it exactly; P starts as their 16x16x32 bf16 step with -z, and
+// the 16x16x32 steps over x and the integers q (exact in fp16 and bf16) follow
+// in ascending K, all in one fp32 accumulator: P = -z X + sum x q.  Then, in fp32,
+//   acc = fma(s, P, acc), groups in ascending order from +0,
 // and one rounding of acc + b.  Nothing but x and s is ever rounded to 16 bits:
 // the product is as exact as one with fp32 weights.  (Rounding s (q - z) to 16
 // bits first, as a 16-bit weight would be, costs a bf16 result half its
-// accuracy.)
+// accuracy.  z as a matrix step, because in the tile kernel the vector work is
+// what does not hide: a second multiply-add per element and group cost a fifth
+// of its time.)
 //
 // Batch invariance.  That order of operations is a function of (K, group)
 // alone.  Every kernel below follows it, however it spreads rows, columns and
@@ -26,8 +29,8 @@
 // mask (and a shift) leaves four bytes q.  As e4m3 such a byte is q 2^-9 (0..7
 // subnormal, 8..15 the first binade), and the conversion with scale 2^9 turns
 // two of them into two 16-bit integers: 7 instructions for 8 weights.
-// Behind the blocks, one dword per (group, output): the scale's 16 bits and the
-// zero point above them.
+// Behind the blocks, one dword per (group, output): the scale's 16 bits, and
+// above them -z as bf16 (exact: eight bits).
 #include "kernel_common.h"
 #include "layer_internal.h"
 
@@ -37,28 +40,29 @@ using namespace dev;
 
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 
+// Dword p (two integers) of the 16x16x32 operand in a packed dword.
+template <int IN>
+__device__ __forceinline__ int decode_pair(unsigned w, int p) {
+  const unsigned v = (p < 2 ? w : w >> 4) & 0x0f0f0f0fu;
+  if constexpr (IN == GEMM_F16)
+    return __builtin_bit_cast(int, p % 2 ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v, 512.0f, true)
+                                         : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v, 512.0f, false));
+  else
+    return __builtin_bit_cast(int, p % 2 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, 512.0f, true)
+                                         : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, 512.0f, false));
+}
+
 // The eight integers of a packed dword as one 16x16x32 operand.
 template <int IN>
 __device__ __forceinline__ i32x4 decode8(unsigned w) {
-  typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
-  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-  const unsigned lo = w & 0x0f0f0f0fu, hi = (w >> 4) & 0x0f0f0f0fu;
   i32x4 r;
-  if constexpr (IN == GEMM_F16) {
-    r[0] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 512.0f, false));
-    r[1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 512.0f, true));
-    r[2] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 512.0f, false));
-    r[3] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 512.0f, true));
-  } else {
-    r[0] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, false));
-    r[1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, true));
-    r[2] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, false));
-    r[3] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, true));
-  }
+#pragma unroll
+  for (int p = 0; p < 4; ++p) r[p] = decode_pair<IN>(w, p);
   return r;
 }
 
-// The right operand of X = sum x: eight ones.
+// The other operand of X = sum x: eight ones.  x is the right operand there, so
+// every register of lane l holds the sum of row l % 16.
 template <int IN>
 __device__ __forceinline__ i32x4 ones8() {
   constexpr int one = IN == GEMM_F16 ? 0x3c003c00 : 0x3f803f80;
@@ -72,7 +76,29 @@ __device__ __forceinline__ float scale_of(unsigned sz) {
   else
     return __uint_as_float(sz << 16);
 }
-__device__ __forceinline__ float zero_of(unsigned sz) { return (float)(sz >> 16); }
+
+// x as three bf16 values whose sum is x: (first | second << 16, third).
+__device__ __forceinline__ i32x2 split3(float x) {
+  const float h = (float)(__bf16)x, r = x - h, m = (float)(__bf16)r;
+  const unsigned short hb = f32_to_bf16(h), mb = f32_to_bf16(m), lb = f32_to_bf16(r - m);
+  return i32x2{(int)(hb | ((unsigned)mb << 16)), (int)lb};
+}
+// -z against the three pieces of X, which take the first three of the step's 32
+// K positions (`first` is all ones in lanes 0..15 and 0 elsewhere).
+__device__ __forceinline__ i32x4 zero_operand(unsigned sz, unsigned first) {
+  const unsigned z = (sz >> 16) & first;
+  return i32x4{(int)(z | (z << 16)), (int)z, 0, 0};
+}
+// The start of P: -z X.  x holds the pieces in its first two dwords; the other
+// two meet zeros.  Chained matrix steps of different opcodes (this one and the
+// fp16 step) overlap in the pipeline without a dependency check between the
+// first's result and the second's accumulator input, so callers hold the
+// starts in place (hold) and leave at least 32 cycles before the next step.
+__device__ __forceinline__ f32x4 start_of_sum(const i32x4& x, const i32x4& z) {
+  return mfma16_v<GEMM_BF16>(x, z, f32x4{});
+}
+// An empty statement that needs v: what makes v stays before it.
+__device__ __forceinline__ void hold(f32x4& v) { asm volatile("" : "+v"(v)); }
 
 // ---- packing ---------------------------------------------------------------
 
@@ -99,8 +125,8 @@ __global__ __launch_bounds__(256) void w4_pack_kernel(const unsigned char* q, un
   packed[i] = r;
 }
 
-// One thread per (group, output): the scale's bits and the zero point (8
-// without zero points); padding outputs get zeros.
+// One thread per (group, output): the scale's bits and the zero point's negative
+// (8 without zero points); padding outputs get zeros.
 __global__ __launch_bounds__(256) void w4_pack_scales_kernel(const unsigned short* scales,
                                                              const unsigned char* zeros,
                                                              unsigned* sz, int64_t N, int64_t np,
@@ -111,7 +137,7 @@ __global__ __launch_bounds__(256) void w4_pack_scales_kernel(const unsigned shor
   unsigned r = 0;
   if (n < N) {
     const int64_t at = n * groups + gr;
-    r = scales[at] | ((zeros ? (unsigned)zeros[at] : 8u) << 16);
+    r = scales[at] | (__float_as_uint(-(zeros ? (float)zeros[at] : 8.0f)) & 0xffff0000u);
   }
   sz[i] = r;
 }
@@ -119,8 +145,8 @@ __global__ __launch_bounds__(256) void w4_pack_scales_kernel(const unsigned shor
 // ---- few rows ----------------------------------------------------------------
 
 // A workgroup of 8 waves owns RB x CB blocks of 16 x 16 outputs.  The waves
-// share K: wave w takes the 128-K blocks w, w + 8, ...; each leaves P - z X of
-// its groups in LDS, and after a barrier one thread per output adds the round's
+// share K: wave w takes the 128-K blocks w, w + 8, ...; each leaves P of its
+// groups in LDS, and after a barrier one thread per output adds the round's
 // groups in ascending order.  So all of a workgroup's weight loads are in
 // flight at once (U KB a wave and round, the next round's issued before this
 // one's arithmetic), while the order of the sum stays the one above.
@@ -148,6 +174,7 @@ __global__ __launch_bounds__(512) void w4_skinny_kernel(W4Args g) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lr = lane % 16, hq = lane / 16;
+  const unsigned first = hq == 0 ? ~0u : 0u;
   const int64_t cgroups = (g.nblocks + CB - 1) / CB;
   const int64_t cg = blockIdx.x % cgroups, rg = blockIdx.x / cgroups;
   const int64_t m0 = rg * (16 * RB), nb0 = cg * CB;
@@ -224,37 +251,40 @@ __global__ __launch_bounds__(512) void w4_skinny_kernel(W4Args g) {
     for (int u = 0; u < U; ++u) {
 #pragma unroll
       for (int s = 0; s < NG; ++s) {
-        f32x4 P[RB][CB], X[RB];
+        f32x4 P[RB][CB];
 #pragma unroll
         for (int i = 0; i < RB; ++i) {
-          X[i] = f32x4{};
+          f32x4 X{};
 #pragma unroll
-          for (int j = 0; j < CB; ++j) P[i][j] = f32x4{};
+          for (int t = s * (G / 32); t < (s + 1) * (G / 32); ++t)
+            X = mfma16_v<IN>(ones8<IN>(), a[u][t][i], X);
+          const i32x2 x3 = split3(X[0]);
+          const i32x4 xs{x3[0], x3[1], 0, 0};
+#pragma unroll
+          for (int j = 0; j < CB; ++j) {
+            P[i][j] = start_of_sum(xs, zero_operand(sz[u][s][j], first));
+            hold(P[i][j]);
+          }
         }
+        asm volatile("s_nop 15\n\ts_nop 15");
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int t = s * (G / 32); t < (s + 1) * (G / 32); ++t) {
           i32x4 b[CB];
 #pragma unroll
           for (int j = 0; j < CB; ++j) b[j] = decode8<IN>(wc[u][j][t]);
 #pragma unroll
-          for (int i = 0; i < RB; ++i) {
-            X[i] = mfma16_v<IN>(a[u][t][i], ones8<IN>(), X[i]);
+          for (int i = 0; i < RB; ++i)
 #pragma unroll
             for (int j = 0; j < CB; ++j) P[i][j] = mfma16_v<IN>(a[u][t][i], b[j], P[i][j]);
-          }
         }
         const int gr = (u * W + w) * NG + s;
 #pragma unroll
         for (int j = 0; j < CB; ++j) {
-          const float z = zero_of(sz[u][s][j]);
           if (hq == 0) scl[buf][gr][16 * j + lr] = scale_of<IN>(sz[u][s][j]);
 #pragma unroll
-          for (int i = 0; i < RB; ++i) {
-            f32x4 v;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = fmaf(-z, X[i][e], P[i][j][e]);
-            *reinterpret_cast<f32x4*>(&part[buf][gr][((i * CB + j) * 64 + lane) * 4]) = v;
-          }
+          for (int i = 0; i < RB; ++i)
+            *reinterpret_cast<f32x4*>(&part[buf][gr][((i * CB + j) * 64 + lane) * 4]) = P[i][j];
         }
       }
     }
@@ -289,10 +319,11 @@ __global__ __launch_bounds__(512) void w4_skinny_kernel(W4Args g) {
 
 // ---- many rows ---------------------------------------------------------------
 
-// X = sum x of every (row, group), fp32 [groups, m_pad], by the chain of the
-// few-rows kernel: one wave per 16 rows and group.  The tile kernel reads it
-// instead of spending a fifth of its matrix steps on it (each column of waves
-// would repeat them).  Rows past M repeat the last row.
+// The three pieces of X = sum x for every (group, row), 8 bytes each,
+// [groups, m_pad], by the chain of the few-rows kernel: one wave per 16 rows and
+// group.  The tile kernel reads them instead of spending a fifth of its matrix
+// steps on X (each column of waves would repeat them).  Rows past M repeat the
+// last row.
 template <int IN, int G>
 __global__ __launch_bounds__(256) void w4_group_sums_kernel(W4Args g) {
   const int lane = threadIdx.x & 63;
@@ -307,23 +338,33 @@ __global__ __launch_bounds__(256) void w4_group_sums_kernel(W4Args g) {
   for (int t = 0; t < G / 32; ++t) a[t] = *reinterpret_cast<const i32x4*>(p + 64 * t);
   f32x4 X{};
 #pragma unroll
-  for (int t = 0; t < G / 32; ++t) X = mfma16_v<IN>(a[t], ones8<IN>(), X);
-  if (lane % 16 == 0)
-    *reinterpret_cast<f32x4*>(g.sums + gr * g.m_pad + m0 + 4 * (lane / 16)) = X;
+  for (int t = 0; t < G / 32; ++t) X = mfma16_v<IN>(ones8<IN>(), a[t], X);
+  if (lane < 16) static_cast<i32x2*>(g.sums)[gr * g.m_pad + row] = split3(X[0]);
 }
 
 constexpr unsigned OOB = 0x80000000u;  // an offset past every buffer: zeros
 
-// 16 bytes per lane from base + off to LDS (lane l at dst + 16 l).  (The
-// host pass, which knows no 16-byte transfers, would drop the kernel's stub.)
-__device__ __forceinline__ void dma16(const void* base, char* dst, unsigned off) {
+// A buffer that starts at base (raw, no limit but the 31-bit offset's).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const void* base) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, 0x7fffffff, 0x00020000);
+}
+// 16 bytes per lane from the buffer's byte off + uni (uni the same for the wave)
+// to LDS (lane l at dst + 16 l).  (The host pass, which knows no 16-byte
+// transfers, would drop the kernel's stub.)
+__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t buf, char* dst, unsigned off, int uni) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(
-      __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, 0x7fffffff, 0x00020000),
-      IMM_LDS(dst), 16, off, 0, 0, 0);
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, IMM_LDS(dst), 16, off, uni, 0, 0);
 #endif
 }
 
+// The same 8 bytes twice, as a 4-dword operand.
+template <int OFF>
+__device__ __forceinline__ i32x4 ds_read_b64_twice_at(unsigned addr) {
+  static_assert(OFF % 8 == 0 && OFF >= 0 && OFF / 8 < 256, "ds_read2 offset field");
+  i32x4 v;
+  asm volatile("ds_read2_b64 %0, %1 offset0:%2 offset1:%2" : "=v"(v) : "v"(addr), "n"(OFF / 8));
+  return v;
+}
 template <int OFF>
 __device__ __forceinline__ unsigned ds_read_b32_at(unsigned addr) {
   static_assert(OFF >= 0 && OFF < 65536, "ds_read offset field");
@@ -332,23 +373,32 @@ __device__ __forceinline__ unsigned ds_read_b32_at(unsigned addr) {
   return v;
 }
 
+// A copy in a register of its own (so that the next stage's weight blocks can
+// land in the ones it came from).
+__device__ __forceinline__ unsigned copied(unsigned v) {
+  unsigned r;
+  asm volatile("v_mov_b32 %0, %1" : "=v"(r) : "v"(v));
+  return r;
+}
+
 // A workgroup of WM x WN waves owns a tile of TM x TN outputs, each wave FM x FN
 // blocks of 16 x 16.  K is walked in stages of one 128-K block.  A ring of NS
-// LDS stages (x rows of 256 bytes, packed weight blocks as they lie in memory;
-// beside it scale words and group sums) is filled by buffer->LDS DMA.  A wave decodes its
+// LDS stages (x rows of 256 bytes, packed weight blocks as they lie in memory,
+// scale words and pieces of X) is filled by buffer->LDS DMA.  A wave decodes its
 // own weight blocks from LDS to registers, sums a group into P on the matrix
-// cores and folds P into acc with two fused multiply-adds an element.  The
-// matrix steps and the vector work (decode 28 instructions a block and stage,
-// fold 8 a block pair and group) take about the same time, so two waves share
-// a SIMD and fill each other's gaps.
+// cores and folds P into acc with one fused multiply-add an element.  Every
+// matrix step is followed by the vector work that fits under it: a quarter of
+// the next block column's decoding and, in the last k-step of a group, the fold
+// of the block column before.
 //
 // LDS reads are inline assembly with explicit waits (the compiler would make
-// each wait for every DMA in flight).  The stage change sits before the last
+// each wait for every DMA in flight), spread between the matrix steps: sixteen
+// of them in a row, in all eight waves, held the steps up for 500 cycles.  The stage change sits before the last
 // k-step: all of the wave's reads of stage t have landed, its DMA of stage t + 1
-// too, and after one barrier the slot of stage t is refilled and the first
-// fragments of stage t + 1 are read under that k-step's arithmetic.  Scale
-// words and sums are read after that barrier, when a group ends, so their ring
-// has one slot more: a refill overwrites those of the stage before.
+// too, and after one barrier the first fragments of stage t + 1 are read under
+// that k-step's arithmetic.  The refill of stage t's slot is spread over the
+// next four k-steps: the eight waves' transfers, issued at once, would stall
+// each other's matrix steps behind them.
 //
 // 16-byte chunk c of an x row r lies at slot c ^ (r & 15): the 16 rows that a
 // quarter of a wave reads at one chunk fall on different banks.
@@ -357,16 +407,22 @@ struct TileShape {
   static constexpr int TM = 16 * FM * WM, TN = 16 * FN * WN, WAVES = WM * WN;
   static constexpr int NG = 128 / G;
   static constexpr int A_STAGE = TM * 256, B_STAGE = TN * 64;
-  static constexpr int RS = 1024 / (TN * 4), RX = 1024 / (TM * 4);  // rows per 1 KB transfer
+  static constexpr int RS = 1024 / (TN * 4), RX = 1024 / (TM * 8);  // rows per 1 KB transfer
   static constexpr int IS = (NG + RS - 1) / RS, IX = (NG + RX - 1) / RX;
   static constexpr int ITEMS = IS + IX;
-  static constexpr int STAGE = A_STAGE + B_STAGE;
-  static constexpr int META = ITEMS * 1024;      // scale words and sums of a stage
-  static constexpr int LDS = NS * STAGE + (NS + 1) * META;
-  static constexpr int DA = A_STAGE / 1024 / WAVES, DB = B_STAGE / 1024 / WAVES;
-  static_assert(DA * WAVES * 1024 == A_STAGE && DB * WAVES * 1024 == B_STAGE, "DMA split");
+  static constexpr int STAGE = A_STAGE + B_STAGE + ITEMS * 1024;
+  static constexpr int LDS = NS * STAGE;
+  // transfers of 1 KB: DA of x rows per wave, then the weight blocks and the
+  // items dealt out to the waves in turn (REST of them, waves below MORE one more)
+  static constexpr int DA = A_STAGE / 1024 / WAVES, NB = B_STAGE / 1024;
+  static constexpr int REST = (NB + ITEMS) / WAVES, MORE = (NB + ITEMS) % WAVES;
+  static constexpr int DMAS = DA + REST + (MORE ? 1 : 0);
+  static_assert(DA * WAVES * 1024 == A_STAGE, "DMA split");
   static_assert(ITEMS <= WAVES && RS >= 1 && RX >= 1, "one scale or sum transfer per wave");
   static_assert(LDS <= 160 * 1024, "LDS");
+  // where the scale words and the pieces of group gi lie behind the blocks
+  static constexpr int sz_at(int gi) { return gi / RS * 1024 + gi % RS * (TN * 4); }
+  static constexpr int x_at(int gi) { return (IS + gi / RX) * 1024 + gi % RX * (TM * 8); }
 };
 
 template <int IN, int G, int FM, int FN, int WM, int WN, int NS>
@@ -385,52 +441,56 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void w4_tile_kernel(W4Args g) {
   const int groups = (int)g.groups;
   const int64_t np = g.nblocks * 16;
 
-  // ---- DMA: this lane's offsets from the stage's first byte
-  unsigned a_off[S::DA], b_off[S::DB];
-  int a_k[S::DA];  // first K element of the chunk within the stage
+  // ---- DMA.  Transfer i of x of this wave fills rows 4 (w DA + i) .. + 3: lane l
+  // brings chunk c of row l / 16, which belongs at slot l % 16.  What depends on
+  // the lane alone is made once (a row past M reads out of range: zeros), what
+  // the wave shares goes into the scalar offset, so that a transfer costs no
+  // vector work.
+  unsigned a_off[S::DA];
 #pragma unroll
   for (int i = 0; i < S::DA; ++i) {
-    const int row = 4 * (w * S::DA + i) + lane / 16;
-    const int c = (lane % 16) ^ (row & 15);
-    a_off[i] = m0 + row < g.M ? (unsigned)(row * g.K * 2 + c * 16) : OOB;
-    a_k[i] = 8 * c;
+    const int row = 4 * (w * S::DA + i) + lane / 16, c = (lane % 16) ^ (row & 15);
+    a_off[i] = m0 + row < g.M ? (unsigned)(lane / 16 * g.K * 2 + c * 16) : OOB;
   }
-#pragma unroll
-  for (int i = 0; i < S::DB; ++i) {
-    const int j = w * S::DB + i;
-    b_off[i] = nb0 + j < g.nblocks ? (unsigned)(j * g.kblocks * 1024 + lane * 16) : OOB;
-  }
-  auto dma_stage = [&](int t) {
-    const int slot = (t % NS) * S::STAGE;
-    // past the last stage every transfer is a zero fill, so that the counts of
-    // transfers in flight never change
-    const bool live = t < nt;
-    const int64_t krem = g.K - (int64_t)t * 128;
-    const char* pa = static_cast<const char*>(g.x) + (m0 * g.K + (int64_t)(live ? t : 0) * 128) * 2;
-    const char* pb = static_cast<const char*>(g.packed) + (nb0 * g.kblocks + (live ? t : 0)) * 1024;
-#pragma unroll
-    for (int i = 0; i < S::DA; ++i)
-      dma16(pa, lds + slot + (w * S::DA + i) * 1024, live && a_k[i] < krem ? a_off[i] : OOB);
-#pragma unroll
-    for (int i = 0; i < S::DB; ++i)
-      dma16(pb, lds + slot + S::A_STAGE + (w * S::DB + i) * 1024,
-            live ? b_off[i] : OOB);
-    if (w < S::ITEMS) {
-      // 1 KB of scale words (rows of TN) or of group sums (rows of TM)
-      const bool sums = w >= S::IS;
-      const int per = sums ? TM / 4 : TN / 4;                   // lanes per row
-      const int item = sums ? w - S::IS : w;
-      const int gi = t * NG + item * (sums ? S::RX : S::RS);    // first group of the item
-      const int gl = item * (sums ? S::RX : S::RS) + lane / per;
-      const int at = (lane % per) * 4;
-      const int64_t pitch = sums ? g.m_pad : np;
-      const char* base = sums ? reinterpret_cast<const char*>(g.sums) + m0 * 4
-                              : reinterpret_cast<const char*>(g.sz) + nb0 * 64;
-      const bool ok = live && gl < NG && t * NG + gl < groups && (sums || nb0 * 16 + at < np);
-      const unsigned off = ok ? (unsigned)((lane / per) * pitch * 4 + at * 4) : OOB;
-      dma16(base + (gi < groups ? gi : 0) * pitch * 4,
-            lds + NS * S::STAGE + (t % (NS + 1)) * S::META + w * 1024, off);
+  const unsigned b_off = lane * 16;
+  // the wave's item, if below ITEMS: 1 KB of scale words (rows of 4 TN bytes) or of
+  // pieces of X (rows of 8 TM bytes), a row per group of the stage
+  const int item = (w + S::WAVES - S::NB % S::WAVES) % S::WAVES;
+  const bool sums = item >= S::IS;
+  const int64_t mpitch = sums ? g.m_pad * 8 : np * 4;
+  const int mrow = sums ? lane / (TM / 2) : lane / (TN / 4);
+  const int mat = (sums ? lane % (TM / 2) : lane % (TN / 4)) * 16;
+  const int mgroup = (sums ? (item - S::IS) * S::RX : item * S::RS) + mrow;  // this lane's group
+  const unsigned m_off = mgroup < NG && mrow < (sums ? S::RX : S::RS) &&
+                                 (sums || nb0 * 64 + mat < np * 4)
+                             ? (unsigned)(mgroup * mpitch + mat)
+                             : OOB;
+  const auto abuf = buffer_at(static_cast<const char*>(g.x) + m0 * g.K * 2);
+  const auto bbuf = buffer_at(static_cast<const char*>(g.packed) + nb0 * g.kblocks * 1024);
+  const auto mbuf = buffer_at(sums ? static_cast<const char*>(g.sums) + m0 * 8
+                                   : reinterpret_cast<const char*>(g.sz) + nb0 * 64);
+  const int a_pitch = (int)(8 * g.K), b_pitch = (int)(g.kblocks * 1024), m_step = (int)(mpitch * NG);
+  // Transfer x of this wave for stage t, into the slot at `slot`.
+  constexpr int DMAS = S::DMAS;
+  const int whole = (int)(g.K / 128);  // stages before a partial one
+  auto dma_one = [&](int t, int slot, int x) {
+    if (x < S::DA) {
+      const int q = w * S::DA + x;
+      unsigned off = a_off[x];
+      if (t >= whole) {  // chunks past K: zeros
+        const int c = (lane % 16) ^ ((4 * q + lane / 16) & 15);
+        off = 8 * c < g.K - (int64_t)t * 128 ? off : OOB;
+      }
+      dma16(abuf, lds + slot + q * 1024, off, q * a_pitch + t * 256);
+      return;
     }
+    const int j = (x - S::DA) * S::WAVES + w;
+    if ((x - S::DA + 1) * S::WAVES <= S::NB || j < S::NB)
+      dma16(bbuf, lds + slot + S::A_STAGE + j * 1024, nb0 + j < g.nblocks ? b_off : OOB,
+            j * b_pitch + t * 1024);
+    else if (j - S::NB < S::ITEMS)
+      dma16(mbuf, lds + slot + S::A_STAGE + S::B_STAGE + item * 1024,
+            t * NG + mgroup < groups ? m_off : OOB, t * m_step);
   };
   auto fence = [&]() { __builtin_amdgcn_sched_barrier(0); };
   auto lds_wait = [&]() {
@@ -438,14 +498,15 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void w4_tile_kernel(W4Args g) {
     __builtin_amdgcn_s_waitcnt(lgkmcnt_imm(0));
     fence();
   };
-  // all transfers of stage t + 1 landed, NS - 2 later stages in flight
-  auto dma_wait = [&]() {
-    constexpr int D = S::DA + S::DB;
+  // All transfers of a stage landed, those of the `later` stages after it in
+  // flight; then every wave's.
+  auto dma_wait = [&](auto LATER) {
+    constexpr int later = decltype(LATER)::value, D = S::DA + S::REST;
     fence();
-    if (w < S::ITEMS)
-      __builtin_amdgcn_s_waitcnt(vmcnt_imm((NS - 2) * (D + 1)));
+    if (w < S::MORE)
+      __builtin_amdgcn_s_waitcnt(vmcnt_imm(later * (D + 1)));
     else
-      __builtin_amdgcn_s_waitcnt(vmcnt_imm((NS - 2) * D));
+      __builtin_amdgcn_s_waitcnt(vmcnt_imm(later * D));
     __builtin_amdgcn_s_barrier();
     fence();
   };
@@ -457,96 +518,125 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void w4_tile_kernel(W4Args g) {
   for (int ks = 0; ks < 4; ++ks)
     a_rd[ks] = lds0 + (wm * FM * 16 + lb) * 256 + (((4 * ks + hq) ^ lb) << 4);
   const unsigned b_rd = lds0 + S::A_STAGE + wn * FN * 1024 + lane * 16;
-  const unsigned s_rd = lds0 + NS * S::STAGE + (wn * FN * 16 + lb) * 4;
-  const unsigned x_rd = lds0 + NS * S::STAGE + S::IS * 1024 + (wm * FM * 16 + 4 * hq) * 4;
+  const unsigned s_rd = lds0 + S::A_STAGE + S::B_STAGE + (wn * FN * 16 + lb) * 4;
+  const unsigned x_rd = lds0 + S::A_STAGE + S::B_STAGE + (wm * FM * 16 + lb) * 8;
+  const unsigned first_lanes = hq == 0 ? ~0u : 0u;
 
   i32x4 A[2][FM], W[FN];
+  i32x4 X[FM];        // pieces (twice) of the next group to start, and its scale words
+  unsigned sz[FN];
   f32x4 P[FM][FN], acc[FM][FN];
 #pragma unroll
   for (int i = 0; i < FM; ++i)
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = P[i][j] = f32x4{};
 
-  auto read_a = [&](auto KS, int slot, i32x4 (&F)[FM]) {
-    constexpr int ks = decltype(KS)::value;
-    static_for<0, FM>([&](auto I) { F[decltype(I)::value] = ds_read_b128_at<decltype(I)::value * 4096>(a_rd[ks] + slot); });
+  // LDS read r of those that a k-step ks issues for the k-step after it, from the
+  // slot at `from`: (after the last k-step of a stage) the weight blocks, the x
+  // fragments and (where a group starts there) its scale words and pieces.
+  auto read_next = [&](auto KS, auto R, int from) {
+    constexpr int ks = (decltype(KS)::value + 1) % 4, nw = ks == 0 ? FN : 0, r = decltype(R)::value;
+    constexpr int gi = ks / KPG;
+    if constexpr (r < nw)
+      W[r] = ds_read_b128_at<r * 1024>(b_rd + from);
+    else if constexpr (r < nw + FM)
+      A[ks & 1][r - nw] = ds_read_b128_at<(r - nw) * 4096>(a_rd[ks] + from);
+    else if constexpr (r < nw + FM + FN)
+      sz[r - nw - FM] = ds_read_b32_at<S::sz_at(gi) + (r - nw - FM) * 64>(s_rd + from);
+    else
+      X[r - nw - FM - FN] = ds_read_b64_twice_at<(r - nw - FM - FN) * 128>(x_rd + (from + S::x_at(gi)));
   };
-  auto read_w = [&](int slot) {
-    static_for<0, FN>([&](auto J) { W[decltype(J)::value] = ds_read_b128_at<decltype(J)::value * 1024>(b_rd + slot); });
-  };
-  for (int t = 0; t < NS; ++t) dma_stage(t);
-  // stage 0 landed: NS - 1 later ones in flight
-  fence();
-  if (w < S::ITEMS)
-    __builtin_amdgcn_s_waitcnt(vmcnt_imm((NS - 1) * (S::DA + S::DB + 1)));
-  else
-    __builtin_amdgcn_s_waitcnt(vmcnt_imm((NS - 1) * (S::DA + S::DB)));
-  __builtin_amdgcn_s_barrier();
-  fence();
-  read_w(0);
-  read_a(std::integral_constant<int, 0>{}, 0, A[0]);
+  // how many there are
+  auto reads_of = [](int ks) { return (ks == 3 ? FN : 0) + FM + ((ks + 1) % KPG == 0 ? FN + FM : 0); };
 
+  for (int t = 0; t < NS && t < nt; ++t) {
+#pragma unroll
+    for (int x = 0; x < DMAS; ++x) dma_one(t, t * S::STAGE, x);
+  }
+  if (nt >= NS)
+    dma_wait(std::integral_constant<int, NS - 1>{});
+  else
+    dma_wait(std::integral_constant<int, 0>{});
+  static_for<0, 2 * (FM + FN)>([&](auto R) { read_next(std::integral_constant<int, 3>{}, R, 0); });
+  lds_wait();
+
+  float sc[FN];
+#pragma unroll
+  for (int j = 0; j < FN; ++j) sc[j] = 0.0f;
+  int slot = 0, prev = 0;  // of stage t, of the stage before
   for (int t = 0; t < nt; ++t) {
-    const int slot = (t % NS) * S::STAGE, next = ((t + 1) % NS) * S::STAGE;
-    const int meta = (t % (NS + 1)) * S::META;
+    const int next = slot + S::STAGE < NS * S::STAGE ? slot + S::STAGE : 0;
     static_for<0, 4>([&](auto KS) {
       constexpr int ks = decltype(KS)::value;
-      constexpr bool ends = (ks + 1) % KPG == 0;  // this k-step ends a group
-      constexpr int gi = ks / KPG;                // the group within the stage
-      lds_wait();  // this k-step's fragments
-      i32x4 b[FN];
+      constexpr bool first = ks % KPG == 0;       // this k-step starts a group
+      constexpr bool ends = (ks + 1) % KPG == 0;  // ... ends one
+      if constexpr (ks > 0) lds_wait();  // this k-step's fragments
+      unsigned wd[FN];
 #pragma unroll
-      for (int j = 0; j < FN; ++j) b[j] = decode8<IN>((unsigned)W[j][ks]);
-      fence();
-      if constexpr (ks < 3) {
-        read_a(std::integral_constant<int, ks + 1>{}, slot, A[(ks + 1) & 1]);
-      } else {
-        dma_wait();
-        dma_stage(t + NS);
-        read_w(next);
-        read_a(std::integral_constant<int, 0>{}, next, A[0]);
-      }
-      fence();
-      unsigned sz[FN];
-      i32x4 X[FM];
-      static_for<0, FM>([&](auto I) {
-        constexpr int i = decltype(I)::value;
-#pragma unroll
-        for (int j = 0; j < FN; ++j)
-          P[i][j] = mfma16_v<IN>(A[ks & 1][i], b[j], ks % KPG == 0 ? f32x4{} : P[i][j]);
-        if constexpr (ends && i == FM - 2) {
-          // the group's scale words and sums, under the rest of its matrix steps
-          fence();
-          static_for<0, FN>([&](auto J) {
-            sz[decltype(J)::value] = ds_read_b32_at<gi * TN * 4 + decltype(J)::value * 64>(s_rd + meta);
-          });
-          static_for<0, FM>([&](auto R) {
-            X[decltype(R)::value] = ds_read_b128_at<gi * TM * 4 + decltype(R)::value * 64>(x_rd + meta);
-          });
-          fence();
-        }
-      });
-      if constexpr (ends) {
-        lds_wait();
-        if (t * NG + gi < groups) {
-          float sc[FN], zn[FN];
-#pragma unroll
-          for (int j = 0; j < FN; ++j) {
-            sc[j] = scale_of<IN>(sz[j]);
-            zn[j] = -zero_of(sz[j]);
-          }
+      for (int j = 0; j < FN; ++j) wd[j] = ks < 3 ? (unsigned)W[j][ks] : copied((unsigned)W[j][ks]);
+      if constexpr (first) {
+        // P starts as -z X.  A group past K gets the scale -0, whose fold (of a
+        // sum of zeros) leaves every acc as it is.
+        const bool exists = t * NG + ks / KPG < groups;
+        static_for<0, FN>([&](auto J) {
+          constexpr int j = decltype(J)::value;
+          const i32x4 z = zero_operand(sz[j], first_lanes);
+          sc[j] = exists ? scale_of<IN>(sz[j]) : -0.0f;
 #pragma unroll
           for (int i = 0; i < FM; ++i) {
-            const f32x4 xs = __builtin_bit_cast(f32x4, X[i]);
-#pragma unroll
-            for (int j = 0; j < FN; ++j)
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                acc[i][j][e] = fmaf(sc[j], fmaf(zn[j], xs[e], P[i][j][e]), acc[i][j][e]);
+            P[i][j] = start_of_sum(X[i], z);
+            hold(P[i][j]);
           }
-        }
+        });
       }
+      i32x4 b = decode8<IN>(wd[0]), bn{};
+      fence();
+      if constexpr (ks == 3) {
+        if (t + NS <= nt)  // the stages t + 2 .. t + NS - 1 are in flight
+          dma_wait(std::integral_constant<int, NS - 2>{});
+        else
+          dma_wait(std::integral_constant<int, 0>{});
+      }
+      auto fold = [&](int i, int j) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(sc[j], P[i][j][e], acc[i][j][e]);
+        // holds the fold at its place (instruction selection may otherwise sink
+        // it past later k-steps, with P alive until there)
+        hold(acc[i][j]);
+      };
+      static_for<0, FN>([&](auto J) {
+        constexpr int j = decltype(J)::value;
+        static_for<0, FM>([&](auto I) {
+          constexpr int i = decltype(I)::value;
+          P[i][j] = mfma16_v<IN>(A[ks & 1][i], b, P[i][j]);
+          if constexpr (j + 1 < FN) {
+#pragma unroll
+            for (int p = i * 4 / FM; p < (i + 1) * 4 / FM; ++p) bn[p] = decode_pair<IN>(wd[j + 1], p);
+          }
+          if constexpr (ends && j > 0) fold(i, j - 1);
+          // the next k-step's LDS reads, over the first three quarters
+          constexpr int blk = j * FM + i, SPAN = FM * FN * 3 / 4, NR = reads_of(ks);
+          static_for<(blk < SPAN ? blk * NR / SPAN : NR), (blk < SPAN ? (blk + 1) * NR / SPAN : NR)>(
+              [&](auto R) { read_next(KS, R, ks == 3 ? next : slot); });
+          // the refill of the slot that the last stage change freed
+          constexpr int at = ((ks + 1) % 4 * FN + j) * FM + i, NB = 4 * FM * FN;
+#pragma unroll
+          for (int x = at * DMAS / NB; x < (at + 1) * DMAS / NB; ++x) {
+            const int r = ks == 3 ? t + NS : t + NS - 1;
+            if (r >= NS && r < nt) dma_one(r, ks == 3 ? slot : prev, x);
+          }
+          fence();
+        });
+        b = bn;
+      });
+      if constexpr (ends) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i) fold(i, FN - 1);
+      }
+      if constexpr (ks == 3) lds_wait();  // before the loop's own register copies
     });
+    prev = slot;
+    slot = next;
   }
   // No transfer or read is in flight when the workgroup ends; the reads of the
   // stage past the last one keep their registers until they have landed.
@@ -558,6 +648,10 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void w4_tile_kernel(W4Args g) {
   for (int i = 0; i < FM; ++i) keep_live<4>(A[0][i]);
 #pragma unroll
   for (int j = 0; j < FN; ++j) keep_live<4>(W[j]);
+#pragma unroll
+  for (int i = 0; i < FM; ++i) keep_live<4>(X[i]);
+#pragma unroll
+  for (int j = 0; j < FN; ++j) asm volatile("" : : "v"(sz[j]));
   fence();
 #pragma unroll
   for (int j = 0; j < FN; ++j) {
@@ -596,9 +690,28 @@ hipError_t launch_skinny(const W4Args& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Which tile takes a grid: 64 x 128 (four waves of 64 x 32; three workgroups
+// share a compute unit and fill each other's waits) or 128 x 256 (eight waves of
+// 64 x 64, alone on its unit).  The large one shares its decoding among more
+// rows and is 5 % faster on a full machine (4096 x 14336, K = 4096, group 128: 532
+// against 558 us), the small one fills small and odd grids (256 x 6144: 49
+// against 74 us, 2048 x 6144: 129 against 147, but 2048 x 4096, four workgroups a
+// unit, 114 against 88).  Cost in us per K = 4096 on 256 units: 72 a round of large
+// tiles; 60 for three small tiles on a unit, 36 and 46 for one or two left over
+// (other groups and K scale all of them).  Bits do not depend on the tile.
+bool large_tiles(int64_t M, int64_t N) {
+  auto per_unit = [&](int64_t tm, int64_t tn) {
+    return (((M + tm - 1) / tm) * ((N + tn - 1) / tn) + 255) / 256;
+  };
+  const int64_t n = per_unit(64, 128), left = n % 3;
+  return 72 * per_unit(128, 256) < n / 3 * 60 + (left == 0 ? 0 : left == 1 ? 36 : 46);
+}
+
 template <int IN, int G>
 hipError_t launch_group(const W4Args& a, hipStream_t s) {
-  if (a.sums) return launch_tile<IN, G, 4, 4, 2, 4, G == 32 ? 2 : 3>(a, s);
+  if (a.sums)
+    return large_tiles(a.M, a.N) ? launch_tile<IN, G, 4, 4, 2, 4, G == 32 ? 2 : 3>(a, s)
+                                 : launch_tile<IN, G, 4, 2, 1, 4, 2>(a, s);
   if (a.M <= 16) return launch_skinny<IN, G, 1, 1>(a, s);
   return launch_skinny<IN, G, 2, 1>(a, s);
 }
@@ -627,9 +740,11 @@ hipError_t launch_w4_pack(int64_t N, int64_t K, int group, const void* q, const 
   return hipGetLastError();
 }
 
-bool w4_uses_tiles(int64_t M, int64_t K) {
-  // the tile kernel's 32-bit offsets within 128 rows of x
-  return M > 64 && K > 0 && 128 * K * 2 < ((int64_t)1 << 31);
+bool w4_uses_tiles(int64_t M, int64_t N, int64_t K, int group) {
+  // the tile kernel's 31-bit offsets: within 128 rows of x, within the scale
+  // words and within the pieces of X
+  const int64_t groups = K / group, wide = N + 16 > 2 * (M + kW4RowPad) ? N + 16 : 2 * (M + kW4RowPad);
+  return M > 64 && K > 0 && 256 * K < kMaxOffset && groups * wide * 4 < kMaxOffset;
 }
 
 hipError_t launch_w4(int in, const W4Args& a, hipStream_t s) {

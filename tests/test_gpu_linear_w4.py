@@ -59,7 +59,9 @@ def check(y, s, group, zeros, bias, dt):
     assert (err <= tol).all(), float((err / tol).max())
 
 
-SHAPES = [(1, 8, 128), (1, 4096, 4096), (3, 264, 256), (16, 1024, 1152), (17, 40, 640), (31, 520, 2048),
+# few rows; the 64 x 128 tile; the 128 x 256 tile (2048 x 4096, which small tiles would fill
+# unevenly); ragged rows and columns
+SHAPES = [(2100, 4000, 256), (2048, 4096, 512), (1, 8, 128), (1, 4096, 4096), (3, 264, 256), (16, 1024, 1152), (17, 40, 640), (31, 520, 2048),
           (64, 256, 14336), (65, 1032, 384), (129, 136, 1024), (300, 512, 512), (1030, 264, 896)]
 
 
@@ -103,10 +105,10 @@ def test_bits_of_the_documented_chain(M, group, dt):
 
 @pytest.mark.parametrize("N,K,group", [(4096, 2048, 128), (1032, 4096, 64), (264, 14336, 32)])
 def test_rows_do_not_depend_on_the_batch(N, K, group):
-    s = make(600, N, K, group, "bf16", 67)
+    s = make(2050, N, K, group, "bf16", 67)
     w = torch_ops.pack_w4(s["q"], s["s"], s["z"])
     y = torch_ops.linear_w4(s["x"], w, bias=s["b"])
-    for lo, hi in ((0, 1), (599, 600), (5, 13), (3, 19), (9, 26), (0, 48), (7, 71), (100, 228), (11, 300)):
+    for lo, hi in ((0, 1), (2049, 2050), (599, 600), (1, 2049), (5, 13), (3, 19), (9, 26), (0, 48), (7, 71), (100, 228), (11, 300)):
         assert torch.equal(torch_ops.linear_w4(s["x"][lo:hi], w, bias=s["b"]), y[lo:hi]), (lo, hi)
 
 
