@@ -152,8 +152,10 @@ gemm_status w4_plan(int64_t M, int64_t N, int64_t K, gemm_dtype dtype, int group
     return GEMM_ERR_UNSUPPORTED;
   const int64_t nblocks = (N + 15) / 16, kblocks = (K + 127) / 128, groups = K / group;
   // one workgroup per 16 x 16 outputs at most, one packing thread per dword
-  if (nblocks * ((M + 15) / 16) > INT_MAX || nblocks * kblocks > INT_MAX ||
-      nblocks * groups > INT_MAX)
+  // (units are counted in 32 bits), and the few-rows kernel's 31-bit offsets: 32
+  // rows of x, a round's 128 groups of scale words
+  if (nblocks * ((M + 15) / 16) > INT_MAX / 2 || nblocks * kblocks > INT_MAX ||
+      nblocks * groups > INT_MAX || 64 * K > kMaxOffset || 512 * N > kMaxOffset)
     return GEMM_ERR_UNSUPPORTED;
   w4_plan_s* p = new (std::nothrow) w4_plan_s{M, N, K, dtype, group, nblocks, kblocks, groups};
   if (!p) return GEMM_ERR_INVALID_VALUE;

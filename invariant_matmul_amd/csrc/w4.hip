@@ -14,9 +14,9 @@
 // and one rounding of acc + b.  Nothing but x and s is ever rounded to 16 bits:
 // the product is as exact as one with fp32 weights.  (Rounding s (q - z) to 16
 // bits first, as a 16-bit weight would be, costs a bf16 result half its
-// accuracy.  z as a matrix step, because in the tile kernel the vector work is
-// what does not hide: a second multiply-add per element and group cost a fifth
-// of its time.)
+// accuracy.  z as a matrix step leaves the vector unit, whose work does not
+// hide in the tile kernel, one multiply-add per element and group; a second one
+// in place of that step was as fast within two per cent.)
 //
 // Batch invariance.  That order of operations is a function of (K, group)
 // alone.  Every kernel below follows it, however it spreads rows, columns and
@@ -142,179 +142,275 @@ __global__ __launch_bounds__(256) void w4_pack_scales_kernel(const unsigned shor
   sz[i] = r;
 }
 
+// A buffer of `bytes` (at most 2^31 - 1 count) from base: what lies past it reads as
+// zeros.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const void* base, int64_t bytes) {
+  const int n = bytes < 0x7fffffff ? (int)bytes : 0x7fffffff;
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, n, 0x00020000);
+}
+// 16 or 4 bytes at off; zeros past the end.  (All of the offset in the lane's
+// operand: the check against the end subtracts a scalar offset from the size,
+// which must not pass it.)
+__device__ __forceinline__ u32x4 load_b128(__amdgpu_buffer_rsrc_t buf, unsigned off) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(buf, off, 0, 0));
+#else
+  return u32x4{};
+#endif
+}
+__device__ __forceinline__ unsigned load_b32(__amdgpu_buffer_rsrc_t buf, unsigned off) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  return __builtin_amdgcn_raw_buffer_load_b32(buf, off, 0, 0);
+#else
+  return 0;
+#endif
+}
+
 // ---- few rows ----------------------------------------------------------------
 
-// A workgroup of 8 waves owns RB x CB blocks of 16 x 16 outputs.  The waves
-// share K: wave w takes the 128-K blocks w, w + 8, ...; each leaves P of its
-// groups in LDS, and after a barrier one thread per output adds the round's
-// groups in ascending order.  So all of a workgroup's weight loads are in
-// flight at once (U KB a wave and round, the next round's issued before this
-// one's arithmetic), while the order of the sum stays the one above.
-template <int IN, int G, int RB, int CB>
+// A workgroup of 8 waves makes a unit of RB x CB blocks of 16 x 16 outputs at a
+// time.  The waves share K: in a round, wave w takes U of the 128-K blocks w,
+// w + 8, ..., and leaves P of its groups in LDS; after a barrier every thread adds
+// the round's groups of its outputs in ascending order, which keeps the order of
+// the sum the one above.  The grid is kSkinnyGroups workgroups at most (two on a
+// compute unit where registers allow: one's sums run under the other's matrix
+// steps) and each walks its units (column groups of a row group) and their rounds
+// as one sequence, with the weights of the next two rounds and the rows and scale
+// words of the next one in flight.  Loads return in order: a round's rows are
+// requested before the weights of the round after it, so waiting for them leaves
+// those in flight.  Few rows and many columns are bound by the stream of the
+// weights (1 x 131072, K = 4096: 65 us, 4.1 TB/s); small grids by the round, some
+// 3 us of latencies (1 x 4096, K = 4096: 5.7 us; one round of four blocks a wave and
+// one workgroup a unit: 6.9), more rows by the reads of x that every column
+// group repeats (see skinny_columns).
+template <int G, int RB, int CB>
 struct SkinnyShape {
   static constexpr int W = 8;
   static constexpr int NG = 128 / G;                  // groups per 128-K block
-  static constexpr int GKB = RB * CB;                 // KB of LDS per group
-  // blocks per wave and round: up to 4, within 32 KB of sums (two buffers)
-  static constexpr int U0 = 32 / (W * NG * GKB);
-  static constexpr int U = U0 < 1 ? 1 : U0 > 4 ? 4 : U0;
-  static constexpr int GPR = W * U * NG;              // groups per round
   static constexpr int ELEMS = 256 * RB * CB;
+  // blocks per wave and round: up to 2, within 32 fragments of x and 64 KB of sums
+  static constexpr int UR = 2 / RB, UL = 64 / (W * NG * RB * CB);
+  static constexpr int U = UL < 1 ? 1 : UL < UR ? UL : UR;
+  static constexpr int GPR = W * U * NG;              // groups per round
   static constexpr int PER = (ELEMS + 511) / 512;     // outputs per thread
-  static constexpr int LDS = 2 * GPR * (ELEMS + 16 * CB) * 4;
+  // sums of two rounds where they fit; one, and a barrier more, where not
+  static constexpr int ROUND = GPR * (ELEMS + 16 * CB) * 4;
+  static constexpr int BUFS = 2 * ROUND <= 160 * 1024 ? 2 : 1;
+  static constexpr int LDS = BUFS * ROUND;
 };
+constexpr int64_t kSkinnyGroups = 512;
 
 template <int IN, int G, int RB, int CB>
-__global__ __launch_bounds__(512) void w4_skinny_kernel(W4Args g) {
-  using S = SkinnyShape<IN, G, RB, CB>;
+__global__ __launch_bounds__(512, 2) void w4_skinny_kernel(W4Args g) {
+  using S = SkinnyShape<G, RB, CB>;
   constexpr int W = S::W, NG = S::NG, U = S::U, GPR = S::GPR, ELEMS = S::ELEMS, PER = S::PER;
   static_assert(S::LDS <= 160 * 1024, "LDS");
-  __shared__ __attribute__((aligned(16))) float part[2][GPR][ELEMS];
-  __shared__ float scl[2][GPR][16 * CB];
+  __shared__ __attribute__((aligned(16))) float part[S::BUFS][GPR][ELEMS];
+  __shared__ float scl[S::BUFS][GPR][16 * CB];
   const int tid = threadIdx.x, lane = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lr = lane % 16, hq = lane / 16;
   const unsigned first = hq == 0 ? ~0u : 0u;
   const int64_t cgroups = (g.nblocks + CB - 1) / CB;
-  const int64_t cg = blockIdx.x % cgroups, rg = blockIdx.x / cgroups;
-  const int64_t m0 = rg * (16 * RB), nb0 = cg * CB;
-  const int kblocks = (int)g.kblocks;
-  const int ksteps = (int)(g.K / 32);
-
-  // rows past M and column blocks past N read the last one there is and are
-  // never stored
-  const char* xrow[RB];
-#pragma unroll
-  for (int i = 0; i < RB; ++i) {
-    const int64_t row = m0 + 16 * i + lr;
-    xrow[i] = static_cast<const char*>(g.x) + ((row < g.M ? row : g.M - 1) * g.K + 8 * hq) * 2;
-  }
-  const u32x4* wblk[CB];
-  const unsigned* szp[CB];
-#pragma unroll
-  for (int j = 0; j < CB; ++j) {
-    const int64_t nb = nb0 + j < g.nblocks ? nb0 + j : g.nblocks - 1;
-    wblk[j] = reinterpret_cast<const u32x4*>(g.packed) + nb * g.kblocks * 64 + lane;
-    szp[j] = g.sz + nb * 16 + lr;
-  }
+  const int64_t units = cgroups * ((g.M + 16 * RB - 1) / (16 * RB));
+  const int kblocks = (int)g.kblocks, ksteps = (int)(g.K / 32);
+  const int rounds = kblocks > 0 ? (kblocks + W * U - 1) / (W * U) : 1;
   const int64_t np = g.nblocks * 16;
 
-  float acc[PER];
-#pragma unroll
-  for (int p = 0; p < PER; ++p) acc[p] = 0.0f;
-
-  const int rounds = (kblocks + W * U - 1) / (W * U);
-  u32x4 wn[U][CB];
-  auto load_w = [&](int r) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int kb = (r * U + u) * W + w;
-#pragma unroll
-      for (int j = 0; j < CB; ++j) {
-        wn[u][j] = u32x4{};
-        if (kb < kblocks) wn[u][j] = wblk[j][(int64_t)kb * 64];
-      }
-    }
+  // A place in the sequence: round r of a unit, and the unit's first row and
+  // column block.
+  struct Place {
+    unsigned unit, rg, cg;
+    int r;
   };
-  load_w(0);
-  for (int r = 0; r < rounds; ++r) {
-    const int buf = r & 1;
-    // this round's rows of x and scales, then the next round's weights
-    i32x4 a[U][4][RB];
-    unsigned sz[U][NG][CB];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int kb = (r * U + u) * W + w;
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int i = 0; i < RB; ++i) {
-          a[u][t][i] = i32x4{};
-          if (kb * 4 + t < ksteps)
-            a[u][t][i] = *reinterpret_cast<const i32x4*>(xrow[i] + (int64_t)(kb * 4 + t) * 64);
-        }
-#pragma unroll
-      for (int s = 0; s < NG; ++s)
-#pragma unroll
-        for (int j = 0; j < CB; ++j) {
-          sz[u][s][j] = 0;
-          if ((int64_t)kb * NG + s < g.groups) sz[u][s][j] = szp[j][((int64_t)kb * NG + s) * np];
-        }
-    }
-    u32x4 wc[U][CB];
+  const unsigned nunits = (unsigned)units, ncg = (unsigned)cgroups;
+  auto place_at = [&](unsigned unit) { return Place{unit, unit / ncg, unit % ncg, 0}; };
+  auto advance = [&](Place& p) {
+    if (++p.r == rounds) p = place_at(p.unit + gridDim.x);
+  };
+  // No load is predicated: what a round reads past the last row, column block,
+  // K block or group is another row's or block's (or, past the end of its
+  // matrix, zeros), goes into sums that nothing adds up, or into rows and columns
+  // that are never stored.  Offsets: the lane's, made once, and the wave's.
+  const unsigned x_off = (unsigned)(lr * g.K * 2 + 16 * hq), x_block = (unsigned)(32 * g.K);
+  const unsigned w_off = lane * 16, w_block = (unsigned)(g.kblocks * 1024);
+  const unsigned s_off = lr * 4, s_group = (unsigned)(np * 4);
+  auto load_weights = [&](const Place& p, u32x4 (&wt)[U][CB]) {
+    const int64_t at = ((int64_t)p.cg * CB * kblocks + (int64_t)p.r * U * W + w) * 1024;
+    const int64_t end = g.nblocks * g.kblocks * 1024;
+    const auto buf = buffer_at(static_cast<const char*>(g.packed) + (at < end ? at : 0),
+                               p.unit < nunits && at < end ? end - at : 0);
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int j = 0; j < CB; ++j) wc[u][j] = wn[u][j];
-    if (r + 1 < rounds) load_w(r + 1);
+      for (int j = 0; j < CB; ++j) wt[u][j] = load_b128(buf, w_off + (u * (W * 1024) + j * w_block));
+  };
+  auto load_rows = [&](const Place& p, i32x4 (&a)[U][4][RB], unsigned (&sz)[U][NG][CB]) {
+    const int64_t m0 = (int64_t)p.rg * (16 * RB), k0 = ((int64_t)p.r * U * W + w) * 128;
+    const int64_t xat = (m0 * g.K + k0) * 2, xend = g.M * g.K * 2;
+    const auto xbuf = buffer_at(static_cast<const char*>(g.x) + (xat < xend ? xat : 0),
+                                p.unit < nunits && xat < xend ? xend - xat : 0);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int s = 0; s < NG; ++s) {
-        f32x4 P[RB][CB];
+      for (int i = 0; i < RB; ++i)
 #pragma unroll
-        for (int i = 0; i < RB; ++i) {
-          f32x4 X{};
+        for (int t = 0; t < 4; ++t)
+          a[u][t][i] = __builtin_bit_cast(i32x4, load_b128(xbuf, x_off + (u * (W * 256) + t * 64 + i * x_block)));
+    const int64_t sat = (k0 / G * np + (int64_t)p.cg * CB * 16) * 4, send = g.groups * np * 4;
+    const auto sbuf = buffer_at(reinterpret_cast<const char*>(g.sz) + (sat < send ? sat : 0),
+                                p.unit < nunits && sat < send ? send - sat : 0);
 #pragma unroll
-          for (int t = s * (G / 32); t < (s + 1) * (G / 32); ++t)
-            X = mfma16_v<IN>(ones8<IN>(), a[u][t][i], X);
-          const i32x2 x3 = split3(X[0]);
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int s = 0; s < NG; ++s)
+#pragma unroll
+        for (int j = 0; j < CB; ++j)
+          sz[u][s][j] = load_b32(sbuf, s_off + ((unsigned)(u * W * NG + s) * s_group + j * 64));
+  };
+
+  u32x4 wt[2][U][CB];
+  i32x4 a[2][U][4][RB];
+  unsigned sz[2][U][NG][CB];
+  float acc[PER];
+#pragma unroll
+  for (int p = 0; p < PER; ++p) acc[p] = 0.0f;
+  Place now = place_at(blockIdx.x), rows = now, weights = now;
+  load_weights(weights, wt[0]);
+  advance(weights);
+  load_rows(rows, a[0], sz[0]);
+  advance(rows);
+  load_weights(weights, wt[1]);
+  advance(weights);
+
+  auto step = [&](auto BUF) {
+    constexpr int buf = decltype(BUF)::value, sums = buf % S::BUFS;
+    // element e of a unit: block e / 256, lane (e / 4) % 64, register e % 4 of its
+    // accumulators
+    auto column = [&](int e) {
+      return ((int64_t)now.cg * CB + (e / 256) % CB) * 16 + (e / 4) % 16;
+    };
+    // (the bias before the loads that stay in flight past its use)
+    float bias[PER];
+#pragma unroll
+    for (int p = 0; p < PER; ++p) {
+      const int e = tid + 512 * p;
+      bias[p] = 0.0f;
+      if (g.bias && now.r == rounds - 1 && e < ELEMS && column(e) < g.N) bias[p] = g.bias[column(e)];
+    }
+    load_rows(rows, a[1 - buf], sz[1 - buf]);
+    advance(rows);
+    // the chains of all the wave's groups side by side: first every start, ...
+    f32x4 P[U][NG][RB][CB];
+#pragma unroll
+    for (int i = 0; i < RB; ++i) {
+      f32x4 X[U][NG];
+#pragma unroll
+      for (int t = 0; t < G / 32; ++t)
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int s = 0; s < NG; ++s)
+            X[u][s] = mfma16_v<IN>(ones8<IN>(), a[buf][u][s * (G / 32) + t][i], t == 0 ? f32x4{} : X[u][s]);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int s = 0; s < NG; ++s) {
+          const i32x2 x3 = split3(X[u][s][0]);
           const i32x4 xs{x3[0], x3[1], 0, 0};
 #pragma unroll
           for (int j = 0; j < CB; ++j) {
-            P[i][j] = start_of_sum(xs, zero_operand(sz[u][s][j], first));
-            hold(P[i][j]);
+            P[u][s][i][j] = start_of_sum(xs, zero_operand(sz[buf][u][s][j], first));
+            hold(P[u][s][i][j]);
           }
         }
-        asm volatile("s_nop 15\n\ts_nop 15");
-        __builtin_amdgcn_sched_barrier(0);
+    }
+    asm volatile("s_nop 15\n\ts_nop 15");
+    __builtin_amdgcn_sched_barrier(0);
+    // ... then the steps over x and q
 #pragma unroll
-        for (int t = s * (G / 32); t < (s + 1) * (G / 32); ++t) {
-          i32x4 b[CB];
+    for (int t = 0; t < G / 32; ++t)
 #pragma unroll
-          for (int j = 0; j < CB; ++j) b[j] = decode8<IN>(wc[u][j][t]);
+      for (int u = 0; u < U; ++u)
 #pragma unroll
-          for (int i = 0; i < RB; ++i)
+        for (int s = 0; s < NG; ++s)
 #pragma unroll
-            for (int j = 0; j < CB; ++j) P[i][j] = mfma16_v<IN>(a[u][t][i], b[j], P[i][j]);
-        }
+          for (int j = 0; j < CB; ++j) {
+            const i32x4 b = decode8<IN>(wt[buf][u][j][s * (G / 32) + t]);
+#pragma unroll
+            for (int i = 0; i < RB; ++i)
+              P[u][s][i][j] = mfma16_v<IN>(a[buf][u][s * (G / 32) + t][i], b, P[u][s][i][j]);
+          }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int s = 0; s < NG; ++s) {
         const int gr = (u * W + w) * NG + s;
 #pragma unroll
         for (int j = 0; j < CB; ++j) {
-          if (hq == 0) scl[buf][gr][16 * j + lr] = scale_of<IN>(sz[u][s][j]);
+          if (hq == 0) scl[sums][gr][16 * j + lr] = scale_of<IN>(sz[buf][u][s][j]);
 #pragma unroll
           for (int i = 0; i < RB; ++i)
-            *reinterpret_cast<f32x4*>(&part[buf][gr][((i * CB + j) * 64 + lane) * 4]) = P[i][j];
+            *reinterpret_cast<f32x4*>(&part[sums][gr][((i * CB + j) * 64 + lane) * 4]) = P[u][s][i][j];
         }
       }
-    }
+    load_weights(weights, wt[buf]);
+    advance(weights);
     // One barrier a round: the buffer filled two rounds on was read before the
-    // next round's barrier.
-    __syncthreads();
-    const int64_t left = g.groups - (int64_t)r * GPR;
+    // next round's barrier.  (Fences of LDS alone: __syncthreads would wait for
+    // the loads in flight.)
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+    const int64_t left = g.groups - (int64_t)now.r * GPR;
     const int ng = left < GPR ? (int)left : GPR;
 #pragma unroll
     for (int p = 0; p < PER; ++p) {
       const int e = tid + 512 * p;
       if (e < ELEMS) {
         const int col = 16 * ((e / 256) % CB) + (e / 4) % 16;
-#pragma unroll 8
-        for (int k = 0; k < ng; ++k) acc[p] = fmaf(scl[buf][k][col], part[buf][k][e], acc[p]);
+        constexpr int C = GPR < 16 ? GPR : 16;  // groups whose sums are read at once
+        static_assert(GPR % C == 0, "round");
+        int k = 0;
+        for (; k + C <= ng; k += C) {
+          float v[C], sc[C];
+#pragma unroll
+          for (int c = 0; c < C; ++c) {
+            v[c] = part[sums][k + c][e];
+            sc[c] = scl[sums][k + c][col];
+          }
+#pragma unroll
+          for (int c = 0; c < C; ++c) acc[p] = fmaf(sc[c], v[c], acc[p]);
+        }
+        for (; k < ng; ++k) acc[p] = fmaf(scl[sums][k][col], part[sums][k][e], acc[p]);
+        if (now.r == rounds - 1) {
+          const int64_t row = (int64_t)now.rg * (16 * RB) + 16 * (e / 256 / CB) + 4 * ((e / 4) % 64 / 16) + e % 4;
+          const int64_t out = column(e);
+          if (row < g.M && out < g.N) store_out<IN>(g.y, row * g.N + out, g.bias ? acc[p] + bias[p] : acc[p]);
+          acc[p] = 0.0f;
+        }
       }
     }
-  }
-#pragma unroll
-  for (int p = 0; p < PER; ++p) {
-    const int e = tid + 512 * p;
-    if (e < ELEMS) {
-      // element e: block e / 256, lane (e / 4) % 64, register e % 4 of its accumulators
-      const int blk = e / 256, ln = (e / 4) % 64;
-      const int64_t row = m0 + 16 * (blk / CB) + 4 * (ln / 16) + e % 4;
-      const int64_t col = (nb0 + blk % CB) * 16 + ln % 16;
-      if (row < g.M && col < g.N)
-        store_out<IN>(g.y, row * g.N + col, g.bias ? acc[p] + g.bias[col] : acc[p]);
+    if constexpr (S::BUFS == 1) {
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+      __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
     }
+    advance(now);
+  };
+  while (now.unit < nunits) {
+    step(std::integral_constant<int, 0>{});
+    if (now.unit >= nunits) break;
+    step(std::integral_constant<int, 1>{});
   }
+}
+
+template <int IN, int G, int RB, int CB>
+hipError_t launch_skinny(const W4Args& a, hipStream_t s) {
+  const int64_t units = (a.nblocks + CB - 1) / CB * ((a.M + 16 * RB - 1) / (16 * RB));
+  hipLaunchKernelGGL((w4_skinny_kernel<IN, G, RB, CB>),
+                     dim3((unsigned)(units < kSkinnyGroups ? units : kSkinnyGroups)), dim3(512), 0, s, a);
+  return hipGetLastError();
 }
 
 // ---- many rows ---------------------------------------------------------------
@@ -344,10 +440,6 @@ __global__ __launch_bounds__(256) void w4_group_sums_kernel(W4Args g) {
 
 constexpr unsigned OOB = 0x80000000u;  // an offset past every buffer: zeros
 
-// A buffer that starts at base (raw, no limit but the 31-bit offset's).
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const void* base) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, 0x7fffffff, 0x00020000);
-}
 // 16 bytes per lane from the buffer's byte off + uni (uni the same for the wave)
 // to LDS (lane l at dst + 16 l).  (The host pass, which knows no 16-byte
 // transfers, would drop the kernel's stub.)
@@ -465,10 +557,10 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void w4_tile_kernel(W4Args g) {
                                  (sums || nb0 * 64 + mat < np * 4)
                              ? (unsigned)(mgroup * mpitch + mat)
                              : OOB;
-  const auto abuf = buffer_at(static_cast<const char*>(g.x) + m0 * g.K * 2);
-  const auto bbuf = buffer_at(static_cast<const char*>(g.packed) + nb0 * g.kblocks * 1024);
+  const auto abuf = buffer_at(static_cast<const char*>(g.x) + m0 * g.K * 2, kMaxOffset * 2);
+  const auto bbuf = buffer_at(static_cast<const char*>(g.packed) + nb0 * g.kblocks * 1024, kMaxOffset * 2);
   const auto mbuf = buffer_at(sums ? static_cast<const char*>(g.sums) + m0 * 8
-                                   : reinterpret_cast<const char*>(g.sz) + nb0 * 64);
+                                   : reinterpret_cast<const char*>(g.sz) + nb0 * 64, kMaxOffset * 2);
   const int a_pitch = (int)(8 * g.K), b_pitch = (int)(g.kblocks * 1024), m_step = (int)(mpitch * NG);
   // Transfer x of this wave for stage t, into the slot at `slot`.
   constexpr int DMAS = S::DMAS;
@@ -683,13 +775,6 @@ hipError_t launch_tile(W4Args a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int IN, int G, int RB, int CB>
-hipError_t launch_skinny(const W4Args& a, hipStream_t s) {
-  const int64_t cg = (a.nblocks + CB - 1) / CB, rg = (a.M + 16 * RB - 1) / (16 * RB);
-  hipLaunchKernelGGL((w4_skinny_kernel<IN, G, RB, CB>), dim3((unsigned)(cg * rg)), dim3(512), 0, s, a);
-  return hipGetLastError();
-}
-
 // Which tile takes a grid: 64 x 128 (four waves of 64 x 32; three workgroups
 // share a compute unit and fill each other's waits) or 128 x 256 (eight waves of
 // 64 x 64, alone on its unit).  The large one shares its decoding among more
@@ -707,13 +792,29 @@ bool large_tiles(int64_t M, int64_t N) {
   return 72 * per_unit(128, 256) < n / 3 * 60 + (left == 0 ? 0 : left == 1 ? 36 : 46);
 }
 
+// Blocks of 16 columns in a unit of the few-rows kernel: the fewest that leave at
+// most one unit for each of 256 compute units, up to four (two for pairs of row
+// blocks with groups of 32, whose sums fill the LDS).  Wide units read x once for
+// more columns and share the chain's fixed costs (64 x 14336, K = 4096: one block
+// 55 us, two 40, four 31; 16 x 14336: 20.6, 17.3, 14.1), narrow ones fill the machine
+// (64 x 4096: two 12.4, four 15.7; 1 x 4096, K = 14336: one 12.5, two 16.9, four 26.3).
+int skinny_columns(int64_t M, int64_t N, int G) {
+  const int64_t units = (N + 15) / 16 * (M <= 16 ? 1 : (M + 31) / 32);
+  return units <= 256 ? 1 : units <= 512 || (G == 32 && M > 16) ? 2 : 4;
+}
+
 template <int IN, int G>
 hipError_t launch_group(const W4Args& a, hipStream_t s) {
   if (a.sums)
     return large_tiles(a.M, a.N) ? launch_tile<IN, G, 4, 4, 2, 4, G == 32 ? 2 : 3>(a, s)
                                  : launch_tile<IN, G, 4, 2, 1, 4, 2>(a, s);
-  if (a.M <= 16) return launch_skinny<IN, G, 1, 1>(a, s);
-  return launch_skinny<IN, G, 2, 1>(a, s);
+  const int cb = skinny_columns(a.M, a.N, G);
+  if (a.M <= 16)
+    return cb == 4 ? launch_skinny<IN, G, 1, 4>(a, s)
+                   : cb == 2 ? launch_skinny<IN, G, 1, 2>(a, s) : launch_skinny<IN, G, 1, 1>(a, s);
+  if constexpr (G != 32)
+    if (cb == 4) return launch_skinny<IN, G, 2, 4>(a, s);
+  return cb == 2 ? launch_skinny<IN, G, 2, 2>(a, s) : launch_skinny<IN, G, 2, 1>(a, s);
 }
 
 template <int IN>
@@ -740,11 +841,20 @@ hipError_t launch_w4_pack(int64_t N, int64_t K, int group, const void* q, const 
   return hipGetLastError();
 }
 
+// The tile kernel takes what the few-rows kernel would need more than three units
+// on a compute unit for (two with shorter groups, which are dearer there).  In us at
+// K = 4096, few rows against tiles: group 128, 256 x 6144 (three units) 42 and
+// 49, 512 x 4096 (four) 54 and 45; group 64, 128 x 6144 (two) 41 and 55,
+// 256 x 6144 (three) 59 and 55; group 32, 128 x 4096 (two) 38 and 57, 512 x 2048 at
+// K = 8192 (eight) 167 and 111.  16 rows are bound by the weights in both, up to the
+// widest: 16 x 131072 74 and 96 us, group 32 140 and 137.
 bool w4_uses_tiles(int64_t M, int64_t N, int64_t K, int group) {
+  const int64_t cb = skinny_columns(M, N, group), cgroups = ((N + 15) / 16 + cb - 1) / cb;
+  if (M <= 16 || cgroups * ((M + 31) / 32) <= (group == 128 ? 3 : 2) * 256) return false;
   // the tile kernel's 31-bit offsets: within 128 rows of x, within the scale
   // words and within the pieces of X
   const int64_t groups = K / group, wide = N + 16 > 2 * (M + kW4RowPad) ? N + 16 : 2 * (M + kW4RowPad);
-  return M > 64 && K > 0 && 256 * K < kMaxOffset && groups * wide * 4 < kMaxOffset;
+  return K > 0 && 256 * K < kMaxOffset && groups * wide * 4 < kMaxOffset;
 }
 
 hipError_t launch_w4(int in, const W4Args& a, hipStream_t s) {

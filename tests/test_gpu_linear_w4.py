@@ -59,9 +59,10 @@ def check(y, s, group, zeros, bias, dt):
     assert (err <= tol).all(), float((err / tol).max())
 
 
-# few rows; the 64 x 128 tile; the 128 x 256 tile (2048 x 4096, which small tiles would fill
-# unevenly); ragged rows and columns
-SHAPES = [(2100, 4000, 256), (2048, 4096, 512), (1, 8, 128), (1, 4096, 4096), (3, 264, 256), (16, 1024, 1152), (17, 40, 640), (31, 520, 2048),
+# few rows, with units of 1, 2 and 4 column blocks; the 64 x 128 tile (545 x 4112); the 128 x 256
+# tile (2048 x 4096, which small tiles would fill unevenly); ragged rows and columns
+SHAPES = [(2100, 4000, 256), (2048, 4096, 512), (545, 4112, 384), (5, 8216, 256), (40, 8216, 384), (9, 4120, 1152),
+          (50, 4120, 1152), (1, 8, 128), (1, 4096, 4096), (3, 264, 256), (16, 1024, 1152), (17, 40, 640), (31, 520, 2048),
           (64, 256, 14336), (65, 1032, 384), (129, 136, 1024), (300, 512, 512), (1030, 264, 896)]
 
 
@@ -79,18 +80,19 @@ def test_against_64_bits(shape, group, dt):
 
 
 @pytest.mark.parametrize("K,group", [(32, 32), (96, 32), (160, 32), (4128, 32), (64, 64), (192, 64), (4160, 64)])
-@pytest.mark.parametrize("M", [1, 20, 90, 400])
-def test_groups_that_end_inside_a_block(K, group, M):
-    s = make(M, 56, K, group, "bf16", K + M)
+@pytest.mark.parametrize("M,N", [(1, 56), (20, 56), (90, 56), (400, 56), (30, 8216), (600, 4112), (1100, 6000)])
+def test_groups_that_end_inside_a_block(K, group, M, N):
+    s = make(M, N, K, group, "bf16", K + M)
     y = torch_ops.linear_w4(s["x"], torch_ops.pack_w4(s["q"], s["s"], s["z"]), bias=s["b"])
     check(y, s, group, True, True, "bf16")
 
 
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
 @pytest.mark.parametrize("group", [32, 64, 128])
-@pytest.mark.parametrize("M", [1, 16, 40, 100, 260, 700])
-def test_bits_of_the_documented_chain(M, group, dt):
-    N, K = 72, 2176
+@pytest.mark.parametrize("M,N", [(1, 72), (16, 72), (40, 72), (100, 72), (260, 72), (700, 72), (3, 8200), (33, 8200),
+                                 (600, 4112), (1100, 6000)])
+def test_bits_of_the_documented_chain(M, N, group, dt):
+    K = 2176
     s = make(M, N, K, group, dt, 61, integers=True)
     y = torch_ops.linear_w4(s["x"], torch_ops.pack_w4(s["q"], s["s"], s["z"]), bias=s["b"])
     q, x = unpacked(s), s["x"].double()
@@ -103,7 +105,7 @@ def test_bits_of_the_documented_chain(M, group, dt):
     assert torch.equal(y, want)
 
 
-@pytest.mark.parametrize("N,K,group", [(4096, 2048, 128), (1032, 4096, 64), (264, 14336, 32)])
+@pytest.mark.parametrize("N,K,group", [(4096, 2048, 128), (1032, 4096, 64), (264, 14336, 32), (8216, 512, 128)])
 def test_rows_do_not_depend_on_the_batch(N, K, group):
     s = make(2050, N, K, group, "bf16", 67)
     w = torch_ops.pack_w4(s["q"], s["s"], s["z"])
@@ -128,16 +130,16 @@ def test_every_code_and_zero_point():
     assert torch.equal(y.double(), torch.stack((v, -2 * v)))
 
 
-@pytest.mark.parametrize("M", [12, 80, 300])
-def test_bad_rows_and_scales_stay_alone(M):
-    s = make(M, 136, 512, 64, "bf16", 71)
+@pytest.mark.parametrize("M,N", [(12, 136), (80, 136), (300, 136), (600, 4112)])
+def test_bad_rows_and_scales_stay_alone(M, N):
+    s = make(M, N, 512, 64, "bf16", 71)
     y = torch_ops.linear_w4(s["x"], torch_ops.pack_w4(s["q"], s["s"], s["z"]))
     x, sc = s["x"].clone(), s["s"].clone()
     x[3, 100], x[M - 1, 511], x[5] = float("nan"), float("inf"), 0
     sc[7, 2], sc[9] = float("nan"), 0
     z = torch_ops.linear_w4(x, torch_ops.pack_w4(s["q"], sc, s["z"]))
     rows = [i for i in range(M) if i not in (3, 5, M - 1)]
-    cols = [j for j in range(136) if j not in (7, 9)]
+    cols = [j for j in range(N) if j not in (7, 9)]
     assert torch.equal(z[rows][:, cols], y[rows][:, cols])
     assert not torch.isfinite(z[3]).any() and not torch.isfinite(z[M - 1][cols]).any()
     assert z[:, 7].isnan().all() and (z[rows, 9] == 0).all() and (z[5, cols] == 0).all()
@@ -163,9 +165,9 @@ def test_views_shapes_and_empty():
     assert torch.equal(torch_ops.linear_w4(s["x"], w.to(dev())), y)
 
 
-@pytest.mark.parametrize("M", [1, 24, 200])
-def test_streams_graphs_and_rows_behind(M):
-    s = make(M, 1032, 1024, 128, "bf16", 79)
+@pytest.mark.parametrize("M,N", [(1, 1032), (24, 1032), (200, 1032), (600, 4112)])
+def test_streams_graphs_and_rows_behind(M, N):
+    s = make(M, N, 1024, 128, "bf16", 79)
     w = torch_ops.pack_w4(s["q"], s["s"], s["z"])
     want = torch_ops.linear_w4(s["x"], w, bias=s["b"])
     side = torch.cuda.Stream()
@@ -184,8 +186,8 @@ def test_streams_graphs_and_rows_behind(M):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want)
-    buf = torch.full((M + 2, 1032), 7.0, dtype=torch.bfloat16, device=dev())
-    plan = imm.w4_plan(M, 1032, 1024, "bf16", 128)
+    buf = torch.full((M + 2, N), 7.0, dtype=torch.bfloat16, device=dev())
+    plan = imm.w4_plan(M, N, 1024, "bf16", 128)
     ws = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device=dev())
     imm.w4_run(plan, s["x"], w.packed, buf[:M], bias=s["b"], workspace=ws)
     assert torch.equal(buf[:M], want) and (buf[M:] == 7).all()

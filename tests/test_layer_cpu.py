@@ -142,7 +142,8 @@ def test_scaled_product_arguments():
     ((4, 64, 256, "f16", 0), UNSUPPORTED), ((4, 64, 256, "f16", -32), UNSUPPORTED),
     ((4, 64, 256, "f32", 128), UNSUPPORTED), ((4, 64, 256, "e4m3", 128), UNSUPPORTED),
     ((1 << 31, 64, 256, "f16", 128), UNSUPPORTED), ((1 << 30, 1 << 20, 256, "f16", 128), UNSUPPORTED),
-    ((4, 1 << 30, 1 << 20, "f16", 128), UNSUPPORTED),
+    ((4, 1 << 30, 1 << 20, "f16", 128), UNSUPPORTED), ((4, 1 << 22, 128, "f16", 128), UNSUPPORTED),
+    ((4, 4000000, 128, "f16", 128), OK), ((4, 64, 1 << 25, "f16", 128), UNSUPPORTED), ((4, 64, 33000064, "f16", 32), OK),
 ])
 def test_w4_plan_arguments(args, want):
     assert status(imm.w4_plan, *args) == want
@@ -170,10 +171,10 @@ def test_w4_arguments():
     assert run(imm.w4_plan(4, 0, 128, "f16"), x=0, packed=0, y=0) == OK
     assert pack(imm.w4_plan(4, 64, 0, "f16"), q=0, s=0, packed=0) == OK
     # many rows: the sums of x per group, rows rounded up to 128
-    many = imm.w4_plan(300, 64, 256, "f16", 64)
-    assert many.workspace_bytes == imm.w4_workspace_size(many) == 4 * 384 * 8
+    many = imm.w4_plan(600, 4112, 256, "f16", 64)
+    assert many.workspace_bytes == imm.w4_workspace_size(many) == 4 * 640 * 8
     assert imm.w4_workspace_size(p) == L.w4_workspace_size(None) == 0
-    assert run(many) == run(many, ws=P, n=4 * 384 * 8 - 1) == WORKSPACE
+    assert run(many) == run(many, ws=P, n=4 * 640 * 8 - 1) == WORKSPACE
     assert run(many, ws=P + 8, n=1 << 20) == INVALID
 
 
