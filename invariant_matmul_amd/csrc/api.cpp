@@ -22,6 +22,7 @@
 #include <new>
 
 #include "host_internal.h"
+#include "layer_internal.h"
 
 using namespace imm;
 
@@ -635,7 +636,10 @@ gemm_status gemm_run_scaled(gemm_plan_t p, const void* A, const void* B, const f
   a.bias = bias;
   a.row_scale = row_scale;
   a.col_scale = col_scale;
-  const hipError_t e = launch_gemm_scaled(*p, p->run_tile, a, static_cast<hipStream_t>(stream));
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const hipError_t e = !p->f8_fp32 && f8_rows_take(p->M, p->N, p->K)
+                           ? launch_f8_rows(p->in, p->out, a, s)
+                           : launch_gemm_scaled(*p, p->run_tile, a, s);
   return e == hipSuccess ? GEMM_OK : hip_fail(e);
 }
 

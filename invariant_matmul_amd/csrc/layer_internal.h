@@ -64,4 +64,9 @@ hipError_t launch_w4_pack(int64_t N, int64_t K, int group, const void* q, const 
                           const void* zeros, void* packed, hipStream_t s);
 hipError_t launch_w4(int in, const W4Args& a, hipStream_t s);
 
+// Few fp8 rows with row and column scales (f8_rows.hip), bitwise equal to
+// launch_gemm_scaled; whether a product runs there.
+bool f8_rows_take(int64_t M, int64_t N, int64_t K);
+hipError_t launch_f8_rows(int in, int out, const ScaledArgs& a, hipStream_t s);
+
 }  // namespace imm

@@ -31,14 +31,13 @@
 // two of them into two 16-bit integers: 7 instructions for 8 weights.
 // Behind the blocks, one dword per (group, output): the scale's 16 bits, and
 // above them -z as bf16 (exact: eight bits).
+#include "buffer_access.h"
 #include "kernel_common.h"
 #include "layer_internal.h"
 
 namespace imm {
 namespace {
 using namespace dev;
-
-typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 
 // Dword p (two integers) of the 16x16x32 operand in a packed dword.
 template <int IN>
@@ -140,30 +139,6 @@ __global__ __launch_bounds__(256) void w4_pack_scales_kernel(const unsigned shor
     r = scales[at] | (__float_as_uint(-(zeros ? (float)zeros[at] : 8.0f)) & 0xffff0000u);
   }
   sz[i] = r;
-}
-
-// A buffer of `bytes` (at most 2^31 - 1 count) from base: what lies past it reads as
-// zeros.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const void* base, int64_t bytes) {
-  const int n = bytes < 0x7fffffff ? (int)bytes : 0x7fffffff;
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, n, 0x00020000);
-}
-// 16 or 4 bytes at off; zeros past the end.  (All of the offset in the lane's
-// operand: the check against the end subtracts a scalar offset from the size,
-// which must not pass it.)
-__device__ __forceinline__ u32x4 load_b128(__amdgpu_buffer_rsrc_t buf, unsigned off) {
-#if defined(__HIP_DEVICE_COMPILE__)
-  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(buf, off, 0, 0));
-#else
-  return u32x4{};
-#endif
-}
-__device__ __forceinline__ unsigned load_b32(__amdgpu_buffer_rsrc_t buf, unsigned off) {
-#if defined(__HIP_DEVICE_COMPILE__)
-  return __builtin_amdgcn_raw_buffer_load_b32(buf, off, 0, 0);
-#else
-  return 0;
-#endif
 }
 
 // ---- few rows ----------------------------------------------------------------
@@ -436,17 +411,6 @@ __global__ __launch_bounds__(256) void w4_group_sums_kernel(W4Args g) {
 #pragma unroll
   for (int t = 0; t < G / 32; ++t) X = mfma16_v<IN>(ones8<IN>(), a[t], X);
   if (lane < 16) static_cast<i32x2*>(g.sums)[gr * g.m_pad + row] = split3(X[0]);
-}
-
-constexpr unsigned OOB = 0x80000000u;  // an offset past every buffer: zeros
-
-// 16 bytes per lane from the buffer's byte off + uni (uni the same for the wave)
-// to LDS (lane l at dst + 16 l).  (The host pass, which knows no 16-byte
-// transfers, would drop the kernel's stub.)
-__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t buf, char* dst, unsigned off, int uni) {
-#if defined(__HIP_DEVICE_COMPILE__)
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, IMM_LDS(dst), 16, off, uni, 0, 0);
-#endif
 }
 
 // The same 8 bytes twice, as a 4-dword operand.
