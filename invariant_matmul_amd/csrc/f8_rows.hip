@@ -7,15 +7,15 @@
 // K = 14336); the time is the stream of the weights, which one chain per output
 // leaves to few workgroups (N / 16 columns' chains on 256 compute units), so each
 // has to keep many bytes in flight.  A workgroup owns 16 CB columns and 16 RB rows.
-// Four waves do nothing but move the columns' weights to a ring of NS LDS stages of
-// 1024 K each, a whole kilobyte of a row per transfer; RB waves multiply, one
-// block of 16 rows each, with their rows' next stage on its way to registers.
-// One barrier a stage: it publishes stage t (each moving wave has waited for
-// its own transfers) and frees the slot of stage t - 1.
+// Four waves do nothing but move rows of x and of the weights to a ring of NS LDS
+// stages of 512 K each; RB waves multiply, one block of 16 rows each.  One
+// barrier a stage: it publishes stage t (each moving wave has waited for its own
+// transfers) and frees the slot of stage t - 1.
 //
-// 16-byte chunk c of column n's kilobyte lies at slot c ^ (n & 15), the low four
-// bits: the 16 columns that a quarter of a wave reads at one chunk fall on
-// different banks.
+// 16-byte chunk c of row r's 512 bytes lies at slot c ^ (r & 15): the 16 rows that a
+// quarter of a wave reads at one chunk fall on different banks.
+#include <climits>
+
 #include "buffer_access.h"
 #include "kernel_common.h"
 #include "layer_internal.h"
@@ -24,12 +24,13 @@ namespace imm {
 namespace {
 using namespace dev;
 
-constexpr int kStageK = 1024, kMovers = 4;
+constexpr int kStageK = 512, kMovers = 4;
 
 template <int IN, int OUT, int RB, int CB, int NS>
 __global__ __launch_bounds__((kMovers + RB) * 64) void f8_rows_kernel(ScaledArgs g) {
-  constexpr int STAGE = 16 * CB * kStageK, T = 16 * CB / kMovers;
-  static_assert(NS * STAGE <= 160 * 1024 && NS >= 2 && (NS - 2) * T < 64, "ring");
+  constexpr int ROWS = 16 * (RB + CB), STAGE = ROWS * kStageK;
+  constexpr int T = ROWS / 2 / kMovers;  // transfers of two rows, per moving wave and stage
+  static_assert(NS * STAGE <= 160 * 1024 && NS >= 2 && NS <= 8 && (NS - 2) * T < 64, "ring");
   __shared__ __attribute__((aligned(1024))) char ring[NS * STAGE];
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -37,23 +38,30 @@ __global__ __launch_bounds__((kMovers + RB) * 64) void f8_rows_kernel(ScaledArgs
   const int K = (int)g.K, nt = (K + kStageK - 1) / kStageK;
 
   if (w >= RB) {
-    // ---- the moving waves: rows p, p + 4, ... of the columns' weights
+    // ---- the moving waves: rows 2 q and 2 q + 1 of the stage, q = p, p + 4, ...;
+    // rows of x first, then the columns' weights
     const int p = w - RB;
-    const auto buf = buffer_at(static_cast<const char*>(g.B) + n0 * K, kMaxOffset * 2);
-    unsigned chunk[T];
+    const auto xbuf = buffer_at(static_cast<const char*>(g.A) + m0 * K, kMaxOffset * 2);
+    const auto wbuf = buffer_at(static_cast<const char*>(g.B) + n0 * K, kMaxOffset * 2);
+    unsigned at[T], chunk[T];
 #pragma unroll
     for (int i = 0; i < T; ++i) {
-      const int r = p + kMovers * i;
-      chunk[i] = n0 + r < g.N ? (unsigned)((lane & 48) | ((lane ^ r) & 15)) * 16 : OOB;
+      const int r = 2 * (p + kMovers * i) + lane / 32, slot = lane % 32;
+      chunk[i] = (unsigned)((slot & 16) | ((slot ^ r) & 15)) * 16;
+      const bool live = i < 2 * RB ? m0 + r < g.M : n0 + (r - 16 * RB) < g.N;
+      at[i] = live ? (unsigned)(lane / 32 * K) + chunk[i] : OOB;
     }
     auto move = [&](int t) {
       char* const slot = ring + t % NS * STAGE;
       const bool partial = (t + 1) * kStageK > K;
 #pragma unroll
       for (int i = 0; i < T; ++i) {
-        const int r = p + kMovers * i;
-        const unsigned off = partial && chunk[i] + t * kStageK >= (unsigned)K ? OOB : chunk[i];
-        dma16(buf, slot + r * kStageK, off, r * K + t * kStageK);
+        const int q = p + kMovers * i;
+        const unsigned off = partial && chunk[i] + t * kStageK >= (unsigned)K ? OOB : at[i];
+        if (i < 2 * RB)
+          dma16(xbuf, slot + q * 1024, off, 2 * q * K + t * kStageK);
+        else
+          dma16(wbuf, slot + q * 1024, off, (2 * q - 16 * RB) * K + t * kStageK);
       }
     };
     // all transfers but those of the last n stages have landed
@@ -61,7 +69,7 @@ __global__ __launch_bounds__((kMovers + RB) * 64) void f8_rows_kernel(ScaledArgs
       __builtin_amdgcn_sched_barrier(0);
       if (n >= NS - 2) __builtin_amdgcn_s_waitcnt(vmcnt_imm((NS - 2) * T));
 #define IMM_LATER(k) else if (NS - 2 > k && n == k) __builtin_amdgcn_s_waitcnt(vmcnt_imm(k * T));
-      IMM_LATER(6) IMM_LATER(5) IMM_LATER(4) IMM_LATER(3) IMM_LATER(2) IMM_LATER(1)
+      IMM_LATER(5) IMM_LATER(4) IMM_LATER(3) IMM_LATER(2) IMM_LATER(1)
 #undef IMM_LATER
       else __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
       __builtin_amdgcn_sched_barrier(0);
@@ -78,23 +86,8 @@ __global__ __launch_bounds__((kMovers + RB) * 64) void f8_rows_kernel(ScaledArgs
   // ---- the multiplying waves
   const int lr = lane % 16, hq = lane / 16;
   const int64_t row0 = m0 + 16 * w;
-  const auto xbuf = buffer_at(static_cast<const char*>(g.A) + row0 * K, kMaxOffset * 2);
-  const unsigned x_off = row0 + lr < g.M ? (unsigned)(lr * K + 32 * hq) : OOB;
-  i32x8 x[2][8];
-  auto load_x = [&](int t, i32x8 (&v)[8]) {
-    const bool partial = (t + 1) * kStageK > K;
-#pragma unroll
-    for (int s = 0; s < 8; ++s)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int k = t * kStageK + s * 128 + e * 16;
-        const unsigned off = partial && k + 32 * hq >= K ? OOB : x_off + k;
-        const i32x4 q = __builtin_bit_cast(i32x4, load_b128(xbuf, off));
-#pragma unroll
-        for (int d = 0; d < 4; ++d) v[s][4 * e + d] = q[d];
-      }
-  };
-  // chunk 8 s + 2 hq + e of column lr: four places, 256 bytes apart for every two steps
+  // chunk 8 s + 2 hq + e of row lr of a block: four places, 256 bytes apart for
+  // every two steps
   int at[2][2];
 #pragma unroll
   for (int o = 0; o < 2; ++o)
@@ -103,41 +96,36 @@ __global__ __launch_bounds__((kMovers + RB) * 64) void f8_rows_kernel(ScaledArgs
   f32x4 acc[CB];
 #pragma unroll
   for (int j = 0; j < CB; ++j) acc[j] = f32x4{};
-  auto stage = [&](auto BUF, int t) {
-    constexpr int b = decltype(BUF)::value;
-    if (t + 1 < nt) load_x(t + 1, x[1 - b]);
+  for (int t = 0; t < nt; ++t) {
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
     const char* const slot = ring + t % NS * STAGE;
+    // the operand of step s from block b of the stage's rows
+    auto operand = [&](int b, int s) {
+      i32x8 v;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const i32x4 q = *reinterpret_cast<const i32x4*>(slot + b * 16 * kStageK + at[s & 1][e] + s / 2 * 256);
+#pragma unroll
+        for (int d = 0; d < 4; ++d) v[4 * e + d] = q[d];
+      }
+      return v;
+    };
     auto steps = [&](int n) {
 #pragma unroll
-      for (int s = 0; s < 8; ++s) {
+      for (int s = 0; s < 4; ++s) {
         if (s >= n) break;
+        const i32x8 a = operand(w, s);
 #pragma unroll
-        for (int j = 0; j < CB; ++j) {
-          i32x8 v;
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const i32x4 q = *reinterpret_cast<const i32x4*>(slot + j * 16 * kStageK + at[s & 1][e] + s / 2 * 256);
-#pragma unroll
-            for (int d = 0; d < 4; ++d) v[4 * e + d] = q[d];
-          }
-          acc[j] = mfma16_f8<IN>(x[b][s], v, acc[j]);
-        }
+        for (int j = 0; j < CB; ++j) acc[j] = mfma16_f8<IN>(a, operand(RB + j, s), acc[j]);
       }
     };
     const int left = K - t * kStageK;
     if (left >= kStageK)
-      steps(8);
+      steps(4);
     else
       steps((left + 127) / 128);
-  };
-  if (nt > 0) load_x(0, x[0]);
-  for (int t = 0; t < nt;) {
-    stage(std::integral_constant<int, 0>{}, t++);
-    if (t >= nt) break;
-    stage(std::integral_constant<int, 1>{}, t++);
   }
 #pragma unroll
   for (int j = 0; j < CB; ++j) {
@@ -156,6 +144,18 @@ __global__ __launch_bounds__((kMovers + RB) * 64) void f8_rows_kernel(ScaledArgs
   }
 }
 
+// Rows of a unit: 16, 32 or 64; units of a grid with cb blocks of columns each.
+// One block where that leaves each of 256 compute units one workgroup, else two,
+// which read x once for both (us with one and two: 64 x 4096, K = 14336 (256 units)
+// 22.9 and 24.9, 16 x 4096, K = 14336 14.1 and 21.0; 16 x 6144, K = 4096 (384) 9.6
+// and 9.2, 64 x 14336 29.1 and 20.9).  Rings of three or four stages, whichever lets
+// two workgroups share a compute unit: eight were slower (16 x 14336: 20.9 against
+// 17.0), as was 128 rows a unit (128 x 4096, K = 14336: 39 against 25.5).
+int64_t units(int64_t M, int64_t N, int cb) {
+  const int64_t rows = M <= 16 ? 16 : M <= 32 ? 32 : 64;
+  return (M + rows - 1) / rows * ((N + 16 * cb - 1) / (16 * cb));
+}
+
 template <int IN, int OUT>
 hipError_t launch_out(const ScaledArgs& a, hipStream_t s) {
   auto launch = [&](auto RB, auto CB, auto NS) {
@@ -166,10 +166,12 @@ hipError_t launch_out(const ScaledArgs& a, hipStream_t s) {
   };
   using I1 = std::integral_constant<int, 1>;
   using I2 = std::integral_constant<int, 2>;
+  using I3 = std::integral_constant<int, 3>;
   using I4 = std::integral_constant<int, 4>;
-  if (a.M <= 16) return launch(I1{}, I1{}, I4{});
-  if (a.M <= 32) return launch(I2{}, I1{}, I4{});
-  return launch(I4{}, I1{}, I4{});
+  const bool one = units(a.M, a.N, 1) <= 256;
+  if (a.M <= 16) return one ? launch(I1{}, I1{}, I4{}) : launch(I1{}, I2{}, I3{});
+  if (a.M <= 32) return one ? launch(I2{}, I1{}, I4{}) : launch(I2{}, I2{}, I4{});
+  return one ? launch(I4{}, I1{}, I3{}) : launch(I4{}, I2{}, I3{});
 }
 
 template <int IN>
@@ -181,8 +183,14 @@ hipError_t launch_in(int out, const ScaledArgs& a, hipStream_t s) {
 
 }  // namespace
 
+// Up to 16 rows always; more while the units are few (in us, this kernel against the
+// tiles: 1 x 4096, K = 14336 12.7 and 73.9, 16 x 131072, K = 4096 109 and 131;
+// 64 x 6144 11.2 and 25.2, 256 x 4096 (512 units of 64 rows) 17.4 and 23.9,
+// 128 x 14336 (896) 35.1 and 26.9; 32 x 28672 (896 units of 32 rows) 34.8 and 37.3,
+// 32 x 57344 61.7 and 61.2).  The transfers' offsets are 31 bits.
 bool f8_rows_take(int64_t M, int64_t N, int64_t K) {
-  return M <= 64 && 64 * K < kMaxOffset;
+  if (64 * K >= kMaxOffset || M > INT_MAX) return false;
+  return M <= 16 || units(M, N, 2) <= (M <= 32 ? 1024 : 512);
 }
 
 hipError_t launch_f8_rows(int in, int out, const ScaledArgs& a, hipStream_t s) {

@@ -47,7 +47,8 @@ def scaled(C, s, bias, out):
 
 # long and short K, small and large B; ragged rows, every tile of the plans
 SHAPES = [(1, 256, 256), (7, 16, 16), (33, 272, 1040), (64, 512, 4096), (100, 4096, 4096), (257, 1040, 528),
-          (300, 6144, 256), (513, 2048, 2048), (1, 4096, 14336), (40, 1024, 8192)]
+          (300, 6144, 256), (513, 2048, 2048), (1, 4096, 14336), (40, 1024, 8192), (1, 16, 1008),
+          (16, 4112, 1040), (17, 4096, 144), (31, 8208, 528), (64, 8208, 2064), (65, 4112, 1536), (250, 2064, 640)]
 
 
 @pytest.mark.parametrize("dt", ["e4m3", "e5m2"])
@@ -82,7 +83,7 @@ def test_against_64_bits(shape, dt, wide):
 def test_rows_do_not_depend_on_the_batch(N, K):
     s = make(700, N, K, "e4m3", 37)
     y = torch_ops.linear_f8(s["x"], s["sx"], s["w"], s["sw"], bias=s["b"])
-    for lo, hi in ((0, 1), (13, 29), (3, 67), (100, 228), (500, 700), (699, 700)):
+    for lo, hi in ((0, 1), (13, 29), (5, 30), (3, 67), (100, 228), (500, 700), (699, 700)):
         p = torch_ops.linear_f8(s["x"][lo:hi], s["sx"][lo:hi], s["w"], s["sw"], bias=s["b"])
         assert torch.equal(p, y[lo:hi]), (lo, hi)
 
@@ -122,7 +123,7 @@ def test_shapes_views_and_empty():
                        torch_ops.linear_f8(s["x"], s["sx"], s["w"], s["sw"], bias=s["b"].half().float()))
 
 
-@pytest.mark.parametrize("shape", [(16, 6144, 1024), (5, 512, 4096), (300, 1024, 1024)])
+@pytest.mark.parametrize("shape", [(16, 6144, 1024), (5, 512, 4096), (300, 1024, 1024), (50, 8208, 528), (700, 4096, 512)])
 def test_streams_graphs_and_rows_behind(shape):
     M, N, K = shape
     s = make(M, N, K, "e4m3", 47)
