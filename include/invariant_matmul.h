@@ -308,7 +308,9 @@ gemm_status gemm_splitk_run_bias(gemm_plan_t plan, const void* A, const void* B,
  * each product and the sum rounded in fp32.  row_scale: device fp32 [M],
  * col_scale: device fp32 [N], 4-byte aligned, both required.  Plans with fp8
  * inputs and GEMM_PLAN_B_TRANSPOSED only (GEMM_ERR_UNSUPPORTED otherwise);
- * GEMM_PLAN_PERSISTENT is ignored.  No passage of the pages defines them. */
+ * GEMM_PLAN_PERSISTENT is ignored.  Few rows, and the few rows that tiles would
+ * leave for another round, run on a kernel of their own with the same bits.  No
+ * passage of the pages defines them. */
 gemm_status gemm_run_scaled(gemm_plan_t plan, const void* A, const void* B, const float* row_scale,
                             const float* col_scale, const float* bias, void* C, void* stream);
 

@@ -123,7 +123,7 @@ int default_run_tile(int64_t N, int64_t K, int eb) {
 // 3 % of it, at 105 shapes, and one at most 11 % slower at the others.  The
 // smaller tile wins a tie.  The 64- and 32-column tiles take 16-bit inputs
 // only.  Bits do not depend on the tile.
-int tile_by_m(int64_t M, int64_t N, int eb, bool b_trans) {
+int tile_by_m(int64_t M, int64_t N, int eb, bool b_trans, int64_t* least = nullptr) {
   struct Cand {
     int tile, rows, cols, per_cu;
     int wave[2], shared[2];  // [K, N] B, transposed B
@@ -151,6 +151,7 @@ int tile_by_m(int64_t M, int64_t N, int eb, bool b_trans) {
       best_cost = cost;
     }
   }
+  if (least) *least = best_cost;
   return kCands[best].tile;
 }
 
@@ -327,6 +328,35 @@ GemmArgs make_args(const gemm_plan_s* p, const void* A, const void* B, void* out
   a.group_m = p->group_m;
   a.scale = p->scale;
   return a;
+}
+
+// The last rows of a scaled product that the few-rows kernel takes, and the tile
+// of the others (bits depend on neither).  All of a few rows; and of many, the
+// at most 64 behind the last whole 128 or 256, where those alone would cost the
+// tiles another round: 2051 x 4096, K = 14336 took 146 us in one launch, and
+// takes 112 in two (2048 rows alone 104).  In tile_by_m's unit (0.2 us at
+// K = 4096) the few-rows kernel costs N / 150 (up to 64 rows: 6144 56 units,
+// 14336 105), and the second launch 20 whatever K is.
+int64_t few_rows(const gemm_plan_s* p, int* tile) {
+  *tile = p->run_tile;
+  if (p->f8_fp32) return 0;
+  if (f8_rows_take(p->M, p->N, p->K)) return p->M;
+  int64_t cost, rest = 0;
+  if (tile_by_m(p->M, p->N, 1, true, &cost) != p->run_tile) return 0;
+  for (int64_t whole = 128; whole <= 256; whole *= 2) {
+    const int64_t few = p->M % whole;
+    if (few == p->M || few == 0 || few > 64 || !f8_rows_take(few, p->N, p->K)) continue;
+    int64_t c;
+    const int t = tile_by_m(p->M - few, p->N, 1, true, &c);
+    if (!dma_offsets_fit(t, p->N, p->K, 1, true)) continue;
+    c += p->N / 150;
+    if (c < cost && (cost - c) * p->K > 20 * 4096) {
+      cost = c;
+      rest = few;
+      *tile = t;
+    }
+  }
+  return rest;
 }
 
 // ---- Ozaki scheme ----------------------------------------------------------
@@ -637,10 +667,26 @@ gemm_status gemm_run_scaled(gemm_plan_t p, const void* A, const void* B, const f
   a.row_scale = row_scale;
   a.col_scale = col_scale;
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  const hipError_t e = !p->f8_fp32 && f8_rows_take(p->M, p->N, p->K)
-                           ? launch_f8_rows(p->in, p->out, a, s)
-                           : launch_gemm_scaled(*p, p->run_tile, a, s);
-  return e == hipSuccess ? GEMM_OK : hip_fail(e);
+  int tile, bm, bn, wm, wn;
+  const int64_t few = few_rows(p, &tile);
+  a.M = p->M - few;
+  if (a.M > 0) {
+    tile_shape(tile, &bm, &bn, &wm, &wn);
+    a.tiles_m = ceil_div(a.M, bm);
+    a.tiles_n = ceil_div(a.N, bn);
+    a.grid = a.tiles_m * a.tiles_n;
+    const hipError_t e = launch_gemm_scaled(*p, tile, a, s);
+    if (e != hipSuccess) return hip_fail(e);
+  }
+  if (few > 0) {
+    a.A = static_cast<const char*>(A) + a.M * p->K;
+    a.C = static_cast<char*>(C) + a.M * p->N * (p->out == GEMM_F32 ? 4 : 2);
+    a.row_scale = row_scale + a.M;
+    a.M = few;
+    const hipError_t e = launch_f8_rows(p->in, p->out, a, s);
+    if (e != hipSuccess) return hip_fail(e);
+  }
+  return GEMM_OK;
 }
 
 void gemm_plan_destroy(gemm_plan_t p) { delete p; }

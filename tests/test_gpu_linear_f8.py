@@ -48,7 +48,8 @@ def scaled(C, s, bias, out):
 # long and short K, small and large B; ragged rows, every tile of the plans
 SHAPES = [(1, 256, 256), (7, 16, 16), (33, 272, 1040), (64, 512, 4096), (100, 4096, 4096), (257, 1040, 528),
           (300, 6144, 256), (513, 2048, 2048), (1, 4096, 14336), (40, 1024, 8192), (1, 16, 1008),
-          (16, 4112, 1040), (17, 4096, 144), (31, 8208, 528), (64, 8208, 2064), (65, 4112, 1536), (250, 2064, 640)]
+          (16, 4112, 1040), (17, 4096, 144), (31, 8208, 528), (64, 8208, 2064), (65, 4112, 1536), (250, 2064, 640),
+          (2051, 4096, 1024), (2112, 4096, 2048), (4097, 4096, 4096)]
 
 
 @pytest.mark.parametrize("dt", ["e4m3", "e5m2"])
@@ -77,6 +78,20 @@ def test_against_64_bits(shape, dt, wide):
     tol = tol + want.abs() * 2.0 ** -8
     err = (y.double() - want).abs()
     assert (err <= tol).all(), float((err / tol).max())
+
+
+def test_rows_behind_whole_rounds_of_tiles():
+    """2048 rows on tiles and 3 on the kernel of few rows, into their places and no further."""
+    s = make(2051, 4096, 4096, "e4m3", 39)
+    y = torch.full((2053, 4096), 7.0, dtype=torch.float32, device=dev())
+    plan = imm.gemm_plan_ex2(2051, 4096, 4096, "e4m3", "f32", flags=imm.PLAN_B_TRANSPOSED | imm.PLAN_TILE_BY_M)
+    imm.gemm_run_scaled(plan, s["x"], s["w"], s["sx"], s["sw"], y[:2051], bias=s["b"])
+    assert (y[2051:] == 7).all()
+    assert torch.equal(y[:2051], torch_ops.linear_f8(s["x"], s["sx"], s["w"], s["sw"], bias=s["b"],
+                                                     out_dtype=torch.float32))
+    for lo, hi in ((2040, 2051), (2048, 2051), (1000, 1100)):
+        assert torch.equal(torch_ops.linear_f8(s["x"][lo:hi], s["sx"][lo:hi], s["w"], s["sw"], bias=s["b"],
+                                               out_dtype=torch.float32), y[lo:hi])
 
 
 @pytest.mark.parametrize("N,K", [(4096, 4096), (1024, 4096), (6144, 512)])
