@@ -89,7 +89,7 @@ gemm_status rms_norm_run(rms_norm_plan_t p, const void* x, const void* residual,
 
 size_t rms_norm_workspace_size(rms_norm_plan_t p) {
   if (!p || is_f8(p->out)) return 0;
-  return (size_t)rms_norm_backward_parts(p->rows, p->cols) * (size_t)p->cols * sizeof(float);
+  return (size_t)rms_norm_backward_groups(p->rows, p->cols) * (size_t)p->cols * sizeof(float);
 }
 
 gemm_status rms_norm_backward(rms_norm_plan_t p, const void* dy, const void* h,

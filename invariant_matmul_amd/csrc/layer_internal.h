@@ -30,14 +30,13 @@ struct RmsNormBwdArgs {
   const float* rstd;
   const void* dh;        // or null
   void* dx;
-  float* parts;          // [rms_norm_backward_parts, cols], or null: no dw
+  float* parts;          // [rms_norm_backward_groups, cols], or null: no dw
   int64_t rows, cols;
 };
 // norm = false: the plain quantisation of rows (out is an fp8 type).
 hipError_t launch_rms_norm(int in, int out, bool norm, const RmsNormArgs& a, hipStream_t s);
 hipError_t launch_rms_norm_backward(int in, const RmsNormBwdArgs& a, void* dweight, hipStream_t s);
 int64_t rms_norm_backward_groups(int64_t rows, int64_t cols);
-int64_t rms_norm_backward_parts(int64_t rows, int64_t cols);
 
 // 4-bit weights (w4.hip).  packed: nblocks x kblocks blocks of 16 outputs x 128 K
 // (1 KB each), followed by sz [groups, 16 nblocks].

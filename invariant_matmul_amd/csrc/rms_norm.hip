@@ -244,10 +244,10 @@ __global__ __launch_bounds__(TPR * RPB) void rms_norm_kernel(RmsNormArgs g) {
 //   dw_k = sum over rows of dy_k n_k.
 // dh is the gradient that reaches the residual stream by its other way; dx is
 // the gradient of x and of the residual alike.  A workgroup takes the rows
-// blockIdx, blockIdx + gridDim, ... and keeps its part of dw in registers;
-// the parts go to a workspace [parts, cols] and a second kernel adds them in
-// ascending order, so the result is a function of the inputs alone (no
-// atomics).
+// blockIdx, blockIdx + gridDim, ... and keeps its part of dw in registers (rows
+// that share a workgroup add theirs in LDS at the end, in ascending order); the
+// parts go to a workspace [parts, cols] and a second kernel adds them in a fixed
+// order, so the result is a function of the inputs alone (no atomics).
 template <int IN, int TPR, int VPT, int RPB>
 __global__ __launch_bounds__(TPR * RPB) void rms_norm_backward_kernel(RmsNormBwdArgs g) {
   static_assert(TPR <= 64 || RPB == 1, "rows that share a workgroup lie inside a wave");
@@ -314,45 +314,70 @@ __global__ __launch_bounds__(TPR * RPB) void rms_norm_backward_kernel(RmsNormBwd
     }
   }
   if (g.parts) {
-    const int64_t part = (int64_t)blockIdx.x * RPB + sub;
+    f32x4* const out = reinterpret_cast<f32x4*>(g.parts + (int64_t)blockIdx.x * g.cols);
+    __shared__ f32x4 mine[RPB > 1 ? RPB : 1][RPB > 1 ? 2 * TPR * VPT : 1];
+    f32x4* const to = RPB > 1 ? mine[sub] : out;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = t + TPR * i;
       if (v < nv) {
-        f32x4* p = reinterpret_cast<f32x4*>(g.parts + part * g.cols) + 2 * v;
-        p[0] = f32x4{dw[i][0], dw[i][1], dw[i][2], dw[i][3]};
-        p[1] = f32x4{dw[i][4], dw[i][5], dw[i][6], dw[i][7]};
+        to[2 * v] = f32x4{dw[i][0], dw[i][1], dw[i][2], dw[i][3]};
+        to[2 * v + 1] = f32x4{dw[i][4], dw[i][5], dw[i][6], dw[i][7]};
+      }
+    }
+    if constexpr (RPB > 1) {
+      __syncthreads();
+      for (int c = threadIdx.x; c < 2 * nv; c += TPR * RPB) {
+        f32x4 a = mine[0][c];
+#pragma unroll
+        for (int r = 1; r < RPB; ++r)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) a[e] += mine[r][c][e];
+        out[c] = a;
       }
     }
   }
 }
 
-// dw = sum of the parts.  A workgroup owns 32 columns: 8 threads across (four
-// columns each) and 32 down, thread row s adding the parts s, s + 32, ... in
-// ascending order; the 32 sums are then added in ascending order.
+// dw = sum of the parts.  A workgroup owns 16 columns: 4 threads across (four
+// columns each) and 64 down, thread row s adding the parts s, s + 64, ... in
+// ascending order, eight loads at a time; then the 16 rows of a wave by halving
+// distances and the waves in ascending order.  Latency bounds it, so few loads
+// follow each other: with 32 columns a workgroup, 32 rows down and a load at a time
+// the backward pass of 2048 x 1040 took 31 us (and left four times the parts),
+// now 8.8, that of 777 x 1040 15.5, now 6.9.
 template <int IN>
 __global__ __launch_bounds__(256) void rms_norm_dweight_kernel(const float* parts, int64_t nparts,
                                                                int64_t cols, void* out) {
-  __shared__ f32x4 sums[32][8];
-  const int c = threadIdx.x % 8, s = threadIdx.x / 8;
-  const int64_t c4 = (int64_t)blockIdx.x * 8 + c, n4 = cols / 4;
-  const f32x4* p = reinterpret_cast<const f32x4*>(parts);
+  __shared__ f32x4 sums[4][4];
+  const int c = threadIdx.x % 4, s = threadIdx.x / 4;
+  const int64_t c4 = (int64_t)blockIdx.x * 4 + c, n4 = cols / 4;
+  const f32x4* const p = reinterpret_cast<const f32x4*>(parts) + c4;
   f32x4 a{};
-  if (c4 < n4) {
-    for (int64_t r = s; r < nparts; r += 32) {
-      const f32x4 v = p[r * n4 + c4];
+  for (int64_t r0 = s; r0 < nparts; r0 += 512) {
+    f32x4 v[8];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) a[e] += v[e];
+    for (int u = 0; u < 8; ++u) {
+      const int64_t r = r0 + 64 * u;
+      v[u] = f32x4{};
+      if (c4 < n4 && r < nparts) v[u] = p[r * n4];
     }
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) a[e] += v[u][e];
   }
-  sums[s][c] = a;
-  __syncthreads();
-  if (s == 0 && c4 < n4) {
-    for (int k = 1; k < 32; ++k) {
-      const f32x4 v = sums[k][c];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) a[e] += v[e];
-    }
+  for (int d = 32; d >= 4; d >>= 1)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) a[e] += __shfl_xor(a[e], d);
+  if (threadIdx.x % 64 < 4) sums[threadIdx.x / 64][c] = a;
+  __syncthreads();
+  if (threadIdx.x < 4 && c4 < n4) {
+#pragma unroll
+    for (int w = 1; w < 4; ++w)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) a[e] += sums[w][c][e];
 #pragma unroll
     for (int e = 0; e < 4; ++e) store_out<IN>(out, c4 * 4 + e, a[e]);
   }
@@ -412,8 +437,8 @@ hipError_t launch_backward_in(const RmsNormBwdArgs& a, void* dweight, hipStream_
     if (e != hipSuccess) return e;
   }
   if (!dweight) return hipSuccess;  // (no rows: dw is the sum of no parts, zero)
-  hipLaunchKernelGGL(rms_norm_dweight_kernel<IN>, dim3((unsigned)((a.cols + 31) / 32)), dim3(256), 0,
-                     s, a.parts, rms_norm_backward_parts(a.rows, a.cols), a.cols, dweight);
+  hipLaunchKernelGGL(rms_norm_dweight_kernel<IN>, dim3((unsigned)((a.cols + 15) / 16)), dim3(256), 0,
+                     s, a.parts, rms_norm_backward_groups(a.rows, a.cols), a.cols, dweight);
   return hipGetLastError();
 }
 
@@ -428,9 +453,6 @@ int rows_per_group(int64_t cols) {
 int64_t rms_norm_backward_groups(int64_t rows, int64_t cols) {
   const int64_t rpb = rows_per_group(cols), all = (rows + rpb - 1) / rpb;
   return all < kRmsNormBwdGroups ? all : kRmsNormBwdGroups;
-}
-int64_t rms_norm_backward_parts(int64_t rows, int64_t cols) {
-  return rms_norm_backward_groups(rows, cols) * rows_per_group(cols);
 }
 
 hipError_t launch_rms_norm(int in, int out, bool norm, const RmsNormArgs& a, hipStream_t s) {
