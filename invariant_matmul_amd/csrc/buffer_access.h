@@ -1,4 +1,4 @@
-// Loads through buffer descriptors: bounds-checked, to registers or to LDS.
+// Transfers from a buffer to LDS, zeros for the lanes that ask for them.
 #pragma once
 
 #include "kernel_common.h"
@@ -8,28 +8,9 @@ namespace dev {
 
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 
-// A buffer of `bytes` (at most 2^31 - 1 count) from base: what lies past it reads as
-// zeros.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const void* base, int64_t bytes) {
-  const int n = bytes < 0x7fffffff ? (int)bytes : 0x7fffffff;
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, n, 0x00020000);
-}
-// 16 or 4 bytes at off; zeros past the end.  (All of the offset in the lane's
-// operand: the check against the end subtracts a scalar offset from the size,
-// which must not pass it.)
-__device__ __forceinline__ u32x4 load_b128(__amdgpu_buffer_rsrc_t buf, unsigned off) {
-#if defined(__HIP_DEVICE_COMPILE__)
-  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(buf, off, 0, 0));
-#else
-  return u32x4{};
-#endif
-}
-__device__ __forceinline__ unsigned load_b32(__amdgpu_buffer_rsrc_t buf, unsigned off) {
-#if defined(__HIP_DEVICE_COMPILE__)
-  return __builtin_amdgcn_raw_buffer_load_b32(buf, off, 0, 0);
-#else
-  return 0;
-#endif
+// The 2^31 - 1 bytes from base.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const void* base) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, 0x7fffffff, 0x00020000);
 }
 
 constexpr unsigned OOB = 0x80000000u;  // an offset past every buffer: zeros

@@ -41,8 +41,8 @@ __global__ __launch_bounds__((kMovers + RB) * 64) void f8_rows_kernel(ScaledArgs
     // ---- the moving waves: rows 2 q and 2 q + 1 of the stage, q = p, p + 4, ...;
     // rows of x first, then the columns' weights
     const int p = w - RB;
-    const auto xbuf = buffer_at(static_cast<const char*>(g.A) + m0 * K, kMaxOffset * 2);
-    const auto wbuf = buffer_at(static_cast<const char*>(g.B) + n0 * K, kMaxOffset * 2);
+    const auto xbuf = buffer_at(static_cast<const char*>(g.A) + m0 * K);
+    const auto wbuf = buffer_at(static_cast<const char*>(g.B) + n0 * K);
     unsigned at[T], chunk[T];
 #pragma unroll
     for (int i = 0; i < T; ++i) {

@@ -151,9 +151,9 @@ gemm_status w4_plan(int64_t M, int64_t N, int64_t K, gemm_dtype dtype, int group
   if (M > INT_MAX || N > INT_MAX || K > INT_MAX || N % 8 != 0 || K % group != 0)
     return GEMM_ERR_UNSUPPORTED;
   const int64_t nblocks = (N + 15) / 16, kblocks = (K + 127) / 128, groups = K / group;
-  // one workgroup per 16 x 16 outputs at most, one packing thread per dword
-  // (units are counted in 32 bits), and the few-rows kernel's 31-bit offsets: 32
-  // rows of x, a round's 128 groups of scale words
+  // one workgroup per 16 x 16 outputs at most, one packing thread per dword, and
+  // the few-rows kernel's 31-bit offsets: 32 rows of x, a stage's groups of scale
+  // words
   if (nblocks * ((M + 15) / 16) > INT_MAX / 2 || nblocks * kblocks > INT_MAX ||
       nblocks * groups > INT_MAX || 64 * K > kMaxOffset || 512 * N > kMaxOffset)
     return GEMM_ERR_UNSUPPORTED;

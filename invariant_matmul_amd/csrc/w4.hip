@@ -143,160 +143,207 @@ __global__ __launch_bounds__(256) void w4_pack_scales_kernel(const unsigned shor
 
 // ---- few rows ----------------------------------------------------------------
 
-// A workgroup of 8 waves makes a unit of RB x CB blocks of 16 x 16 outputs at a
-// time.  The waves share K: in a round, wave w takes U of the 128-K blocks w,
-// w + 8, ..., and leaves P of its groups in LDS; after a barrier every thread adds
-// the round's groups of its outputs in ascending order, which keeps the order of
-// the sum the one above.  The grid is kSkinnyGroups workgroups at most (two on a
-// compute unit where registers allow: one's sums run under the other's matrix
-// steps) and each walks its units (column groups of a row group) and their rounds
-// as one sequence, with the weights of the next two rounds and the rows and scale
-// words of the next one in flight.  Loads return in order: a round's rows are
-// requested before the weights of the round after it, so waiting for them leaves
-// those in flight.  Few rows and many columns are bound by the stream of the
-// weights (1 x 131072, K = 4096: 65 us, 4.1 TB/s); small grids by the round, some
-// 3 us of latencies (1 x 4096, K = 4096: 5.7 us; one round of four blocks a wave and
-// one workgroup a unit: 6.9), more rows by the reads of x that every column
-// group repeats (see skinny_columns).
-template <int G, int RB, int CB>
-struct SkinnyShape {
-  static constexpr int W = 8;
-  static constexpr int NG = 128 / G;                  // groups per 128-K block
-  static constexpr int ELEMS = 256 * RB * CB;
-  // blocks per wave and round: up to 2, within 32 fragments of x and 64 KB of sums
-  static constexpr int UR = 2 / RB, UL = 64 / (W * NG * RB * CB);
-  static constexpr int U = UL < 1 ? 1 : UL < UR ? UL : UR;
-  static constexpr int GPR = W * U * NG;              // groups per round
-  static constexpr int PER = (ELEMS + 511) / 512;     // outputs per thread
-  // sums of two rounds where they fit; one, and a barrier more, where not
-  static constexpr int ROUND = GPR * (ELEMS + 16 * CB) * 4;
-  static constexpr int BUFS = 2 * ROUND <= 160 * 1024 ? 2 : 1;
-  static constexpr int LDS = BUFS * ROUND;
+// A workgroup makes a unit of RB x CB blocks of 16 x 16 outputs.  Four waves do
+// nothing but move: rows of x, weight blocks and scale words go to a ring of NS
+// LDS stages of SB 128-K blocks.  SB / U H waves multiply, each U blocks of the
+// stage (for half of the unit's columns, or rows, where H is 2), and leave P of
+// their groups in LDS; behind the next barrier every thread adds the stage's groups
+// of its outputs in ascending order, which keeps the order of the sum the one
+// above.  One barrier a stage publishes stage t (each moving wave has waited for
+// its own transfers) and the sums of stage t - 1, and frees the slot of stage
+// t - 1; where LDS holds the sums of one stage only, another lets them be added.
+//
+// 16-byte chunk c of row r of x lies at slot c ^ (r & 15) of the row: the 16 rows
+// that a quarter of a wave reads at one chunk fall on different banks.  XR rows
+// of x are kept: 16 RB, or 4 where M <= 4, so that the ring holds more weights.
+//
+// Measured at K = 4096, group 128 (in brackets what a kernel without the moving
+// waves took, each wave loading its own rows and blocks to registers): 1 x 4096
+// 5.3 us (5.7), 1 x 14336 9.9 (13.1; 3 TB/s), 1 x 131072 62 (64; 4.3 TB/s),
+// 16 x 14336 11.3 (14.2), 64 x 4096 9.7 (12.3), 256 x 4096 24.6 (29.8).  Single
+// units are bound by a stage's latency, LDS to sums; wide grids of few rows by the
+// weights; more rows by LDS, which x passes once for every column group.
+template <int G, int RB, int CB, int XR, int SB, int U, int H>
+struct RowsShape {
+  static constexpr int MOVERS = 4, WAVES = SB / U * H, THREADS = 64 * (MOVERS + WAVES);
+  static constexpr int RBW = H == 2 && CB == 1 ? RB / 2 : RB;  // blocks of a wave
+  static constexpr int CBW = H == 2 && CB > 1 ? CB / 2 : CB;
+  static constexpr int NG = 128 / G, GPS = SB * NG;            // groups per stage
+  static constexpr int XROW = SB * 256, XBYTES = XR * XROW, WBYTES = CB * SB * 1024;
+  static constexpr int SZ = (GPS * CB * 64 + 1023) / 1024;     // transfers of scale words
+  static constexpr int STAGE = XBYTES + WBYTES + SZ * 1024;
+  static constexpr int T = (XBYTES + WBYTES) / 1024 / MOVERS;  // transfers of each moving wave
+  static_assert(T * MOVERS * 1024 == XBYTES + WBYTES, "transfers");
+  static constexpr int LPB = XR == 4 ? 16 : 64;                // lanes whose outputs are kept
+  static constexpr int ELEMS = 4 * LPB * RB * CB;
+  static constexpr int V = ELEMS > 64 * WAVES ? ELEMS / (64 * WAVES) : 1;  // outputs of a thread
+  static_assert(V <= 4, "outputs of a thread share a lane");
+  static constexpr int SUMS = GPS * (ELEMS + 16 * CB) * 4, ALL = 160 * 1024;
+  static constexpr int BUFS = 2 * SUMS + 2 * STAGE <= ALL ? 2 : 1;
+  static constexpr int fit = (ALL - BUFS * SUMS) / STAGE, flight = 2 + 63 / (T + (SZ + MOVERS - 1) / MOVERS);
+  static constexpr int least = fit < flight ? fit : flight;
+  static constexpr int NS = least < 8 ? least : 8;
+  static_assert(NS >= 2, "LDS");
 };
-constexpr int64_t kSkinnyGroups = 512;
 
-template <int IN, int G, int RB, int CB>
-__global__ __launch_bounds__(512, 2) void w4_skinny_kernel(W4Args g) {
-  using S = SkinnyShape<G, RB, CB>;
-  constexpr int W = S::W, NG = S::NG, U = S::U, GPR = S::GPR, ELEMS = S::ELEMS, PER = S::PER;
-  static_assert(S::LDS <= 160 * 1024, "LDS");
-  __shared__ __attribute__((aligned(16))) float part[S::BUFS][GPR][ELEMS];
-  __shared__ float scl[S::BUFS][GPR][16 * CB];
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int lr = lane % 16, hq = lane / 16;
-  const unsigned first = hq == 0 ? ~0u : 0u;
-  const int64_t cgroups = (g.nblocks + CB - 1) / CB;
-  const int64_t units = cgroups * ((g.M + 16 * RB - 1) / (16 * RB));
-  const int kblocks = (int)g.kblocks, ksteps = (int)(g.K / 32);
-  const int rounds = kblocks > 0 ? (kblocks + W * U - 1) / (W * U) : 1;
+template <int IN, int G, int RB, int CB, int XR, int SB, int U, int H>
+__global__ __launch_bounds__((4 + SB / U * H) * 64) void w4_rows_kernel(W4Args g) {
+  using S = RowsShape<G, RB, CB, XR, SB, U, H>;
+  constexpr int NG = S::NG, GPS = S::GPS, NS = S::NS, RBW = S::RBW, CBW = S::CBW, V = S::V;
+  __shared__ __attribute__((aligned(1024))) char ring[NS * S::STAGE];
+  __shared__ __attribute__((aligned(16))) float part[S::BUFS][GPS][S::ELEMS];
+  __shared__ float scl[S::BUFS][GPS][16 * CB];
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const unsigned cgroups = (unsigned)((g.nblocks + CB - 1) / CB);
+  const int64_t nb0 = (int64_t)(blockIdx.x % cgroups) * CB, m0 = (int64_t)(blockIdx.x / cgroups) * (16 * RB);
+  const int K = (int)g.K, kblocks = (int)g.kblocks, nt = (kblocks + SB - 1) / SB;
   const int64_t np = g.nblocks * 16;
-
-  // A place in the sequence: round r of a unit, and the unit's first row and
-  // column block.
-  struct Place {
-    unsigned unit, rg, cg;
-    int r;
-  };
-  const unsigned nunits = (unsigned)units, ncg = (unsigned)cgroups;
-  auto place_at = [&](unsigned unit) { return Place{unit, unit / ncg, unit % ncg, 0}; };
-  auto advance = [&](Place& p) {
-    if (++p.r == rounds) p = place_at(p.unit + gridDim.x);
-  };
-  // No load is predicated: what a round reads past the last row, column block,
-  // K block or group is another row's or block's (or, past the end of its
-  // matrix, zeros), goes into sums that nothing adds up, or into rows and columns
-  // that are never stored.  Offsets: the lane's, made once, and the wave's.
-  const unsigned x_off = (unsigned)(lr * g.K * 2 + 16 * hq), x_block = (unsigned)(32 * g.K);
-  const unsigned w_off = lane * 16, w_block = (unsigned)(g.kblocks * 1024);
-  const unsigned s_off = lr * 4, s_group = (unsigned)(np * 4);
-  auto load_weights = [&](const Place& p, u32x4 (&wt)[U][CB]) {
-    const int64_t at = ((int64_t)p.cg * CB * kblocks + (int64_t)p.r * U * W + w) * 1024;
-    const int64_t end = g.nblocks * g.kblocks * 1024;
-    const auto buf = buffer_at(static_cast<const char*>(g.packed) + (at < end ? at : 0),
-                               p.unit < nunits && at < end ? end - at : 0);
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int j = 0; j < CB; ++j) wt[u][j] = load_b128(buf, w_off + (u * (W * 1024) + j * w_block));
-  };
-  auto load_rows = [&](const Place& p, i32x4 (&a)[U][4][RB], unsigned (&sz)[U][NG][CB]) {
-    const int64_t m0 = (int64_t)p.rg * (16 * RB), k0 = ((int64_t)p.r * U * W + w) * 128;
-    const int64_t xat = (m0 * g.K + k0) * 2, xend = g.M * g.K * 2;
-    const auto xbuf = buffer_at(static_cast<const char*>(g.x) + (xat < xend ? xat : 0),
-                                p.unit < nunits && xat < xend ? xend - xat : 0);
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int i = 0; i < RB; ++i)
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-          a[u][t][i] = __builtin_bit_cast(i32x4, load_b128(xbuf, x_off + (u * (W * 256) + t * 64 + i * x_block)));
-    const int64_t sat = (k0 / G * np + (int64_t)p.cg * CB * 16) * 4, send = g.groups * np * 4;
-    const auto sbuf = buffer_at(reinterpret_cast<const char*>(g.sz) + (sat < send ? sat : 0),
-                                p.unit < nunits && sat < send ? send - sat : 0);
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int s = 0; s < NG; ++s)
-#pragma unroll
-        for (int j = 0; j < CB; ++j)
-          sz[u][s][j] = load_b32(sbuf, s_off + ((unsigned)(u * W * NG + s) * s_group + j * 64));
+  auto barrier = [&]() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
   };
 
-  u32x4 wt[2][U][CB];
-  i32x4 a[2][U][4][RB];
-  unsigned sz[2][U][NG][CB];
-  float acc[PER];
+  if (w >= S::WAVES) {
+    // ---- the moving waves: kilobytes p, p + 4, ... of a stage (x, then weights), and
+    // kilobytes p, p + 4, ... of its scale words
+    constexpr int T = S::T, XT = S::XBYTES / 1024;
+    const int p = w - S::WAVES;
+    const auto xbuf = buffer_at(static_cast<const char*>(g.x) + m0 * K * 2);
+    const auto wbuf = buffer_at(static_cast<const char*>(g.packed) + nb0 * kblocks * 1024);
+    const int64_t sz_step = (int64_t)GPS * np * 4;
+    const char* sz = reinterpret_cast<const char*>(g.sz) + nb0 * 64;
+    auto move = [&](int t) {
+      char* const slot = ring + t % NS * S::STAGE;
 #pragma unroll
-  for (int p = 0; p < PER; ++p) acc[p] = 0.0f;
-  Place now = place_at(blockIdx.x), rows = now, weights = now;
-  load_weights(weights, wt[0]);
-  advance(weights);
-  load_rows(rows, a[0], sz[0]);
-  advance(rows);
-  load_weights(weights, wt[1]);
-  advance(weights);
-
-  auto step = [&](auto BUF) {
-    constexpr int buf = decltype(BUF)::value, sums = buf % S::BUFS;
-    // element e of a unit: block e / 256, lane (e / 4) % 64, register e % 4 of its
-    // accumulators
-    auto column = [&](int e) {
-      return ((int64_t)now.cg * CB + (e / 256) % CB) * 16 + (e / 4) % 16;
+      for (int i = 0; i < T; ++i) {
+        const int q = p + 4 * i;  // below XT for all four waves or for none
+        if (4 * i < XT) {
+          const int r = q / (SB / 4), c = q % (SB / 4) * 64 + ((lane & 48) | ((lane ^ r) & 15));
+          const bool live = m0 + r < g.M && t * (SB * 128) + 8 * c < K;
+          dma16(xbuf, slot + q * 1024, live ? (unsigned)(c * 16) : OOB, r * K * 2 + t * S::XROW);
+        } else {
+          const int j = (q - XT) / SB, kb = (q - XT) % SB;
+          const bool live = nb0 + j < g.nblocks && t * SB + kb < kblocks;
+          dma16(wbuf, slot + q * 1024, live ? (unsigned)lane * 16 : OOB, (j * kblocks + t * SB + kb) * 1024);
+        }
+      }
+#pragma unroll
+      for (int q = p; q < S::SZ; q += 4) {
+        const int sg = (q * 64 + lane) / (4 * CB), sc = (q * 64 + lane) % (4 * CB);
+        const bool live = sg < GPS && t * GPS + sg < g.groups && nb0 * 16 + 4 * sc < np;
+        dma16(buffer_at(sz), slot + S::XBYTES + S::WBYTES + q * 1024,
+              live ? (unsigned)(sg * np * 4 + sc * 16) : OOB, 0);
+      }
+      sz += sz_step;
     };
-    // (the bias before the loads that stay in flight past its use)
-    float bias[PER];
-#pragma unroll
-    for (int p = 0; p < PER; ++p) {
-      const int e = tid + 512 * p;
-      bias[p] = 0.0f;
-      if (g.bias && now.r == rounds - 1 && e < ELEMS && column(e) < g.N) bias[p] = g.bias[column(e)];
+    // all transfers but those of the last n stages have landed
+    auto wait = [&](int n) {
+      auto upto = [&](auto ONE) {
+        constexpr int each = T + S::SZ / 4 + decltype(ONE)::value;
+        if (n >= NS - 2) __builtin_amdgcn_s_waitcnt(vmcnt_imm((NS - 2) * each));
+#define IMM_LATER(k) else if (NS - 2 > k && n == k) __builtin_amdgcn_s_waitcnt(vmcnt_imm(k * each));
+        IMM_LATER(5) IMM_LATER(4) IMM_LATER(3) IMM_LATER(2) IMM_LATER(1)
+#undef IMM_LATER
+        else __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+      };
+      __builtin_amdgcn_sched_barrier(0);
+      if (p < S::SZ % 4)
+        upto(std::integral_constant<int, 1>{});
+      else
+        upto(std::integral_constant<int, 0>{});
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    for (int t = 0; t < NS - 1 && t < nt; ++t) move(t);
+    for (int t = 0; t < nt; ++t) {
+      wait(nt - 1 - t);
+      __builtin_amdgcn_s_barrier();
+      if (t + NS - 1 < nt) move(t + NS - 1);
+      if (S::BUFS == 1) __builtin_amdgcn_s_barrier();
     }
-    load_rows(rows, a[1 - buf], sz[1 - buf]);
-    advance(rows);
-    // the chains of all the wave's groups side by side: first every start, ...
-    f32x4 P[U][NG][RB][CB];
+    if (S::BUFS == 2) __builtin_amdgcn_s_barrier();
+    return;
+  }
+
+  // ---- the multiplying waves
+  const int tid = threadIdx.x, lr = lane % 16, hq = lane / 16;
+  const unsigned first = hq == 0 ? ~0u : 0u;
+  constexpr int KW = SB / U;
+  const int kb0 = w % KW, half = w / KW;  // blocks kb0, kb0 + KW, ...
+  const int i0 = CB == 1 ? half * RBW : 0, j0 = CB == 1 ? 0 : half * CBW;
+  const int xr = lr % XR;  // (row blocks i of 16 rows follow each other)
+  int x_at[4];
 #pragma unroll
-    for (int i = 0; i < RB; ++i) {
+  for (int t = 0; t < 4; ++t) x_at[t] = (i0 * 16 + xr) * S::XROW + kb0 * 256 + (((4 * t + hq) ^ xr) & 15) * 16;
+  // this thread's outputs: V floats from e of the unit, registers e % 4 .. of a lane
+  const int e = V * tid, eb = e / (4 * S::LPB), el = e / 4 % S::LPB;
+  float acc[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) acc[v] = 0.0f;
+  auto add_sums = [&](int t) {
+    const int buf = t % S::BUFS, left = (int)(g.groups - (int64_t)t * GPS);
+    if (S::ELEMS < 64 * S::WAVES && e >= S::ELEMS) return;
+    const int col = 16 * (eb % CB) + el % 16;
+    float p[GPS][V], s[GPS];
+#pragma unroll
+    for (int k = 0; k < GPS; ++k) {
+      s[k] = scl[buf][k][col];
+#pragma unroll
+      for (int v = 0; v < V; ++v) p[k][v] = part[buf][k][e + v];
+    }
+#pragma unroll
+    for (int k = 0; k < GPS; ++k)
+      if (k < left)
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] = fmaf(s[k], p[k][v], acc[v]);
+  };
+  for (int t = 0; t < nt; ++t) {
+    barrier();
+    const char* const slot = ring + t % NS * S::STAGE;
+    const int buf = t % S::BUFS;
+    i32x4 a[U][4][RBW];
+    u32x4 wt[U][CBW];
+    unsigned sz[U][NG][CBW];
+#pragma unroll
+    for (int b = 0; b < U; ++b) {
+#pragma unroll
+      for (int i = 0; i < RBW; ++i)
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          a[b][u][i] = *reinterpret_cast<const i32x4*>(slot + x_at[u] + b * (KW * 256) + i * 16 * S::XROW);
+#pragma unroll
+      for (int j = 0; j < CBW; ++j) {
+        const int kb = kb0 + b * KW;
+        wt[b][j] = *reinterpret_cast<const u32x4*>(slot + S::XBYTES + ((j0 + j) * SB + kb) * 1024 + lane * 16);
+#pragma unroll
+        for (int s = 0; s < NG; ++s)
+          sz[b][s][j] = *reinterpret_cast<const unsigned*>(slot + S::XBYTES + S::WBYTES +
+                                                           ((kb * NG + s) * CB + j0 + j) * 64 + lr * 4);
+      }
+    }
+    // the chains of all the wave's groups side by side: first every start, ...
+    f32x4 P[U][NG][RBW][CBW];
+#pragma unroll
+    for (int i = 0; i < RBW; ++i) {
       f32x4 X[U][NG];
 #pragma unroll
-      for (int t = 0; t < G / 32; ++t)
+      for (int u = 0; u < G / 32; ++u)
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int b = 0; b < U; ++b)
 #pragma unroll
           for (int s = 0; s < NG; ++s)
-            X[u][s] = mfma16_v<IN>(ones8<IN>(), a[buf][u][s * (G / 32) + t][i], t == 0 ? f32x4{} : X[u][s]);
+            X[b][s] = mfma16_v<IN>(ones8<IN>(), a[b][s * (G / 32) + u][i], u == 0 ? f32x4{} : X[b][s]);
 #pragma unroll
-      for (int u = 0; u < U; ++u)
+      for (int b = 0; b < U; ++b)
 #pragma unroll
         for (int s = 0; s < NG; ++s) {
-          const i32x2 x3 = split3(X[u][s][0]);
+          const i32x2 x3 = split3(X[b][s][0]);
           const i32x4 xs{x3[0], x3[1], 0, 0};
 #pragma unroll
-          for (int j = 0; j < CB; ++j) {
-            P[u][s][i][j] = start_of_sum(xs, zero_operand(sz[buf][u][s][j], first));
-            hold(P[u][s][i][j]);
+          for (int j = 0; j < CBW; ++j) {
+            P[b][s][i][j] = start_of_sum(xs, zero_operand(sz[b][s][j], first));
+            hold(P[b][s][i][j]);
           }
         }
     }
@@ -304,88 +351,71 @@ __global__ __launch_bounds__(512, 2) void w4_skinny_kernel(W4Args g) {
     __builtin_amdgcn_sched_barrier(0);
     // ... then the steps over x and q
 #pragma unroll
-    for (int t = 0; t < G / 32; ++t)
+    for (int u = 0; u < G / 32; ++u)
 #pragma unroll
-      for (int u = 0; u < U; ++u)
+      for (int b = 0; b < U; ++b)
 #pragma unroll
         for (int s = 0; s < NG; ++s)
 #pragma unroll
-          for (int j = 0; j < CB; ++j) {
-            const i32x4 b = decode8<IN>(wt[buf][u][j][s * (G / 32) + t]);
+          for (int j = 0; j < CBW; ++j) {
+            const i32x4 q = decode8<IN>(wt[b][j][s * (G / 32) + u]);
 #pragma unroll
-            for (int i = 0; i < RB; ++i)
-              P[u][s][i][j] = mfma16_v<IN>(a[buf][u][s * (G / 32) + t][i], b, P[u][s][i][j]);
+            for (int i = 0; i < RBW; ++i)
+              P[b][s][i][j] = mfma16_v<IN>(a[b][s * (G / 32) + u][i], q, P[b][s][i][j]);
           }
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int b = 0; b < U; ++b)
 #pragma unroll
       for (int s = 0; s < NG; ++s) {
-        const int gr = (u * W + w) * NG + s;
+        const int gr = (kb0 + b * KW) * NG + s;
 #pragma unroll
-        for (int j = 0; j < CB; ++j) {
-          if (hq == 0) scl[sums][gr][16 * j + lr] = scale_of<IN>(sz[buf][u][s][j]);
+        for (int j = 0; j < CBW; ++j) {
+          if (hq == 0 && i0 == 0) scl[buf][gr][16 * (j0 + j) + lr] = scale_of<IN>(sz[b][s][j]);
 #pragma unroll
-          for (int i = 0; i < RB; ++i)
-            *reinterpret_cast<f32x4*>(&part[sums][gr][((i * CB + j) * 64 + lane) * 4]) = P[u][s][i][j];
+          for (int i = 0; i < RBW; ++i)
+            if (S::LPB == 64 || lane < S::LPB)
+              *reinterpret_cast<f32x4*>(&part[buf][gr][(((i0 + i) * CB + j0 + j) * S::LPB + lane) * 4]) =
+                  P[b][s][i][j];
         }
       }
-    load_weights(weights, wt[buf]);
-    advance(weights);
-    // One barrier a round: the buffer filled two rounds on was read before the
-    // next round's barrier.  (Fences of LDS alone: __syncthreads would wait for
-    // the loads in flight.)
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-    const int64_t left = g.groups - (int64_t)now.r * GPR;
-    const int ng = left < GPR ? (int)left : GPR;
-#pragma unroll
-    for (int p = 0; p < PER; ++p) {
-      const int e = tid + 512 * p;
-      if (e < ELEMS) {
-        const int col = 16 * ((e / 256) % CB) + (e / 4) % 16;
-        constexpr int C = GPR < 16 ? GPR : 16;  // groups whose sums are read at once
-        static_assert(GPR % C == 0, "round");
-        int k = 0;
-        for (; k + C <= ng; k += C) {
-          float v[C], sc[C];
-#pragma unroll
-          for (int c = 0; c < C; ++c) {
-            v[c] = part[sums][k + c][e];
-            sc[c] = scl[sums][k + c][col];
-          }
-#pragma unroll
-          for (int c = 0; c < C; ++c) acc[p] = fmaf(sc[c], v[c], acc[p]);
-        }
-        for (; k < ng; ++k) acc[p] = fmaf(scl[sums][k][col], part[sums][k][e], acc[p]);
-        if (now.r == rounds - 1) {
-          const int64_t row = (int64_t)now.rg * (16 * RB) + 16 * (e / 256 / CB) + 4 * ((e / 4) % 64 / 16) + e % 4;
-          const int64_t out = column(e);
-          if (row < g.M && out < g.N) store_out<IN>(g.y, row * g.N + out, g.bias ? acc[p] + bias[p] : acc[p]);
-          acc[p] = 0.0f;
-        }
-      }
-    }
     if constexpr (S::BUFS == 1) {
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-      __builtin_amdgcn_s_barrier();
-      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+      barrier();
+      add_sums(t);
+    } else if (t > 0) {
+      add_sums(t - 1);
     }
-    advance(now);
-  };
-  while (now.unit < nunits) {
-    step(std::integral_constant<int, 0>{});
-    if (now.unit >= nunits) break;
-    step(std::integral_constant<int, 1>{});
+  }
+  if constexpr (S::BUFS == 2) {
+    barrier();
+    if (nt > 0) add_sums(nt - 1);
+  }
+  if (S::ELEMS < 64 * S::WAVES && e >= S::ELEMS) return;
+  const int64_t col = (nb0 + eb % CB) * 16 + el % 16;
+  if (col >= g.N) return;
+  const float bias = g.bias ? g.bias[col] : 0.0f;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int64_t row = m0 + 16 * (eb / CB) + 4 * (el / 16) + (e + v) % 4;
+    if (row < g.M) store_out<IN>(g.y, row * g.N + col, g.bias ? acc[v] + bias : acc[v]);
   }
 }
 
-template <int IN, int G, int RB, int CB>
-hipError_t launch_skinny(const W4Args& a, hipStream_t s) {
-  const int64_t units = (a.nblocks + CB - 1) / CB * ((a.M + 16 * RB - 1) / (16 * RB));
-  hipLaunchKernelGGL((w4_skinny_kernel<IN, G, RB, CB>),
-                     dim3((unsigned)(units < kSkinnyGroups ? units : kSkinnyGroups)), dim3(512), 0, s, a);
-  return hipGetLastError();
+template <int IN, int G, int RB, int CB, int XR, int SB, int U, int H>
+hipError_t launch_rows(const W4Args& a, hipStream_t s) {
+  // at most 2^21 workgroups a launch (column groups stay below 2^19)
+  const int64_t cgroups = (a.nblocks + CB - 1) / CB, most = ((int64_t)1 << 21) / cgroups * (16 * RB);
+  for (int64_t m = 0; m < a.M; m += most) {
+    W4Args b = a;
+    b.M = a.M - m < most ? a.M - m : most;
+    b.x = static_cast<const char*>(a.x) + m * a.K * 2;
+    b.y = static_cast<char*>(a.y) + m * a.N * 2;
+    const int64_t units = cgroups * ((b.M + 16 * RB - 1) / (16 * RB));
+    hipLaunchKernelGGL((w4_rows_kernel<IN, G, RB, CB, XR, SB, U, H>), dim3((unsigned)units),
+                       dim3(RowsShape<G, RB, CB, XR, SB, U, H>::THREADS), 0, s, b);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 // ---- many rows ---------------------------------------------------------------
@@ -521,10 +551,10 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void w4_tile_kernel(W4Args g) {
                                  (sums || nb0 * 64 + mat < np * 4)
                              ? (unsigned)(mgroup * mpitch + mat)
                              : OOB;
-  const auto abuf = buffer_at(static_cast<const char*>(g.x) + m0 * g.K * 2, kMaxOffset * 2);
-  const auto bbuf = buffer_at(static_cast<const char*>(g.packed) + nb0 * g.kblocks * 1024, kMaxOffset * 2);
+  const auto abuf = buffer_at(static_cast<const char*>(g.x) + m0 * g.K * 2);
+  const auto bbuf = buffer_at(static_cast<const char*>(g.packed) + nb0 * g.kblocks * 1024);
   const auto mbuf = buffer_at(sums ? static_cast<const char*>(g.sums) + m0 * 8
-                                   : reinterpret_cast<const char*>(g.sz) + nb0 * 64, kMaxOffset * 2);
+                                   : reinterpret_cast<const char*>(g.sz) + nb0 * 64);
   const int a_pitch = (int)(8 * g.K), b_pitch = (int)(g.kblocks * 1024), m_step = (int)(mpitch * NG);
   // Transfer x of this wave for stage t, into the slot at `slot`.
   constexpr int DMAS = S::DMAS;
@@ -758,13 +788,13 @@ bool large_tiles(int64_t M, int64_t N) {
 
 // Blocks of 16 columns in a unit of the few-rows kernel: the fewest that leave at
 // most one unit for each of 256 compute units, up to four (two for pairs of row
-// blocks with groups of 32, whose sums fill the LDS).  Wide units read x once for
-// more columns and share the chain's fixed costs (64 x 14336, K = 4096: one block
-// 55 us, two 40, four 31; 16 x 14336: 20.6, 17.3, 14.1), narrow ones fill the machine
-// (64 x 4096: two 12.4, four 15.7; 1 x 4096, K = 14336: one 12.5, two 16.9, four 26.3).
-int skinny_columns(int64_t M, int64_t N, int G) {
+// blocks with groups below 128, whose sums fill the LDS).  Wide units read x once
+// for more columns and share the chain's fixed costs, narrow ones fill the machine
+// (us, one, two and four blocks, in the kernel's first form: 64 x 14336, K = 4096
+// 55, 40, 31; 1 x 4096, K = 14336 12.5, 16.9, 26.3).
+int few_rows_columns(int64_t M, int64_t N, int G) {
   const int64_t units = (N + 15) / 16 * (M <= 16 ? 1 : (M + 31) / 32);
-  return units <= 256 ? 1 : units <= 512 || (G == 32 && M > 16) ? 2 : 4;
+  return units <= 256 ? 1 : units <= 512 || (G != 128 && M > 16) ? 2 : 4;
 }
 
 template <int IN, int G>
@@ -772,13 +802,24 @@ hipError_t launch_group(const W4Args& a, hipStream_t s) {
   if (a.sums)
     return large_tiles(a.M, a.N) ? launch_tile<IN, G, 4, 4, 2, 4, G == 32 ? 2 : 3>(a, s)
                                  : launch_tile<IN, G, 4, 2, 1, 4, 2>(a, s);
-  const int cb = skinny_columns(a.M, a.N, G);
+  const int cb = few_rows_columns(a.M, a.N, G);
+  // Stages of eight blocks where a column block is all a unit has (at 16 rows; four
+  // blocks: 16 x 4096, K = 14336 18.7 us against 13.8), of sixteen at 4 rows, two
+  // blocks a wave (eight, one a wave: 1 x 4096, K = 14336 12.8 against 10.8); of four
+  // where x or the sums take the LDS.  More waves beat more blocks a wave where both
+  // fit (16 x 14336, K = 4096: 11.4 us, with two blocks on half the waves 13.1).
+  constexpr bool FINE = G == 32;  // many sums: less of LDS is left for the stages
+  if (a.M <= 4)
+    return cb == 4   ? launch_rows<IN, G, 1, 4, 4, 8, 1, 1>(a, s)
+           : cb == 2 ? launch_rows<IN, G, 1, 2, 4, FINE ? 8 : 16, FINE ? 1 : 2, 1>(a, s)
+                     : launch_rows<IN, G, 1, 1, 4, FINE ? 8 : 16, FINE ? 1 : 2, 1>(a, s);
   if (a.M <= 16)
-    return cb == 4 ? launch_skinny<IN, G, 1, 4>(a, s)
-                   : cb == 2 ? launch_skinny<IN, G, 1, 2>(a, s) : launch_skinny<IN, G, 1, 1>(a, s);
-  if constexpr (G != 32)
-    if (cb == 4) return launch_skinny<IN, G, 2, 4>(a, s);
-  return cb == 2 ? launch_skinny<IN, G, 2, 2>(a, s) : launch_skinny<IN, G, 2, 1>(a, s);
+    return cb == 4   ? launch_rows<IN, G, 1, 4, 16, 4, 1, 2>(a, s)
+           : cb == 2 ? launch_rows<IN, G, 1, 2, 16, FINE ? 4 : 8, 1, FINE ? 2 : 1>(a, s)
+                     : launch_rows<IN, G, 1, 1, 16, 8, 1, 1>(a, s);
+  if constexpr (G == 128)
+    if (cb == 4) return launch_rows<IN, G, 2, 4, 32, 4, 1, 2>(a, s);
+  return cb == 2 ? launch_rows<IN, G, 2, 2, 32, 4, 1, 2>(a, s) : launch_rows<IN, G, 2, 1, 32, 4, 1, 2>(a, s);
 }
 
 template <int IN>
@@ -805,16 +846,16 @@ hipError_t launch_w4_pack(int64_t N, int64_t K, int group, const void* q, const 
   return hipGetLastError();
 }
 
-// The tile kernel takes what the few-rows kernel would need more than three units
-// on a compute unit for (two with shorter groups, which are dearer there).  In us at
-// K = 4096, few rows against tiles: group 128, 256 x 6144 (three units) 42 and
-// 49, 512 x 4096 (four) 54 and 45; group 64, 128 x 6144 (two) 41 and 55,
-// 256 x 6144 (three) 59 and 55; group 32, 128 x 4096 (two) 38 and 57, 512 x 2048 at
-// K = 8192 (eight) 167 and 111.  16 rows are bound by the weights in both, up to the
-// widest: 16 x 131072 74 and 96 us, group 32 140 and 137.
+// The tile kernel takes what would be many units of the few-rows kernel.  In us at
+// K = 4096, few rows against tiles: group 128, 256 x 6144 (768 units) 36 and 49,
+// 128 x 14336 (896) 47 and 50, 512 x 4096 (1024) 48 and 44; group 64, 256 x 4096 (1024)
+// 43 and 49, 128 x 6144 (768) 33 and 55, 96 x 14336 (1344) 62 and 56; group 32,
+// 128 x 4096 (512) 37 and 57, 256 x 4096 (1024) 71 and 57.  16 rows are bound by the
+// weights in both, up to the widest: 16 x 131072 75 and 96 us, group 32 139 and 137.
 bool w4_uses_tiles(int64_t M, int64_t N, int64_t K, int group) {
-  const int64_t cb = skinny_columns(M, N, group), cgroups = ((N + 15) / 16 + cb - 1) / cb;
-  if (M <= 16 || cgroups * ((M + 31) / 32) <= (group == 128 ? 3 : 2) * 256) return false;
+  const int64_t cb = few_rows_columns(M, N, group), cgroups = ((N + 15) / 16 + cb - 1) / cb;
+  const int64_t most = group == 128 ? 960 : group == 64 ? 1024 : 512;
+  if (M <= 16 || cgroups * ((M + 31) / 32) <= most) return false;
   // the tile kernel's 31-bit offsets: within 128 rows of x, within the scale
   // words and within the pieces of X
   const int64_t groups = K / group, wide = N + 16 > 2 * (M + kW4RowPad) ? N + 16 : 2 * (M + kW4RowPad);
