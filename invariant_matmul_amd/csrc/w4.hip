@@ -349,6 +349,9 @@ __global__ __launch_bounds__((4 + SB / U * H) * 64) void w4_rows_kernel(W4Args g
     }
     asm volatile("s_nop 15\n\ts_nop 15");
     __builtin_amdgcn_sched_barrier(0);
+    // (the sums of the stage before under this one's matrix steps: 29 x 4096,
+    // K = 14336, group 64 23.4 us, behind them 26.0)
+    if (S::BUFS == 2 && t > 0) add_sums(t - 1);
     // ... then the steps over x and q
 #pragma unroll
     for (int u = 0; u < G / 32; ++u)
@@ -381,8 +384,6 @@ __global__ __launch_bounds__((4 + SB / U * H) * 64) void w4_rows_kernel(W4Args g
     if constexpr (S::BUFS == 1) {
       barrier();
       add_sums(t);
-    } else if (t > 0) {
-      add_sums(t - 1);
     }
   }
   if constexpr (S::BUFS == 2) {
