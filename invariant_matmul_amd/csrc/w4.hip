@@ -285,18 +285,22 @@ __global__ __launch_bounds__((4 + SB / U * H) * 64) void w4_rows_kernel(W4Args g
     const int buf = t % S::BUFS, left = (int)(g.groups - (int64_t)t * GPS);
     if (S::ELEMS < 64 * S::WAVES && e >= S::ELEMS) return;
     const int col = 16 * (eb % CB) + el % 16;
-    float p[GPS][V], s[GPS];
+    constexpr int C = GPS < 16 ? GPS : 16;  // groups whose sums are read at once
 #pragma unroll
-    for (int k = 0; k < GPS; ++k) {
-      s[k] = scl[buf][k][col];
+    for (int k0 = 0; k0 < GPS; k0 += C) {
+      float p[C][V], s[C];
 #pragma unroll
-      for (int v = 0; v < V; ++v) p[k][v] = part[buf][k][e + v];
+      for (int k = 0; k < C; ++k) {
+        s[k] = scl[buf][k0 + k][col];
+#pragma unroll
+        for (int v = 0; v < V; ++v) p[k][v] = part[buf][k0 + k][e + v];
+      }
+#pragma unroll
+      for (int k = 0; k < C; ++k)
+        if (k0 + k < left)
+#pragma unroll
+          for (int v = 0; v < V; ++v) acc[v] = fmaf(s[k], p[k][v], acc[v]);
     }
-#pragma unroll
-    for (int k = 0; k < GPS; ++k)
-      if (k < left)
-#pragma unroll
-        for (int v = 0; v < V; ++v) acc[v] = fmaf(s[k], p[k][v], acc[v]);
   };
   for (int t = 0; t < nt; ++t) {
     barrier();
