@@ -514,9 +514,9 @@ typedef struct w4_plan_s* w4_plan_t;
 
 /* Plan y[M, N] = x[M, K] W^T.  dtype: GEMM_F16 or GEMM_BF16 (of x, the scales
  * and y).  GEMM_ERR_INVALID_VALUE for a negative size or a NULL handle,
- * GEMM_ERR_UNSUPPORTED for other types, groups or sizes (M up to 2^31 - 1,
- * N up to 4194176 and K up to 33553408, at most 2^30 blocks of 16 x 16 outputs
- * and fewer than 2^31 blocks of 16 x 128 and pairs of an output and a group). */
+ * GEMM_ERR_UNSUPPORTED for other types, groups or sizes (N up to
+ * 4194176 and K up to 33553408, fewer than 2^24 tiles of 64 x 128 outputs and
+ * 2^31 blocks of 16 x 128 weights and pairs of an output block and a group). */
 gemm_status w4_plan(int64_t M, int64_t N, int64_t K, gemm_dtype dtype, int group, w4_plan_t* plan);
 
 /* Bytes of the packed weight, which (N, K, group) alone fix: any plan with

@@ -14,8 +14,6 @@
 //
 // 16-byte chunk c of row r's 512 bytes lies at slot c ^ (r & 15): the 16 rows that a
 // quarter of a wave reads at one chunk fall on different banks.
-#include <climits>
-
 #include "buffer_access.h"
 #include "kernel_common.h"
 #include "layer_internal.h"
@@ -189,7 +187,8 @@ hipError_t launch_in(int out, const ScaledArgs& a, hipStream_t s) {
 // 128 x 14336 (896) 35.1 and 26.9; 32 x 28672 (896 units of 32 rows) 34.8 and 37.3,
 // 32 x 57344 61.7 and 61.2).  The transfers' offsets are 31 bits.
 bool f8_rows_take(int64_t M, int64_t N, int64_t K) {
-  if (64 * K >= kMaxOffset || M > INT_MAX) return false;
+  // (and a launch holds fewer than 2^32 threads)
+  if (64 * K >= kMaxOffset || N > (int64_t)1 << 27) return false;
   return M <= 16 || units(M, N, 2) <= (M <= 32 ? 1024 : 512);
 }
 

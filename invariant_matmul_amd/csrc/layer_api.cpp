@@ -151,10 +151,10 @@ gemm_status w4_plan(int64_t M, int64_t N, int64_t K, gemm_dtype dtype, int group
   if (M > INT_MAX || N > INT_MAX || K > INT_MAX || N % 8 != 0 || K % group != 0)
     return GEMM_ERR_UNSUPPORTED;
   const int64_t nblocks = (N + 15) / 16, kblocks = (K + 127) / 128, groups = K / group;
-  // one workgroup per 16 x 16 outputs at most, one packing thread per dword, and
-  // the few-rows kernel's 31-bit offsets: 32 rows of x, a stage's groups of scale
-  // words
-  if (nblocks * ((M + 15) / 16) > INT_MAX / 2 || nblocks * kblocks > INT_MAX ||
+  // fewer than 2^32 threads on tiles of 64 x 128, 31-bit counts of blocks and
+  // groups, and the few-rows kernel's 31-bit offsets: 32 rows of x, a stage's
+  // groups of scale words
+  if ((M + 63) / 64 * ((N + 127) / 128) >= (int64_t)1 << 24 || nblocks * kblocks > INT_MAX ||
       nblocks * groups > INT_MAX || 64 * K > kMaxOffset || 512 * N > kMaxOffset)
     return GEMM_ERR_UNSUPPORTED;
   w4_plan_s* p = new (std::nothrow) w4_plan_s{M, N, K, dtype, group, nblocks, kblocks, groups};

@@ -406,12 +406,28 @@ void with_row_shape(int64_t cols, F&& f) {
 
 template <int IN, int OUT, bool NORM>
 hipError_t launch_rows(const RmsNormArgs& a, hipStream_t s) {
+  hipError_t e = hipSuccess;
   with_row_shape(a.cols, [&](auto shape) {
     using S = decltype(shape);
-    const dim3 grid((unsigned)((a.rows + S::RPB - 1) / S::RPB)), block(S::TPR * S::RPB);
-    hipLaunchKernelGGL((rms_norm_kernel<IN, OUT, NORM, S::TPR, S::VPT, S::RPB>), grid, block, 0, s, a);
+    // (a launch holds fewer than 2^32 threads)
+    constexpr int64_t most = ((int64_t)1 << 31) / S::TPR;
+    constexpr int out_bytes = OUT == IN ? 2 : 1;
+    auto at = [&](const void* p, int64_t bytes) { return p ? static_cast<const char*>(p) + bytes : nullptr; };
+    for (int64_t r = 0; r < a.rows && e == hipSuccess; r += most) {
+      RmsNormArgs b = a;
+      b.rows = a.rows - r < most ? a.rows - r : most;
+      b.x = at(a.x, r * a.cols * 2);
+      b.residual = at(a.residual, r * a.cols * 2);
+      b.residual_out = const_cast<char*>(at(a.residual_out, r * a.cols * 2));
+      b.out = const_cast<char*>(at(a.out, r * a.cols * out_bytes));
+      b.row_scale = a.row_scale ? a.row_scale + r : nullptr;
+      b.rstd = a.rstd ? a.rstd + r : nullptr;
+      const dim3 grid((unsigned)((b.rows + S::RPB - 1) / S::RPB)), block(S::TPR * S::RPB);
+      hipLaunchKernelGGL((rms_norm_kernel<IN, OUT, NORM, S::TPR, S::VPT, S::RPB>), grid, block, 0, s, b);
+      e = hipGetLastError();
+    }
   });
-  return hipGetLastError();
+  return e;
 }
 
 template <int IN>

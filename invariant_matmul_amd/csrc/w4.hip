@@ -101,27 +101,27 @@ __device__ __forceinline__ void hold(f32x4& v) { asm volatile("" : "+v"(v)); }
 
 // ---- packing ---------------------------------------------------------------
 
-// One thread per packed dword.  q [N, K / 2]: byte j of a row holds element 2 j
+// A thread per packed dword (or several, past the threads of a launch).  q [N, K / 2]: byte j of a row holds element 2 j
 // in its low and 2 j + 1 in its high half.
 __global__ __launch_bounds__(256) void w4_pack_kernel(const unsigned char* q, unsigned* packed,
                                                       int64_t N, int64_t K, int64_t kblocks,
                                                       int64_t dwords) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= dwords) return;
-  const int t = (int)(i & 3), lane = (int)(i >> 2) & 63;
-  const int64_t blk = i >> 8, kb = blk % kblocks, nb = blk / kblocks;
-  const int64_t n = nb * 16 + lane % 16, k = kb * 128 + 32 * t + 8 * (lane / 16);
-  unsigned r = 0;
-  if (n < N && k < K) {
-    // K is a multiple of 32, so the eight elements lie in the row
-    const unsigned char* p = q + (n * K + k) / 2;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < dwords; i += (int64_t)gridDim.x * 256) {
+    const int t = (int)(i & 3), lane = (int)(i >> 2) & 63;
+    const int64_t blk = i >> 8, kb = blk % kblocks, nb = blk / kblocks;
+    const int64_t n = nb * 16 + lane % 16, k = kb * 128 + 32 * t + 8 * (lane / 16);
+    unsigned r = 0;
+    if (n < N && k < K) {
+      // K is a multiple of 32, so the eight elements lie in the row
+      const unsigned char* p = q + (n * K + k) / 2;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const unsigned v = (p[e >> 1] >> (4 * (e & 1))) & 15u;
-      r |= v << (8 * (e & 3) + 4 * (e >> 2));
+      for (int e = 0; e < 8; ++e) {
+        const unsigned v = (p[e >> 1] >> (4 * (e & 1))) & 15u;
+        r |= v << (8 * (e & 3) + 4 * (e >> 2));
+      }
     }
+    packed[i] = r;
   }
-  packed[i] = r;
 }
 
 // One thread per (group, output): the scale's bits and the zero point's negative
@@ -841,7 +841,8 @@ hipError_t launch_w4_pack(int64_t N, int64_t K, int group, const void* q, const 
   const int64_t nblocks = (N + 15) / 16, kblocks = (K + 127) / 128, groups = K / group;
   const int64_t dwords = nblocks * kblocks * 256, pairs = groups * nblocks * 16;
   unsigned* const out = static_cast<unsigned*>(packed);
-  hipLaunchKernelGGL(w4_pack_kernel, dim3((unsigned)((dwords + 255) / 256)), dim3(256), 0, s,
+  const int64_t groups_of_256 = (dwords + 255) / 256, most = (int64_t)1 << 20;
+  hipLaunchKernelGGL(w4_pack_kernel, dim3((unsigned)(groups_of_256 < most ? groups_of_256 : most)), dim3(256), 0, s,
                      static_cast<const unsigned char*>(q), out, N, K, kblocks, dwords);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;

@@ -165,6 +165,19 @@ def test_streams_graphs_and_rows_behind(shape):
     assert (buf[M:] == 7).all()
 
 
+@pytest.mark.parametrize("M", [1, 50, 600])
+def test_weights_past_32_bits(M):
+    """A weight of more than 2^32 bytes: its last columns against their own product."""
+    N, K = (1 << 19) + 16, 8208
+    g = torch.Generator(device=dev()).manual_seed(97)
+    w = torch.randint(0, 0x78, (N, K), generator=g, dtype=torch.uint8, device=dev()).view(torch.float8_e4m3fn)
+    x = torch.randn(M, K, generator=g, device=dev()).to(torch.float8_e4m3fn)
+    sx, sw = torch.rand(M, generator=g, device=dev()), torch.rand(N, generator=g, device=dev()) * 2.0 ** -12
+    y = torch_ops.linear_f8(x, sx, w, sw)
+    for lo, hi in ((0, 64), (1 << 18, (1 << 18) + 64), (N - 64, N)):
+        assert torch.equal(y[:, lo:hi], torch_ops.linear_f8(x, sx, w[lo:hi], sw[lo:hi]))
+
+
 def test_norm_quant_product_together():
     """What a serving layer runs: norm with the residual to fp8 rows, then the product."""
     g = torch.Generator().manual_seed(53)

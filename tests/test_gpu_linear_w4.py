@@ -193,6 +193,19 @@ def test_streams_graphs_and_rows_behind(M, N):
     assert torch.equal(buf[:M], want) and (buf[M:] == 7).all()
 
 
+@pytest.mark.parametrize("M", [1, 20, 800])
+def test_weights_past_32_bits(M):
+    """A weight of more than 2^32 dwords and bytes: its last columns against their own product."""
+    N, K = 262144 + 16, 131072
+    g = torch.Generator(device=dev()).manual_seed(97)
+    q = torch.randint(0, 256, (N, K // 2), generator=g, dtype=torch.uint8, device=dev())
+    sc = (torch.rand(N, K // 128, generator=g, device=dev()) * K ** -0.5).bfloat16()
+    x = torch.randn(M, K, generator=g, device=dev()).bfloat16()
+    y = torch_ops.linear_w4(x, torch_ops.pack_w4(q, sc))
+    for lo, hi in ((0, 64), (131072, 131136), (N - 64, N)):
+        assert torch.equal(y[:, lo:hi], torch_ops.linear_w4(x, torch_ops.pack_w4(q[lo:hi], sc[lo:hi])))
+
+
 def test_norm_then_product():
     """What a serving layer runs: norm with the residual, then the 4-bit product."""
     s = make(33, 520, 1024, 128, "bf16", 83)

@@ -365,3 +365,21 @@ def test_refusals_on_the_gpu():
     # beyond one allocation: the rows of a larger plan do not fit in these operands
     big = imm.rms_norm_plan(1 << 24, 1024, "bf16")
     assert L.rms_norm_run(big.handle, x.data_ptr(), 0, 0, out.data_ptr(), 0, 0, 0, 0) == 1
+
+
+def test_more_rows_than_one_launch_holds():
+    """2^28 + 5 rows of 8 (16 threads a row): the rows behind the first launch's threads."""
+    rows = (1 << 28) + 5
+    x = torch.empty(rows, 8, dtype=torch.bfloat16, device=dev())
+    g = torch.Generator().manual_seed(91)
+    part = torch.randn(64, 8, generator=g).bfloat16().to(dev())
+    x.zero_()
+    places = ((0, 64), ((1 << 27) - 32, (1 << 27) + 32), (rows - 64, rows))
+    for lo, hi in places:
+        x[lo:hi] = part
+    want = torch_ops.rms_norm(part, None, 1e-6)
+    y = torch_ops.rms_norm(x, None, 1e-6)
+    for lo, hi in places:
+        assert torch.equal(y[lo:hi], want)
+    assert (y[1000:2000] == 0).all()
+    assert torch.equal(torch_ops.rms_norm_forward(x)[2][rows - 64:], torch_ops.rms_norm_forward(part)[2])

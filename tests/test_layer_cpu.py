@@ -143,6 +143,7 @@ def test_scaled_product_arguments():
     ((4, 64, 256, "f32", 128), UNSUPPORTED), ((4, 64, 256, "e4m3", 128), UNSUPPORTED),
     ((1 << 31, 64, 256, "f16", 128), UNSUPPORTED), ((1 << 30, 1 << 20, 256, "f16", 128), UNSUPPORTED),
     ((4, 1 << 30, 1 << 20, "f16", 128), UNSUPPORTED), ((4, 1 << 22, 128, "f16", 128), UNSUPPORTED),
+    ((1 << 30, 128, 128, "f16", 128), UNSUPPORTED), (((1 << 30) - 64, 128, 128, "f16", 128), OK),
     ((4, 4000000, 128, "f16", 128), OK), ((4, 64, 1 << 25, "f16", 128), UNSUPPORTED), ((4, 64, 33000064, "f16", 32), OK),
 ])
 def test_w4_plan_arguments(args, want):
