@@ -162,7 +162,9 @@ __global__ __launch_bounds__(256) void w4_pack_scales_kernel(const unsigned shor
 // 5.3 us (5.7), 1 x 14336 9.9 (13.1; 3 TB/s), 1 x 131072 62 (64; 4.3 TB/s),
 // 16 x 14336 11.3 (14.2), 64 x 4096 9.7 (12.3), 256 x 4096 24.6 (29.8).  Single
 // units are bound by a stage's latency, LDS to sums; wide grids of few rows by the
-// weights; more rows by LDS, which x passes once for every column group.
+// weights; more rows by LDS, which x passes once for every column group.  (A wave per block
+// of outputs, over all of K and without exchanged sums, costs some 430 cycles for 128
+// K: 29 x 4096, K = 14336, group 64 31.7 us against 23.9.)
 template <int G, int RB, int CB, int XR, int SB, int U, int H>
 struct RowsShape {
   static constexpr int MOVERS = 4, WAVES = SB / U * H, THREADS = 64 * (MOVERS + WAVES);
