@@ -551,7 +551,7 @@ class RmsNormPlan:
         if h:
             self._lib.rms_norm_plan_destroy(h)
 
-    @property
+    @functools.cached_property
     def workspace_bytes(self) -> int:
         return rms_norm_workspace_size(self)
 

@@ -245,7 +245,8 @@ def _w4_plan(M: int, N: int, K: int, dtype, group: int):
 def _dense(t: torch.Tensor) -> torch.Tensor:
     """t itself if the kernels can read it in place (contiguous, 16-byte
     aligned), else a copy."""
-    t = t.contiguous()
+    if not t.is_contiguous():
+        return t.contiguous()
     return t if t.data_ptr() % 16 == 0 else t.clone()
 
 
@@ -255,10 +256,11 @@ def _ptr(t) -> int:
 
 def _stream_of(where: str, device) -> int:
     """The current stream of the current device, which must be the tensors'."""
-    if device.index != torch.cuda.current_device():
+    index = device.index
+    if index != torch._C._cuda_getDevice():
         raise ValueError(f"{where}: the tensors are on {device}, but the current device is "
                          f"cuda:{torch.cuda.current_device()}")
-    return torch._C._cuda_getCurrentRawStream(device.index)
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _done(status: int, where: str):
@@ -273,14 +275,15 @@ def _refuse_grad(where: str, *tensors):
 
 
 def _check_norm(where: str, x, weight, residual):
-    if not (x.is_cuda and x.dtype in _DT and x.dim() >= 1 and x.shape[-1] % 8 == 0):
+    shape, dtype, device = x.shape, x.dtype, x.device
+    if not (x.is_cuda and dtype in _DT and shape and shape[-1] % 8 == 0):
         raise ValueError(f"{where}: needs an fp16/bf16 CUDA tensor whose last size is a multiple "
-                         f"of 8, got {tuple(x.shape)} {x.dtype} on {x.device}")
-    if weight is not None and (weight.dtype != x.dtype or weight.device != x.device
-                               or weight.shape != x.shape[-1:]):
-        raise ValueError(f"{where}: weight must hold {x.shape[-1]} values of {x.dtype} on {x.device}")
-    if residual is not None and (residual.dtype != x.dtype or residual.device != x.device
-                                 or residual.shape != x.shape):
+                         f"of 8, got {tuple(shape)} {dtype} on {device}")
+    if weight is not None and (weight.dtype != dtype or weight.device != device
+                               or weight.shape != shape[-1:]):
+        raise ValueError(f"{where}: weight must hold {shape[-1]} values of {dtype} on {device}")
+    if residual is not None and (residual.dtype != dtype or residual.device != device
+                                 or residual.shape != shape):
         raise ValueError(f"{where}: residual must have the shape, type and device of x")
 
 
@@ -292,26 +295,33 @@ def _check_f8_rows(where: str, x, dtype):
 
 def _norm(where, x, weight, eps, residual, out_dtype, want_rstd):
     """(out, stream, row_scale or None, rstd or None), the outputs new tensors."""
-    stream = _stream_of(where, x.device)
-    cols = x.shape[-1]
+    shape, device = x.shape, x.device
+    stream = _stream_of(where, device)
+    cols = shape[-1]
     rows = x.numel() // cols if cols else 0
     plan = _norm_plan(rows, cols, x.dtype, out_dtype, eps)
     x = _dense(x)
     out = torch.empty_like(x, dtype=out_dtype)
-    h = x if residual is None else torch.empty_like(x)
-    scale = rstd = None
+    h, scale, rstd = x, None, None
+    w_at = r_at = h_at = scale_at = rstd_at = 0
+    if residual is not None:
+        h = torch.empty_like(x)
+        residual = _dense(residual)
+        r_at, h_at = residual.data_ptr(), h.data_ptr()
+    if weight is not None:
+        weight = _dense(weight)
+        w_at = weight.data_ptr()
     if out_dtype in _F8:
-        scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        scale = torch.empty(shape[:-1], dtype=torch.float32, device=device)
+        scale_at = scale.data_ptr()
     if want_rstd:
-        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        rstd = torch.empty(shape[:-1], dtype=torch.float32, device=device)
+        rstd_at = rstd.data_ptr()
     if rows:
-        if weight is not None:
-            weight = _dense(weight)
-        if residual is not None:
-            residual = _dense(residual)
-        _done(lib().rms_norm_run(plan.handle, x.data_ptr(), _ptr(residual), _ptr(weight),
-                                 out.data_ptr(), _ptr(scale), 0 if residual is None else h.data_ptr(),
-                                 _ptr(rstd), stream), where)
+        status = lib().rms_norm_run(plan.handle, x.data_ptr(), r_at, w_at, out.data_ptr(), scale_at,
+                                    h_at, rstd_at, stream)
+        if status:
+            raise GemmError(status, where)
     return out, h, scale, rstd
 
 
@@ -331,12 +341,13 @@ def rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight, rstd: torch.Ten
     residual alike; dweight is None without a weight or with weight_grad=False."""
     where = "rms_norm_backward"
     _check_norm(where, h, weight, dy)
-    if dh is not None:
-        _check_norm(where, h, None, dh)
-    if rstd.dtype != torch.float32 or rstd.shape != h.shape[:-1] or rstd.device != h.device:
+    shape, device = h.shape, h.device
+    if dh is not None and (dh.dtype != h.dtype or dh.device != device or dh.shape != shape):
+        raise ValueError("rms_norm_backward: dh must have the shape, type and device of h")
+    if rstd.dtype != torch.float32 or rstd.shape != shape[:-1] or rstd.device != device:
         raise ValueError("rms_norm_backward: rstd must hold one float32 value per row of h")
-    stream = _stream_of(where, h.device)
-    cols = h.shape[-1]
+    stream = _stream_of(where, device)
+    cols = shape[-1]
     rows = h.numel() // cols if cols else 0
     plan = _norm_plan(rows, cols, h.dtype, h.dtype, 0.0)  # eps acts through rstd alone
     dy, h, rstd = _dense(dy), _dense(h), rstd.contiguous()
@@ -348,7 +359,7 @@ def rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight, rstd: torch.Ten
         if weight_grad:
             dw = torch.empty_like(weight)
             nws = plan.workspace_bytes
-            ws = torch.empty(nws, dtype=torch.uint8, device=h.device)
+            ws = torch.empty(nws, dtype=torch.uint8, device=device)
     if dh is not None:
         dh = _dense(dh)
     _done(lib().rms_norm_backward(plan.handle, dy.data_ptr(), h.data_ptr(), _ptr(weight),
