@@ -8,6 +8,8 @@ before the rounding to the output type (half a step).  Bitwise: for integer x a
 group's sums are exact, so the documented chain of fused multiply-adds can be
 replayed in 64 bits, rounding to fp32 after each.
 """
+import threading
+
 import pytest
 import torch
 
@@ -219,6 +221,44 @@ def test_norm_then_product():
     for i in (0, 20, 32):
         h1, _ = torch_ops.rms_norm(s["x"][i:i + 1], nw, 1e-6, residual=r[i:i + 1])
         assert torch.equal(torch_ops.linear_w4(h1, w, bias=s["b"])[0], y[i])
+
+
+def test_threads_on_their_own_streams():
+    """Four host threads, a batch size each, through norm, fp8 and 4-bit products at once."""
+    N, K = 4112, 1024
+    g = torch.Generator(device=dev()).manual_seed(101)
+    q = torch.randint(0, 256, (N, K // 2), generator=g, dtype=torch.uint8, device=dev())
+    w4 = torch_ops.pack_w4(q, (torch.rand(N, K // 64, generator=g, device=dev()) * 0.01).bfloat16())
+    w8, s8 = torch_ops.quantize_rows(torch.randn(N, K, generator=g, device=dev()).bfloat16())
+    nw = torch.rand(K, generator=g, device=dev()).bfloat16()
+    xs = [torch.randn(m, K, generator=g, device=dev()).bfloat16() for m in (1, 20, 600, 1100)]
+
+    def run(x):
+        h, stream = torch_ops.rms_norm(x, nw, 1e-6, residual=x)
+        r8, sx = torch_ops.quantize_rows(h)
+        return torch_ops.linear_w4(h, w4), torch_ops.linear_f8(r8, sx, w8, s8), stream
+
+    want = [run(x) for x in xs]
+    torch.cuda.synchronize()
+    wrong, done = [], []
+
+    def worker(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for k in range(12):
+                got = run(xs[i])
+                if k % 4 == 3:
+                    torch.cuda.current_stream().synchronize()
+                    if not all(torch.equal(a, b) for a, b in zip(got, want[i])):
+                        wrong.append((i, k))
+            torch.cuda.current_stream().synchronize()
+        done.append(i)
+
+    threads = [threading.Thread(target=worker, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert sorted(done) == [0, 1, 2, 3] and not wrong
 
 
 def test_refusals_on_the_gpu():
