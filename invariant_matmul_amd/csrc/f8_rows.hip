@@ -10,7 +10,11 @@
 // Four waves do nothing but move rows of x and of the weights to a ring of NS LDS
 // stages of 512 K each; RB waves multiply, one block of 16 rows each.  One
 // barrier a stage: it publishes stage t (each moving wave has waited for its own
-// transfers) and frees the slot of stage t - 1.
+// transfers) and frees the slot of stage t - 1.  Measured: 1 x 4096, K = 14336
+// 12.6 us (4.7 TB/s), 16 x 6144, K = 4096 9.2 us, of which some 3 are the launch and
+// the first loads; two or eight moving waves are within 5 % of four, waves that load x
+// to their own registers (16 rows of 64 bytes an instruction) took 18.8 us
+// against 14.1 at 16 x 4096, K = 14336.
 //
 // 16-byte chunk c of row r's 512 bytes lies at slot c ^ (r & 15): the 16 rows that a
 // quarter of a wave reads at one chunk fall on different banks.
