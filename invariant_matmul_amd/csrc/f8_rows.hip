@@ -146,15 +146,23 @@ __global__ __launch_bounds__((kMovers + RB) * 64) void f8_rows_kernel(ScaledArgs
   }
 }
 
-// Rows of a unit: 16, 32 or 64; units of a grid with cb blocks of columns each.
-// One block where that leaves each of 256 compute units one workgroup, else two,
+// Rows of a unit: the least of 16, 32 and 64 that leaves each of 256 compute units
+// one unit of a column block (us with it and with 64 rows: 64 x 1024, K = 4096 4.8 and
+// 6.2, 64 x 512, K = 14336 8.7 and 13.1, 64 x 2048, K = 4096 5.6 and 6.4); one of 16 or
+// 32 for as few rows.
+int64_t unit_rows(int64_t M, int64_t N) {
+  const int64_t blocks = (N + 15) / 16;
+  return M <= 16 || (M + 15) / 16 * blocks <= 256 ? 16 : M <= 32 || (M + 31) / 32 * blocks <= 256 ? 32 : 64;
+}
+
+// Units of a grid with cb blocks of columns each.  One block where that leaves each of 256 compute units one workgroup, else two,
 // which read x once for both (us with one and two: 64 x 4096, K = 14336 (256 units)
 // 22.9 and 24.9, 16 x 4096, K = 14336 14.1 and 21.0; 16 x 6144, K = 4096 (384) 9.6
 // and 9.2, 64 x 14336 29.1 and 20.9).  Rings of three or four stages, whichever lets
 // two workgroups share a compute unit: eight were slower (16 x 14336: 20.9 against
 // 17.0), as was 128 rows a unit (128 x 4096, K = 14336: 39 against 25.5).
 int64_t units(int64_t M, int64_t N, int cb) {
-  const int64_t rows = M <= 16 ? 16 : M <= 32 ? 32 : 64;
+  const int64_t rows = unit_rows(M, N);
   return (M + rows - 1) / rows * ((N + 16 * cb - 1) / (16 * cb));
 }
 
@@ -171,8 +179,9 @@ hipError_t launch_out(const ScaledArgs& a, hipStream_t s) {
   using I3 = std::integral_constant<int, 3>;
   using I4 = std::integral_constant<int, 4>;
   const bool one = units(a.M, a.N, 1) <= 256;
-  if (a.M <= 16) return one ? launch(I1{}, I1{}, I4{}) : launch(I1{}, I2{}, I3{});
-  if (a.M <= 32) return one ? launch(I2{}, I1{}, I4{}) : launch(I2{}, I2{}, I4{});
+  const int64_t rows = unit_rows(a.M, a.N);
+  if (rows == 16) return one ? launch(I1{}, I1{}, I4{}) : launch(I1{}, I2{}, I3{});
+  if (rows == 32) return one ? launch(I2{}, I1{}, I4{}) : launch(I2{}, I2{}, I4{});
   return one ? launch(I4{}, I1{}, I3{}) : launch(I4{}, I2{}, I3{});
 }
 

@@ -49,7 +49,7 @@ def scaled(C, s, bias, out):
 SHAPES = [(1, 256, 256), (7, 16, 16), (33, 272, 1040), (64, 512, 4096), (100, 4096, 4096), (257, 1040, 528),
           (300, 6144, 256), (513, 2048, 2048), (1, 4096, 14336), (40, 1024, 8192), (1, 16, 1008),
           (16, 4112, 1040), (17, 4096, 144), (31, 8208, 528), (64, 8208, 2064), (65, 4112, 1536), (250, 2064, 640),
-          (2051, 4096, 1024), (2112, 4096, 2048), (4097, 4096, 4096)]
+          (64, 4096, 528), (60, 2000, 2000), (300, 240, 2064), (2051, 4096, 1024), (2112, 4096, 2048), (4097, 4096, 4096)]
 
 
 @pytest.mark.parametrize("dt", ["e4m3", "e5m2"])

@@ -64,7 +64,7 @@ def check(y, s, group, zeros, bias, dt):
 # few rows, with units of 1, 2 and 4 column blocks; the 64 x 128 tile (545 x 4112); the 128 x 256
 # tile (2048 x 4096, which small tiles would fill unevenly); ragged rows and columns
 SHAPES = [(2100, 4000, 256), (2048, 4096, 512), (545, 4112, 384), (5, 8216, 256), (40, 8216, 384), (9, 4120, 1152),
-          (50, 4120, 1152), (1, 8, 128), (1, 4096, 4096), (3, 264, 256), (16, 1024, 1152), (17, 40, 640), (31, 520, 2048),
+          (50, 4120, 1152), (29, 4096, 640), (100, 1024, 384), (1, 8, 128), (1, 4096, 4096), (3, 264, 256), (16, 1024, 1152), (17, 40, 640), (31, 520, 2048),
           (64, 256, 14336), (65, 1032, 384), (129, 136, 1024), (300, 512, 512), (1030, 264, 896)]
 
 
@@ -91,7 +91,7 @@ def test_groups_that_end_inside_a_block(K, group, M, N):
 
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
 @pytest.mark.parametrize("group", [32, 64, 128])
-@pytest.mark.parametrize("M,N", [(1, 72), (16, 72), (40, 72), (100, 72), (260, 72), (700, 72), (3, 8200), (33, 8200),
+@pytest.mark.parametrize("M,N", [(1, 72), (16, 72), (40, 72), (100, 72), (260, 72), (700, 72), (3, 8200), (33, 8200), (29, 4096), (100, 1024),
                                  (600, 4112), (1100, 6000)])
 def test_bits_of_the_documented_chain(M, N, group, dt):
     K = 2176
