@@ -451,7 +451,9 @@ void ozaki_plan_destroy(ozaki_plan_t plan);
  * weight, cols and eps.  The sum of squares is fp32: a row with magnitudes above
  * 2^63 overflows it (rstd = 0).  A row that holds a NaN or an infinity is NaN where
  * the formula is (a 16-bit output), or NaN throughout (an fp8 output, whose
- * row_scale is then infinite or NaN); other rows are unaffected.
+ * row_scale is then infinite or NaN); other rows are unaffected.  Rows without
+ * columns (cols = 0) have row_scale = 2^-120, the scale of a row of zeros, and
+ * rstd = NaN, 0 / 0; their matrices, weight and row_scale may then be NULL.
  * No passage of the pages defines these calls.
  * ------------------------------------------------------------------------- */
 typedef struct rms_norm_plan_s* rms_norm_plan_t;

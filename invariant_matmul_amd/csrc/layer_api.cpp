@@ -65,21 +65,23 @@ gemm_status rms_norm_run(rms_norm_plan_t p, const void* x, const void* residual,
                          const void* weight, void* out, float* row_scale, void* residual_out,
                          float* rstd, void* stream) {
   if (!p) return GEMM_ERR_INVALID_VALUE;
-  if (p->rows == 0 || p->cols == 0) return GEMM_OK;
-  const bool f8 = is_f8(p->out);
-  if (!good(x, 16) || !good(out, 16) || !aligned(weight, 16) || !aligned(rstd, 4))
+  // (rows without columns still have their values per row)
+  const bool f8 = is_f8(p->out), any = p->cols > 0;
+  if (p->rows == 0 || (!any && !row_scale && !rstd)) return GEMM_OK;
+  if ((any && (!good(x, 16) || !good(out, 16))) || !aligned(weight, 16) || !aligned(rstd, 4))
     return GEMM_ERR_INVALID_VALUE;
-  if (!residual != !residual_out || !aligned(residual, 16) || !aligned(residual_out, 16))
+  if (any && (!residual != !residual_out || !aligned(residual, 16) || !aligned(residual_out, 16)))
     return GEMM_ERR_INVALID_VALUE;
-  if (f8 ? !good(row_scale, 4) : row_scale != nullptr) return GEMM_ERR_INVALID_VALUE;
+  if (f8 ? (any && !row_scale) || !aligned(row_scale, 4) : row_scale != nullptr)
+    return GEMM_ERR_INVALID_VALUE;
   const size_t n = (size_t)p->rows * (size_t)p->cols;
   const size_t per_row = (size_t)p->rows * sizeof(float);
-  const gemm_status st = check_device_operands({{x, 2 * n},
-                                                {residual, 2 * n},
-                                                {weight, 2 * (size_t)p->cols},
-                                                {out, f8 ? n : 2 * n},
+  const gemm_status st = check_device_operands({{any ? x : nullptr, 2 * n},
+                                                {any ? residual : nullptr, 2 * n},
+                                                {any ? weight : nullptr, 2 * (size_t)p->cols},
+                                                {any ? out : nullptr, f8 ? n : 2 * n},
                                                 {row_scale, per_row},
-                                                {residual_out, 2 * n},
+                                                {any ? residual_out : nullptr, 2 * n},
                                                 {rstd, per_row}});
   if (st != GEMM_OK) return st;
   const RmsNormArgs a{x,    residual, weight,  out,     row_scale, residual_out,
@@ -133,10 +135,13 @@ gemm_status quantize_rows(int64_t rows, int64_t cols, gemm_dtype in, gemm_dtype 
   if (!is_f8(out)) return GEMM_ERR_UNSUPPORTED;
   gemm_status st = check_rows(rows, cols, in, out);
   if (st != GEMM_OK) return st;
-  if (rows == 0 || cols == 0) return GEMM_OK;
-  if (!good(x, 16) || !good(q, 16) || !good(row_scale, 4)) return GEMM_ERR_INVALID_VALUE;
+  const bool any = cols > 0;
+  if (rows == 0 || (!any && !row_scale)) return GEMM_OK;
+  if ((any && (!good(x, 16) || !good(q, 16))) || !good(row_scale, 4)) return GEMM_ERR_INVALID_VALUE;
   const size_t n = (size_t)rows * (size_t)cols;
-  st = check_device_operands({{x, 2 * n}, {q, n}, {row_scale, (size_t)rows * sizeof(float)}});
+  st = check_device_operands({{any ? x : nullptr, 2 * n},
+                              {any ? q : nullptr, n},
+                              {row_scale, (size_t)rows * sizeof(float)}});
   if (st != GEMM_OK) return st;
   const RmsNormArgs a{x,       nullptr, nullptr, q,   row_scale, nullptr,
                       nullptr, rows,    cols,    0.0f};

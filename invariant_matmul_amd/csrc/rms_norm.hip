@@ -137,7 +137,7 @@ __global__ __launch_bounds__(TPR * RPB) void rms_norm_kernel(RmsNormArgs g) {
   const int t = threadIdx.x % TPR;
   const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
   const bool live = row < g.rows;
-  const int nv = (int)(g.cols / 8);
+  const int nv = (int)(g.cols / 8);  // 0: only row_scale (2^-120) and rstd (0 / 0) are written
   const int64_t base = row * nv;
 
   u32x4 h[VPT], w[VPT];

@@ -58,6 +58,7 @@ from __future__ import annotations
 
 import contextlib
 import functools
+import math
 import threading
 import warnings
 
@@ -306,7 +307,7 @@ def _norm(where, x, weight, eps, residual, out_dtype, want_rstd):
     shape, device = x.shape, x.device
     stream = _stream_of(where, device)
     cols = shape[-1]
-    rows = x.numel() // cols if cols else 0
+    rows = x.numel() // cols if cols else math.prod(shape[:-1])
     plan = _norm_plan(rows, cols, x.dtype, out_dtype, eps)
     x = _dense(x)
     out = torch.empty_like(x, dtype=out_dtype)
@@ -435,9 +436,9 @@ def quantize_rows(x: torch.Tensor, dtype=torch.float8_e4m3fn):
     x = _dense(x)
     q = torch.empty_like(x, dtype=dtype)
     scale = _per_row(x.shape, x.device)
-    cols = x.shape[-1]
-    if x.numel():
-        _done(lib().quantize_rows(x.numel() // cols, cols, _dtype_code(x.dtype), _dtype_code(dtype),
+    rows = scale.numel()
+    if rows:
+        _done(lib().quantize_rows(rows, x.shape[-1], _dtype_code(x.dtype), _dtype_code(dtype),
                                   x.data_ptr(), q.data_ptr(), scale.data_ptr(), stream), where)
     return q, scale
 
