@@ -47,7 +47,8 @@ The operators around a linear layer keep the same promise, row by row:
 
 rms_norm takes part in autograd (its backward pass is a kernel of the library;
 the weight's gradient is the one result that sums over rows).  The others are
-for serving and refuse inputs that require a gradient:
+for serving and refuse inputs that require a gradient.  None has a derivative in
+forward mode: all refuse dual tensors.
 
     wq, ws = torch_ops.quantize_rows(W)                # once
     y = torch_ops.linear_f8(q, s, wq, ws)              # fp8 rows and their scales
@@ -63,6 +64,7 @@ import threading
 import warnings
 
 import torch
+from torch.autograd import forward_ad
 
 from . import (PLAN_B_TRANSPOSED, PLAN_FP8_FP32_ACCUM, PLAN_TILE_BY_M, GemmError, _dtype_code,
                gemm_plan_ex2, gemm_run, gemm_splitk_run, gemm_workspace_size, lib, ozaki_plan,
@@ -281,6 +283,15 @@ def _refuse_grad(where: str, *tensors):
     if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
         raise ValueError(f"{where} has no backward pass: call it under torch.no_grad() or with "
                          "detached tensors")
+    _refuse_tangent(where, *tensors)
+
+
+def _refuse_tangent(where: str, *tensors):
+    """Dual tensors of torch.autograd.forward_ad hold a tangent that requires_grad does not
+    show (nor does torch.no_grad() stop it), and that a new tensor would not have."""
+    if forward_ad._current_level >= 0 and any(  # inside a dual_level()
+            t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors):
+        raise ValueError(f"{where} has no forward-mode derivative: call it with the primals of dual tensors")
 
 
 def _check_norm(where: str, x, weight, residual):
@@ -339,6 +350,7 @@ def rms_norm_forward(x: torch.Tensor, weight=None, eps: float = 1e-6, residual=N
     and the fp32 reciprocal root mean square of each row of h, which
     rms_norm_backward takes.  No autograd: rms_norm is the differentiable form."""
     _check_norm("rms_norm_forward", x, weight, residual)
+    _refuse_tangent("rms_norm_forward", x, weight, residual)
     y, h, _, rstd = _norm("rms_norm_forward", x, weight, eps, residual, x.dtype, True)
     return y, h, rstd
 
@@ -355,6 +367,7 @@ def rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight, rstd: torch.Ten
         raise ValueError("rms_norm_backward: dh must have the shape, type and device of h")
     if rstd.dtype != torch.float32 or rstd.shape != shape[:-1] or rstd.device != device:
         raise ValueError("rms_norm_backward: rstd must hold one float32 value per row of h")
+    _refuse_tangent(where, dy, h, weight, rstd, dh)
     stream = _stream_of(where, device)
     cols = shape[-1]
     rows = h.numel() // cols if cols else 0
@@ -402,8 +415,10 @@ def rms_norm(x: torch.Tensor, weight=None, eps: float = 1e-6, residual=None):
     With a residual, h = x + residual, rounded to x's type, and the result is
     (y, h).  x, weight and residual are fp16 or bf16 of one type, the last
     size a multiple of 8 and at most 32768; statistics are fp32.  Row i of the
-    result depends on row i alone.  Differentiable."""
+    result depends on row i alone.  Differentiable in reverse mode, once (dual
+    tensors of torch.autograd.forward_ad are refused)."""
     _check_norm("rms_norm", x, weight, residual)
+    _refuse_tangent("rms_norm", x, weight, residual)
     if torch.is_grad_enabled() and (x.requires_grad or (weight is not None and weight.requires_grad)
                                     or (residual is not None and residual.requires_grad)):
         return _RmsNorm.apply(x, weight, residual, eps)
