@@ -448,8 +448,12 @@ void ozaki_plan_destroy(ozaki_plan_t plan);
  *   row_scale = max(max_k |t_k| / FMAX, 2^-120), FMAX = 448 (e4m3) or 57344
  *       (e5m2), and out = round8(t / row_scale): the row is out * row_scale.
  * Row i of every output is a bitwise function of row i of the inputs, the
- * weight, cols and eps.  The sum of squares is fp32: a row with magnitudes above
- * 2^63 overflows it (rstd = 0).  A row that holds a NaN or an infinity is NaN where
+ * weight, cols and eps.  Sums are fp32; where a row's sum of squares would leave
+ * fp32's range, its values are multiplied by a power of two first, so finite rows of
+ * every magnitude have the formula's result.  (rstd itself is an fp32 number: above
+ * 2^126 it keeps 21 bits or more, and with eps = 0 it is infinite for a row whose root
+ * mean square is below 2^-128: out is right there, gradients are not finite.)
+ * A row that holds a NaN or an infinity is NaN where
  * the formula is (a 16-bit output), or NaN throughout (an fp8 output, whose
  * row_scale is then infinite or NaN); other rows are unaffected.  Rows without
  * columns (cols = 0) have row_scale = 2^-120, the scale of a row of zeros, and
