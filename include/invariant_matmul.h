@@ -446,7 +446,8 @@ void ozaki_plan_destroy(ozaki_plan_t plan);
  *   rstd = 1 / sqrt(sum_k h_k^2 / cols + eps), t_k = (h_k rstd) weight_k, fp32;
  *   out = round(t) in the input's type, or, with an fp8 output,
  *   row_scale = max(max_k |t_k| / FMAX, 2^-120), FMAX = 448 (e4m3) or 57344
- *       (e5m2), and out = round8(t / row_scale): the row is out * row_scale.
+ *       (e5m2), and out = round8(t / row_scale), both quotients rounded in fp32: the
+ *       row is out * row_scale.
  * Row i of every output is a bitwise function of row i of the inputs, the
  * weight, cols and eps.  Sums are fp32; where a row's sum of squares would leave
  * fp32's range, its values are multiplied by a power of two first, so finite rows of
