@@ -31,6 +31,8 @@
 // two of them into two 16-bit integers: 7 instructions for 8 weights.
 // Behind the blocks, one dword per (group, output): the scale's 16 bits, and
 // above them -z as bf16 (exact: eight bits).
+#include <algorithm>
+
 #include "buffer_access.h"
 #include "kernel_common.h"
 #include "layer_internal.h"
@@ -124,21 +126,21 @@ __global__ __launch_bounds__(256) void w4_pack_kernel(const unsigned char* q, un
   }
 }
 
-// One thread per (group, output): the scale's bits and the zero point's negative
-// (8 without zero points); padding outputs get zeros.
+// A thread per (group, output), or several: the scale's bits and the zero point's
+// negative (8 without zero points); padding outputs get zeros.
 __global__ __launch_bounds__(256) void w4_pack_scales_kernel(const unsigned short* scales,
                                                              const unsigned char* zeros,
                                                              unsigned* sz, int64_t N, int64_t np,
                                                              int64_t groups) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= groups * np) return;
-  const int64_t n = i % np, gr = i / np;
-  unsigned r = 0;
-  if (n < N) {
-    const int64_t at = n * groups + gr;
-    r = scales[at] | (__float_as_uint(-(zeros ? (float)zeros[at] : 8.0f)) & 0xffff0000u);
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < groups * np; i += (int64_t)gridDim.x * 256) {
+    const int64_t n = i % np, gr = i / np;
+    unsigned r = 0;
+    if (n < N) {
+      const int64_t at = n * groups + gr;
+      r = scales[at] | (__float_as_uint(-(zeros ? (float)zeros[at] : 8.0f)) & 0xffff0000u);
+    }
+    sz[i] = r;
   }
-  sz[i] = r;
 }
 
 // ---- few rows ----------------------------------------------------------------
@@ -845,12 +847,13 @@ hipError_t launch_w4_pack(int64_t N, int64_t K, int group, const void* q, const 
   const int64_t nblocks = (N + 15) / 16, kblocks = (K + 127) / 128, groups = K / group;
   const int64_t dwords = nblocks * kblocks * 256, pairs = groups * nblocks * 16;
   unsigned* const out = static_cast<unsigned*>(packed);
-  const int64_t groups_of_256 = (dwords + 255) / 256, most = (int64_t)1 << 20;
-  hipLaunchKernelGGL(w4_pack_kernel, dim3((unsigned)(groups_of_256 < most ? groups_of_256 : most)), dim3(256), 0, s,
-                     static_cast<const unsigned char*>(q), out, N, K, kblocks, dwords);
+  // (a launch holds fewer than 2^32 threads)
+  auto grid = [](int64_t items) { return dim3((unsigned)std::min((items + 255) / 256, (int64_t)1 << 20)); };
+  hipLaunchKernelGGL(w4_pack_kernel, grid(dwords), dim3(256), 0, s, static_cast<const unsigned char*>(q),
+                     out, N, K, kblocks, dwords);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(w4_pack_scales_kernel, dim3((unsigned)((pairs + 255) / 256)), dim3(256), 0, s,
+  hipLaunchKernelGGL(w4_pack_scales_kernel, grid(pairs), dim3(256), 0, s,
                      static_cast<const unsigned short*>(scales),
                      static_cast<const unsigned char*>(zeros), out + dwords, N, nblocks * 16, groups);
   return hipGetLastError();
