@@ -308,7 +308,9 @@ gemm_status gemm_splitk_run_bias(gemm_plan_t plan, const void* A, const void* B,
  * each product and the sum rounded in fp32.  row_scale: device fp32 [M],
  * col_scale: device fp32 [N], 4-byte aligned, both required.  Plans with fp8
  * inputs and GEMM_PLAN_B_TRANSPOSED only (GEMM_ERR_UNSUPPORTED otherwise);
- * GEMM_PLAN_PERSISTENT is ignored.  Few rows, and the few rows that tiles would
+ * GEMM_PLAN_PERSISTENT is ignored.  sum_ij is the fp8 step's (8 neighbouring products
+ * in a window of 13 binades, then fp32), or with GEMM_PLAN_FP8_FP32_ACCUM the fp16
+ * step's, on the tiles at every M.  Few rows, and the few rows that tiles would
  * leave for another round, run on a kernel of their own with the same bits.  No
  * passage of the pages defines them. */
 gemm_status gemm_run_scaled(gemm_plan_t plan, const void* A, const void* B, const float* row_scale,
@@ -513,7 +515,9 @@ gemm_status quantize_rows(int64_t rows, int64_t cols, gemm_dtype in, gemm_dtype 
  * a group run over x and the integers q on the matrix cores in fp32:
  *   X = sum_k x;  P = -zero X + sum_k x q;  acc = fma(scale, P, acc)
  * with the groups in ascending order, and y = round(acc + bias): no weight is
- * rounded.  Row i of y is a bitwise function of row i of x, of the weights and
+ * rounded.  P is a difference of two fp32 sums: its error goes with sum_k |x| (q + zero)
+ * (x with q = zero throughout need not give 0), and bf16 x for which that passes 2^128
+ * overflows.  Row i of y is a bitwise function of row i of x, of the weights and
  * bias, N, K and group.  A row of x that holds a NaN or an infinity has no
  * finite element in y.  No passage of the pages defines these calls.
  * ------------------------------------------------------------------------- */

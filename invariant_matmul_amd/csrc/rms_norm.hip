@@ -11,11 +11,12 @@
 // All of it is one pass over memory: a row's 16-byte vectors stay in the
 // registers of the threads that own the row between the sum of squares, the
 // maximum and the store, so each input is read once and each output written
-// once.  The bytes bound it: about 10 operations an element, against 6 bytes
-// (16-bit, with a residual 8) that the vector units could fill with 30.  Measured:
-// 8191 x 8192 fp16 with a residual 94 us (5.7 TB/s), 4096 x 4096 bf16 backward 27 us
-// (5 TB/s), 4099 x 14336 fp16 to e4m3 with a residual 76 us (5.4 TB/s), 32776 x 128
-// with a residual 7.1 us (4.7 TB/s), one row of 4096 2.8 us: a launch and a round trip to memory.
+// once.  The bytes bound it: about 10 operations an element, against 4 bytes (16-bit;
+// with a residual 8) in whose time the vector units could do 20.  Measured:
+// 8191 x 8192 fp16 with a residual 97 to 99 us (5.4 TB/s), 4096 x 4096 bf16 backward 28 us
+// (5 TB/s), 4099 x 14336 fp16 to e4m3 with a residual 93 us (4.4 TB/s), 32776 x 128
+// without one 5.8 us (2.9 TB/s), one row of 4096 2.9 us: a launch and a round trip to
+// memory.
 //
 // Batch invariance.  The threads of a row, the vectors each of them holds and
 // the order of the sum (own elements in ascending order, lanes by halving

@@ -11,12 +11,14 @@
 // the 16x16x32 steps over x and the integers q (exact in fp16 and bf16) follow
 // in ascending K, all in one fp32 accumulator: P = -z X + sum x q.  Then, in fp32,
 //   acc = fma(s, P, acc), groups in ascending order from +0,
-// and one rounding of acc + b.  Nothing but x and s is ever rounded to 16 bits:
-// the product is as exact as one with fp32 weights.  (Rounding s (q - z) to 16
-// bits first, as a 16-bit weight would be, costs a bf16 result half its
-// accuracy.  z as a matrix step leaves the vector unit, whose work does not
-// hide in the tile kernel, one multiply-add per element and group; a second one
-// in place of that step was as fast within two per cent.)
+// and one rounding of acc + b.  Nothing but x and s is ever rounded to 16 bits.
+// (Rounding s (q - z) to 16 bits first, as a 16-bit weight would be, costs a bf16
+// result half its accuracy.)  P is a difference of two sums, so its fp32 error goes
+// with sum |x| (q + z), not with sum |x| |q - z| as that of fp32 weights would: x
+// with q = z throughout need not give 0, and a group of bf16 x whose sum |x| (q + z)
+// passes 2^128 overflows though its sum x (q - z) may not.  (z as a matrix step leaves
+// the vector unit, whose work does not hide in the tile kernel, one multiply-add per
+// element and group; a second one in place of that step was as fast within two per cent.)
 //
 // Batch invariance.  That order of operations is a function of (K, group)
 // alone.  Every kernel below follows it, however it spreads rows, columns and
@@ -103,8 +105,9 @@ __device__ __forceinline__ void hold(f32x4& v) { asm volatile("" : "+v"(v)); }
 
 // ---- packing ---------------------------------------------------------------
 
-// A thread per packed dword (or several, past the threads of a launch).  q [N, K / 2]: byte j of a row holds element 2 j
-// in its low and 2 j + 1 in its high half.
+// A thread per packed dword (or several, past the threads of a launch).
+// q [N, K / 2]: byte j of a row holds element 2 j in its low and 2 j + 1 in its high
+// half.
 __global__ __launch_bounds__(256) void w4_pack_kernel(const unsigned char* q, unsigned* packed,
                                                       int64_t N, int64_t K, int64_t kblocks,
                                                       int64_t dwords) {
@@ -785,8 +788,11 @@ hipError_t launch_tile(W4Args a, hipStream_t s) {
 // against 558 us), the small one fills small and odd grids (256 x 6144: 49
 // against 74 us, 2048 x 6144: 129 against 147, but 2048 x 4096, four workgroups a
 // unit, 114 against 88).  Cost in us per K = 4096 on 256 units: 72 a round of large
-// tiles; 60 for three small tiles on a unit, 36 and 46 for one or two left over
-// (other groups and K scale all of them).  Bits do not depend on the tile.
+// tiles; 60 for three small tiles on a unit, 36 and 46 for one or two left over.
+// Other groups and K scale all of them: at ten grids (256 to 4096 rows, 4096 to 14336
+// columns) in both types the rule's tile is the faster one, or within 4 %, for
+// groups 64 (2048 x 6144: small 148, large 171 us; 2048 x 4096: 108, 96) and 32
+// (203, 230; 142, 132) as for 128.  Bits do not depend on the tile.
 bool large_tiles(int64_t M, int64_t N) {
   auto per_unit = [&](int64_t tm, int64_t tn) {
     return (((M + tm - 1) / tm) * ((N + tn - 1) / tn) + 255) / 256;

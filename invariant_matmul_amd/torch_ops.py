@@ -474,10 +474,12 @@ def linear_f8(x: torch.Tensor, x_scale: torch.Tensor, weight: torch.Tensor,
     x [..., K] and weight [N, K] are float8_e4m3fn or float8_e5m2 (both the
     same; K and N multiples of 16), x_scale fp32 [...] (one per row) and
     weight_scale fp32 [N], as rms_norm_quant and quantize_rows leave them.
-    The products are summed on the fp8 matrix step, scaled by row and by
+    The products are summed on the fp8 matrix step (8 neighbours in a window of 13
+    binades, then fp32), scaled by row and by
     column in fp32, the bias added in fp32, and the result rounded once to
     out_dtype (bf16, fp16 or fp32).  fp32_accum=True sums on the fp16 step
-    instead (half the matrix rate, the fp32 error bound for every K).  Row i of
+    instead (half the matrix rate, no kernel of few rows; the fp32 error bound for
+    every K).  Row i of
     y depends on row i of x, its scale and the weight alone."""
     where = "linear_f8"
     dev = x.device
@@ -564,8 +566,9 @@ def pack_w4(q: torch.Tensor, scales: torch.Tensor, zeros=None) -> W4Weight:
 
 def linear_w4(x: torch.Tensor, weight: W4Weight, bias=None) -> torch.Tensor:
     """y = x @ W^T + bias for a packed 4-bit weight W [N, K] and x [..., K] of the
-    type of its scales.  Sums are fp32 over the exact integers, scales applied
-    per group in fp32, one rounding at the end.  Row i of y depends on row i
+    type of its scales.  Sums are fp32 over the exact integers (sum x q less zero
+    times sum x, so their error goes with |x| (q + zero)), scales applied per group
+    in fp32, one rounding at the end.  Row i of y depends on row i
     of x and the weight alone, for every number of rows."""
     where = "linear_w4"
     dev = x.device
