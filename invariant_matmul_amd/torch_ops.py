@@ -518,11 +518,17 @@ def linear_f8(x: torch.Tensor, x_scale: torch.Tensor, weight: torch.Tensor,
 
 
 class W4Weight:
-    """A 4-bit weight [N, K] as linear_w4 reads it (made by pack_w4)."""
+    """A 4-bit weight [N, K] as linear_w4 reads it: made by pack_w4, or again from its
+    packed bytes (a contiguous uint8 vector, as pack_w4 left it) and sizes."""
 
     __slots__ = ("packed", "N", "K", "group", "dtype")
 
     def __init__(self, packed: torch.Tensor, N: int, K: int, group: int, dtype: torch.dtype):
+        # linear_w4 reads by the sizes: fewer bytes would be read past their end
+        size = w4_packed_size(_w4_plan(1, N, K, dtype, group))
+        if packed.dtype != torch.uint8 or packed.shape != (size,) or not packed.is_contiguous():
+            raise ValueError(f"W4Weight: [{N}, {K}] in groups of {group} is a contiguous uint8 vector of {size} "
+                             f"bytes, got {tuple(packed.shape)} {packed.dtype}")
         self.packed, self.N, self.K, self.group, self.dtype = packed, N, K, group, dtype
 
     def to(self, device) -> "W4Weight":

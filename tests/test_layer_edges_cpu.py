@@ -1,5 +1,12 @@
-"""Host-side checks of the norm and fp8 calls at sizes of zero (no GPU needed)."""
+"""Host-side checks of the calls around a linear layer (no GPU needed): sizes of zero in
+the norm and fp8 calls, and the packed bytes of a 4-bit weight."""
+import copy
+
+import pytest
+import torch
+
 import invariant_matmul_amd as imm
+from invariant_matmul_amd import torch_ops
 
 OK, INVALID = 0, 1
 P = 4096  # an aligned address that no check reads
@@ -25,3 +32,22 @@ def test_arguments_of_rows_without_columns():
 
     assert quantize() == quantize(rows=0) == quantize(rows=0, scale=P) == OK
     assert quantize(scale=P + 1) == INVALID
+
+
+def test_packed_bytes_of_a_4_bit_weight():
+    size = imm.w4_packed_size(imm.w4_plan(1, 56, 256, "f16", 64))
+    packed = torch.zeros(size, dtype=torch.uint8)
+    w = torch_ops.W4Weight(packed, 56, 256, 64, torch.float16)
+    for same in (w.to("cpu"), copy.deepcopy(w)):
+        assert (same.N, same.K, same.group, same.dtype) == (56, 256, 64, torch.float16)
+        assert torch.equal(same.packed, packed)
+    torch_ops.W4Weight(packed[:0], 0, 256, 64, torch.float16)
+    for bad in (packed[:-1], packed[:-16], torch.zeros(2 * size, dtype=torch.uint8)[::2], packed.view(4, -1),
+                packed.view(torch.int8), packed.view(torch.int16)):
+        with pytest.raises(ValueError):
+            torch_ops.W4Weight(bad, 56, 256, 64, torch.float16)
+    for sizes in ((72, 256, 64), (56, 384, 64), (56, 256, 32)):
+        with pytest.raises(ValueError):
+            torch_ops.W4Weight(packed, *sizes, torch.float16)
+    with pytest.raises(imm.GemmError):
+        torch_ops.W4Weight(packed, 56, 256, 48, torch.float16)
