@@ -554,6 +554,178 @@ gemm_status w4_run(w4_plan_t plan, const void* x, const void* packed, const floa
 
 void w4_plan_destroy(w4_plan_t plan);
 
+/* ---------------------------------------------------------------------------
+ * Norm and rotation of the query and key heads: what stands between the
+ * projection of a layer's input and attention.  For every token t and head,
+ *   n = x / sqrt(sum_d x_d^2 / dim + eps), y = n weight (y = x without the norm),
+ *   angle_i = positions[axis(i), t] inv_freq[i] for i < rot / 2, in fp64,
+ *   (z_a, z_b) = (y_a cos - y_b sin, y_b cos + y_a sin) with (a, b) =
+ *       (i, i + rot / 2), or (2 i, 2 i + 1) if interleaved,
+ *   z_d = y_d from rot on, out = round(z).
+ * axis(i): the frequencies are cut into `axes` sections (time, height, width of a
+ * video; one axis for text), and those of section s turn by positions[s].
+ * q and k are fp16 or bf16, element d of head h of token t at
+ * t token_stride + h head_stride + d (strides in elements, multiples of 8: both may lie in
+ * the output of a fused projection).  The outputs are contiguous [tokens, heads, dim].
+ * Sums are fp32 and out is rounded once.  A head of the result is a bitwise function of
+ * that head, its position, the weight and the sizes.  No passage of the pages
+ * defines these calls.
+ * ------------------------------------------------------------------------- */
+typedef struct head_rope_plan_s* head_rope_plan_t;
+
+/* Plan the call.  dim a multiple of 8 up to 512, rot a multiple of 16 up to dim (0: no
+ * rotation); norm: 0 or 1; eps finite and >= 0; axes 1 to 4, sections: the frequencies
+ * of each axis, which add up to rot / 2 (NULL for one axis).
+ * GEMM_ERR_INVALID_VALUE for a negative size, sections that do not add up or a NULL
+ * handle, GEMM_ERR_UNSUPPORTED for other types or sizes. */
+gemm_status head_rope_plan(int64_t tokens, int q_heads, int k_heads, int dim, int rot,
+                           gemm_dtype dtype, int norm, float eps, int interleaved, int axes,
+                           const int* sections, head_rope_plan_t* plan);
+
+/* The outputs, on `stream`.  positions: int64 [axes, tokens]; inv_freq: fp64 [rot / 2];
+ * weights: [dim] in the input's type, or NULL for ones (NULL without the norm).
+ * Tensors of heads and weights are 16-byte aligned.  No operand may overlap an output. */
+gemm_status head_rope_run(head_rope_plan_t plan, const void* q, int64_t q_token_stride,
+                          int64_t q_head_stride, const void* k, int64_t k_token_stride,
+                          int64_t k_head_stride, const int64_t* positions, const double* inv_freq,
+                          const void* q_weight, const void* k_weight, void* q_out, void* k_out,
+                          void* stream);
+
+/* Bytes of workspace head_rope_backward needs for the weights' gradients; 0
+ * without the norm or for a NULL plan. */
+size_t head_rope_workspace_size(head_rope_plan_t plan);
+
+/* The gradients: dq_out and dk_out, those of the outputs, contiguous; dq and dk, those of q
+ * and k, contiguous; dq_weight and dk_weight: [dim] in the input's type, each may be
+ * NULL (both: no workspace is needed).  q and k are read with the norm only.
+ * The weights' gradients sum tokens and heads in an order that the sizes fix, without atomics. */
+gemm_status head_rope_backward(head_rope_plan_t plan, const void* dq_out, const void* dk_out,
+                               const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                               const void* k, int64_t k_token_stride, int64_t k_head_stride,
+                               const int64_t* positions, const double* inv_freq,
+                               const void* q_weight, const void* k_weight, void* dq, void* dk,
+                               void* dq_weight, void* dk_weight, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+void head_rope_plan_destroy(head_rope_plan_t plan);
+
+/* ---------------------------------------------------------------------------
+ * Attention of packed sequences:
+ *   o_i = sum_j p_ij v_j,  p_ij = e^(scale q_i k_j) / e^lse_i,
+ *   lse_i = ln sum_j e^(scale q_i k_j)
+ * over the keys j that query i sees.  Sequence b has the n queries cu_q[b] ..
+ * cu_q[b + 1] - 1 and the m keys from cu_k[b] on: up to cu_k[b + 1], or k_lens[b]
+ * of them (a cache with room).  With `causal`, query i of n sees the keys j <= m - n + i,
+ * otherwise all; query head h uses key head h / (q_heads / k_heads).  A
+ * query without keys has o = 0 and lse = -infinity, also a row of q in no sequence.
+ *
+ * q [q_rows, q_heads, dim], k and v [k_rows, k_heads, dim] are fp16 or bf16 with
+ * strides as above; dim a multiple of 8 up to 128.  o is contiguous, lse fp32
+ * [q_rows, q_heads].  Logits, statistics and sums are fp32; probabilities (about
+ * the running maximum, so at most 1) are rounded to the input's type for their product
+ * with v.
+ *
+ * A row of o is a bitwise function of its query and of the keys and values it sees,
+ * in their order (and of dim and scale): not of the number of queries of the call or
+ * of its sequence, other sequences, room in a cache, or max_q.  A prompt taken at
+ * once, in pieces or token by token over a cache has the same bits.  What lies in k and
+ * v where a row does not see it does not reach the row, NaN included.
+ *
+ * cu_q, cu_k (int32 [batch + 1]) and k_lens (int32 [batch]) are device memory, read by the
+ * kernels: values that ascend, from 0 to the rows.  Others are clamped to the operands:
+ * results are then unspecified, but nothing outside is touched.  No passage of the
+ * pages defines these calls.
+ * ------------------------------------------------------------------------- */
+typedef struct attention_plan_s* attention_plan_t;
+
+/* Plan the call.  max_q: no sequence has more queries (0: q_rows).  A small max_q is
+ * what selects the kernel of few rows; a sequence with more queries than max_q says
+ * then has NaN in the rows past it.  scale > 0.  GEMM_ERR_INVALID_VALUE for a
+ * negative size, batch < 1 or a NULL handle, GEMM_ERR_UNSUPPORTED for other types, sizes
+ * (k_rows up to 2^30, q_rows q_heads below 2^31) or scales. */
+gemm_status attention_plan(int64_t q_rows, int64_t k_rows, int64_t batch, int q_heads, int k_heads,
+                           int dim, gemm_dtype dtype, int causal, float scale, int64_t max_q,
+                           attention_plan_t* plan);
+
+/* Bytes of workspace attention_run needs: the chunks' results of few rows, 0 otherwise. */
+size_t attention_workspace_size(attention_plan_t plan);
+
+/* o, and for the backward pass lse and o_low, on `stream`.  o_low has the form of o and
+ * receives what the rounding of o left, rounded to the type; each may be NULL.  cu_q and cu_k may both be NULL for one sequence of all
+ * rows.  q, k, v and o are 16-byte aligned, strides multiples of 8 elements. */
+gemm_status attention_run(attention_plan_t plan, const void* q, int64_t q_token_stride,
+                          int64_t q_head_stride, const void* k, int64_t k_token_stride,
+                          int64_t k_head_stride, const void* v, int64_t v_token_stride,
+                          int64_t v_head_stride, const int* cu_q, const int* cu_k,
+                          const int* k_lens, void* o, void* o_low, float* lse, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace attention_backward needs: sum_d do o of every row. */
+size_t attention_backward_workspace_size(attention_plan_t plan);
+
+/* The gradients dq, dk and dv (contiguous) from that of o (contiguous), o, o_low (or NULL:
+ * then the rounding of o is in the gradients) and lse:
+ *   ds_ij = p_ij (do_i v_j - sum_d do_id (o + o_low)_id), dv_j = sum_i p_ij do_i,
+ *   dq_i = scale sum_j ds_ij k_j, dk_j = scale sum_i ds_ij q_i,
+ * p and ds rounded to the input's type for their products (fp16: a ds below 2^-25 is
+ * lost, so gradients need the scaling of the loss that fp16 training has).  Rows in no
+ * sequence and keys past k_lens have zero gradients.  Sums in a fixed order, without
+ * atomics: the gradients of a sequence are a bitwise function of it alone. */
+gemm_status attention_backward(attention_plan_t plan, const void* d_o, const void* q,
+                               int64_t q_token_stride, int64_t q_head_stride, const void* k,
+                               int64_t k_token_stride, int64_t k_head_stride, const void* v,
+                               int64_t v_token_stride, int64_t v_head_stride, const void* o,
+                               const void* o_low, const float* lse, const int* cu_q, const int* cu_k,
+                               const int* k_lens, void* dq, void* dk, void* dv, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+void attention_plan_destroy(attention_plan_t plan);
+
+/* ---------------------------------------------------------------------------
+ * Log probabilities of given tokens, the entropy and the most likely tokens of
+ * rows of logits (the last product's output): with max = max_v x_v and
+ * log_sum = ln sum_v e^(x_v - max),
+ *   logprob[n] = (x[token_n] - max) - log_sum, entropy = -sum_v p_v ln p_v,
+ * and the `top` tokens of the largest logits with their log probabilities, the
+ * largest first, the lower token first among equals (NaN counts as the largest).
+ * A token below 0 is no token (logprob 0, no gradient); one from vocab on gives NaN.
+ * A logit of -infinity has probability 0; a row that holds NaN or +infinity, or
+ * -infinity alone, has NaN results.  logits: fp32, fp16 or bf16, row i from element
+ * i row_stride on (any stride: rows need no alignment).  Sums are fp32.  Row i of every
+ * output is a bitwise function of row i.  No passage of the pages defines these
+ * calls.
+ * ------------------------------------------------------------------------- */
+typedef struct logprobs_plan_s* logprobs_plan_t;
+
+/* Plan the call.  tokens_per_row 0 to 1024, top 0 to 64, vocab up to 2^22.
+ * GEMM_ERR_INVALID_VALUE for a negative size, vocab < 1, top > vocab or a NULL handle,
+ * GEMM_ERR_UNSUPPORTED for other types or sizes. */
+gemm_status logprobs_plan(int64_t rows, int64_t vocab, int tokens_per_row, int top,
+                          gemm_dtype dtype, logprobs_plan_t* plan);
+
+/* Bytes of workspace logprobs_run needs (few rows are cut into parts). */
+size_t logprobs_workspace_size(logprobs_plan_t plan);
+
+/* tokens: int64 [rows, tokens_per_row]; logprob: fp32 [rows, tokens_per_row]; entropy:
+ * fp32 [rows]; norm: fp32 [rows, 2], (max, log_sum) for the backward pass, or NULL;
+ * top_logprob: fp32 and top_token: int64 [rows, top] (NULL where top is 0). */
+gemm_status logprobs_run(logprobs_plan_t plan, const void* logits, int64_t row_stride,
+                         const int64_t* tokens, float* logprob, float* entropy, float* norm,
+                         float* top_logprob, int64_t* top_token, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/* The gradient of the logits, contiguous [rows, vocab] in their type, rounded once:
+ *   d_logits_v = sum_n g_n (1[v = token_n] - p_v) - h p_v (ln p_v + entropy)
+ * with g = d_logprob [rows, tokens_per_row] and h = d_entropy [rows], each fp32 or NULL.
+ * norm and entropy as logprobs_run left them; d_logits 16-byte aligned, and no operand's
+ * memory. */
+gemm_status logprobs_backward(logprobs_plan_t plan, const float* d_logprob, const float* d_entropy,
+                              const void* logits, int64_t row_stride, const int64_t* tokens,
+                              const float* norm, const float* entropy, void* d_logits,
+                              void* stream);
+
+void logprobs_plan_destroy(logprobs_plan_t plan);
+
 /* Name of a status ("GEMM_OK", ...); a static string.  Housekeeping. */
 const char* gemm_status_string(gemm_status status);
 

@@ -33,6 +33,11 @@ __all__ = [
     "LAYER_SYMBOLS", "RmsNormPlan", "rms_norm_plan", "rms_norm_run", "rms_norm_workspace_size",
     "rms_norm_backward", "quantize_rows", "W4Plan", "w4_plan", "w4_packed_size", "w4_pack",
     "w4_workspace_size", "w4_run",
+    "DECODER_SYMBOLS", "HeadRopePlan", "head_rope_plan", "head_rope_workspace_size",
+    "head_rope_run", "head_rope_backward", "AttentionPlan", "attention_plan",
+    "attention_workspace_size", "attention_backward_workspace_size", "attention_run",
+    "attention_backward", "LogprobsPlan", "logprobs_plan", "logprobs_workspace_size",
+    "logprobs_run", "logprobs_backward",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libinvariant_matmul.so")
@@ -61,6 +66,15 @@ LAYER_SYMBOLS = (
     "rms_norm_plan", "rms_norm_run", "rms_norm_workspace_size", "rms_norm_backward",
     "rms_norm_plan_destroy", "quantize_rows", "w4_plan", "w4_packed_size", "w4_pack",
     "w4_workspace_size", "w4_run", "w4_plan_destroy",
+)
+# The calls between and behind the products of a decoder: norms of heads with their
+# rotation, attention, log probabilities of tokens.
+DECODER_SYMBOLS = (
+    "head_rope_plan", "head_rope_workspace_size", "head_rope_run", "head_rope_backward",
+    "head_rope_plan_destroy", "attention_plan", "attention_workspace_size",
+    "attention_backward_workspace_size", "attention_run", "attention_backward",
+    "attention_plan_destroy", "logprobs_plan", "logprobs_workspace_size", "logprobs_run",
+    "logprobs_backward", "logprobs_plan_destroy",
 )
 
 
@@ -172,7 +186,34 @@ def lib() -> ctypes.CDLL:
         L.w4_run.argtypes = [vp] * 6 + [sz, vp]
         L.w4_plan_destroy.argtypes = [vp]
         L.w4_plan_destroy.restype = None
-        for f in ("gemm_run_scaled", "rms_norm_plan", "rms_norm_run", "rms_norm_backward",
+        heads = [vp, i64, i64]  # a tensor of heads: address, token and head strides
+        L.head_rope_plan.argtypes = [i64, i32, i32, i32, i32, i32, i32, f32, i32, i32,
+                                     ctypes.POINTER(i32), pp]
+        L.head_rope_workspace_size.argtypes = [vp]
+        L.head_rope_workspace_size.restype = sz
+        L.head_rope_run.argtypes = [vp] + 2 * heads + [vp] * 7
+        L.head_rope_backward.argtypes = [vp] * 3 + 2 * heads + [vp] * 9 + [sz, vp]
+        L.head_rope_plan_destroy.argtypes = [vp]
+        L.head_rope_plan_destroy.restype = None
+        L.attention_plan.argtypes = [i64, i64, i64, i32, i32, i32, i32, i32, f32, i64, pp]
+        L.attention_workspace_size.argtypes = [vp]
+        L.attention_workspace_size.restype = sz
+        L.attention_backward_workspace_size.argtypes = [vp]
+        L.attention_backward_workspace_size.restype = sz
+        L.attention_run.argtypes = [vp] + 3 * heads + [vp] * 7 + [sz, vp]
+        L.attention_backward.argtypes = [vp, vp] + 3 * heads + [vp] * 10 + [sz, vp]
+        L.attention_plan_destroy.argtypes = [vp]
+        L.attention_plan_destroy.restype = None
+        L.logprobs_plan.argtypes = [i64, i64, i32, i32, i32, pp]
+        L.logprobs_workspace_size.argtypes = [vp]
+        L.logprobs_workspace_size.restype = sz
+        L.logprobs_run.argtypes = [vp, vp, i64] + [vp] * 7 + [sz, vp]
+        L.logprobs_backward.argtypes = [vp] * 4 + [i64] + [vp] * 5
+        L.logprobs_plan_destroy.argtypes = [vp]
+        L.logprobs_plan_destroy.restype = None
+        for f in ("head_rope_plan", "head_rope_run", "head_rope_backward", "attention_plan",
+                  "attention_run", "attention_backward", "logprobs_plan", "logprobs_run",
+                  "logprobs_backward", "gemm_run_scaled", "rms_norm_plan", "rms_norm_run", "rms_norm_backward",
                   "quantize_rows", "w4_plan", "w4_pack", "w4_run", "gemm_plan", "gemm_plan_ex", "gemm_plan_ex2", "gemm_plan_info",
                   "gemm_plan_tile_of", "gemm_run", "gemm_run_bias", "gemm_splitk_run",
                   "gemm_splitk_run_bias", "gemm_splitk_run_noalloc", "gemm_last_hip_error", "ozaki_plan", "ozaki_plan_info",
@@ -679,3 +720,254 @@ def w4_run(plan: W4Plan, x, packed, y, bias=None, workspace=None, stream=None,
     _check(lib().w4_run(plan.handle, _addr(x), _addr(packed), _addr(bias), _addr(y),
                         _addr(workspace), _ws_bytes(workspace, workspace_bytes),
                         _stream(stream, x, y)), "w4_run")
+
+
+# ---- Norm and rotation of heads ----------------------------------------------------
+
+class HeadRopePlan:
+    """Owns a head_rope_plan_t; destroyed with the object."""
+
+    def __init__(self, handle: int, tokens: int, heads, dim: int, rot: int, dtype: int, axes: int):
+        self.handle = handle
+        self.tokens, self.heads, self.dim, self.rot = tokens, heads, dim, rot
+        self.dtype, self.axes = dtype, axes
+        self._lib = lib()
+
+    def __del__(self):
+        h, self.handle = getattr(self, "handle", None), None
+        if h:
+            self._lib.head_rope_plan_destroy(h)
+
+    @functools.cached_property
+    def workspace_bytes(self) -> int:
+        return head_rope_workspace_size(self)
+
+
+def head_rope_plan(tokens: int, q_heads: int, k_heads: int, dim: int, rot: int, dtype,
+                   norm: bool = True, eps: float = 1e-6, interleaved: bool = False,
+                   sections=None) -> HeadRopePlan:
+    """Plan the norm and rotation of heads; sections: the frequencies of each axis."""
+    axes = 1 if sections is None else len(sections)
+    arr = None if sections is None else (ctypes.c_int * max(1, axes))(*sections)
+    dt, h = _dtype_code(dtype), ctypes.c_void_p()
+    _check(lib().head_rope_plan(tokens, q_heads, k_heads, dim, rot, dt, int(norm), eps,
+                                int(interleaved), axes, arr, ctypes.byref(h)), "head_rope_plan")
+    return HeadRopePlan(h.value, tokens, (q_heads, k_heads), dim, rot, dt, axes)
+
+
+def _heads(t, name, dtype_code, shape):
+    """Address and strides of a [tokens, heads, dim] tensor whose heads are contiguous."""
+    if tuple(t.shape) != tuple(shape) or _dtype_code(t.dtype) != dtype_code:
+        raise ValueError(f"{name} is {tuple(t.shape)} {t.dtype}, the plan expects {tuple(shape)}, "
+                         f"code {dtype_code}")
+    if t.stride(2) != 1:
+        raise ValueError(f"{name}: the elements of a head must be contiguous")
+    _check_device(t, name)
+    return t.data_ptr(), t.stride(0), t.stride(1)
+
+
+def _check_typed(t, name, dtype_name, numel):
+    if t is None or isinstance(t, int):
+        return
+    if str(t.dtype) != f"torch.{dtype_name}" or t.numel() != numel or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype_name} tensor of {numel} elements")
+    _check_device(t, name)
+
+
+def _check_rope(plan, positions, inv_freq, q_weight, k_weight):
+    _check_typed(positions, "positions", "int64", plan.axes * plan.tokens)
+    _check_typed(inv_freq, "inv_freq", "float64", plan.rot // 2)
+    _check_tensor(q_weight, "q_weight", plan.dtype, plan.dim)
+    _check_tensor(k_weight, "k_weight", plan.dtype, plan.dim)
+
+
+def head_rope_run(plan: HeadRopePlan, q, k, positions, inv_freq, q_out, k_out, q_weight=None,
+                  k_weight=None, stream=None) -> None:
+    """q_out and k_out [tokens, heads, dim] from q and k, whose heads may be strided."""
+    shapes = [(plan.tokens, n, plan.dim) for n in plan.heads]
+    _check_rope(plan, positions, inv_freq, q_weight, k_weight)
+    for t, name, s in ((q_out, "q_out", shapes[0]), (k_out, "k_out", shapes[1])):
+        _check_tensor(t, name, plan.dtype, s[0] * s[1] * s[2])
+    _check(lib().head_rope_run(plan.handle, *_heads(q, "q", plan.dtype, shapes[0]),
+                               *_heads(k, "k", plan.dtype, shapes[1]), _addr(positions),
+                               _addr(inv_freq), _addr(q_weight), _addr(k_weight), _addr(q_out),
+                               _addr(k_out), _stream(stream, q, k)), "head_rope_run")
+
+
+def head_rope_workspace_size(plan: HeadRopePlan) -> int:
+    return int(lib().head_rope_workspace_size(plan.handle))
+
+
+def head_rope_backward(plan: HeadRopePlan, dq_out, dk_out, q, k, positions, inv_freq, dq, dk,
+                       q_weight=None, k_weight=None, dq_weight=None, dk_weight=None,
+                       workspace=None, stream=None, workspace_bytes=None) -> None:
+    """dq and dk (and the weights' gradients, with a workspace) from those of the outputs."""
+    shapes = [(plan.tokens, n, plan.dim) for n in plan.heads]
+    _check_rope(plan, positions, inv_freq, q_weight, k_weight)
+    for t, name, s in ((dq_out, "dq_out", 0), (dk_out, "dk_out", 1), (dq, "dq", 0), (dk, "dk", 1)):
+        _check_tensor(t, name, plan.dtype, shapes[s][0] * shapes[s][1] * shapes[s][2])
+    _check_tensor(dq_weight, "dq_weight", plan.dtype, plan.dim)
+    _check_tensor(dk_weight, "dk_weight", plan.dtype, plan.dim)
+    _check_ws_device(workspace)
+    _check(lib().head_rope_backward(plan.handle, _addr(dq_out), _addr(dk_out),
+                                    *_heads(q, "q", plan.dtype, shapes[0]),
+                                    *_heads(k, "k", plan.dtype, shapes[1]), _addr(positions),
+                                    _addr(inv_freq), _addr(q_weight), _addr(k_weight), _addr(dq),
+                                    _addr(dk), _addr(dq_weight), _addr(dk_weight), _addr(workspace),
+                                    _ws_bytes(workspace, workspace_bytes), _stream(stream, q, k)),
+           "head_rope_backward")
+
+
+# ---- Attention ----------------------------------------------------------------------
+
+class AttentionPlan:
+    """Owns an attention_plan_t; destroyed with the object."""
+
+    def __init__(self, handle: int, q_rows, k_rows, batch, q_heads, k_heads, dim, dtype):
+        self.handle = handle
+        self.q_rows, self.k_rows, self.batch = q_rows, k_rows, batch
+        self.q_heads, self.k_heads, self.dim, self.dtype = q_heads, k_heads, dim, dtype
+        self._lib = lib()
+
+    def __del__(self):
+        h, self.handle = getattr(self, "handle", None), None
+        if h:
+            self._lib.attention_plan_destroy(h)
+
+    @functools.cached_property
+    def workspace_bytes(self) -> int:
+        return attention_workspace_size(self)
+
+    @functools.cached_property
+    def backward_workspace_bytes(self) -> int:
+        return attention_backward_workspace_size(self)
+
+
+def attention_plan(q_rows: int, k_rows: int, batch: int, q_heads: int, k_heads: int, dim: int,
+                   dtype, causal: bool = True, scale=None, max_q: int = 0) -> AttentionPlan:
+    """Plan attention of packed sequences; scale: dim ** -0.5 by default."""
+    dt, h = _dtype_code(dtype), ctypes.c_void_p()
+    scale = (dim ** -0.5 if dim > 0 else 1.0) if scale is None else scale
+    _check(lib().attention_plan(q_rows, k_rows, batch, q_heads, k_heads, dim, dt, int(causal), scale,
+                                max_q, ctypes.byref(h)), "attention_plan")
+    return AttentionPlan(h.value, q_rows, k_rows, batch, q_heads, k_heads, dim, dt)
+
+
+def attention_workspace_size(plan: AttentionPlan) -> int:
+    return int(lib().attention_workspace_size(plan.handle))
+
+
+def attention_backward_workspace_size(plan: AttentionPlan) -> int:
+    return int(lib().attention_backward_workspace_size(plan.handle))
+
+
+def _qkv(plan, q, k, v, cu_q, cu_k, k_lens):
+    _check_typed(cu_q, "cu_q", "int32", plan.batch + 1)
+    _check_typed(cu_k, "cu_k", "int32", plan.batch + 1)
+    _check_typed(k_lens, "k_lens", "int32", plan.batch)
+    keys = (plan.k_rows, plan.k_heads, plan.dim)
+    return (*_heads(q, "q", plan.dtype, (plan.q_rows, plan.q_heads, plan.dim)),
+            *_heads(k, "k", plan.dtype, keys), *_heads(v, "v", plan.dtype, keys))
+
+
+def attention_run(plan: AttentionPlan, q, k, v, o, cu_q=None, cu_k=None, k_lens=None, lse=None,
+                  o_low=None, workspace=None, stream=None, workspace_bytes=None) -> None:
+    """o [q_rows, q_heads, dim] (and lse and o_low) from q, k and v, whose heads may be strided."""
+    heads = _qkv(plan, q, k, v, cu_q, cu_k, k_lens)
+    _check_tensor(o, "o", plan.dtype, plan.q_rows * plan.q_heads * plan.dim)
+    _check_tensor(o_low, "o_low", plan.dtype, plan.q_rows * plan.q_heads * plan.dim)
+    _check_tensor(lse, "lse", DTYPE["f32"], plan.q_rows * plan.q_heads)
+    _check_ws_device(workspace)
+    _check(lib().attention_run(plan.handle, *heads, _addr(cu_q), _addr(cu_k), _addr(k_lens), _addr(o),
+                               _addr(o_low), _addr(lse), _addr(workspace), _ws_bytes(workspace, workspace_bytes),
+                               _stream(stream, q, o)), "attention_run")
+
+
+def attention_backward(plan: AttentionPlan, d_o, q, k, v, o, lse, dq, dk, dv, cu_q=None, cu_k=None,
+                       k_lens=None, o_low=None, workspace=None, stream=None, workspace_bytes=None) -> None:
+    """dq, dk and dv (contiguous) from the gradient of o, o, lse and o_low."""
+    heads = _qkv(plan, q, k, v, cu_q, cu_k, k_lens)
+    rows, keys = plan.q_rows * plan.q_heads, plan.k_rows * plan.k_heads * plan.dim
+    for t, name, n in ((d_o, "d_o", rows * plan.dim), (o, "o", rows * plan.dim), (o_low, "o_low", rows * plan.dim),
+                       (dq, "dq", rows * plan.dim), (dk, "dk", keys), (dv, "dv", keys)):
+        _check_tensor(t, name, plan.dtype, n)
+    _check_tensor(lse, "lse", DTYPE["f32"], rows)
+    _check_ws_device(workspace)
+    _check(lib().attention_backward(plan.handle, _addr(d_o), *heads, _addr(o), _addr(o_low), _addr(lse), _addr(cu_q),
+                                    _addr(cu_k), _addr(k_lens), _addr(dq), _addr(dk), _addr(dv),
+                                    _addr(workspace), _ws_bytes(workspace, workspace_bytes),
+                                    _stream(stream, q, dq)), "attention_backward")
+
+
+# ---- Log probabilities of tokens ----------------------------------------------------
+
+class LogprobsPlan:
+    """Owns a logprobs_plan_t; destroyed with the object."""
+
+    def __init__(self, handle: int, rows: int, vocab: int, tokens_per_row: int, top: int, dtype: int):
+        self.handle = handle
+        self.rows, self.vocab, self.dtype = rows, vocab, dtype
+        self.tokens_per_row, self.top = tokens_per_row, top
+        self._lib = lib()
+
+    def __del__(self):
+        h, self.handle = getattr(self, "handle", None), None
+        if h:
+            self._lib.logprobs_plan_destroy(h)
+
+    @functools.cached_property
+    def workspace_bytes(self) -> int:
+        return logprobs_workspace_size(self)
+
+
+def logprobs_plan(rows: int, vocab: int, dtype, tokens_per_row: int = 1, top: int = 0) -> LogprobsPlan:
+    """Plan the log probabilities of tokens_per_row tokens and the top tokens of each row."""
+    dt, h = _dtype_code(dtype), ctypes.c_void_p()
+    _check(lib().logprobs_plan(rows, vocab, tokens_per_row, top, dt, ctypes.byref(h)), "logprobs_plan")
+    return LogprobsPlan(h.value, rows, vocab, tokens_per_row, top, dt)
+
+
+def logprobs_workspace_size(plan: LogprobsPlan) -> int:
+    return int(lib().logprobs_workspace_size(plan.handle))
+
+
+def _logits(plan, logits):
+    if tuple(logits.shape) != (plan.rows, plan.vocab) or _dtype_code(logits.dtype) != plan.dtype:
+        raise ValueError(f"logits are {tuple(logits.shape)} {logits.dtype}, the plan expects "
+                         f"{(plan.rows, plan.vocab)}, code {plan.dtype}")
+    if plan.vocab > 1 and logits.stride(1) != 1:
+        raise ValueError("logits: the elements of a row must be contiguous")
+    _check_device(logits, "logits")
+    return logits.data_ptr(), logits.stride(0)
+
+
+def logprobs_run(plan: LogprobsPlan, logits, tokens, logprob, entropy, norm=None, top_logprob=None,
+                 top_token=None, workspace=None, stream=None, workspace_bytes=None) -> None:
+    """logprob, entropy, norm and the top tokens of the rows of logits."""
+    n, f32 = plan.rows * plan.tokens_per_row, DTYPE["f32"]
+    _check_typed(tokens, "tokens", "int64", n)
+    _check_tensor(logprob, "logprob", f32, n)
+    _check_tensor(entropy, "entropy", f32, plan.rows)
+    _check_tensor(norm, "norm", f32, 2 * plan.rows)
+    _check_tensor(top_logprob, "top_logprob", f32, plan.rows * plan.top)
+    _check_typed(top_token, "top_token", "int64", plan.rows * plan.top)
+    _check_ws_device(workspace)
+    _check(lib().logprobs_run(plan.handle, *_logits(plan, logits), _addr(tokens), _addr(logprob),
+                              _addr(entropy), _addr(norm), _addr(top_logprob), _addr(top_token),
+                              _addr(workspace), _ws_bytes(workspace, workspace_bytes),
+                              _stream(stream, logits)), "logprobs_run")
+
+
+def logprobs_backward(plan: LogprobsPlan, logits, tokens, norm, entropy, d_logits, d_logprob=None,
+                      d_entropy=None, stream=None) -> None:
+    """d_logits from the gradients of logprob and entropy."""
+    n, f32 = plan.rows * plan.tokens_per_row, DTYPE["f32"]
+    _check_typed(tokens, "tokens", "int64", n)
+    _check_tensor(norm, "norm", f32, 2 * plan.rows)
+    _check_tensor(entropy, "entropy", f32, plan.rows)
+    _check_tensor(d_logprob, "d_logprob", f32, n)
+    _check_tensor(d_entropy, "d_entropy", f32, plan.rows)
+    _check_tensor(d_logits, "d_logits", plan.dtype, plan.rows * plan.vocab)
+    _check(lib().logprobs_backward(plan.handle, _addr(d_logprob), _addr(d_entropy),
+                                   *_logits(plan, logits), _addr(tokens), _addr(norm), _addr(entropy),
+                                   _addr(d_logits), _stream(stream, logits)), "logprobs_backward")

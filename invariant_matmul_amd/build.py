@@ -19,7 +19,9 @@ LIB = os.path.join(HERE, "libinvariant_matmul.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 
 SOURCES = ["api.cpp", "gemm_kernels.hip", "gemm_dma.hip", "ozaki.hip", "noalloc.hip",
-           "rms_norm.hip", "w4.hip", "f8_rows.hip", "layer_api.cpp"]
+           "rms_norm.hip", "w4.hip", "f8_rows.hip", "layer_api.cpp",
+           "head_rope.hip", "attention.hip", "attention_backward.hip", "token_logprobs.hip",
+           "decoder_api.cpp"]
 # The benchmark's HBM read probe: a library of its own, never linked into the GEMM library.
 PROBE_SOURCES = ["hbm_probe.hip"]
 PROBE_LIB = os.path.join(HERE, "libimm_hbm_probe.so")

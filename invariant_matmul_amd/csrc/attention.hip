@@ -1,0 +1,541 @@
+// Attention over packed sequences and caches:
+//   o_i = sum_j p_ij v_j, p_ij = e^(scale q_i k_j) / sum_j e^(scale q_i k_j),
+// over the keys j that query i sees; lse_i = ln of that sum.
+//
+// A row's bits are a function of its query and the keys and values it sees, in
+// their order, alone: they do not depend on how many queries the call holds, on the other
+// sequences, on the room behind a cache or on which kernel runs.  A prompt
+// taken at once, in pieces or token by token gives the same bits.  For that, every
+// kernel sums in one order.  Keys are cut from the sequence's first one on into
+// chunks of 256 and steps of 64.  Within a chunk the running maximum, sum and
+// output go from step to step (each step: S on the matrix cores, p about the
+// running maximum, p rounded to the input's type, two steps of 32 keys
+// into the output's chain); a chunk's results start anew, and chunks are joined
+// in ascending order by fp32 products with powers of two and one fma.  So chunks
+// can be worked on by workgroups of their own (few rows) or one after the other
+// (many rows).
+#include "attention_common.h"
+
+namespace imm {
+namespace {
+using namespace dev;
+
+// ---- Many rows -----------------------------------------------------------------
+// A workgroup takes 256 rows of a key head, 32 a wave, and walks through their keys
+// 64 at a time: the next step's keys and values travel through registers into the
+// other half of a two-stage LDS buffer while this one's are used.
+constexpr int kWaves = 8, kThreads = 64 * kWaves;
+constexpr int kRows = 32 * kWaves;
+
+// Slot i of a tile that this thread moves (row, slot of the row).
+template <int DP>
+struct Mover {
+  static constexpr int N = kTile * TileOf<DP>::SLOTS / kThreads;
+  u32x4 k[N], v[N];
+  __device__ __forceinline__ static int row(int i) { return (threadIdx.x + i * kThreads) / TileOf<DP>::SLOTS; }
+  __device__ __forceinline__ static int slot(int i) { return threadIdx.x % TileOf<DP>::SLOTS; }
+  // rows from `left` on are zeros
+  __device__ __forceinline__ void load(const char* kt, const char* vt, int64_t k_bytes, int64_t v_bytes,
+                                       int left, int dim) {
+    const auto kb = buffer_at(kt), vb = buffer_at(vt);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const bool ok = row(i) < left && slot(i) * 8 < dim;
+      k[i] = load_b128(kb, ok ? (unsigned)(row(i) * (int)k_bytes + slot(i) * 16) : OOB);
+      v[i] = load_b128(vb, ok ? (unsigned)(row(i) * (int)v_bytes + slot(i) * 16) : OOB);
+    }
+  }
+  __device__ __forceinline__ void store(char* kt, char* vt) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int at = TileOf<DP>::at(row(i), slot(i));
+      *reinterpret_cast<u32x4*>(kt + at) = k[i];
+      *reinterpret_cast<u32x4*>(vt + at) = v[i];
+    }
+  }
+};
+
+template <int IN>
+__device__ __forceinline__ bool not_finite(unsigned two) {
+  constexpr unsigned E = IN == GEMM_F16 ? 0x7c00u : 0x7f80u;
+  return (two & E) == E || (two & (E << 16)) == (E << 16);
+}
+
+template <int IN, int DP>
+__global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttnArgs a) {
+  using T = TileOf<DP>;
+  __shared__ __attribute__((aligned(16))) char lds[2][2][kTile * T::PITCH];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x / 64, quad = lane / 16, col = lane % 16;
+  // heads vary fastest: neighbouring workgroups go to different XCDs, so a key
+  // head's workgroups meet in few of the L2s.  The last rows (the most keys) first.
+  const int64_t tiles = gridDim.x / a.k_heads;
+  const int kh = blockIdx.x % a.k_heads;
+  const int64_t tile = tiles - 1 - blockIdx.x / a.k_heads;
+  const int seg = segment_of_tile(a, tile, kRows);
+  const Sequence s = segment(a, seg);
+  const int64_t r0 = (tile - (s.q0 * a.group / kRows + seg)) * kRows;
+  const int64_t rows = s.n * a.group;
+  if (r0 >= rows) return;
+
+  // this lane's rows: column `col` of the two blocks of 16 of its wave
+  int64_t row[2];
+  int seen[2];
+  i32x4 qf[2][T::KS];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    row[i] = r0 + 32 * wave + 16 * i + col;
+    const int64_t t = row[i] / a.group;
+    const int h = (int)(row[i] - t * a.group);
+    seen[i] = (int)keys_seen(a, s, t);
+    const char* const q = static_cast<const char*>(a.q) + 2 * ((s.q0 + t) * a.q_token + (kh * a.group + h) * a.q_head);
+#pragma unroll
+    for (int ks = 0; ks < T::KS; ++ks) {
+      const int d = 32 * ks + 8 * quad;
+      qf[i][ks] = i32x4{};
+      if (row[i] < rows && d < a.dim) qf[i][ks] = *reinterpret_cast<const i32x4*>(q + 2 * d);
+    }
+  }
+  // keys that any row of the workgroup, and of the wave, sees, and those that all of
+  // the wave's see (rows past the end see none, which needs no mask)
+  auto seen_of = [&](int64_t r) { return (int)keys_seen(a, s, (r < rows ? r : rows - 1) / a.group); };
+  const int need = __builtin_amdgcn_readfirstlane(seen_of(r0 + kRows - 1));
+  const int64_t w0 = r0 + 32 * wave;
+  const int wave_need = __builtin_amdgcn_readfirstlane(w0 < rows ? seen_of(w0 + 31) : 0);
+  const int wave_all = __builtin_amdgcn_readfirstlane(w0 < rows ? seen_of(w0) : 0);
+
+  f32x4 O[2][T::DB], o[2][T::DB];
+  float M[2], L[2], m[2], l[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    M[i] = kNegInf;
+    L[i] = 0.0f;
+#pragma unroll
+    for (int d = 0; d < T::DB; ++d) O[i][d] = f32x4{};
+  }
+
+  const int64_t k_bytes = 2 * a.k_token, v_bytes = 2 * a.v_token;
+  const char* const kp = static_cast<const char*>(a.k) + 2 * (s.k0 * a.k_token + kh * a.k_head);
+  const char* const vp = static_cast<const char*>(a.v) + 2 * (s.k0 * a.v_token + kh * a.v_head);
+  Mover<DP> next;
+  auto fetch = [&](int64_t k0) {
+    next.load(kp + k0 * k_bytes, vp + k0 * v_bytes, k_bytes, v_bytes, (int)(s.m - k0 < kTile ? s.m - k0 : kTile), a.dim);
+  };
+  // values behind the last key that some rows see (a NaN there must not reach the rows
+  // that do not: 0 times it is one)
+  auto clean = [&](int k0) {
+    if (k0 + kTile <= seen_of(r0)) return false;  // all rows see all of them
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < Mover<DP>::N; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) bad |= not_finite<IN>(next.v[i][e]);
+    return bad;
+  };
+  if (need > 0) {
+    fetch(0);
+  }
+  bool poison = need > 0 && __syncthreads_or(clean(0));
+  auto put = [&](int stage) {
+    if (poison) {
+#pragma unroll
+      for (int i = 0; i < Mover<DP>::N; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          constexpr unsigned E = IN == GEMM_F16 ? 0x7c00u : 0x7f80u;
+          unsigned v = next.v[i][e];
+          if ((v & E) == E) v &= 0xffff0000u;
+          if ((v & (E << 16)) == (E << 16)) v &= 0xffffu;
+          next.v[i][e] = v;
+        }
+    }
+    next.store(lds[stage][0], lds[stage][1]);
+  };
+  if (need > 0) put(0);
+  __syncthreads();
+
+  int stage = 0;
+  for (int k0 = 0; k0 < need; k0 += kTile) {
+    const bool more = k0 + kTile < need;
+    if (more) fetch(k0 + kTile);
+    const char* const kt = lds[stage][0];
+    const char* const vt = lds[stage][1];
+    if (k0 % kAttnChunk == 0) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        m[i] = kNegInf;
+        l[i] = 0.0f;
+#pragma unroll
+        for (int d = 0; d < T::DB; ++d) o[i][d] = f32x4{};
+      }
+    }
+    if (k0 < wave_need) {
+      f32x4 sc[2][4];
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        sc[0][b] = sc[1][b] = f32x4{};
+#pragma unroll
+        for (int ks = 0; ks < T::KS; ++ks) {
+          const i32x4 kf = row_fragment<DP>(kt, b, ks);
+          sc[0][b] = mfma16_v<IN>(kf, qf[0][ks], sc[0][b]);
+          sc[1][b] = mfma16_v<IN>(kf, qf[1][ks], sc[1][b]);
+        }
+      }
+      if (k0 + kTile > wave_all) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int b = 0; b < 4; ++b)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (k0 + 16 * b + 4 * quad + r >= seen[i]) sc[i][b][r] = kNegInf;
+      }
+      i32x4 pf[2][2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float to = fmaxf(m[i], row_max(lane_max(sc[i])) * a.scale_log2);
+        const float f = shrink(m[i], to);
+        m[i] = to;
+        l[i] = l[i] * f + probabilities(sc[i], a.scale_log2, to);
+#pragma unroll
+        for (int d = 0; d < T::DB; ++d) o[i][d] *= f;
+        pf[i][0] = pack_blocks<IN>(sc[i][0], sc[i][1]);
+        pf[i][1] = pack_blocks<IN>(sc[i][2], sc[i][3]);
+      }
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int d = 0; d < T::DB; ++d) {
+          const i32x4 vf = column_fragment<DP>(vt, p, d);
+          o[0][d] = mfma16_v<IN>(vf, pf[0][p], o[0][d]);
+          o[1][d] = mfma16_v<IN>(vf, pf[1][p], o[1][d]);
+        }
+      if (poison) {
+        // the values that were taken out, for the rows that see them
+        for (int j = 0; j < kTile && k0 + j < s.m; ++j) {
+          const unsigned short* const v = reinterpret_cast<const unsigned short*>(vp + (k0 + j) * v_bytes);
+#pragma unroll
+          for (int d = 0; d < T::DB; ++d)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const int at = 16 * d + 4 * quad + r;
+              if (at >= a.dim) continue;
+              constexpr unsigned E = IN == GEMM_F16 ? 0x7c00u : 0x7f80u;
+              if ((v[at] & E) != E) continue;
+              const float bad = IN == GEMM_F16 ? (float)__builtin_bit_cast(_Float16, v[at])
+                                               : __uint_as_float((unsigned)v[at] << 16);
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                if (k0 + j < seen[i]) o[i][d][r] += bad;
+            }
+        }
+      }
+    }
+    if ((k0 + kTile) % kAttnChunk == 0 || !more) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        // (a chunk that the row does not see leaves it as it is, to the sign of a zero)
+        if (k0 / kAttnChunk * kAttnChunk < seen[i]) {
+          const Join j = join_chunk(M[i], m[i]);
+          M[i] = j.m;
+          L[i] = joined(L[i], row_sum(l[i]), j);
+#pragma unroll
+          for (int d = 0; d < T::DB; ++d)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) O[i][d][r] = joined(O[i][d][r], o[i][d][r], j);
+        }
+      }
+    }
+    if (more) {
+      poison = __syncthreads_or(clean(k0 + kTile));
+      stage ^= 1;
+      put(stage);
+      __syncthreads();
+    }
+  }
+
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (row[i] >= rows) continue;
+    const int64_t t = row[i] / a.group;
+    const int64_t head = kh * a.group + (row[i] - t * a.group);
+    const int64_t at = (s.q0 + t) * a.q_heads + head;
+    // a row without keys is zero; one whose keys are all -infinity is 0 / 0
+    const float inv = seen[i] == 0 ? 0.0f : 1.0f / L[i];
+#pragma unroll
+    for (int d = 0; d < T::DB; ++d) {
+      const int c = 16 * d + 4 * quad;
+      if (c >= a.dim) continue;
+      const f32x4 x = O[i][d] * inv;
+      const i32x2 y{pack2<IN>(x[0], x[1]), pack2<IN>(x[2], x[3])};
+      const int64_t to = 2 * (at * a.dim + c);
+      *reinterpret_cast<i32x2*>(static_cast<char*>(a.o) + to) = y;
+      if (a.o_low)
+        *reinterpret_cast<i32x2*>(static_cast<char*>(a.o_low) + to) =
+            i32x2{pack2_rest<IN>(x[0], x[1], y[0]), pack2_rest<IN>(x[2], x[3], y[1])};
+    }
+    if (a.lse && quad == 0)
+      a.lse[at] = seen[i] == 0 ? kNegInf : (M[i] + __builtin_amdgcn_logf(L[i])) * kLn2;
+  }
+}
+
+// ---- Few rows ------------------------------------------------------------------
+// A workgroup takes one chunk of 256 keys of one key head, all of whose bytes it asks for
+// at once: the keys as fragments in registers (each of the four waves its step of 64), the
+// values through registers to LDS.  Each wave makes its step's logits and their
+// maximum; with the maxima of the steps before, which LDS holds, every wave has the
+// running maximum that one wave alone would have had, so the probabilities are
+// those of the chain; then each wave takes a quarter of the output's dimensions through
+// all four steps.
+constexpr int kFewWaves = 4, kFewThreads = 64 * kFewWaves;
+
+template <int IN, int DP>
+__global__ __launch_bounds__(kFewThreads, 2) void attention_few_kernel(AttnArgs a) {
+  using T = TileOf<DP>;
+  __shared__ __attribute__((aligned(16))) char vt[kFewWaves][kTile * T::PITCH];
+  __shared__ i32x4 pl[kFewWaves][2][64];
+  __shared__ float ml[kFewWaves][16], sl[kFewWaves][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x / 64, quad = lane / 16, col = lane % 16;
+  const int kh = blockIdx.x % a.k_heads;
+  const int64_t slot = blockIdx.x / a.k_heads;
+  // the sequence of this chunk slot: sequence b's begin at k_start(b) / 256 + b
+  int lo = 0, hi = a.batch - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (k_start(a, mid) / kAttnChunk + mid <= slot) lo = mid;
+    else hi = mid - 1;
+  }
+  const Sequence s = segment(a, lo + 1);
+  const int64_t c0 = (slot - s.slot0) * kAttnChunk;
+  if (c0 < 0 || c0 >= s.m || s.n == 0) return;
+  const int64_t queries = s.n < a.max_q ? s.n : a.max_q;
+  if (c0 >= keys_seen(a, s, queries - 1)) return;
+  const int left = (int)(s.m - c0 < kAttnChunk ? s.m - c0 : kAttnChunk);
+
+  const auto kb = buffer_at(static_cast<const char*>(a.k) + 2 * ((s.k0 + c0) * a.k_token + kh * a.k_head));
+  const auto vb = buffer_at(static_cast<const char*>(a.v) + 2 * ((s.k0 + c0) * a.v_token + kh * a.v_head));
+  i32x4 kf[4][T::KS];
+#pragma unroll
+  for (int b = 0; b < 4; ++b)
+#pragma unroll
+    for (int ks = 0; ks < T::KS; ++ks) {
+      const int key = 64 * wave + 16 * b + col, d = 32 * ks + 8 * quad;
+      kf[b][ks] = __builtin_bit_cast(
+          i32x4, load_b128(kb, key < left && d < a.dim ? (unsigned)(key * (int)(2 * a.k_token) + 2 * d) : OOB));
+    }
+  constexpr int NV = kAttnChunk * T::SLOTS / kFewThreads;
+  u32x4 vv[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int at = threadIdx.x + i * kFewThreads, key = at / T::SLOTS, c = at % T::SLOTS;
+    vv[i] = load_b128(vb, key < left && c * 8 < a.dim ? (unsigned)(key * (int)(2 * a.v_token) + c * 16) : OOB);
+  }
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int at = threadIdx.x + i * kFewThreads, key = at / T::SLOTS, c = at % T::SLOTS;
+    *reinterpret_cast<u32x4*>(&vt[key / kTile][T::at(key % kTile, c)]) = vv[i];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) bad |= not_finite<IN>(vv[i][e]);
+  }
+  // rows that do not see all of the chunk: values that are not finite are taken out of it,
+  // and added for the rows that see them
+  const bool poison = __syncthreads_or(bad) && c0 + left > keys_seen(a, s, 0);
+  if (poison) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int at = threadIdx.x + i * kFewThreads, key = at / T::SLOTS, c = at % T::SLOTS;
+      u32x4 v = vv[i];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        constexpr unsigned E = IN == GEMM_F16 ? 0x7c00u : 0x7f80u;
+        if ((v[e] & E) == E) v[e] &= 0xffff0000u;
+        if ((v[e] & (E << 16)) == (E << 16)) v[e] &= 0xffffu;
+      }
+      *reinterpret_cast<u32x4*>(&vt[key / kTile][T::at(key % kTile, c)]) = v;
+    }
+    __syncthreads();
+  }
+
+  const int64_t rows = queries * a.group;
+  for (int64_t r0 = 0; r0 < rows; r0 += 16) {
+    const int64_t row = r0 + col, t = row / a.group;
+    const int h = (int)(row - t * a.group);
+    const int seen = (int)clamp64((row < rows ? keys_seen(a, s, t) : 0) - c0, 0, kAttnChunk);
+    f32x4 sc[4];
+    {
+      const char* const q = static_cast<const char*>(a.q) + 2 * ((s.q0 + t) * a.q_token + (kh * a.group + h) * a.q_head);
+      i32x4 qf[T::KS];
+#pragma unroll
+      for (int ks = 0; ks < T::KS; ++ks) {
+        const int d = 32 * ks + 8 * quad;
+        qf[ks] = i32x4{};
+        if (row < rows && d < a.dim) qf[ks] = *reinterpret_cast<const i32x4*>(q + 2 * d);
+      }
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        sc[b] = f32x4{};
+#pragma unroll
+        for (int ks = 0; ks < T::KS; ++ks) sc[b] = mfma16_v<IN>(kf[b][ks], qf[ks], sc[b]);
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (64 * wave + 16 * b + 4 * quad + r >= seen) sc[b][r] = kNegInf;
+    const float mine = row_max(lane_max(sc)) * a.scale_log2;
+    if (quad == 0) ml[wave][col] = mine;
+    __syncthreads();
+    float m[kFewWaves];
+    m[0] = ml[0][col];
+#pragma unroll
+    for (int w = 1; w < kFewWaves; ++w) m[w] = fmaxf(m[w - 1], ml[w][col]);
+    const float about = wave == 0 ? m[0] : wave == 1 ? m[1] : wave == 2 ? m[2] : m[3];
+    sl[wave][lane] = probabilities(sc, a.scale_log2, about);
+    pl[wave][0][lane] = pack_blocks<IN>(sc[0], sc[1]);
+    pl[wave][1][lane] = pack_blocks<IN>(sc[2], sc[3]);
+    __syncthreads();
+    f32x4 o[(T::DB + kFewWaves - 1) / kFewWaves];
+#pragma unroll
+    for (auto& x : o) x = f32x4{};
+    float l = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kFewWaves; ++w) {
+      // (steps past the row's last key add nothing and shrink nothing)
+      const float f = w == 0 ? shrink(kNegInf, m[0]) : shrink(m[w - 1], m[w]);
+      l = l * f + sl[w][lane];
+#pragma unroll
+      for (int i = 0; i < (T::DB + kFewWaves - 1) / kFewWaves; ++i) {
+        const int d = kFewWaves * i + wave;
+        if (d < T::DB) {
+          o[i] *= f;
+#pragma unroll
+          for (int p = 0; p < 2; ++p) o[i] = mfma16_v<IN>(column_fragment<DP>(vt[w], p, d), pl[w][p][lane], o[i]);
+        }
+      }
+    }
+    l = row_sum(l);
+    const int64_t at = (slot * a.k_heads + kh) * a.part_rows + row;
+    if (row < rows) {
+      if (wave == 0 && quad == 0) {
+        a.part_ml[2 * at] = m[kFewWaves - 1];
+        a.part_ml[2 * at + 1] = l;
+      }
+#pragma unroll
+      for (int i = 0; i < (T::DB + kFewWaves - 1) / kFewWaves; ++i) {
+        const int d = 16 * (kFewWaves * i + wave) + 4 * quad;
+        if (d < a.dim && d < DP) {
+          if (poison) {
+            for (int j = 0; j < seen; ++j) {
+              const unsigned short* const v = reinterpret_cast<const unsigned short*>(
+                  static_cast<const char*>(a.v) + 2 * ((s.k0 + c0 + j) * a.v_token + kh * a.v_head));
+              constexpr unsigned E = IN == GEMM_F16 ? 0x7c00u : 0x7f80u;
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+                if ((v[d + r] & E) == E)
+                  o[i][r] += IN == GEMM_F16 ? (float)__builtin_bit_cast(_Float16, v[d + r])
+                                            : __uint_as_float((unsigned)v[d + r] << 16);
+            }
+          }
+          *reinterpret_cast<f32x4*>(a.part_o + at * a.dim + d) = o[i];
+        }
+      }
+    }
+    __syncthreads();  // before the next rows use ml, sl and pl
+  }
+}
+
+// The chunks of a row, joined in ascending order: a wave per query and head, two
+// dimensions a lane.
+template <int IN>
+__global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
+  const int lane = threadIdx.x & 63;
+  const int64_t at = (int64_t)blockIdx.x * 4 + threadIdx.x / 64;
+  if (at >= a.q_rows * a.q_heads) return;
+  const int64_t q = at / a.q_heads;
+  const int head = (int)(at - q * a.q_heads), kh = head / a.group;
+  const int seg = segment_of_row(a, q);
+  const Sequence s = segment(a, seg);
+  const int64_t t = q - s.q0;
+  const bool said = t < a.max_q || seg == 0 || seg > a.batch;  // (rows in no sequence have no keys)
+  const int64_t seen = keys_seen(a, s, t);
+  const int64_t row = t * a.group + (head - kh * a.group);
+  float M = kNegInf, L = 0.0f, O0 = 0.0f, O1 = 0.0f;
+  const bool mine = 2 * lane < a.dim;
+  if (said) {
+    const int64_t first = (s.slot0 * a.k_heads + kh) * a.part_rows + row;
+    const int64_t step = (int64_t)a.k_heads * a.part_rows;
+    const int chunks = (int)((seen + kAttnChunk - 1) / kAttnChunk);
+    constexpr int U = 8;
+    for (int c0 = 0; c0 < chunks; c0 += U) {
+      float2 ml[U], o[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t i = first + (c0 + u) * step;
+        ml[u] = float2{0, 0};
+        o[u] = float2{0, 0};
+        if (c0 + u < chunks) {
+          ml[u] = reinterpret_cast<const float2*>(a.part_ml)[i];
+          if (mine) o[u] = *reinterpret_cast<const float2*>(a.part_o + i * a.dim + 2 * lane);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (c0 + u < chunks) {
+          const Join j = join_chunk(M, ml[u].x);
+          M = j.m;
+          L = joined(L, ml[u].y, j);
+          O0 = joined(O0, o[u].x, j);
+          O1 = joined(O1, o[u].y, j);
+        }
+      }
+    }
+  } else {
+    L = O0 = O1 = __builtin_nanf("");  // a sequence longer than the call said
+  }
+  const bool empty = seen == 0 && said;
+  const float inv = empty ? 0.0f : 1.0f / L;
+  if (mine) {
+    const int y = pack2<IN>(O0 * inv, O1 * inv);
+    const int64_t to = (at * a.dim) / 2 + lane;
+    static_cast<int*>(a.o)[to] = y;
+    if (a.o_low) static_cast<int*>(a.o_low)[to] = pack2_rest<IN>(O0 * inv, O1 * inv, y);
+  }
+  if (a.lse && lane == 0) a.lse[at] = empty ? kNegInf : (M + __builtin_amdgcn_logf(L)) * kLn2;
+}
+
+template <int IN, int DP>
+hipError_t launch_in(const AttnArgs& a, hipStream_t s) {
+  if (a.part_o) {
+    if (a.chunks > 0)
+      hipLaunchKernelGGL((attention_few_kernel<IN, DP>), dim3((unsigned)(a.chunks * a.k_heads)),
+                         dim3(kFewThreads), 0, s, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(attention_join_kernel<IN>, dim3((unsigned)((a.q_rows * a.q_heads + 3) / 4)),
+                       dim3(256), 0, s, a);
+    return hipGetLastError();
+  }
+  const int64_t tiles = a.q_rows * a.group / kRows + a.batch + 2;
+  hipLaunchKernelGGL((attention_kernel<IN, DP>), dim3((unsigned)(tiles * a.k_heads)), dim3(kThreads), 0,
+                     s, a);
+  return hipGetLastError();
+}
+
+template <int IN>
+hipError_t launch_dim(const AttnArgs& a, hipStream_t s) {
+  if (a.dim <= 64) return launch_in<IN, 64>(a, s);
+  if (a.dim <= 96) return launch_in<IN, 96>(a, s);
+  return launch_in<IN, 128>(a, s);
+}
+
+}  // namespace
+
+bool attention_few_rows(int64_t max_q, int group) { return max_q * group <= kAttnFewRows; }
+int64_t attention_chunk_slots(int64_t k_rows, int batch) { return k_rows / kAttnChunk + batch; }
+
+hipError_t launch_attention(int in, const AttnArgs& a, hipStream_t s) {
+  return in == GEMM_F16 ? launch_dim<GEMM_F16>(a, s) : launch_dim<GEMM_BF16>(a, s);
+}
+
+}  // namespace imm

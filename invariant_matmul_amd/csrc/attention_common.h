@@ -1,0 +1,221 @@
+// Parts that the attention kernels share: sequences, tiles in LDS, matrix steps
+// and the softmax of a step.
+//
+// Layout.  The rows of a sequence that share a key head are one matrix: row
+// r = t group + h is query t of the sequence and query head h of the key
+// head's group.  All products run on the 16x16x32 step with the operand whose
+// index stays in a lane as the second one: S^T = K Q^T leaves a lane the logits of
+// one row (lane % 16) against keys 4 (lane / 16) + 0..3 of each block of 16, and
+// these are, as they lie, the second operand of O^T = V^T P^T: the step sums over
+// its 32 places in an order of its own, and its place 8 q + j stands for key
+// 4 q + j of the first block of 16 (j < 4) or key 4 q + j - 4 of the second.
+// The first operand, V^T, comes in the same order from a transposing LDS read.  So
+// no probability ever moves between lanes, and the sum of a row's
+// probabilities is a sum within four lanes.
+#pragma once
+
+#include "buffer_access.h"
+#include "decoder_internal.h"
+#include "kernel_common.h"
+
+namespace imm {
+namespace dev {
+
+constexpr int kTile = kAttnTile;
+constexpr float kNegInf = -__builtin_inff();
+constexpr float kLn2 = 0.693147180559945309417f;
+
+// A sequence of a call: its rows of q and its keys.  What the device's arrays say is
+// clamped to the operands, so that no contents of theirs reach outside.
+struct Sequence {
+  int64_t q0, k0;   // first query, first key row
+  int64_t n, m;     // queries, keys
+  int64_t slot0;    // its first chunk slot
+};
+
+__device__ __forceinline__ int64_t clamp64(int64_t v, int64_t lo, int64_t hi) {
+  return v < lo ? lo : v > hi ? hi : v;
+}
+// Segment i of the queries: 0 and batch + 1 are the rows before the first and
+// behind the last sequence (they have no keys).
+__device__ __forceinline__ int64_t q_start(const AttnArgs& a, int i) {
+  if (i <= 0) return 0;
+  if (!a.cu_q) return i == 1 ? 0 : a.q_rows;
+  return i > a.batch + 1 ? a.q_rows : clamp64(a.cu_q[i - 1], 0, a.q_rows);
+}
+__device__ __forceinline__ int64_t k_start(const AttnArgs& a, int b) {
+  if (!a.cu_k) return b == 0 ? 0 : a.k_rows;
+  return clamp64(a.cu_k[b], 0, a.k_rows);
+}
+__device__ __forceinline__ Sequence segment(const AttnArgs& a, int i) {
+  Sequence s{};
+  s.q0 = q_start(a, i);
+  const int64_t end = i == a.batch + 1 ? a.q_rows : q_start(a, i + 1);
+  s.n = end > s.q0 ? end - s.q0 : 0;
+  if (i >= 1 && i <= a.batch) {
+    s.k0 = k_start(a, i - 1);
+    const int64_t ke = k_start(a, i);
+    s.m = ke > s.k0 ? ke - s.k0 : 0;
+    if (a.k_lens) s.m = clamp64(a.k_lens[i - 1], 0, s.m);
+    s.slot0 = s.k0 / kAttnChunk + (i - 1);
+  }
+  return s;
+}
+// Tiles of `rows` packed rows: segment i begins at tile start(i) group / rows + i,
+// so that every segment has the tiles it needs and no sum over segments is taken.
+// The last segment that begins at or before tile t:
+__device__ __forceinline__ int segment_of_tile(const AttnArgs& a, int64_t t, int rows) {
+  int lo = 0, hi = a.batch + 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (q_start(a, mid) * a.group / rows + mid <= t) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+__device__ __forceinline__ int segment_of_row(const AttnArgs& a, int64_t row) {
+  int lo = 0, hi = a.batch + 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (q_start(a, mid) <= row) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// 16 bytes of a buffer; zeros past its end.
+__device__ __forceinline__ u32x4 load_b128(__amdgpu_buffer_rsrc_t buf, unsigned off) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(buf, off, 0, 0));
+#else
+  return u32x4{};
+#endif
+}
+
+// A tile of rows in LDS: 16-byte slot c of row r lies at slot c ^ (r % SLOTS).  The 16
+// rows of a fragment read are then on different banks.
+template <int DP>
+struct TileOf {
+  static constexpr int SLOTS = DP <= 64 ? 8 : 16;
+  static constexpr int PITCH = SLOTS * 16;
+  static constexpr int KS = DP / 32;   // steps over the dimension
+  static constexpr int DB = DP / 16;   // blocks of it
+  __device__ __forceinline__ static int at(int row, int slot) {
+    return row * PITCH + ((slot ^ (row & (SLOTS - 1))) * 16);
+  }
+};
+
+// Rows 16 b + lane % 16 of a tile, dimensions 32 ks + 8 (lane / 16) .. + 7.
+template <int DP>
+__device__ __forceinline__ i32x4 row_fragment(const char* tile, int b, int ks) {
+  const int l = threadIdx.x & 63;
+  return *reinterpret_cast<const i32x4*>(tile + TileOf<DP>::at(16 * b + l % 16, 4 * ks + l / 16));
+}
+
+// The transposed piece: dimension 16 db + lane % 16 of the rows 4 q + 0..3 of the
+// blocks 2 s and 2 s + 1 of 16 rows, q = lane / 16.
+template <int DP>
+__device__ __forceinline__ i32x4 column_fragment(const char* tile, int s, int db) {
+  i32x4 r{};
+#if defined(__HIP_DEVICE_COMPILE__)
+  typedef short v4i16 __attribute__((ext_vector_type(4)));
+  typedef __attribute__((address_space(3))) v4i16 lds_v4;
+  const int l = threadIdx.x & 63;
+  const int row = 32 * s + 4 * (l / 16) + (l % 16) / 4, c = l % 4;
+  const int at = TileOf<DP>::at(row, 2 * db + c / 2) + (c % 2) * 8;
+  const i32x2 lo = __builtin_bit_cast(i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4*)(tile + at)));
+  const i32x2 hi = __builtin_bit_cast(
+      i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4*)(tile + at + 16 * TileOf<DP>::PITCH)));
+  r = i32x4{lo[0], lo[1], hi[0], hi[1]};
+#endif
+  return r;
+}
+
+template <int IN>
+__device__ __forceinline__ int pack2(float a, float b) {
+  if constexpr (IN == GEMM_F16) {
+    typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(int, f16x2{(_Float16)a, (_Float16)b});
+  } else {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(int, bf16x2{(__bf16)a, (__bf16)b});
+  }
+}
+// What rounding to IN left of a pair, rounded to IN.
+template <int IN>
+__device__ __forceinline__ int pack2_rest(float a, float b, int rounded) {
+  if constexpr (IN == GEMM_F16) {
+    typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+    const f16x2 r = __builtin_bit_cast(f16x2, rounded);
+    return pack2<IN>(a - (float)r[0], b - (float)r[1]);
+  } else {
+    return pack2<IN>(a - __uint_as_float((unsigned)rounded << 16),
+                     b - __uint_as_float((unsigned)rounded & 0xffff0000u));
+  }
+}
+// Two blocks of 16 keys of one row set as the second operand of a step.
+template <int IN>
+__device__ __forceinline__ i32x4 pack_blocks(const f32x4& a, const f32x4& b) {
+  return i32x4{pack2<IN>(a[0], a[1]), pack2<IN>(a[2], a[3]), pack2<IN>(b[0], b[1]),
+               pack2<IN>(b[2], b[3])};
+}
+
+// Over the four lanes of a row.
+__device__ __forceinline__ float row_max(float v) {
+  v = fmaxf(v, __shfl_xor(v, 16));
+  return fmaxf(v, __shfl_xor(v, 32));
+}
+__device__ __forceinline__ float row_sum(float v) {
+  v += __shfl_xor(v, 16);
+  return v + __shfl_xor(v, 32);
+}
+
+// The largest of a step's logits of a row, in its own lane.  (A NaN is left out here and
+// shows in the probabilities.)
+__device__ __forceinline__ float lane_max(const f32x4 (&s)[4]) {
+  float m = kNegInf;
+#pragma unroll
+  for (int b = 0; b < 4; ++b)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) m = fmaxf(m, s[b][r]);
+  return m;
+}
+// What a running maximum that grew from a to b leaves of earlier sums.
+__device__ __forceinline__ float shrink(float a, float b) {
+  return a == b ? 1.0f : __builtin_amdgcn_exp2f(a - b);
+}
+// Probabilities about the maximum m (scaled; of a row without any, 0), in place;
+// their sum in the lane.
+__device__ __forceinline__ float probabilities(f32x4 (&s)[4], float scale_log2, float m) {
+  const float about = m == kNegInf ? 0.0f : m;
+  float sum = 0.0f;
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) s[b][r] = __builtin_amdgcn_exp2f(fmaf(s[b][r], scale_log2, -about));
+    sum += (s[b][0] + s[b][1]) + (s[b][2] + s[b][3]);
+  }
+  return sum;
+}
+
+// The result of the keys so far and that of one more chunk:
+// o = o a + chunk_o b, l = l a + chunk_l b.
+struct Join {
+  float m, a, b;
+};
+__device__ __forceinline__ Join join_chunk(float m, float chunk_m) {
+  const float to = fmaxf(m, chunk_m);
+  return Join{to, shrink(m, to), shrink(chunk_m, to)};
+}
+__device__ __forceinline__ float joined(float o, float chunk_o, const Join& j) {
+  return fmaf(chunk_o, j.b, o * j.a);
+}
+
+// Keys that query t of a sequence sees: [0, seen).
+__device__ __forceinline__ int64_t keys_seen(const AttnArgs& a, const Sequence& s, int64_t t) {
+  if (t >= s.n) return 0;
+  return a.causal ? clamp64(s.m - s.n + t + 1, 0, s.m) : s.m;
+}
+
+}  // namespace dev
+}  // namespace imm

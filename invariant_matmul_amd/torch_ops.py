@@ -54,6 +54,16 @@ forward mode: all refuse dual tensors.
     y = torch_ops.linear_f8(q, s, wq, ws)              # fp8 rows and their scales
     w4 = torch_ops.pack_w4(q4, scales, zeros)          # once
     y = torch_ops.linear_w4(x, w4, bias)               # 4-bit weights
+
+So do the operators between and behind a decoder's products, which take part in
+autograd like rms_norm:
+
+    q, k = torch_ops.qk_norm_rope(q, k, positions, inv_freq, wq, wk)  # heads: norm, rotation
+    o = torch_ops.attention(q, k, v, cu_q, cu_k)       # packed sequences, or new tokens over a cache
+    logprob, entropy = torch_ops.token_logprobs(logits, tokens)
+
+A row of attention has the same bits whether its prompt is taken at once, in pieces or token by
+token, and whatever else shares the call.
 """
 from __future__ import annotations
 
@@ -61,18 +71,23 @@ import contextlib
 import functools
 import math
 import threading
+import typing
 import warnings
 
 import torch
 from torch.autograd import forward_ad
 
 from . import (PLAN_B_TRANSPOSED, PLAN_FP8_FP32_ACCUM, PLAN_TILE_BY_M, GemmError, _dtype_code,
-               gemm_plan_ex2, gemm_run, gemm_splitk_run, gemm_workspace_size, lib, ozaki_plan,
-               ozaki_run, ozaki_workspace_size, rms_norm_plan, w4_packed_size, w4_plan)
+               attention_plan, gemm_plan_ex2, gemm_run, gemm_splitk_run, gemm_workspace_size,
+               head_rope_plan, lib, logprobs_plan, ozaki_plan, ozaki_run, ozaki_workspace_size,
+               rms_norm_plan, w4_packed_size, w4_plan)
 
 __all__ = ["mm", "addmm", "linear", "matmul", "batch_invariant_mode", "supported",
            "rms_norm", "rms_norm_forward", "rms_norm_backward", "rms_norm_quant", "quantize_rows",
-           "linear_f8", "W4Weight", "pack_w4", "linear_w4"]
+           "linear_f8", "W4Weight", "pack_w4", "linear_w4",
+           "qk_norm_rope", "qk_norm_rope_backward", "attention", "AttentionSaved", "attention_forward",
+           "attention_backward", "token_logprobs", "token_logprobs_forward",
+           "token_logprobs_backward"]
 
 _DT = {torch.float16: "f16", torch.bfloat16: "bf16"}
 
@@ -596,6 +611,438 @@ def linear_w4(x: torch.Tensor, weight: W4Weight, bias=None) -> torch.Tensor:
         _done(lib().w4_run(plan.handle, x.data_ptr(), weight.packed.data_ptr(), _ptr(bias),
                            y.data_ptr(), _ptr(ws), nws, stream), where)
     return y
+
+
+# ---- Between and behind the products of a decoder -----------------------------------
+
+@functools.lru_cache(maxsize=512)
+def _rope_plan(tokens, q_heads, k_heads, dim, rot, dtype, norm, eps, interleaved, sections):
+    return head_rope_plan(tokens, q_heads, k_heads, dim, rot, dtype, norm, eps, interleaved, sections)
+
+
+@functools.lru_cache(maxsize=512)
+def _attention_plan(q_rows, k_rows, batch, q_heads, k_heads, dim, dtype, causal, scale, max_q):
+    return attention_plan(q_rows, k_rows, batch, q_heads, k_heads, dim, dtype, causal, scale, max_q)
+
+
+@functools.lru_cache(maxsize=512)
+def _logprobs_plan(rows, vocab, dtype, n, top):
+    return logprobs_plan(rows, vocab, dtype, n, top)
+
+
+_MOST_STRIDE = 1 << 21  # elements between tokens that the kernels take (256 of them within 31 bits)
+
+
+def _in_place(t: torch.Tensor):
+    """(t, token stride, head stride) of heads [tokens, heads, dim] as the kernels read
+    them: t itself if its heads are contiguous and in 16-byte steps, else a copy."""
+    a, b, c = t.stride()
+    if c == 1 and a % 8 == 0 and b % 8 == 0 and 0 <= a <= _MOST_STRIDE and t.data_ptr() % 16 == 0:
+        return t, a, b
+    t = t.contiguous()
+    if t.data_ptr() % 16:
+        t = t.clone()
+    return t, t.shape[1] * t.shape[2], t.shape[2]
+
+
+def _needs_grad(*tensors) -> bool:
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+
+
+def _check_rope(where, q, k, positions, inv_freq, q_weight, k_weight, norm, sections):
+    """(device, tokens, dim, plan-ready sections)"""
+    dtype, device = q.dtype, q.device
+    if not (q.is_cuda and dtype in _DT and q.dim() == 3 and k.dim() == 3 and k.dtype == dtype
+            and k.device == device and k.shape[0] == q.shape[0] and k.shape[2] == q.shape[2]
+            and q.shape[2] > 0 and q.shape[2] % 8 == 0):
+        raise ValueError(f"{where}: needs fp16/bf16 CUDA tensors q [T, q_heads, D] and k [T, k_heads, D] of one "
+                         f"type, D a multiple of 8; got {tuple(q.shape)} {q.dtype} on {q.device} and "
+                         f"{tuple(k.shape)} {k.dtype} on {k.device}")
+    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or inv_freq.device != device:
+        raise ValueError(f"{where}: inv_freq must be a float64 vector on {device}")
+    if sections is not None:
+        sections = tuple(int(n) for n in sections)
+        if not sections or min(sections) < 0 or sum(sections) != inv_freq.shape[0]:
+            raise ValueError(f"{where}: sections {sections} must add up to the {inv_freq.shape[0]} frequencies")
+    want = (q.shape[0],) if sections is None else (len(sections), q.shape[0])
+    if positions.dtype != torch.int64 or positions.shape != want or positions.device != device:
+        raise ValueError(f"{where}: positions must be int64 {want} on {device}, got {positions.dtype} "
+                         f"{tuple(positions.shape)} on {positions.device}")
+    for w in (q_weight, k_weight):
+        if w is not None and (not norm or w.dtype != dtype or w.device != device or w.shape != q.shape[2:]):
+            raise ValueError(f"{where}: a weight must hold {q.shape[2]} values of {dtype} on {device} (and needs "
+                             "norm=True)")
+    return sections
+
+
+def _rope_forward(where, q, k, positions, inv_freq, q_weight, k_weight, eps, norm, interleaved, sections):
+    device = q.device
+    stream = _stream_of(where, device)
+    T, hq, D = q.shape
+    hk = k.shape[1]
+    plan = _rope_plan(T, hq, hk, D, 2 * inv_freq.shape[0], q.dtype, norm, eps if norm else 0.0, interleaved,
+                      sections)
+    q, q_token, q_head = _in_place(q)
+    k, k_token, k_head = _in_place(k)
+    positions, inv_freq = positions.contiguous(), inv_freq.contiguous()
+    if q_weight is not None:
+        q_weight = _dense(q_weight)
+    if k_weight is not None:
+        k_weight = _dense(k_weight)
+    q_out = torch.empty(T, hq, D, dtype=q.dtype, device=device)
+    k_out = torch.empty(T, hk, D, dtype=q.dtype, device=device)
+    _done(lib().head_rope_run(plan.handle, q.data_ptr(), q_token, q_head, k.data_ptr(), k_token, k_head,
+                              positions.data_ptr(), inv_freq.data_ptr(), _ptr(q_weight), _ptr(k_weight),
+                              q_out.data_ptr(), k_out.data_ptr(), stream), where)
+    return q_out, k_out
+
+
+def qk_norm_rope_backward(dq_out, dk_out, q, k, positions, inv_freq, q_weight=None, k_weight=None,
+                          eps: float = 1e-6, *, norm: bool = True, interleaved: bool = False, sections=None,
+                          weight_grads: bool = True):
+    """(dq, dk, dq_weight, dk_weight) of qk_norm_rope from the gradients of its results and
+    its arguments.  A weight's gradient is None without that weight or with
+    weight_grads=False."""
+    where = "qk_norm_rope_backward"
+    sections = _check_rope(where, q, k, positions, inv_freq, q_weight, k_weight, norm, sections)
+    for d, t in ((dq_out, q), (dk_out, k)):
+        if d.shape != t.shape or d.dtype != t.dtype or d.device != t.device:
+            raise ValueError(f"{where}: the gradients must have the shapes, type and device of q and k")
+    _refuse_tangent(where, dq_out, dk_out, q, k, inv_freq, q_weight, k_weight)
+    device = q.device
+    stream = _stream_of(where, device)
+    T, hq, D = q.shape
+    hk = k.shape[1]
+    plan = _rope_plan(T, hq, hk, D, 2 * inv_freq.shape[0], q.dtype, norm, eps if norm else 0.0, interleaved,
+                      sections)
+    q, q_token, q_head = _in_place(q)
+    k, k_token, k_head = _in_place(k)
+    positions, inv_freq = positions.contiguous(), inv_freq.contiguous()
+    dq_out, dk_out = _dense(dq_out), _dense(dk_out)
+    dq = torch.empty(T, hq, D, dtype=q.dtype, device=device)
+    dk = torch.empty(T, hk, D, dtype=q.dtype, device=device)
+    dws, ws, nws = [None, None], None, 0
+    if weight_grads and (q_weight is not None or k_weight is not None):
+        dws = [torch.empty(D, dtype=q.dtype, device=device) if w is not None else None for w in (q_weight, k_weight)]
+        nws = plan.workspace_bytes
+        ws = torch.empty(nws, dtype=torch.uint8, device=device)
+    if q_weight is not None:
+        q_weight = _dense(q_weight)
+    if k_weight is not None:
+        k_weight = _dense(k_weight)
+    _done(lib().head_rope_backward(plan.handle, dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), q_token, q_head,
+                                   k.data_ptr(), k_token, k_head, positions.data_ptr(), inv_freq.data_ptr(),
+                                   _ptr(q_weight), _ptr(k_weight), dq.data_ptr(), dk.data_ptr(), _ptr(dws[0]),
+                                   _ptr(dws[1]), _ptr(ws), nws, stream), where)
+    return dq, dk, dws[0], dws[1]
+
+
+class _QkNormRope(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, q_weight, k_weight, positions, inv_freq, eps, norm, interleaved, sections):
+        ctx.save_for_backward(q, k, q_weight, k_weight, positions, inv_freq)
+        ctx.options = (eps, norm, interleaved, sections)
+        return _rope_forward("qk_norm_rope", q, k, positions, inv_freq, q_weight, k_weight, eps, norm, interleaved,
+                             sections)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dq_out, dk_out):
+        q, k, q_weight, k_weight, positions, inv_freq = ctx.saved_tensors
+        eps, norm, interleaved, sections = ctx.options
+        need = ctx.needs_input_grad
+        grads = qk_norm_rope_backward(dq_out, dk_out, q, k, positions, inv_freq, q_weight, k_weight, eps, norm=norm,
+                                      interleaved=interleaved, sections=sections, weight_grads=need[2] or need[3])
+        return (*(g if n else None for g, n in zip(grads, need)), None, None, None, None, None, None)
+
+
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, q_weight=None,
+                 k_weight=None, eps: float = 1e-6, *, norm: bool = True, interleaved: bool = False, sections=None):
+    """(q', k'): the root-mean-square norm of every head of q [T, q_heads, D] and
+    k [T, k_heads, D] (weights [D] or None for ones; norm=False leaves it out), and the
+    rotation of its first 2 len(inv_freq) elements by the token's position.
+
+    positions: int64 [T]; inv_freq: float64 [R / 2], R a multiple of 16 up to D, the angle per
+    position (base ** (-2 i / R), or scaled); pairs are (i, i + R / 2), or (2 i, 2 i + 1)
+    with interleaved=True.  Several axes (time, height and width of images and video):
+    sections gives the number of frequencies of each (up to 4), positions is [axes, T].
+    Angles are fp64 until they lose their whole turns.  q and k are fp16 or bf16, D a
+    multiple of 8 up to 512; they may be views into a fused projection's output.  One launch, new
+    tensors.  Differentiable once in reverse mode with respect to q, k and weights."""
+    where = "qk_norm_rope"
+    sections = _check_rope(where, q, k, positions, inv_freq, q_weight, k_weight, norm, sections)
+    _refuse_tangent(where, q, k, inv_freq, q_weight, k_weight)
+    if _needs_grad(inv_freq):
+        raise ValueError(f"{where} has no gradient of inv_freq: call it with a detached tensor")
+    if _needs_grad(q, k, q_weight, k_weight):
+        return _QkNormRope.apply(q, k, q_weight, k_weight, positions, inv_freq, eps, norm, interleaved, sections)
+    return _rope_forward(where, q, k, positions, inv_freq, q_weight, k_weight, eps, norm, interleaved, sections)
+
+
+def _check_attention(where, q, k, v, cu_q, cu_k, k_lens):
+    """(cu_k, batch)"""
+    dtype, device = q.dtype, q.device
+    if not (q.is_cuda and dtype in _DT and q.dim() == 3 and k.dim() == 3 and v.shape == k.shape
+            and k.dtype == v.dtype == dtype and k.device == v.device == device and k.shape[2] == q.shape[2]
+            and 0 < q.shape[2] <= 128 and q.shape[2] % 8 == 0 and k.shape[1] > 0 and q.shape[1] > 0
+            and q.shape[1] % k.shape[1] == 0):
+        raise ValueError(f"{where}: needs fp16/bf16 CUDA tensors of one type, q [Tq, q_heads, D], k and v [Tk, k_heads, "
+                         f"D], D a multiple of 8 up to 128 and q_heads a multiple of k_heads; got {tuple(q.shape)} "
+                         f"{q.dtype} on {q.device}, {tuple(k.shape)} {k.dtype} on {k.device} and {tuple(v.shape)} "
+                         f"{v.dtype} on {v.device}")
+    if cu_q is None:
+        if cu_k is not None:
+            raise ValueError(f"{where}: cu_k needs cu_q")
+        batch = 1
+    else:
+        cu_k = cu_q if cu_k is None else cu_k
+        batch = cu_q.numel() - 1
+        for t in (cu_q, cu_k):
+            if t.dtype != torch.int32 or t.shape != (batch + 1,) or batch < 1 or t.device != device:
+                raise ValueError(f"{where}: cu_q and cu_k must be int32 vectors of sequences + 1 values on {device}")
+    if k_lens is not None and (k_lens.dtype != torch.int32 or k_lens.shape != (batch,) or k_lens.device != device):
+        raise ValueError(f"{where}: k_lens must be int32 ({batch},) on {device}")
+    return cu_k, batch
+
+
+class AttentionSaved(typing.NamedTuple):
+    """What attention's backward pass takes beside its inputs and result."""
+    lse: torch.Tensor    # ln sum_j e^(scale q k_j) of every query and head, fp32 [Tq, q_heads]
+    o_low: torch.Tensor  # what the rounding of o left, rounded to the type
+
+
+def _attention(where, q, k, v, cu_q, cu_k, batch, k_lens, max_q, causal, scale, save):
+    device = q.device
+    stream = _stream_of(where, device)
+    Tq, hq, D = q.shape
+    Tk, hk, _ = k.shape
+    plan = _attention_plan(Tq, Tk, batch, hq, hk, D, q.dtype, causal, scale, max_q or 0)
+    q, q_token, q_head = _in_place(q)
+    k, k_token, k_head = _in_place(k)
+    v, v_token, v_head = _in_place(v)
+    if cu_q is not None:
+        cu_q, cu_k = cu_q.contiguous(), cu_k.contiguous()
+    if k_lens is not None:
+        k_lens = k_lens.contiguous()
+    o = torch.empty(Tq, hq, D, dtype=q.dtype, device=device)
+    lse = o_low = None
+    if save:
+        lse, o_low = torch.empty(Tq, hq, dtype=torch.float32, device=device), torch.empty_like(o)
+    nws = plan.workspace_bytes
+    ws = torch.empty(nws, dtype=torch.uint8, device=device) if nws else None
+    _done(lib().attention_run(plan.handle, q.data_ptr(), q_token, q_head, k.data_ptr(), k_token, k_head, v.data_ptr(),
+                              v_token, v_head, _ptr(cu_q), _ptr(cu_k), _ptr(k_lens), o.data_ptr(), _ptr(o_low),
+                              _ptr(lse), _ptr(ws), nws, stream), where)
+    return o, AttentionSaved(lse, o_low)
+
+
+def attention_forward(q, k, v, cu_q=None, cu_k=None, *, k_lens=None, max_q=None, causal: bool = True, scale=None):
+    """(o, saved): attention's result and what attention_backward takes: saved.lse, ln
+    sum_j e^(scale q k_j) of every query and head, fp32 [Tq, q_heads], and saved.o_low, what
+    the rounding of o left.  No autograd: attention is the differentiable form."""
+    where = "attention_forward"
+    cu_k, batch = _check_attention(where, q, k, v, cu_q, cu_k, k_lens)
+    _refuse_tangent(where, q, k, v)
+    return _attention(where, q, k, v, cu_q, cu_k, batch, k_lens, max_q, causal, scale, True)
+
+
+def attention_backward(do, q, k, v, o, saved, cu_q=None, cu_k=None, *, k_lens=None, causal: bool = True, scale=None):
+    """(dq, dk, dv) of attention from the gradient of o and what attention_forward took
+    and gave (o, saved).  Keys past k_lens and rows in no sequence have zero gradients."""
+    where = "attention_backward"
+    cu_k, batch = _check_attention(where, q, k, v, cu_q, cu_k, k_lens)
+    lse, o_low = saved
+    for t in (do, o, o_low):
+        if t.shape != q.shape or t.dtype != q.dtype or t.device != q.device:
+            raise ValueError(f"{where}: o, its gradient and o_low must have the shape, type and device of q")
+    if lse.dtype != torch.float32 or lse.shape != q.shape[:2] or lse.device != q.device:
+        raise ValueError(f"{where}: lse must be float32 {tuple(q.shape[:2])} on {q.device}")
+    _refuse_tangent(where, do, q, k, v, o, lse, o_low)
+    device = q.device
+    stream = _stream_of(where, device)
+    Tq, hq, D = q.shape
+    Tk, hk, _ = k.shape
+    plan = _attention_plan(Tq, Tk, batch, hq, hk, D, q.dtype, causal, scale, 0)
+    q, q_token, q_head = _in_place(q)
+    k, k_token, k_head = _in_place(k)
+    v, v_token, v_head = _in_place(v)
+    do, o, o_low, lse = _dense(do), _dense(o), _dense(o_low), lse.contiguous()
+    if cu_q is not None:
+        cu_q, cu_k = cu_q.contiguous(), cu_k.contiguous()
+    if k_lens is not None:
+        k_lens = k_lens.contiguous()
+    dq = torch.empty(Tq, hq, D, dtype=q.dtype, device=device)
+    dk = torch.empty(Tk, hk, D, dtype=q.dtype, device=device)
+    dv = torch.empty(Tk, hk, D, dtype=q.dtype, device=device)
+    nws = plan.backward_workspace_bytes
+    ws = torch.empty(nws, dtype=torch.uint8, device=device) if nws else None
+    _done(lib().attention_backward(plan.handle, do.data_ptr(), q.data_ptr(), q_token, q_head, k.data_ptr(), k_token,
+                                   k_head, v.data_ptr(), v_token, v_head, o.data_ptr(), o_low.data_ptr(),
+                                   lse.data_ptr(), _ptr(cu_q), _ptr(cu_k), _ptr(k_lens), dq.data_ptr(), dk.data_ptr(),
+                                   dv.data_ptr(), _ptr(ws), nws, stream), where)
+    return dq, dk, dv
+
+
+class _Attention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, cu_q, cu_k, batch, k_lens, max_q, causal, scale):
+        o, saved = _attention("attention", q, k, v, cu_q, cu_k, batch, k_lens, max_q, causal, scale, True)
+        ctx.save_for_backward(q, k, v, o, *saved, cu_q, cu_k, k_lens)
+        ctx.options = (causal, scale)
+        return o
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, do):
+        q, k, v, o, lse, o_low, cu_q, cu_k, k_lens = ctx.saved_tensors
+        causal, scale = ctx.options
+        grads = attention_backward(do, q, k, v, o, AttentionSaved(lse, o_low), cu_q, cu_k, k_lens=k_lens, causal=causal, scale=scale)
+        return (*(g if n else None for g, n in zip(grads, ctx.needs_input_grad)),) + (None,) * 7
+
+
+def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q=None, cu_k=None, *, k_lens=None, max_q=None,
+              causal: bool = True, scale=None) -> torch.Tensor:
+    """Attention of packed sequences, o [Tq, q_heads, D] from q [Tq, q_heads, D], k and v
+    [Tk, k_heads, D] (fp16 or bf16, D a multiple of 8 up to 128, views allowed; query head h
+    uses key head h // (q_heads // k_heads)); scale is D ** -0.5 by default.
+
+    cu_q, cu_k: int32 [B + 1] on the device, where sequence b's queries and keys begin
+    (cu_k is cu_q by default; without both there is one sequence); k_lens: int32 [B], how many keys
+    of its part of k and v a sequence has (a cache with room).  With causal=True
+    query i of n sees the keys j <= m - n + i: the last query sees all.  A query
+    without keys, and a row of q in no sequence, is zero.
+    max_q: no sequence has more queries; a decode step says 1 (or the number of drafted
+    tokens), which selects the kernel that cuts long caches into parts.
+
+    The bits of a row depend on its query and the keys and values it sees alone: a prompt
+    taken at once, in pieces over a cache or token by token gives the same, whatever else shares
+    the call.  Differentiable once in reverse mode."""
+    where = "attention"
+    cu_k, batch = _check_attention(where, q, k, v, cu_q, cu_k, k_lens)
+    _refuse_tangent(where, q, k, v)
+    if _needs_grad(q, k, v):
+        return _Attention.apply(q, k, v, cu_q, cu_k, batch, k_lens, max_q, causal, scale)
+    return _attention(where, q, k, v, cu_q, cu_k, batch, k_lens, max_q, causal, scale, False)[0]
+
+
+_LOGITS = (torch.float32, torch.float16, torch.bfloat16)
+
+
+def _check_logits(where, logits, tokens):
+    """(rows, vocabulary, tokens of a row)"""
+    if not (logits.is_cuda and logits.dtype in _LOGITS and logits.dim() >= 1 and logits.shape[-1] > 0):
+        raise ValueError(f"{where}: needs fp32/fp16/bf16 CUDA logits [..., V], got {tuple(logits.shape)} {logits.dtype} "
+                         f"on {logits.device}")
+    lead = logits.shape[:-1]
+    if tokens.dtype != torch.int64 or tokens.device != logits.device or not (
+            tokens.shape == lead or tokens.shape[:-1] == lead and tokens.dim() == logits.dim()):
+        raise ValueError(f"{where}: tokens must be int64 {tuple(lead)} or {tuple(lead)} + (n,) on {logits.device}, got "
+                         f"{tokens.dtype} {tuple(tokens.shape)} on {tokens.device}")
+    return math.prod(lead), logits.shape[-1], 1 if tokens.shape == lead else tokens.shape[-1]
+
+
+def _rows_of(logits: torch.Tensor):
+    """(logits or a copy, row stride) with contiguous rows a stride apart."""
+    V = logits.shape[-1]
+    if logits.dim() == 2 and (logits.stride(1) == 1 or V == 1) and logits.stride(0) >= 0:
+        return logits, logits.stride(0)
+    return logits.contiguous(), V
+
+
+def _token_logprobs(where, logits, tokens, top, want_norm):
+    rows, V, n = _check_logits(where, logits, tokens)
+    if not isinstance(top, int) or top < 0 or top > min(64, V):
+        raise ValueError(f"{where}: top must be an integer from 0 to min(64, V), got {top}")
+    device, lead = logits.device, logits.shape[:-1]
+    stream = _stream_of(where, device)
+    plan = _logprobs_plan(rows, V, logits.dtype, n, top)
+    logits, stride = _rows_of(logits)
+    tokens = tokens.contiguous()
+    f32 = torch.float32
+    lp = torch.empty(tokens.shape, dtype=f32, device=device)
+    ent = torch.empty(lead, dtype=f32, device=device)
+    norm = torch.empty(*lead, 2, dtype=f32, device=device) if want_norm else None
+    top_lp = top_tok = None
+    if top:
+        top_lp = torch.empty(*lead, top, dtype=f32, device=device)
+        top_tok = torch.empty(*lead, top, dtype=torch.int64, device=device)
+    nws = plan.workspace_bytes
+    ws = torch.empty(nws, dtype=torch.uint8, device=device) if nws else None
+    _done(lib().logprobs_run(plan.handle, logits.data_ptr(), stride, tokens.data_ptr(), lp.data_ptr(), ent.data_ptr(),
+                             _ptr(norm), _ptr(top_lp), _ptr(top_tok), _ptr(ws), nws, stream), where)
+    return lp, ent, norm, top_lp, top_tok
+
+
+def token_logprobs_forward(logits, tokens):
+    """(logprob, entropy, norm): norm [..., 2] holds the largest logit of each row and
+    ln sum e^(logit - largest), which token_logprobs_backward takes.  No autograd:
+    token_logprobs is the differentiable form."""
+    where = "token_logprobs_forward"
+    _refuse_tangent(where, logits)
+    return _token_logprobs(where, logits, tokens, 0, True)[:3]
+
+
+def token_logprobs_backward(dlogprob, dentropy, logits, tokens, norm, entropy):
+    """The gradient of the logits, contiguous, in their type, from those of logprob and entropy
+    (fp32; either may be None) and what token_logprobs_forward took and gave."""
+    where = "token_logprobs_backward"
+    rows, V, n = _check_logits(where, logits, tokens)
+    device, lead = logits.device, logits.shape[:-1]
+    for t, shape in ((dlogprob, tokens.shape), (dentropy, lead), (norm, (*lead, 2)), (entropy, lead)):
+        if t is not None and (t.dtype != torch.float32 or t.shape != shape or t.device != device):
+            raise ValueError(f"{where}: dlogprob, dentropy, norm and entropy must be float32 of the shapes that "
+                             f"token_logprobs_forward gives on {device}; got {t.dtype} {tuple(t.shape)} on {t.device}")
+    _refuse_tangent(where, dlogprob, dentropy, logits, norm, entropy)
+    stream = _stream_of(where, device)
+    plan = _logprobs_plan(rows, V, logits.dtype, n, 0)
+    logits, stride = _rows_of(logits)
+    tokens, norm, entropy = tokens.contiguous(), norm.contiguous(), entropy.contiguous()
+    if dlogprob is not None:
+        dlogprob = dlogprob.contiguous()
+    if dentropy is not None:
+        dentropy = dentropy.contiguous()
+    dx = torch.empty(*lead, V, dtype=logits.dtype, device=device)
+    _done(lib().logprobs_backward(plan.handle, _ptr(dlogprob), _ptr(dentropy), logits.data_ptr(), stride,
+                                  tokens.data_ptr(), norm.data_ptr(), entropy.data_ptr(), dx.data_ptr(), stream), where)
+    return dx
+
+
+class _TokenLogprobs(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, tokens, top):
+        lp, ent, norm, top_lp, top_tok = _token_logprobs("token_logprobs", logits, tokens, top, True)
+        ctx.save_for_backward(logits, tokens, norm, ent)
+        ctx.set_materialize_grads(False)
+        if not top:
+            return lp, ent
+        ctx.mark_non_differentiable(top_lp, top_tok)
+        return lp, ent, top_lp, top_tok
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dlogprob, dentropy, *_):
+        logits, tokens, norm, ent = ctx.saved_tensors
+        if dlogprob is None and dentropy is None:
+            return None, None, None
+        return token_logprobs_backward(dlogprob, dentropy, logits, tokens, norm, ent), None, None
+
+
+def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, top: int = 0):
+    """(logprob, entropy): the log probability of each given token and the entropy of each row
+    of logits [..., V] (fp32, fp16 or bf16), both fp32; tokens is int64 [...] or [..., n].
+    With top > 0 (at most 64) (logprob, entropy, top_logprob, top_token): the top most likely tokens of
+    each row, [..., top], the most likely first, the lower token first among equals (no
+    gradient flows through these).
+
+    A token below 0 is padding (logprob 0, no gradient), one from V on gives NaN.  A logit
+    of -infinity has probability 0.  The logits are read once; rows may be strided.
+    Row i of the results depends on row i alone.  Differentiable once in reverse mode."""
+    where = "token_logprobs"
+    _refuse_tangent(where, logits)
+    if _needs_grad(logits):
+        return _TokenLogprobs.apply(logits, tokens, top)
+    lp, ent, _, top_lp, top_tok = _token_logprobs(where, logits, tokens, top, False)
+    return (lp, ent, top_lp, top_tok) if top else (lp, ent)
 
 
 _mode_lock = threading.Lock()
