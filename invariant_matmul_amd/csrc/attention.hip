@@ -22,36 +22,35 @@ using namespace dev;
 
 // ---- Many rows -----------------------------------------------------------------
 // A workgroup takes 256 rows of a key head, 32 a wave, and walks through their keys
-// 64 at a time: the next step's keys and values travel through registers into the
-// other half of a two-stage LDS buffer while this one's are used.
+// 64 at a time: the next step's keys and values go by DMA into the other half of a
+// two-stage LDS buffer while this one's are used.
 constexpr int kWaves = 8, kThreads = 64 * kWaves;
 constexpr int kRows = 32 * kWaves;
 
-// Slot i of a tile that this thread moves (row, slot of the row).
+// Moves a tile of keys or values to LDS; what lies past its `left` rows or past the
+// dimension is zeros.  A wave fills 1 KB at a time, lane l the 16 bytes at 16 l: each
+// lane fetches what belongs in its fixed slot.
 template <int DP>
 struct Mover {
   static constexpr int N = kTile * TileOf<DP>::SLOTS / kThreads;
-  u32x4 k[N], v[N];
-  __device__ __forceinline__ static int row(int i) { return (threadIdx.x + i * kThreads) / TileOf<DP>::SLOTS; }
-  __device__ __forceinline__ static int slot(int i) { return threadIdx.x % TileOf<DP>::SLOTS; }
-  // rows from `left` on are zeros
-  __device__ __forceinline__ void load(const char* kt, const char* vt, int64_t k_bytes, int64_t v_bytes,
-                                       int left, int dim) {
-    const auto kb = buffer_at(kt), vb = buffer_at(vt);
+  unsigned off[N];  // from the tile's first row
+  __device__ __forceinline__ Mover(int64_t row_bytes, int dim) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const bool ok = row(i) < left && slot(i) * 8 < dim;
-      k[i] = load_b128(kb, ok ? (unsigned)(row(i) * (int)k_bytes + slot(i) * 16) : OOB);
-      v[i] = load_b128(vb, ok ? (unsigned)(row(i) * (int)v_bytes + slot(i) * 16) : OOB);
+      const int at = threadIdx.x + i * kThreads;
+      const int row = at / TileOf<DP>::SLOTS;
+      const int slot = (at % TileOf<DP>::SLOTS) ^ (row & (TileOf<DP>::SLOTS - 1));
+      off[i] = slot * 8 < dim ? (unsigned)(row * (int)row_bytes + slot * 16) : OOB;
     }
   }
-  __device__ __forceinline__ void store(char* kt, char* vt) const {
+  __device__ __forceinline__ void move(const char* from, char* to, int64_t left, int64_t row_bytes, int dim) const {
+    // (rows behind the last: past the buffer's end, or, where rows overlap, values that no row sees)
+    const int rows = (int)(left < kTile ? left : kTile);
+    const auto buf = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(from), 0,
+                                                       (rows - 1) * (int)row_bytes + 2 * dim, 0x00020000);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int at = TileOf<DP>::at(row(i), slot(i));
-      *reinterpret_cast<u32x4*>(kt + at) = k[i];
-      *reinterpret_cast<u32x4*>(vt + at) = v[i];
-    }
+    for (int i = 0; i < N; ++i)
+      dma16(buf, to + (__builtin_amdgcn_readfirstlane(threadIdx.x & ~63) + i * kThreads) * 16, off[i], 0);
   }
 };
 
@@ -60,11 +59,141 @@ __device__ __forceinline__ bool not_finite(unsigned two) {
   constexpr unsigned E = IN == GEMM_F16 ? 0x7c00u : 0x7f80u;
   return (two & E) == E || (two & (E << 16)) == (E << 16);
 }
+// ... and zeros in the place of values that are not finite.
+template <int IN>
+__device__ __forceinline__ u32x4 only_finite(u32x4 v) {
+  constexpr unsigned E = IN == GEMM_F16 ? 0x7c00u : 0x7f80u;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if ((v[e] & E) == E) v[e] &= 0xffff0000u;
+    if ((v[e] & (E << 16)) == (E << 16)) v[e] &= 0xffffu;
+  }
+  return v;
+}
+
+// The rows of a wave through one step.
+template <int IN, int DP>
+struct WaveRows {
+  using T = TileOf<DP>;
+  i32x4 q[2][T::KS];
+  f32x4 O[2][T::DB], o[2][T::DB];  // of the chunks so far, of this chunk
+  float M[2], L[2], m[2], l[2];
+  int seen[2];                     // keys of this lane's rows
+  Lanes<DP> at;
+  float scale_log2;
+
+  __device__ __forceinline__ void clear_all() {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      M[i] = kNegInf;
+      L[i] = 0.0f;
+#pragma unroll
+      for (int d = 0; d < T::DB; ++d) O[i][d] = f32x4{};
+    }
+  }
+  __device__ __forceinline__ void clear_chunk() {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      m[i] = kNegInf;
+      l[i] = 0.0f;
+#pragma unroll
+      for (int d = 0; d < T::DB; ++d) o[i][d] = f32x4{};
+    }
+  }
+  // masked: some row of the wave does not see all of the step's keys
+  __device__ __forceinline__ void step(const char* kt, const char* vt, int k0, bool masked) {
+    const int quad = (threadIdx.x & 63) / 16;
+    at.again();
+    f32x4 sc[2][4];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      sc[0][b] = sc[1][b] = f32x4{};
+#pragma unroll
+      for (int ks = 0; ks < T::KS; ++ks) {
+        const i32x4 kf = row_fragment<DP>(kt, at, b, ks);
+        sc[0][b] = mfma16_v<IN>(kf, q[0][ks], sc[0][b]);
+        sc[1][b] = mfma16_v<IN>(kf, q[1][ks], sc[1][b]);
+      }
+    }
+    if (masked) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (k0 + 16 * b + 4 * quad + r >= seen[i]) sc[i][b][r] = kNegInf;
+    }
+    i32x4 pf[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float to = fmaxf(m[i], row_max(lane_max(sc[i])) * scale_log2);
+      const float f = shrink(m[i], to);
+      m[i] = to;
+      l[i] = l[i] * f + probabilities(sc[i], scale_log2, to);
+      // (a product with 1 changes nothing: most steps of a chunk find no larger logit)
+      if (__any(f != 1.0f)) {
+#pragma unroll
+        for (int d = 0; d < T::DB; ++d) o[i][d] *= f;
+      }
+      pf[i][0] = pack_blocks<IN>(sc[i][0], sc[i][1]);
+      pf[i][1] = pack_blocks<IN>(sc[i][2], sc[i][3]);
+    }
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int d = 0; d < T::DB; ++d) {
+        const i32x4 vf = column_fragment<DP>(vt, at, p, d);
+        o[0][d] = mfma16_v<IN>(vf, pf[0][p], o[0][d]);
+        o[1][d] = mfma16_v<IN>(vf, pf[1][p], o[1][d]);
+      }
+  }
+  // The values of a step that are not finite, for the rows that see them.
+  __device__ __forceinline__ void add_not_finite(const char* v, int64_t v_bytes, int k0, int end, int dim) {
+    const int quad = (threadIdx.x & 63) / 16;
+    constexpr unsigned E = IN == GEMM_F16 ? 0x7c00u : 0x7f80u;
+    for (int j = k0; j < k0 + kTile && j < end; ++j) {
+      const unsigned short* const row = reinterpret_cast<const unsigned short*>(v + j * v_bytes);
+#pragma unroll
+      for (int d = 0; d < T::DB; ++d)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int at = 16 * d + 4 * quad + r;
+          if (at >= dim || (row[at] & E) != E) continue;
+          const unsigned short bits = row[at];
+          const float bad = IN == GEMM_F16 ? (float)__builtin_bit_cast(_Float16, bits)
+                                           : __uint_as_float((unsigned)bits << 16);
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (j < seen[i]) o[i][d][r] += bad;
+        }
+    }
+  }
+  // The end of the chunk that begins at c0.
+  __device__ __forceinline__ void join(int c0) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      // (a chunk that the row does not see leaves it as it is, to the sign of a zero)
+      if (c0 < seen[i]) {
+        const Join j = join_chunk(M[i], m[i]);
+        M[i] = j.m;
+        L[i] = joined(L[i], row_sum(l[i]), j);
+#pragma unroll
+        for (int d = 0; d < T::DB; ++d)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) O[i][d][r] = joined(O[i][d][r], o[i][d][r], j);
+      }
+    }
+  }
+};
 
 template <int IN, int DP>
 __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttnArgs a) {
   using T = TileOf<DP>;
-  __shared__ __attribute__((aligned(16))) char lds[2][2][kTile * T::PITCH];
+  // (arrays of their own: the compiler then knows that a transfer into one stage does not
+  // touch the other, and lets the reads of that go on)
+  __shared__ __attribute__((aligned(1024))) char k_a[kTile * T::PITCH], v_a[kTile * T::PITCH];
+  __shared__ __attribute__((aligned(1024))) char k_b[kTile * T::PITCH], v_b[kTile * T::PITCH];
   const int lane = threadIdx.x & 63, wave = threadIdx.x / 64, quad = lane / 16, col = lane % 16;
   // heads vary fastest: neighbouring workgroups go to different XCDs, so a key
   // head's workgroups meet in few of the L2s.  The last rows (the most keys) first.
@@ -78,194 +207,91 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttnArgs a) {
   if (r0 >= rows) return;
 
   // this lane's rows: column `col` of the two blocks of 16 of its wave
-  int64_t row[2];
-  int seen[2];
-  i32x4 qf[2][T::KS];
+  WaveRows<IN, DP> w;
+  w.scale_log2 = a.scale_log2;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    row[i] = r0 + 32 * wave + 16 * i + col;
-    const int64_t t = row[i] / a.group;
-    const int h = (int)(row[i] - t * a.group);
-    seen[i] = (int)keys_seen(a, s, t);
+    const int64_t row = r0 + 32 * wave + 16 * i + col, t = row / a.group;
+    const int h = (int)(row - t * a.group);
+    w.seen[i] = (int)keys_seen(a, s, t);
     const char* const q = static_cast<const char*>(a.q) + 2 * ((s.q0 + t) * a.q_token + (kh * a.group + h) * a.q_head);
 #pragma unroll
     for (int ks = 0; ks < T::KS; ++ks) {
       const int d = 32 * ks + 8 * quad;
-      qf[i][ks] = i32x4{};
-      if (row[i] < rows && d < a.dim) qf[i][ks] = *reinterpret_cast<const i32x4*>(q + 2 * d);
+      w.q[i][ks] = i32x4{};
+      if (row < rows && d < a.dim) w.q[i][ks] = *reinterpret_cast<const i32x4*>(q + 2 * d);
     }
   }
   // keys that any row of the workgroup, and of the wave, sees, and those that all of
-  // the wave's see (rows past the end see none, which needs no mask)
+  // them see (rows past the end see none, which needs no mask)
   auto seen_of = [&](int64_t r) { return (int)keys_seen(a, s, (r < rows ? r : rows - 1) / a.group); };
   const int need = __builtin_amdgcn_readfirstlane(seen_of(r0 + kRows - 1));
+  const int all_see = __builtin_amdgcn_readfirstlane(seen_of(r0));
   const int64_t w0 = r0 + 32 * wave;
   const int wave_need = __builtin_amdgcn_readfirstlane(w0 < rows ? seen_of(w0 + 31) : 0);
   const int wave_all = __builtin_amdgcn_readfirstlane(w0 < rows ? seen_of(w0) : 0);
-
-  f32x4 O[2][T::DB], o[2][T::DB];
-  float M[2], L[2], m[2], l[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    M[i] = kNegInf;
-    L[i] = 0.0f;
-#pragma unroll
-    for (int d = 0; d < T::DB; ++d) O[i][d] = f32x4{};
-  }
+  w.clear_all();
 
   const int64_t k_bytes = 2 * a.k_token, v_bytes = 2 * a.v_token;
   const char* const kp = static_cast<const char*>(a.k) + 2 * (s.k0 * a.k_token + kh * a.k_head);
   const char* const vp = static_cast<const char*>(a.v) + 2 * (s.k0 * a.v_token + kh * a.v_head);
-  Mover<DP> next;
-  auto fetch = [&](int64_t k0) {
-    next.load(kp + k0 * k_bytes, vp + k0 * v_bytes, k_bytes, v_bytes, (int)(s.m - k0 < kTile ? s.m - k0 : kTile), a.dim);
+  const Mover<DP> km(k_bytes, a.dim), vm(v_bytes, a.dim);
+  auto fetch = [&](int k0, char* kt, char* vt) {
+    km.move(kp + k0 * k_bytes, kt, s.m - k0, k_bytes, a.dim);
+    vm.move(vp + k0 * v_bytes, vt, s.m - k0, v_bytes, a.dim);
   };
-  // values behind the last key that some rows see (a NaN there must not reach the rows
-  // that do not: 0 times it is one)
-  auto clean = [&](int k0) {
-    if (k0 + kTile <= seen_of(r0)) return false;  // all rows see all of them
+  auto landed = [&]() {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+  };
+  // A step that some rows do not see all of: values that are not finite are taken out of it (0
+  // times a NaN would reach the rows that do not see it) and added for the rows that do.
+  auto clean = [&](char* vt) {
     bool bad = false;
+    u32x4* const mine = reinterpret_cast<u32x4*>(vt) + threadIdx.x;
+    constexpr int N = Mover<DP>::N;
 #pragma unroll
-    for (int i = 0; i < Mover<DP>::N; ++i)
+    for (int i = 0; i < N; ++i) {
+      const u32x4 v = mine[i * kThreads];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) bad |= not_finite<IN>(next.v[i][e]);
-    return bad;
-  };
-  if (need > 0) {
-    fetch(0);
-  }
-  bool poison = need > 0 && __syncthreads_or(clean(0));
-  auto put = [&](int stage) {
-    if (poison) {
-#pragma unroll
-      for (int i = 0; i < Mover<DP>::N; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          constexpr unsigned E = IN == GEMM_F16 ? 0x7c00u : 0x7f80u;
-          unsigned v = next.v[i][e];
-          if ((v & E) == E) v &= 0xffff0000u;
-          if ((v & (E << 16)) == (E << 16)) v &= 0xffffu;
-          next.v[i][e] = v;
-        }
+      for (int e = 0; e < 4; ++e) bad |= not_finite<IN>(v[e]);
     }
-    next.store(lds[stage][0], lds[stage][1]);
+    if (!__syncthreads_or(bad)) return false;
+#pragma unroll
+    for (int i = 0; i < N; ++i) mine[i * kThreads] = only_finite<IN>(mine[i * kThreads]);
+    __syncthreads();
+    return true;
   };
-  if (need > 0) put(0);
-  __syncthreads();
-
-  int stage = 0;
-  for (int k0 = 0; k0 < need; k0 += kTile) {
-    const bool more = k0 + kTile < need;
-    if (more) fetch(k0 + kTile);
-    const char* const kt = lds[stage][0];
-    const char* const vt = lds[stage][1];
-    if (k0 % kAttnChunk == 0) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        m[i] = kNegInf;
-        l[i] = 0.0f;
-#pragma unroll
-        for (int d = 0; d < T::DB; ++d) o[i][d] = f32x4{};
-      }
-    }
+  auto one = [&](int k0, char* kt, char* vt, char* next_k, char* next_v) {
+    landed();  // this step's tiles are there, and the other stage has been read
+    if (k0 + kTile < need) fetch(k0 + kTile, next_k, next_v);
+    if (k0 % kAttnChunk == 0) w.clear_chunk();
+    const bool poison = k0 + kTile > all_see && clean(vt);
     if (k0 < wave_need) {
-      f32x4 sc[2][4];
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        sc[0][b] = sc[1][b] = f32x4{};
-#pragma unroll
-        for (int ks = 0; ks < T::KS; ++ks) {
-          const i32x4 kf = row_fragment<DP>(kt, b, ks);
-          sc[0][b] = mfma16_v<IN>(kf, qf[0][ks], sc[0][b]);
-          sc[1][b] = mfma16_v<IN>(kf, qf[1][ks], sc[1][b]);
-        }
-      }
-      if (k0 + kTile > wave_all) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int b = 0; b < 4; ++b)
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              if (k0 + 16 * b + 4 * quad + r >= seen[i]) sc[i][b][r] = kNegInf;
-      }
-      i32x4 pf[2][2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float to = fmaxf(m[i], row_max(lane_max(sc[i])) * a.scale_log2);
-        const float f = shrink(m[i], to);
-        m[i] = to;
-        l[i] = l[i] * f + probabilities(sc[i], a.scale_log2, to);
-#pragma unroll
-        for (int d = 0; d < T::DB; ++d) o[i][d] *= f;
-        pf[i][0] = pack_blocks<IN>(sc[i][0], sc[i][1]);
-        pf[i][1] = pack_blocks<IN>(sc[i][2], sc[i][3]);
-      }
-#pragma unroll
-      for (int p = 0; p < 2; ++p)
-#pragma unroll
-        for (int d = 0; d < T::DB; ++d) {
-          const i32x4 vf = column_fragment<DP>(vt, p, d);
-          o[0][d] = mfma16_v<IN>(vf, pf[0][p], o[0][d]);
-          o[1][d] = mfma16_v<IN>(vf, pf[1][p], o[1][d]);
-        }
-      if (poison) {
-        // the values that were taken out, for the rows that see them
-        for (int j = 0; j < kTile && k0 + j < s.m; ++j) {
-          const unsigned short* const v = reinterpret_cast<const unsigned short*>(vp + (k0 + j) * v_bytes);
-#pragma unroll
-          for (int d = 0; d < T::DB; ++d)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const int at = 16 * d + 4 * quad + r;
-              if (at >= a.dim) continue;
-              constexpr unsigned E = IN == GEMM_F16 ? 0x7c00u : 0x7f80u;
-              if ((v[at] & E) != E) continue;
-              const float bad = IN == GEMM_F16 ? (float)__builtin_bit_cast(_Float16, v[at])
-                                               : __uint_as_float((unsigned)v[at] << 16);
-#pragma unroll
-              for (int i = 0; i < 2; ++i)
-                if (k0 + j < seen[i]) o[i][d][r] += bad;
-            }
-        }
-      }
+      w.step(kt, vt, k0, k0 + kTile > wave_all);
+      if (poison) w.add_not_finite(vp, v_bytes, k0, (int)s.m, a.dim);
     }
-    if ((k0 + kTile) % kAttnChunk == 0 || !more) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        // (a chunk that the row does not see leaves it as it is, to the sign of a zero)
-        if (k0 / kAttnChunk * kAttnChunk < seen[i]) {
-          const Join j = join_chunk(M[i], m[i]);
-          M[i] = j.m;
-          L[i] = joined(L[i], row_sum(l[i]), j);
-#pragma unroll
-          for (int d = 0; d < T::DB; ++d)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) O[i][d][r] = joined(O[i][d][r], o[i][d][r], j);
-        }
-      }
-    }
-    if (more) {
-      poison = __syncthreads_or(clean(k0 + kTile));
-      stage ^= 1;
-      put(stage);
-      __syncthreads();
-    }
+    if ((k0 + kTile) % kAttnChunk == 0 || k0 + kTile >= need) w.join(k0 / kAttnChunk * kAttnChunk);
+  };
+  if (need > 0) fetch(0, k_a, v_a);
+  for (int k0 = 0; k0 < need; k0 += 2 * kTile) {
+    one(k0, k_a, v_a, k_b, v_b);
+    if (k0 + kTile < need) one(k0 + kTile, k_b, v_b, k_a, v_a);
   }
 
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    if (row[i] >= rows) continue;
-    const int64_t t = row[i] / a.group;
-    const int64_t head = kh * a.group + (row[i] - t * a.group);
-    const int64_t at = (s.q0 + t) * a.q_heads + head;
+    const int64_t row = r0 + 32 * wave + 16 * i + col;
+    if (row >= rows) continue;
+    const int64_t t = row / a.group;
+    const int64_t at = (s.q0 + t) * a.q_heads + kh * a.group + (row - t * a.group);
     // a row without keys is zero; one whose keys are all -infinity is 0 / 0
-    const float inv = seen[i] == 0 ? 0.0f : 1.0f / L[i];
+    const float inv = w.seen[i] == 0 ? 0.0f : 1.0f / w.L[i];
 #pragma unroll
     for (int d = 0; d < T::DB; ++d) {
       const int c = 16 * d + 4 * quad;
       if (c >= a.dim) continue;
-      const f32x4 x = O[i][d] * inv;
+      const f32x4 x = w.O[i][d] * inv;
       const i32x2 y{pack2<IN>(x[0], x[1]), pack2<IN>(x[2], x[3])};
       const int64_t to = 2 * (at * a.dim + c);
       *reinterpret_cast<i32x2*>(static_cast<char*>(a.o) + to) = y;
@@ -274,7 +300,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttnArgs a) {
             i32x2{pack2_rest<IN>(x[0], x[1], y[0]), pack2_rest<IN>(x[2], x[3], y[1])};
     }
     if (a.lse && quad == 0)
-      a.lse[at] = seen[i] == 0 ? kNegInf : (M[i] + __builtin_amdgcn_logf(L[i])) * kLn2;
+      a.lse[at] = w.seen[i] == 0 ? kNegInf : (w.M[i] + __builtin_amdgcn_logf(w.L[i])) * kLn2;
   }
 }
 
@@ -344,19 +370,13 @@ __global__ __launch_bounds__(kFewThreads, 2) void attention_few_kernel(AttnArgs 
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int at = threadIdx.x + i * kFewThreads, key = at / T::SLOTS, c = at % T::SLOTS;
-      u32x4 v = vv[i];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        constexpr unsigned E = IN == GEMM_F16 ? 0x7c00u : 0x7f80u;
-        if ((v[e] & E) == E) v[e] &= 0xffff0000u;
-        if ((v[e] & (E << 16)) == (E << 16)) v[e] &= 0xffffu;
-      }
-      *reinterpret_cast<u32x4*>(&vt[key / kTile][T::at(key % kTile, c)]) = v;
+      *reinterpret_cast<u32x4*>(&vt[key / kTile][T::at(key % kTile, c)]) = only_finite<IN>(vv[i]);
     }
     __syncthreads();
   }
 
   const int64_t rows = queries * a.group;
+  const Lanes<DP> lanes;
   for (int64_t r0 = 0; r0 < rows; r0 += 16) {
     const int64_t row = r0 + col, t = row / a.group;
     const int h = (int)(row - t * a.group);
@@ -410,7 +430,7 @@ __global__ __launch_bounds__(kFewThreads, 2) void attention_few_kernel(AttnArgs 
         if (d < T::DB) {
           o[i] *= f;
 #pragma unroll
-          for (int p = 0; p < 2; ++p) o[i] = mfma16_v<IN>(column_fragment<DP>(vt[w], p, d), pl[w][p][lane], o[i]);
+          for (int p = 0; p < 2; ++p) o[i] = mfma16_v<IN>(column_fragment<DP>(vt[w], lanes, p, d), pl[w][p][lane], o[i]);
         }
       }
     }

@@ -152,6 +152,7 @@ __global__ __launch_bounds__(kThreads, 1) void attention_dkv_kernel(AttnArgs a) 
     put(0);
   }
   __syncthreads();
+  Lanes<DP> lanes;
   int stage = 0;
   for (int64_t r0 = from; r0 < rows; r0 += kTile) {
     const bool more = r0 + kTile < rows;
@@ -169,8 +170,8 @@ __global__ __launch_bounds__(kThreads, 1) void attention_dkv_kernel(AttnArgs a) 
           sc[b][0] = sc[b][1] = dp[b][0] = dp[b][1] = f32x4{};
 #pragma unroll
           for (int ks = 0; ks < T::KS; ++ks) {
-            const i32x4 qf = row_fragment<DP>(qt, 2 * half + b, ks);
-            const i32x4 gf = row_fragment<DP>(gt, 2 * half + b, ks);
+            const i32x4 qf = row_fragment<DP>(qt, lanes, 2 * half + b, ks);
+            const i32x4 gf = row_fragment<DP>(gt, lanes, 2 * half + b, ks);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               sc[b][j] = mfma16_v<IN>(qf, kf[j][ks], sc[b][j]);
@@ -203,8 +204,8 @@ __global__ __launch_bounds__(kThreads, 1) void attention_dkv_kernel(AttnArgs a) 
         }
 #pragma unroll
         for (int d = 0; d < T::DB; ++d) {
-          const i32x4 gf = column_fragment<DP>(gt, half, d);
-          const i32x4 qf = column_fragment<DP>(qt, half, d);
+          const i32x4 gf = column_fragment<DP>(gt, lanes, half, d);
+          const i32x4 qf = column_fragment<DP>(qt, lanes, half, d);
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             dv[j][d] = mfma16_v<IN>(gf, pf[j], dv[j][d]);
@@ -305,6 +306,7 @@ __global__ __launch_bounds__(kThreads, 1) void attention_dq_kernel(AttnArgs a) {
     put(0);
   }
   __syncthreads();
+  Lanes<DP> lanes;
   int stage = 0;
   for (int k0 = 0; k0 < need; k0 += kTile) {
     const bool more = k0 + kTile < need;
@@ -321,8 +323,8 @@ __global__ __launch_bounds__(kThreads, 1) void attention_dq_kernel(AttnArgs a) {
           sc[0][b] = sc[1][b] = dp[0][b] = dp[1][b] = f32x4{};
 #pragma unroll
           for (int ks = 0; ks < T::KS; ++ks) {
-            const i32x4 kf = row_fragment<DP>(kt, 2 * half + b, ks);
-            const i32x4 vf = row_fragment<DP>(vt, 2 * half + b, ks);
+            const i32x4 kf = row_fragment<DP>(kt, lanes, 2 * half + b, ks);
+            const i32x4 vf = row_fragment<DP>(vt, lanes, 2 * half + b, ks);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               sc[i][b] = mfma16_v<IN>(kf, qf[i][ks], sc[i][b]);
@@ -345,7 +347,7 @@ __global__ __launch_bounds__(kThreads, 1) void attention_dq_kernel(AttnArgs a) {
         }
 #pragma unroll
         for (int d = 0; d < T::DB; ++d) {
-          const i32x4 kf = column_fragment<DP>(kt, half, d);
+          const i32x4 kf = column_fragment<DP>(kt, lanes, half, d);
           dq[0][d] = mfma16_v<IN>(kf, sf[0], dq[0][d]);
           dq[1][d] = mfma16_v<IN>(kf, sf[1], dq[1][d]);
         }

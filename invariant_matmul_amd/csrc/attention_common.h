@@ -105,27 +105,38 @@ struct TileOf {
   }
 };
 
+// Where a lane's pieces of a tile lie.  Slots are XORed, so a piece's place is that of the
+// first one XOR a constant: `again` keeps the compiler from holding all of them in
+// registers over a loop.
+template <int DP>
+struct Lanes {
+  unsigned row, column;
+  __device__ __forceinline__ Lanes() {
+    const int l = threadIdx.x & 63, r = 4 * (l / 16) + (l % 16) / 4;
+    row = TileOf<DP>::at(l % 16, l / 16);
+    column = TileOf<DP>::at(r, (l % 4) / 2) + (l % 2) * 8;
+  }
+  __device__ __forceinline__ void again() { asm volatile("" : "+v"(row), "+v"(column)); }
+};
+
 // Rows 16 b + lane % 16 of a tile, dimensions 32 ks + 8 (lane / 16) .. + 7.
 template <int DP>
-__device__ __forceinline__ i32x4 row_fragment(const char* tile, int b, int ks) {
-  const int l = threadIdx.x & 63;
-  return *reinterpret_cast<const i32x4*>(tile + TileOf<DP>::at(16 * b + l % 16, 4 * ks + l / 16));
+__device__ __forceinline__ i32x4 row_fragment(const char* tile, const Lanes<DP>& at, int b, int ks) {
+  return *reinterpret_cast<const i32x4*>(tile + (at.row ^ (64 * ks)) + 16 * TileOf<DP>::PITCH * b);
 }
 
 // The transposed piece: dimension 16 db + lane % 16 of the rows 4 q + 0..3 of the
 // blocks 2 s and 2 s + 1 of 16 rows, q = lane / 16.
 template <int DP>
-__device__ __forceinline__ i32x4 column_fragment(const char* tile, int s, int db) {
+__device__ __forceinline__ i32x4 column_fragment(const char* tile, const Lanes<DP>& at, int s, int db) {
   i32x4 r{};
 #if defined(__HIP_DEVICE_COMPILE__)
   typedef short v4i16 __attribute__((ext_vector_type(4)));
   typedef __attribute__((address_space(3))) v4i16 lds_v4;
-  const int l = threadIdx.x & 63;
-  const int row = 32 * s + 4 * (l / 16) + (l % 16) / 4, c = l % 4;
-  const int at = TileOf<DP>::at(row, 2 * db + c / 2) + (c % 2) * 8;
-  const i32x2 lo = __builtin_bit_cast(i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4*)(tile + at)));
+  const char* const p = tile + (at.column ^ (32 * db)) + 32 * TileOf<DP>::PITCH * s;
+  const i32x2 lo = __builtin_bit_cast(i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4*)p));
   const i32x2 hi = __builtin_bit_cast(
-      i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4*)(tile + at + 16 * TileOf<DP>::PITCH)));
+      i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4*)(p + 16 * TileOf<DP>::PITCH)));
   r = i32x4{lo[0], lo[1], hi[0], hi[1]};
 #endif
   return r;
@@ -160,14 +171,35 @@ __device__ __forceinline__ i32x4 pack_blocks(const f32x4& a, const f32x4& b) {
                pack2<IN>(b[2], b[3])};
 }
 
-// Over the four lanes of a row.
+// Over the four lanes of a row.  (The swaps of 16 and 32 lanes hand every lane both values.)
+struct Both {
+  float a, b;
+};
+__device__ __forceinline__ Both swap16(float v) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return Both{__uint_as_float(r[0]), __uint_as_float(r[1])};
+#else
+  return Both{v, v};
+#endif
+}
+__device__ __forceinline__ Both swap32(float v) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return Both{__uint_as_float(r[0]), __uint_as_float(r[1])};
+#else
+  return Both{v, v};
+#endif
+}
 __device__ __forceinline__ float row_max(float v) {
-  v = fmaxf(v, __shfl_xor(v, 16));
-  return fmaxf(v, __shfl_xor(v, 32));
+  const Both x = swap16(v);
+  const Both y = swap32(fmaxf(x.a, x.b));
+  return fmaxf(y.a, y.b);
 }
 __device__ __forceinline__ float row_sum(float v) {
-  v += __shfl_xor(v, 16);
-  return v + __shfl_xor(v, 32);
+  const Both x = swap16(v);
+  const Both y = swap32(x.a + x.b);
+  return y.a + y.b;
 }
 
 // The largest of a step's logits of a row, in its own lane.  (A NaN is left out here and
