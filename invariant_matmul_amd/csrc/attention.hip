@@ -24,7 +24,7 @@ using namespace dev;
 // A workgroup takes 256 rows of a key head, 32 a wave, and walks through their keys
 // 64 at a time: the next step's keys and values go by DMA into the other half of a
 // two-stage LDS buffer while this one's are used.
-constexpr int kWaves = 8, kThreads = 64 * kWaves;
+constexpr int kWaves = 4, kThreads = 64 * kWaves;
 constexpr int kRows = 32 * kWaves;
 
 // Moves a tile of keys or values to LDS; what lies past its `left` rows or past the
@@ -127,11 +127,11 @@ struct WaveRows {
     i32x4 pf[2][2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float to = fmaxf(m[i], row_max(lane_max(sc[i])) * scale_log2);
+      const float to = reference(m[i], row_max(lane_max(sc[i])) * scale_log2);
       const float f = shrink(m[i], to);
       m[i] = to;
       l[i] = l[i] * f + probabilities(sc[i], scale_log2, to);
-      // (a product with 1 changes nothing: most steps of a chunk find no larger logit)
+      // (a product with 1 changes nothing)
       if (__any(f != 1.0f)) {
 #pragma unroll
         for (int d = 0; d < T::DB; ++d) o[i][d] *= f;
@@ -407,9 +407,9 @@ __global__ __launch_bounds__(kFewThreads, 2) void attention_few_kernel(AttnArgs 
     if (quad == 0) ml[wave][col] = mine;
     __syncthreads();
     float m[kFewWaves];
-    m[0] = ml[0][col];
+    m[0] = reference(kNegInf, ml[0][col]);
 #pragma unroll
-    for (int w = 1; w < kFewWaves; ++w) m[w] = fmaxf(m[w - 1], ml[w][col]);
+    for (int w = 1; w < kFewWaves; ++w) m[w] = reference(m[w - 1], ml[w][col]);
     const float about = wave == 0 ? m[0] : wave == 1 ? m[1] : wave == 2 ? m[2] : m[3];
     sl[wave][lane] = probabilities(sc, a.scale_log2, about);
     pl[wave][0][lane] = pack_blocks<IN>(sc[0], sc[1]);
@@ -421,7 +421,6 @@ __global__ __launch_bounds__(kFewThreads, 2) void attention_few_kernel(AttnArgs 
     float l = 0.0f;
 #pragma unroll
     for (int w = 0; w < kFewWaves; ++w) {
-      // (steps past the row's last key add nothing and shrink nothing)
       const float f = w == 0 ? shrink(kNegInf, m[0]) : shrink(m[w - 1], m[w]);
       l = l * f + sl[w][lane];
 #pragma unroll

@@ -212,11 +212,20 @@ __device__ __forceinline__ float lane_max(const f32x4 (&s)[4]) {
     for (int r = 0; r < 4; ++r) m = fmaxf(m, s[b][r]);
   return m;
 }
-// What a running maximum that grew from a to b leaves of earlier sums.
-__device__ __forceinline__ float shrink(float a, float b) {
-  return a == b ? 1.0f : __builtin_amdgcn_exp2f(a - b);
+// The reference of a row's probabilities, from step to step: the largest scaled logit of the
+// step where it was last set.  It is set again only where a logit passes it by more than
+// 8 (binary): probabilities are then at most 2^8, which fp32 sums and 16-bit values hold
+// as well as 1, and the sums so far, which a new reference makes a pass over the
+// output's registers for, mostly stay as they are.  A rule of the row's own logits.
+__device__ __forceinline__ float reference(float m, float step_max) {
+  return step_max > m + 8.0f ? step_max : m;
 }
-// Probabilities about the maximum m (scaled; of a row without any, 0), in place;
+// What a reference that grew from a to b leaves of earlier sums (without any, there is nothing
+// to change).
+__device__ __forceinline__ float shrink(float a, float b) {
+  return a == b || a == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(a - b);
+}
+// Probabilities about the reference m (of a row without any, 0), in place;
 // their sum in the lane.
 __device__ __forceinline__ float probabilities(f32x4 (&s)[4], float scale_log2, float m) {
   const float about = m == kNegInf ? 0.0f : m;
