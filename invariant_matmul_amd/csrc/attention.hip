@@ -29,28 +29,29 @@ constexpr int kRows = 32 * kWaves;
 
 // Moves a tile of keys or values to LDS; what lies past its `left` rows or past the
 // dimension is zeros.  A wave fills 1 KB at a time, lane l the 16 bytes at 16 l: each
-// lane fetches what belongs in its fixed slot.
+// lane fetches what belongs in its fixed slot.  The workgroup's next rows have a buffer of
+// their own, so that one offset serves all.
 template <int DP>
 struct Mover {
-  static constexpr int N = kTile * TileOf<DP>::SLOTS / kThreads;
-  unsigned off[N];  // from the tile's first row
+  static constexpr int N = kTile * TileOf<DP>::SLOTS / kThreads, ROWS = kThreads / TileOf<DP>::SLOTS;
+  static_assert(ROWS % TileOf<DP>::SLOTS == 0, "the rows of a thread have the same slot");
+  unsigned off;  // of the thread's first row
   __device__ __forceinline__ Mover(int64_t row_bytes, int dim) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int at = threadIdx.x + i * kThreads;
-      const int row = at / TileOf<DP>::SLOTS;
-      const int slot = (at % TileOf<DP>::SLOTS) ^ (row & (TileOf<DP>::SLOTS - 1));
-      off[i] = slot * 8 < dim ? (unsigned)(row * (int)row_bytes + slot * 16) : OOB;
-    }
+    const int row = threadIdx.x / TileOf<DP>::SLOTS;
+    const int slot = (threadIdx.x % TileOf<DP>::SLOTS) ^ (row & (TileOf<DP>::SLOTS - 1));
+    off = slot * 8 < dim ? (unsigned)(row * (int)row_bytes + slot * 16) : OOB;
   }
   __device__ __forceinline__ void move(const char* from, char* to, int64_t left, int64_t row_bytes, int dim) const {
     // (rows behind the last: past the buffer's end, or, where rows overlap, values that no row sees)
     const int rows = (int)(left < kTile ? left : kTile);
-    const auto buf = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(from), 0,
-                                                       (rows - 1) * (int)row_bytes + 2 * dim, 0x00020000);
+    char* const mine = to + __builtin_amdgcn_readfirstlane(threadIdx.x & ~63) * 16;
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-      dma16(buf, to + (__builtin_amdgcn_readfirstlane(threadIdx.x & ~63) + i * kThreads) * 16, off[i], 0);
+    for (int i = 0; i < N; ++i) {
+      const int last = rows - 1 - i * ROWS;
+      const auto buf = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(from) + i * ROWS * row_bytes, 0,
+                                                         last < 0 ? 0 : last * (int)row_bytes + 2 * dim, 0x00020000);
+      dma16(buf, mine + i * kThreads * 16, off, 0);
+    }
   }
 };
 
@@ -69,6 +70,21 @@ __device__ __forceinline__ u32x4 only_finite(u32x4 v) {
     if ((v[e] & (E << 16)) == (E << 16)) v[e] &= 0xffffu;
   }
   return v;
+}
+
+// ... and the others' values, zeros in the place of the finite ones.
+template <int IN>
+__device__ __forceinline__ f32x4 only_not_finite(i32x2 four) {
+  f32x4 f;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const unsigned bits = ((unsigned)four[r / 2] >> (16 * (r % 2))) & 0xffffu;
+    constexpr unsigned E = IN == GEMM_F16 ? 0x7c00u : 0x7f80u;
+    // (infinity or NaN in fp32: an fp16 fraction moves up with its sign)
+    const unsigned wide = IN == GEMM_F16 ? (bits & 0x8000u) << 16 | 0x7f800000u | (bits & 0x3ffu) << 13 : bits << 16;
+    f[r] = (bits & E) == E ? __uint_as_float(wide) : 0.0f;
+  }
+  return f;
 }
 
 // The rows of a wave through one step.
@@ -151,22 +167,16 @@ struct WaveRows {
   // The values of a step that are not finite, for the rows that see them.
   __device__ __forceinline__ void add_not_finite(const char* v, int64_t v_bytes, int k0, int end, int dim) {
     const int quad = (threadIdx.x & 63) / 16;
-    constexpr unsigned E = IN == GEMM_F16 ? 0x7c00u : 0x7f80u;
     for (int j = k0; j < k0 + kTile && j < end; ++j) {
-      const unsigned short* const row = reinterpret_cast<const unsigned short*>(v + j * v_bytes);
 #pragma unroll
-      for (int d = 0; d < T::DB; ++d)
+      for (int d = 0; d < T::DB; ++d) {
+        const int c = 16 * d + 4 * quad;
+        i32x2 x{};
+        if (c < dim) x = *reinterpret_cast<const i32x2*>(v + j * v_bytes + 2 * c);
+        const f32x4 bad = only_not_finite<IN>(x);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int at = 16 * d + 4 * quad + r;
-          if (at >= dim || (row[at] & E) != E) continue;
-          const unsigned short bits = row[at];
-          const float bad = IN == GEMM_F16 ? (float)__builtin_bit_cast(_Float16, bits)
-                                           : __uint_as_float((unsigned)bits << 16);
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            if (j < seen[i]) o[i][d][r] += bad;
-        }
+        for (int i = 0; i < 2; ++i) o[i][d] += j < seen[i] ? bad : f32x4{};
+      }
     }
   }
   // The end of the chunk that begins at c0.
@@ -178,10 +188,15 @@ struct WaveRows {
         const Join j = join_chunk(M[i], m[i]);
         M[i] = j.m;
         L[i] = joined(L[i], row_sum(l[i]), j);
+        // (a product with 1 changes nothing)
+        if (__any(j.a != 1.0f)) {
+#pragma unroll
+          for (int d = 0; d < T::DB; ++d) O[i][d] *= j.a;
+        }
 #pragma unroll
         for (int d = 0; d < T::DB; ++d)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) O[i][d][r] = joined(O[i][d][r], o[i][d][r], j);
+          for (int r = 0; r < 4; ++r) O[i][d][r] = fmaf(o[i][d][r], j.b, O[i][d][r]);
       }
     }
   }
@@ -445,16 +460,9 @@ __global__ __launch_bounds__(kFewThreads, 2) void attention_few_kernel(AttnArgs 
         const int d = 16 * (kFewWaves * i + wave) + 4 * quad;
         if (d < a.dim && d < DP) {
           if (poison) {
-            for (int j = 0; j < seen; ++j) {
-              const unsigned short* const v = reinterpret_cast<const unsigned short*>(
-                  static_cast<const char*>(a.v) + 2 * ((s.k0 + c0 + j) * a.v_token + kh * a.v_head));
-              constexpr unsigned E = IN == GEMM_F16 ? 0x7c00u : 0x7f80u;
-#pragma unroll
-              for (int r = 0; r < 4; ++r)
-                if ((v[d + r] & E) == E)
-                  o[i][r] += IN == GEMM_F16 ? (float)__builtin_bit_cast(_Float16, v[d + r])
-                                            : __uint_as_float((unsigned)v[d + r] << 16);
-            }
+            const char* v = static_cast<const char*>(a.v) + 2 * ((s.k0 + c0) * a.v_token + kh * a.v_head + d);
+            for (int j = 0; j < seen; ++j, v += 2 * a.v_token)
+              o[i] += only_not_finite<IN>(*reinterpret_cast<const i32x2*>(v));
           }
           *reinterpret_cast<f32x4*>(a.part_o + at * a.dim + d) = o[i];
         }

@@ -239,14 +239,14 @@ __device__ __forceinline__ float probabilities(f32x4 (&s)[4], float scale_log2, 
   return sum;
 }
 
-// The result of the keys so far and that of one more chunk:
-// o = o a + chunk_o b, l = l a + chunk_l b.
+// The result of the keys so far and that of one more chunk, about a reference that follows the
+// chunks' as theirs follow the logits: o = o a + chunk_o b, l = l a + chunk_l b.
 struct Join {
   float m, a, b;
 };
 __device__ __forceinline__ Join join_chunk(float m, float chunk_m) {
-  const float to = fmaxf(m, chunk_m);
-  return Join{to, shrink(m, to), shrink(chunk_m, to)};
+  const float to = reference(m, chunk_m);
+  return Join{to, shrink(m, to), chunk_m == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(chunk_m - to)};
 }
 __device__ __forceinline__ float joined(float o, float chunk_o, const Join& j) {
   return fmaf(chunk_o, j.b, o * j.a);
