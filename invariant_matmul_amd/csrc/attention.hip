@@ -107,16 +107,9 @@ struct WaveRows {
       for (int d = 0; d < T::DB; ++d) O[i][d] = f32x4{};
     }
   }
-  __device__ __forceinline__ void clear_chunk() {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      m[i] = kNegInf;
-      l[i] = 0.0f;
-#pragma unroll
-      for (int d = 0; d < T::DB; ++d) o[i][d] = f32x4{};
-    }
-  }
-  // masked: some row of the wave does not see all of the step's keys
+  // FIRST: the first step of a chunk.  masked: some row of the wave does not see all of the
+  // step's keys.
+  template <bool FIRST>
   __device__ __forceinline__ void step(const char* kt, const char* vt, int k0, bool masked) {
     const int quad = (threadIdx.x & 63) / 16;
     at.again();
@@ -143,14 +136,21 @@ struct WaveRows {
     i32x4 pf[2][2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float to = reference(m[i], row_max(lane_max(sc[i])) * scale_log2);
-      const float f = shrink(m[i], to);
-      m[i] = to;
-      l[i] = l[i] * f + probabilities(sc[i], scale_log2, to);
-      // (a product with 1 changes nothing)
-      if (__any(f != 1.0f)) {
+      const float top = lane_max(sc[i]) * scale_log2;
+      if constexpr (FIRST) {
+        m[i] = reference(kNegInf, row_max(top));
+        l[i] = probabilities(sc[i], scale_log2, m[i]);
+      } else {
+        // (no lane has a logit that sets the reference of its row again: nothing changes)
+        if (__any(reference(m[i], top) != m[i])) {
+          const float to = reference(m[i], row_max(top));
+          const float f = shrink(m[i], to);
+          m[i] = to;
+          l[i] *= f;
 #pragma unroll
-        for (int d = 0; d < T::DB; ++d) o[i][d] *= f;
+          for (int d = 0; d < T::DB; ++d) o[i][d] *= f;
+        }
+        l[i] += probabilities(sc[i], scale_log2, m[i]);
       }
       pf[i][0] = pack_blocks<IN>(sc[i][0], sc[i][1]);
       pf[i][1] = pack_blocks<IN>(sc[i][2], sc[i][3]);
@@ -160,8 +160,8 @@ struct WaveRows {
 #pragma unroll
       for (int d = 0; d < T::DB; ++d) {
         const i32x4 vf = column_fragment<DP>(vt, at, p, d);
-        o[0][d] = mfma16_v<IN>(vf, pf[0][p], o[0][d]);
-        o[1][d] = mfma16_v<IN>(vf, pf[1][p], o[1][d]);
+        o[0][d] = mfma16_v<IN>(vf, pf[0][p], FIRST && p == 0 ? f32x4{} : o[0][d]);
+        o[1][d] = mfma16_v<IN>(vf, pf[1][p], FIRST && p == 0 ? f32x4{} : o[1][d]);
       }
   }
   // The values of a step that are not finite, for the rows that see them.
@@ -277,21 +277,25 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttnArgs a) {
     __syncthreads();
     return true;
   };
-  auto one = [&](int k0, char* kt, char* vt, char* next_k, char* next_v) {
+  auto one = [&](auto first, int k0, char* kt, char* vt, char* next_k, char* next_v) {
     landed();  // this step's tiles are there, and the other stage has been read
     if (k0 + kTile < need) fetch(k0 + kTile, next_k, next_v);
-    if (k0 % kAttnChunk == 0) w.clear_chunk();
     const bool poison = k0 + kTile > all_see && clean(vt);
     if (k0 < wave_need) {
-      w.step(kt, vt, k0, k0 + kTile > wave_all);
+      w.template step<decltype(first)::value>(kt, vt, k0, k0 + kTile > wave_all);
       if (poison) w.add_not_finite(vp, v_bytes, k0, (int)s.m, a.dim);
     }
-    if ((k0 + kTile) % kAttnChunk == 0 || k0 + kTile >= need) w.join(k0 / kAttnChunk * kAttnChunk);
   };
+  const std::true_type first;
+  const std::false_type further;
   if (need > 0) fetch(0, k_a, v_a);
-  for (int k0 = 0; k0 < need; k0 += 2 * kTile) {
-    one(k0, k_a, v_a, k_b, v_b);
-    if (k0 + kTile < need) one(k0 + kTile, k_b, v_b, k_a, v_a);
+  for (int c0 = 0; c0 < need; c0 += kAttnChunk) {
+    one(first, c0, k_a, v_a, k_b, v_b);
+    for (int k0 = c0 + kTile; k0 < c0 + kAttnChunk && k0 < need; k0 += 2 * kTile) {
+      one(further, k0, k_b, v_b, k_a, v_a);
+      if (k0 + kTile < c0 + kAttnChunk && k0 + kTile < need) one(further, k0 + kTile, k_a, v_a, k_b, v_b);
+    }
+    if (c0 < wave_need) w.join(c0);
   }
 
 #pragma unroll
