@@ -133,6 +133,10 @@ struct WaveRows {
           for (int r = 0; r < 4; ++r)
             if (k0 + 16 * b + 4 * quad + r >= seen[i]) sc[i][b][r] = kNegInf;
     }
+    constexpr int PRE = 4;
+    i32x4 pre[PRE];
+#pragma unroll
+    for (int d = 0; d < PRE; ++d) pre[d] = column_fragment<DP>(vt, at, 0, d);
     i32x4 pf[2][2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -159,7 +163,7 @@ struct WaveRows {
     for (int p = 0; p < 2; ++p)
 #pragma unroll
       for (int d = 0; d < T::DB; ++d) {
-        const i32x4 vf = column_fragment<DP>(vt, at, p, d);
+        const i32x4 vf = p == 0 && d < PRE ? pre[d < PRE ? d : 0] : column_fragment<DP>(vt, at, p, d);
         o[0][d] = mfma16_v<IN>(vf, pf[0][p], FIRST && p == 0 ? f32x4{} : o[0][d]);
         o[1][d] = mfma16_v<IN>(vf, pf[1][p], FIRST && p == 0 ? f32x4{} : o[1][d]);
       }
