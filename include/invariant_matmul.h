@@ -660,7 +660,7 @@ gemm_status attention_run(attention_plan_t plan, const void* q, int64_t q_token_
                           const int* k_lens, void* o, void* o_low, float* lse, void* workspace,
                           size_t workspace_bytes, void* stream);
 
-/* Bytes of workspace attention_backward needs: sum_d do o of every row. */
+/* Bytes of workspace attention_backward needs: two numbers a row and head. */
 size_t attention_backward_workspace_size(attention_plan_t plan);
 
 /* The gradients dq, dk and dv (contiguous) from that of o (contiguous), o, o_low (or NULL:

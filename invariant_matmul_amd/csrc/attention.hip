@@ -24,36 +24,7 @@ using namespace dev;
 // A workgroup takes 256 rows of a key head, 32 a wave, and walks through their keys
 // 64 at a time: the next step's keys and values go by DMA into the other half of a
 // two-stage LDS buffer while this one's are used.
-constexpr int kWaves = 4, kThreads = 64 * kWaves;
 constexpr int kRows = 32 * kWaves;
-
-// Moves a tile of keys or values to LDS; what lies past its `left` rows or past the
-// dimension is zeros.  A wave fills 1 KB at a time, lane l the 16 bytes at 16 l: each
-// lane fetches what belongs in its fixed slot.  The workgroup's next rows have a buffer of
-// their own, so that one offset serves all.
-template <int DP>
-struct Mover {
-  static constexpr int N = kTile * TileOf<DP>::SLOTS / kThreads, ROWS = kThreads / TileOf<DP>::SLOTS;
-  static_assert(ROWS % TileOf<DP>::SLOTS == 0, "the rows of a thread have the same slot");
-  unsigned off;  // of the thread's first row
-  __device__ __forceinline__ Mover(int64_t row_bytes, int dim) {
-    const int row = threadIdx.x / TileOf<DP>::SLOTS;
-    const int slot = (threadIdx.x % TileOf<DP>::SLOTS) ^ (row & (TileOf<DP>::SLOTS - 1));
-    off = slot * 8 < dim ? (unsigned)(row * (int)row_bytes + slot * 16) : OOB;
-  }
-  __device__ __forceinline__ void move(const char* from, char* to, int64_t left, int64_t row_bytes, int dim) const {
-    // (rows behind the last: past the buffer's end, or, where rows overlap, values that no row sees)
-    const int rows = (int)(left < kTile ? left : kTile);
-    char* const mine = to + __builtin_amdgcn_readfirstlane(threadIdx.x & ~63) * 16;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int last = rows - 1 - i * ROWS;
-      const auto buf = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(from) + i * ROWS * row_bytes, 0,
-                                                         last < 0 ? 0 : last * (int)row_bytes + 2 * dim, 0x00020000);
-      dma16(buf, mine + i * kThreads * 16, off, 0);
-    }
-  }
-};
 
 template <int IN>
 __device__ __forceinline__ bool not_finite(unsigned two) {
@@ -213,7 +184,8 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttnArgs a) {
   // touch the other, and lets the reads of that go on)
   __shared__ __attribute__((aligned(1024))) char k_a[kTile * T::PITCH], v_a[kTile * T::PITCH];
   __shared__ __attribute__((aligned(1024))) char k_b[kTile * T::PITCH], v_b[kTile * T::PITCH];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x / 64, quad = lane / 16, col = lane % 16;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int quad = lane / 16, col = lane % 16;
   // heads vary fastest: neighbouring workgroups go to different XCDs, so a key
   // head's workgroups meet in few of the L2s.  The last rows (the most keys) first.
   const int64_t tiles = gridDim.x / a.k_heads;
@@ -258,10 +230,6 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttnArgs a) {
   auto fetch = [&](int k0, char* kt, char* vt) {
     km.move(kp + k0 * k_bytes, kt, s.m - k0, k_bytes, a.dim);
     vm.move(vp + k0 * v_bytes, vt, s.m - k0, v_bytes, a.dim);
-  };
-  auto landed = [&]() {
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
   };
   // A step that some rows do not see all of: values that are not finite are taken out of it (0
   // times a NaN would reach the rows that do not see it) and added for the rows that do.
@@ -343,7 +311,8 @@ __global__ __launch_bounds__(kFewThreads, 2) void attention_few_kernel(AttnArgs 
   __shared__ __attribute__((aligned(16))) char vt[kFewWaves][kTile * T::PITCH];
   __shared__ i32x4 pl[kFewWaves][2][64];
   __shared__ float ml[kFewWaves][16], sl[kFewWaves][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x / 64, quad = lane / 16, col = lane % 16;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int quad = lane / 16, col = lane % 16;
   const int kh = blockIdx.x % a.k_heads;
   const int64_t slot = blockIdx.x / a.k_heads;
   // the sequence of this chunk slot: sequence b's begin at k_start(b) / 256 + b

@@ -4,10 +4,14 @@
 //   ds_ij = p_ij (do_i v_j - delta_i)
 //   dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i
 //
-// Three kernels: delta; dk and dv, a workgroup per 128 keys of a key head, which walks
-// through the rows that see them; dq, a workgroup per 128 rows, which walks through
-// their keys.  p and ds are made twice, so that every sum is one chain in one workgroup:
-// no atomics, and the gradients of a sequence depend on that sequence alone.
+// One kernel makes lse and delta of every row ready, one makes the gradients: its workgroups
+// have a role each, dq of 128 rows, which walk through their keys, and dk or dv of 128
+// keys, which walk through the rows that see them.  p is made by all three and ds by two,
+// so that every sum is one chain in one workgroup: no atomics, and the gradients of a
+// sequence depend on that sequence alone.  dk and dv apart cost one product more (q k twice)
+// than together, but fit a wave into half of a SIMD's registers: with both at once
+// (254 + 256 registers, one wave a SIMD) that kernel took 3180 us for 8192 keys of 8 heads
+// and 32 query heads of 128.
 // p and ds are rounded to the input's type for their products, all else is fp32.
 #include "attention_common.h"
 #include "rows16.h"
@@ -16,12 +20,11 @@ namespace imm {
 namespace {
 using namespace dev;
 
-constexpr int kWaves = 4, kThreads = 64 * kWaves;
-constexpr int kKeys = 32 * kWaves;   // keys of a workgroup (dk, dv)
-constexpr int kRows = 32 * kWaves;   // rows of a workgroup (dq)
+constexpr int kBlock = 32 * kWaves;  // rows (dq) or keys (dk, dv) of a workgroup
 constexpr float kLog2e = 1.44269504088896340736f;
 
-// delta: 16 lanes a row, 8 elements each.  With o alone, the rounding of o is as large a part of
+// -lse log2(e) and delta of every row in the order of the packed rows, [key head][query][head
+// of the group]; 16 lanes a row, 8 elements each.  With o alone, the rounding of o is as large a part of
 // the gradients' error as the rounding of ds; with what it left (o_low) that is gone
 // (1500 bf16 keys of 128: dq is off by 0.00245 of itself instead of 0.00305, where its own
 // rounding makes 0.00166).
@@ -45,7 +48,13 @@ __global__ __launch_bounds__(256) void attention_delta_kernel(AttnArgs a) {
   }
 #pragma unroll
   for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
-  if (c == 0 && at < a.q_rows * a.q_heads) a.delta[at] = sum;
+  if (c == 0 && at < a.q_rows * a.q_heads) {
+    const int64_t q = at / a.q_heads;
+    const int head = (int)(at - q * a.q_heads), kh = head / a.group;
+    const int64_t to = ((int64_t)kh * a.q_rows + q) * a.group + (head - kh * a.group);
+    a.stats[to] = -a.lse[at] * kLog2e;
+    a.stats[a.q_rows * a.q_heads + to] = sum;
+  }
 }
 
 // A row set as the second operand: rows (lane % 16), dimensions 32 ks + 8 quad.
@@ -59,342 +68,338 @@ __device__ __forceinline__ void row_operand(i32x4 (&f)[TileOf<DP>::KS], const ch
   }
 }
 
+// Two sets of 16 results, dimension by row or key, to 16-bit rows.
+template <int IN, int DP>
+__device__ __forceinline__ void store_rows(const f32x4 (&x)[TileOf<DP>::DB], float scale, void* to, int64_t at, int dim) {
+  const int quad = (threadIdx.x & 63) / 16;
+#pragma unroll
+  for (int d = 0; d < TileOf<DP>::DB; ++d) {
+    const int c = 16 * d + 4 * quad;
+    const f32x4 y = x[d] * scale;
+    if (c < dim)
+      *reinterpret_cast<i32x2*>(static_cast<char*>(to) + 2 * (at + c)) = i32x2{pack2<IN>(y[0], y[1]), pack2<IN>(y[2], y[3])};
+  }
+}
+
+template <int DP>
+struct Stages {  // (arrays of their own, as in the forward kernel)
+  char *x0, *y0, *x1, *y1;
+  float *n0, *d0, *n1, *d1;
+};
+
+// dq of the rows from r0 on.
+template <int IN, int DP>
+__device__ __forceinline__ void rows_role(const AttnArgs& a, int64_t tile, int kh, const Stages<DP>& st) {
+  using T = TileOf<DP>;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int quad = lane / 16, col = lane % 16;
+  const int seg = segment_of_tile(a, tile, kBlock);
+  const Sequence s = segment(a, seg);
+  const int64_t r0 = (tile - (s.q0 * a.group / kBlock + seg)) * kBlock;
+  const int64_t rows = s.n * a.group;
+  if (r0 >= rows) return;
+
+  int seen[2];
+  float nl[2], delta[2];
+  i32x4 qf[2][T::KS], gf[2][T::KS];
+  f32x4 dq[2][T::DB];
+  const int64_t w0 = r0 + 32 * wave;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int64_t row = w0 + 16 * i + col, t = row / a.group;
+    const int64_t h = kh * a.group + (row - t * a.group);
+    const bool live = row < rows;
+    seen[i] = (int)keys_seen(a, s, t);
+    const int64_t at = ((int64_t)kh * a.q_rows + s.q0) * a.group + row;
+    nl[i] = live ? a.stats[at] : 0.0f;
+    delta[i] = live ? a.stats[a.q_rows * a.q_heads + at] : 0.0f;
+    row_operand<DP>(qf[i], static_cast<const char*>(a.q) + 2 * ((s.q0 + t) * a.q_token + h * a.q_head), live, a.dim);
+    row_operand<DP>(gf[i], static_cast<const char*>(a.d_o) + 2 * ((s.q0 + t) * a.q_heads + h) * a.dim, live, a.dim);
+#pragma unroll
+    for (int d = 0; d < T::DB; ++d) dq[i][d] = f32x4{};
+  }
+  auto seen_of = [&](int64_t r) { return (int)keys_seen(a, s, (r < rows ? r : rows - 1) / a.group); };
+  const int need = __builtin_amdgcn_readfirstlane(seen_of(r0 + kBlock - 1));
+  const int wave_need = __builtin_amdgcn_readfirstlane(w0 < rows ? seen_of(w0 + 31) : 0);
+  const int wave_all = __builtin_amdgcn_readfirstlane(w0 < rows ? seen_of(w0) : 0);
+
+  const int64_t k_bytes = 2 * a.k_token, v_bytes = 2 * a.v_token;
+  const char* const kp = static_cast<const char*>(a.k) + 2 * (s.k0 * a.k_token + kh * a.k_head);
+  const char* const vp = static_cast<const char*>(a.v) + 2 * (s.k0 * a.v_token + kh * a.v_head);
+  const Mover<DP> km(k_bytes, a.dim), vm(v_bytes, a.dim);
+  Lanes<DP> lanes;
+  auto fetch = [&](int k0, char* kt, char* vt) {
+    km.move(kp + k0 * k_bytes, kt, s.m - k0, k_bytes, a.dim);
+    vm.move(vp + k0 * v_bytes, vt, s.m - k0, v_bytes, a.dim);
+  };
+  auto one = [&](int k0, const char* kt, const char* vt, char* next_k, char* next_v) {
+    landed();
+    if (k0 + kTile < need) fetch(k0 + kTile, next_k, next_v);
+    if (k0 >= wave_need) return;
+    const bool all = k0 + kTile <= wave_all;
+    lanes.again();
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      f32x4 sc[2][2], dp[2][2];  // [row set][block of keys]
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        sc[0][b] = sc[1][b] = dp[0][b] = dp[1][b] = f32x4{};
+#pragma unroll
+        for (int ks = 0; ks < T::KS; ++ks) {
+          const i32x4 kf = row_fragment<DP>(kt, lanes, 2 * half + b, ks);
+          const i32x4 vf = row_fragment<DP>(vt, lanes, 2 * half + b, ks);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            sc[i][b] = mfma16_v<IN>(kf, qf[i][ks], sc[i][b]);
+            dp[i][b] = mfma16_v<IN>(vf, gf[i][ks], dp[i][b]);
+          }
+        }
+      }
+      i32x4 sf[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float p = __builtin_amdgcn_exp2f(fmaf(sc[i][b][r], a.scale_log2, nl[i]));
+            dp[i][b][r] = p * (dp[i][b][r] - delta[i]);
+          }
+        if (!all) {
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (k0 + 32 * half + 16 * b + 4 * quad + r >= seen[i]) dp[i][b][r] = 0.0f;
+        }
+        sf[i] = pack_blocks<IN>(dp[i][0], dp[i][1]);
+      }
+#pragma unroll
+      for (int d = 0; d < T::DB; ++d) {
+        const i32x4 kf = column_fragment<DP>(kt, lanes, half, d);
+        dq[0][d] = mfma16_v<IN>(kf, sf[0], dq[0][d]);
+        dq[1][d] = mfma16_v<IN>(kf, sf[1], dq[1][d]);
+      }
+    }
+  };
+  if (need > 0) fetch(0, st.x0, st.y0);
+  for (int k0 = 0; k0 < need; k0 += 2 * kTile) {
+    one(k0, st.x0, st.y0, st.x1, st.y1);
+    if (k0 + kTile < need) one(k0 + kTile, st.x1, st.y1, st.x0, st.y0);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int64_t row = w0 + 16 * i + col, t = row / a.group;
+    const int64_t h = kh * a.group + (row - t * a.group);
+    if (row < rows) store_rows<IN, DP>(dq[i], a.scale, a.dq, ((s.q0 + t) * a.q_heads + h) * a.dim, a.dim);
+  }
+}
+
 // Segment i of the keys: as for the queries, with the rows before and behind the sequences.
 __device__ __forceinline__ int64_t key_start(const AttnArgs& a, int i) {
   return i <= 0 ? 0 : i > a.batch + 1 ? a.k_rows : k_start(a, i - 1);
 }
 
-template <int IN, int DP>
-__global__ __launch_bounds__(kThreads, 1) void attention_dkv_kernel(AttnArgs a) {
+// Moves 64 packed rows of a sequence's q or do to LDS (rows past the last: zeros).  The rows of
+// a thread keep their query and head as counts that advance by 64 rows.
+template <int DP>
+struct RowMover {
+  static constexpr int N = kTile * TileOf<DP>::SLOTS / kThreads, ROWS = kThreads / TileOf<DP>::SLOTS;
+  int query[N], head[N];  // of the group
+  int first, first_head;  // of the step's first row
+  int per, rest;          // queries of 64 rows, and the heads left over
+  unsigned slot;          // its byte, or OOB
+  __device__ __forceinline__ RowMover(int from, int group, int dim) {
+    per = kTile / group;
+    rest = kTile - per * group;
+    first = __builtin_amdgcn_readfirstlane(from / group);
+    first_head = from - first * group;
+    const int row = threadIdx.x / TileOf<DP>::SLOTS;
+    const int c = (threadIdx.x % TileOf<DP>::SLOTS) ^ (row & (TileOf<DP>::SLOTS - 1));
+    slot = c * 8 < dim ? c * 16 : OOB;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int r = from + row + i * ROWS;
+      query[i] = r / group;
+      head[i] = r - query[i] * group;
+    }
+  }
+  __device__ __forceinline__ void advance(int& q, int& h, int group) const {
+    h += rest;
+    const bool over = h >= group;
+    h -= over ? group : 0;
+    q += over ? per + 1 : per;
+  }
+  __device__ __forceinline__ void advance(int group) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) advance(query[i], head[i], group);
+    advance(first, first_head, group);
+  }
+  // base: the sequence's first query's first head of the group
+  __device__ __forceinline__ void move(const char* base, int64_t token_bytes, int64_t head_bytes, int64_t queries,
+                                       char* to) const {
+    const auto buf = buffer_at(base + first * token_bytes);
+    char* const mine = to + __builtin_amdgcn_readfirstlane(threadIdx.x & ~63) * 16;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const unsigned off = (unsigned)((query[i] - first) * (int)token_bytes) + (unsigned)(head[i] * (int)head_bytes) + slot;
+      dma16(buf, mine + i * kThreads * 16, query[i] < queries && slot != OOB ? off : OOB, 0);
+    }
+  }
+};
+
+// dk (DK) or dv of the keys of a tile.
+template <int IN, int DP, bool DK>
+__device__ __forceinline__ void keys_role(const AttnArgs& a, int64_t tile, int kh, const Stages<DP>& st) {
   using T = TileOf<DP>;
-  __shared__ __attribute__((aligned(16))) char lds[2][2][kTile * T::PITCH];
-  __shared__ __attribute__((aligned(16))) float stat[2][2][kTile];
-  __shared__ __attribute__((aligned(16))) int sees[2][kTile];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x / 64, quad = lane / 16, col = lane % 16;
-  const int kh = blockIdx.x % a.k_heads;
-  const int64_t tile = blockIdx.x / a.k_heads;  // the first keys (the most rows) first
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int quad = lane / 16, col = lane % 16;
   int lo = 0, hi = a.batch + 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) / 2;
-    if (key_start(a, mid) / kKeys + mid <= tile) lo = mid;
+    if (key_start(a, mid) / kBlock + mid <= tile) lo = mid;
     else hi = mid - 1;
   }
   const int64_t k_first = key_start(a, lo);
   const int64_t k_end = lo == a.batch + 1 ? a.k_rows : key_start(a, lo + 1);
-  const int64_t c0 = (tile - (k_first / kKeys + lo)) * kKeys;  // of the segment
+  const int64_t c0 = (tile - (k_first / kBlock + lo)) * kBlock;  // of the segment
   if (c0 >= k_end - k_first) return;
   const Sequence s = segment(a, lo);
-  const int64_t rows = s.n * a.group;
+  const int rows = (int)(s.n * a.group);
   const int64_t w0 = c0 + 32 * wave;
-
-  i32x4 kf[2][T::KS], vf[2][T::KS];
-  f32x4 dk[2][T::DB], dv[2][T::DB];
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int64_t key = w0 + 16 * j + col;
-    const bool ok = key < s.m;
-    row_operand<DP>(kf[j], static_cast<const char*>(a.k) + 2 * ((k_first + key) * a.k_token + kh * a.k_head), ok, a.dim);
-    row_operand<DP>(vf[j], static_cast<const char*>(a.v) + 2 * ((k_first + key) * a.v_token + kh * a.v_head), ok, a.dim);
-#pragma unroll
-    for (int d = 0; d < T::DB; ++d) dk[j][d] = dv[j][d] = f32x4{};
-  }
-  // the first query that sees a key
+  // the first row that sees a key
   auto first_row = [&](int64_t key) {
     if (key >= s.m) return rows;
-    return a.causal ? clamp64(key - (s.m - s.n), 0, s.n) * a.group : (int64_t)0;
+    return a.causal ? (int)clamp64(key - (s.m - s.n), 0, s.n) * a.group : 0;
   };
-  const int64_t from = first_row(c0) / kTile * kTile;
-  const int64_t wave_from = first_row(w0);
-
-  constexpr int N = kTile * T::SLOTS / kThreads;
-  u32x4 nq[N], ng[N];
-  float n_lse = 0.0f, n_delta = 0.0f;
-  int n_seen = 0;
-  auto fetch = [&](int64_t r0) {
+  i32x4 kf[2][T::KS], vf[DK ? 2 : 1][T::KS];
+  f32x4 sum[2][T::DB];
+  int from_row[2];
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int at = threadIdx.x + i * kThreads, r = at / T::SLOTS, c = at % T::SLOTS;
-      const int64_t row = r0 + r, t = row / a.group;
-      const int64_t h = kh * a.group + (row - t * a.group);
-      nq[i] = ng[i] = u32x4{};
-      if (row < rows && c * 8 < a.dim) {
-        nq[i] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(a.q) + 2 * ((s.q0 + t) * a.q_token + h * a.q_head) + 16 * c);
-        ng[i] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(a.d_o) + 2 * ((s.q0 + t) * a.q_heads + h) * a.dim + 16 * c);
-      }
-    }
-    if (threadIdx.x < kTile) {
-      const int64_t row = r0 + threadIdx.x, t = row / a.group;
-      n_seen = 0;
-      n_lse = n_delta = 0.0f;
-      if (row < rows) {
-        const int64_t at = (s.q0 + t) * a.q_heads + kh * a.group + (row - t * a.group);
-        n_seen = (int)keys_seen(a, s, t);
-        n_lse = a.lse[at] * kLog2e;
-        n_delta = a.delta[at];
-      }
-    }
-  };
-  auto put = [&](int stage) {
+  for (int j = 0; j < 2; ++j) {
+    const int64_t key = w0 + 16 * j + col;
+    row_operand<DP>(kf[j], static_cast<const char*>(a.k) + 2 * ((k_first + key) * a.k_token + kh * a.k_head), key < s.m, a.dim);
+    if constexpr (DK)
+      row_operand<DP>(vf[j], static_cast<const char*>(a.v) + 2 * ((k_first + key) * a.v_token + kh * a.v_head), key < s.m, a.dim);
+    from_row[j] = first_row(key);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int at = threadIdx.x + i * kThreads, r = at / T::SLOTS, c = at % T::SLOTS;
-      *reinterpret_cast<u32x4*>(lds[stage][0] + T::at(r, c)) = nq[i];
-      *reinterpret_cast<u32x4*>(lds[stage][1] + T::at(r, c)) = ng[i];
-    }
-    if (threadIdx.x < kTile) {
-      stat[stage][0][threadIdx.x] = n_lse;
-      stat[stage][1][threadIdx.x] = n_delta;
-      sees[stage][threadIdx.x] = n_seen;
-    }
-  };
-  if (from < rows) {
-    fetch(from);
-    put(0);
+    for (int d = 0; d < T::DB; ++d) sum[j][d] = f32x4{};
   }
-  __syncthreads();
+  const int from = first_row(c0) / kTile * kTile;
+  const int wave_from = first_row(w0), wave_all = first_row(w0 + 31);
+
+  const char* const qp = static_cast<const char*>(a.q) + 2 * (s.q0 * a.q_token + (int64_t)kh * a.group * a.q_head);
+  const char* const gp = static_cast<const char*>(a.d_o) + 2 * (s.q0 * a.q_heads + (int64_t)kh * a.group) * a.dim;
+  const float* const stats = a.stats + ((int64_t)kh * a.q_rows + s.q0) * a.group;
+  const int64_t all_rows = a.q_rows * a.q_heads;
+  RowMover<DP> rm(from, a.group, a.dim);
   Lanes<DP> lanes;
-  int stage = 0;
-  for (int64_t r0 = from; r0 < rows; r0 += kTile) {
-    const bool more = r0 + kTile < rows;
-    if (more) fetch(r0 + kTile);
-    const char* const qt = lds[stage][0];
-    const char* const gt = lds[stage][1];
-    if (r0 + kTile > wave_from && w0 < s.m) {
-      // all rows of the step see all of the wave's keys
-      const bool all = r0 + kTile <= rows && w0 + 32 <= sees[stage][0];
+  auto fetch = [&](int r0, char* qt, char* gt, float* nl, float* delta) {
+    rm.move(qp, 2 * a.q_token, 2 * a.q_head, s.n, qt);
+    rm.move(gp, 2 * (int64_t)a.q_heads * a.dim, 2 * a.dim, s.n, gt);
+    rm.advance(a.group);
+    // a wave moves each of the two numbers of the rows
+    if (wave < (DK ? 2 : 1)) {
+      const auto buf = buffer_at(stats + (wave ? all_rows : 0) + r0);
+      dma4(buf, reinterpret_cast<char*>(wave ? delta : nl), r0 + lane < rows ? (unsigned)(lane * 4) : OOB);
+    }
+  };
+  auto one = [&](int r0, const char* qt, const char* gt, const float* nls, const float* deltas, char* next_q, char* next_g,
+                 float* next_n, float* next_d) {
+    landed();
+    if (r0 + kTile < rows) fetch(r0 + kTile, next_q, next_g, next_n, next_d);
+    if (r0 + kTile <= wave_from) return;
+    const bool all = r0 >= wave_all;  // (rows past the last are zeros and add nothing)
+    lanes.again();
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        f32x4 sc[2][2], dp[2][2];  // [block of rows][block of keys]
+    for (int half = 0; half < 2; ++half) {
+      f32x4 sc[2][2], dp[2][2];  // [block of rows][block of keys]
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          sc[b][0] = sc[b][1] = dp[b][0] = dp[b][1] = f32x4{};
+      for (int b = 0; b < 2; ++b) {
+        sc[b][0] = sc[b][1] = dp[b][0] = dp[b][1] = f32x4{};
 #pragma unroll
-          for (int ks = 0; ks < T::KS; ++ks) {
-            const i32x4 qf = row_fragment<DP>(qt, lanes, 2 * half + b, ks);
+        for (int ks = 0; ks < T::KS; ++ks) {
+          const i32x4 qf = row_fragment<DP>(qt, lanes, 2 * half + b, ks);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) sc[b][j] = mfma16_v<IN>(qf, kf[j][ks], sc[b][j]);
+          if constexpr (DK) {
             const i32x4 gf = row_fragment<DP>(gt, lanes, 2 * half + b, ks);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              sc[b][j] = mfma16_v<IN>(qf, kf[j][ks], sc[b][j]);
-              dp[b][j] = mfma16_v<IN>(gf, vf[j][ks], dp[b][j]);
-            }
-          }
-        }
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          const int at = 32 * half + 16 * b + 4 * quad;
-          const f32x4 lse = *reinterpret_cast<const f32x4*>(&stat[stage][0][at]);
-          const f32x4 delta = *reinterpret_cast<const f32x4*>(&stat[stage][1][at]);
-          const i32x4 seen = *reinterpret_cast<const i32x4*>(&sees[stage][at]);
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              float p = __builtin_amdgcn_exp2f(fmaf(sc[b][j][r], a.scale_log2, -lse[r]));
-              if (!all && w0 + 16 * j + col >= seen[r]) p = 0.0f;
-              const bool off = !all && w0 + 16 * j + col >= seen[r];
-              sc[b][j][r] = p;
-              dp[b][j][r] = off ? 0.0f : p * (dp[b][j][r] - delta[r]);
-            }
-        }
-        i32x4 pf[2], sf[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          pf[j] = pack_blocks<IN>(sc[0][j], sc[1][j]);
-          sf[j] = pack_blocks<IN>(dp[0][j], dp[1][j]);
-        }
-#pragma unroll
-        for (int d = 0; d < T::DB; ++d) {
-          const i32x4 gf = column_fragment<DP>(gt, lanes, half, d);
-          const i32x4 qf = column_fragment<DP>(qt, lanes, half, d);
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            dv[j][d] = mfma16_v<IN>(gf, pf[j], dv[j][d]);
-            dk[j][d] = mfma16_v<IN>(qf, sf[j], dk[j][d]);
+            for (int j = 0; j < 2; ++j) dp[b][j] = mfma16_v<IN>(gf, vf[j][ks], dp[b][j]);
           }
         }
       }
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const int at = 32 * half + 16 * b + 4 * quad;
+        const f32x4 nl = *reinterpret_cast<const f32x4*>(nls + at);
+        f32x4 delta{};
+        if constexpr (DK) delta = *reinterpret_cast<const f32x4*>(deltas + at);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float p = __builtin_amdgcn_exp2f(fmaf(sc[b][j][r], a.scale_log2, nl[r]));
+            sc[b][j][r] = DK ? p * (dp[b][j][r] - delta[r]) : p;
+          }
+          if (!all) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (r0 + at + r < from_row[j]) sc[b][j][r] = 0.0f;
+          }
+        }
+      }
+      const i32x4 f0 = pack_blocks<IN>(sc[0][0], sc[1][0]), f1 = pack_blocks<IN>(sc[0][1], sc[1][1]);
+#pragma unroll
+      for (int d = 0; d < T::DB; ++d) {
+        const i32x4 x = column_fragment<DP>(DK ? qt : gt, lanes, half, d);
+        sum[0][d] = mfma16_v<IN>(x, f0, sum[0][d]);
+        sum[1][d] = mfma16_v<IN>(x, f1, sum[1][d]);
+      }
     }
-    if (more) {
-      stage ^= 1;
-      put(stage);
-    }
-    __syncthreads();
+  };
+  if (from < rows) fetch(from, st.x0, st.y0, st.n0, st.d0);
+  for (int r0 = from; r0 < rows; r0 += 2 * kTile) {
+    one(r0, st.x0, st.y0, st.n0, st.d0, st.x1, st.y1, st.n1, st.d1);
+    if (r0 + kTile < rows) one(r0 + kTile, st.x1, st.y1, st.n1, st.d1, st.x0, st.y0, st.n0, st.d0);
   }
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const int64_t key = w0 + 16 * j + col;
-    if (key >= k_end - k_first) continue;
-    const int64_t at = ((k_first + key) * a.k_heads + kh) * a.dim;
-#pragma unroll
-    for (int d = 0; d < T::DB; ++d) {
-      const int c = 16 * d + 4 * quad;
-      if (c < a.dim) {
-        const f32x4 x = dk[j][d] * a.scale, y = dv[j][d];
-        *reinterpret_cast<i32x2*>(static_cast<char*>(a.dk) + 2 * (at + c)) = i32x2{pack2<IN>(x[0], x[1]), pack2<IN>(x[2], x[3])};
-        *reinterpret_cast<i32x2*>(static_cast<char*>(a.dv) + 2 * (at + c)) = i32x2{pack2<IN>(y[0], y[1]), pack2<IN>(y[2], y[3])};
-      }
-    }
+    if (key < k_end - k_first)
+      store_rows<IN, DP>(sum[j], DK ? a.scale : 1.0f, DK ? a.dk : a.dv, ((k_first + key) * a.k_heads + kh) * a.dim, a.dim);
   }
 }
 
+// Workgroups: the tiles of keys for dk, of rows for dq, of keys for dv; a key head's tiles in
+// descending order of work.
 template <int IN, int DP>
-__global__ __launch_bounds__(kThreads, 1) void attention_dq_kernel(AttnArgs a) {
-  using T = TileOf<DP>;
-  __shared__ __attribute__((aligned(16))) char lds[2][2][kTile * T::PITCH];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x / 64, quad = lane / 16, col = lane % 16;
-  const int64_t tiles = gridDim.x / a.k_heads;
+__global__ __launch_bounds__(kThreads, 2) void attention_backward_kernel(AttnArgs a) {
+  constexpr int BYTES = kTile * TileOf<DP>::PITCH;
+  __shared__ __attribute__((aligned(1024))) char x0[BYTES], y0[BYTES], x1[BYTES], y1[BYTES];
+  __shared__ __attribute__((aligned(256))) float n0[kTile], d0[kTile], n1[kTile], d1[kTile];
+  const Stages<DP> st{x0, y0, x1, y1, n0, d0, n1, d1};
   const int kh = blockIdx.x % a.k_heads;
-  const int64_t tile = tiles - 1 - blockIdx.x / a.k_heads;
-  const int seg = segment_of_tile(a, tile, kRows);
-  const Sequence s = segment(a, seg);
-  const int64_t r0 = (tile - (s.q0 * a.group / kRows + seg)) * kRows;
-  const int64_t rows = s.n * a.group;
-  if (r0 >= rows) return;
-
-  int64_t out[2];
-  bool live[2];
-  int seen[2];
-  float lse[2], delta[2];
-  i32x4 qf[2][T::KS], gf[2][T::KS];
-  f32x4 dq[2][T::DB];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int64_t row = r0 + 32 * wave + 16 * i + col, t = row / a.group;
-    const int64_t h = kh * a.group + (row - t * a.group);
-    live[i] = row < rows;
-    out[i] = (s.q0 + t) * a.q_heads + h;
-    seen[i] = (int)keys_seen(a, s, t);
-    lse[i] = live[i] ? a.lse[out[i]] * kLog2e : 0.0f;
-    delta[i] = live[i] ? a.delta[out[i]] : 0.0f;
-    row_operand<DP>(qf[i], static_cast<const char*>(a.q) + 2 * ((s.q0 + t) * a.q_token + h * a.q_head), live[i], a.dim);
-    row_operand<DP>(gf[i], static_cast<const char*>(a.d_o) + 2 * out[i] * a.dim, live[i], a.dim);
-#pragma unroll
-    for (int d = 0; d < T::DB; ++d) dq[i][d] = f32x4{};
-  }
-  auto seen_of = [&](int64_t r) { return (int)keys_seen(a, s, (r < rows ? r : rows - 1) / a.group); };
-  const int need = __builtin_amdgcn_readfirstlane(seen_of(r0 + kRows - 1));
-  const int64_t w0 = r0 + 32 * wave;
-  const int wave_need = __builtin_amdgcn_readfirstlane(w0 < rows ? seen_of(w0 + 31) : 0);
-  const int wave_all = __builtin_amdgcn_readfirstlane(w0 + 31 < rows ? seen_of(w0) : 0);
-
-  const int64_t k_bytes = 2 * a.k_token, v_bytes = 2 * a.v_token;
-  const char* const kp = static_cast<const char*>(a.k) + 2 * (s.k0 * a.k_token + kh * a.k_head);
-  const char* const vp = static_cast<const char*>(a.v) + 2 * (s.k0 * a.v_token + kh * a.v_head);
-  constexpr int N = kTile * T::SLOTS / kThreads;
-  u32x4 nk[N], nv[N];
-  auto fetch = [&](int64_t k0) {
-    const auto kb = buffer_at(kp + k0 * k_bytes), vb = buffer_at(vp + k0 * v_bytes);
-    const int left = (int)(s.m - k0 < kTile ? s.m - k0 : kTile);
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int at = threadIdx.x + i * kThreads, r = at / T::SLOTS, c = at % T::SLOTS;
-      const bool ok = r < left && c * 8 < a.dim;
-      nk[i] = load_b128(kb, ok ? (unsigned)(r * (int)k_bytes + c * 16) : OOB);
-      nv[i] = load_b128(vb, ok ? (unsigned)(r * (int)v_bytes + c * 16) : OOB);
-    }
-  };
-  auto put = [&](int stage) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int at = threadIdx.x + i * kThreads, r = at / T::SLOTS, c = at % T::SLOTS;
-      *reinterpret_cast<u32x4*>(lds[stage][0] + T::at(r, c)) = nk[i];
-      *reinterpret_cast<u32x4*>(lds[stage][1] + T::at(r, c)) = nv[i];
-    }
-  };
-  if (need > 0) {
-    fetch(0);
-    put(0);
-  }
-  __syncthreads();
-  Lanes<DP> lanes;
-  int stage = 0;
-  for (int k0 = 0; k0 < need; k0 += kTile) {
-    const bool more = k0 + kTile < need;
-    if (more) fetch(k0 + kTile);
-    const char* const kt = lds[stage][0];
-    const char* const vt = lds[stage][1];
-    if (k0 < wave_need) {
-      const bool all = k0 + kTile <= wave_all;
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        f32x4 sc[2][2], dp[2][2];  // [row set][block of keys]
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          sc[0][b] = sc[1][b] = dp[0][b] = dp[1][b] = f32x4{};
-#pragma unroll
-          for (int ks = 0; ks < T::KS; ++ks) {
-            const i32x4 kf = row_fragment<DP>(kt, lanes, 2 * half + b, ks);
-            const i32x4 vf = row_fragment<DP>(vt, lanes, 2 * half + b, ks);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              sc[i][b] = mfma16_v<IN>(kf, qf[i][ks], sc[i][b]);
-              dp[i][b] = mfma16_v<IN>(vf, gf[i][ks], dp[i][b]);
-            }
-          }
-        }
-        i32x4 sf[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-#pragma unroll
-          for (int b = 0; b < 2; ++b)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const bool off = !all && k0 + 32 * half + 16 * b + 4 * quad + r >= seen[i];
-              const float p = __builtin_amdgcn_exp2f(fmaf(sc[i][b][r], a.scale_log2, -lse[i]));
-              dp[i][b][r] = off ? 0.0f : p * (dp[i][b][r] - delta[i]);
-            }
-          sf[i] = pack_blocks<IN>(dp[i][0], dp[i][1]);
-        }
-#pragma unroll
-        for (int d = 0; d < T::DB; ++d) {
-          const i32x4 kf = column_fragment<DP>(kt, lanes, half, d);
-          dq[0][d] = mfma16_v<IN>(kf, sf[0], dq[0][d]);
-          dq[1][d] = mfma16_v<IN>(kf, sf[1], dq[1][d]);
-        }
-      }
-    }
-    if (more) {
-      stage ^= 1;
-      put(stage);
-    }
-    __syncthreads();
-  }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    if (!live[i]) continue;
-#pragma unroll
-    for (int d = 0; d < T::DB; ++d) {
-      const int c = 16 * d + 4 * quad;
-      if (c < a.dim) {
-        const f32x4 x = dq[i][d] * a.scale;
-        *reinterpret_cast<i32x2*>(static_cast<char*>(a.dq) + 2 * (out[i] * a.dim + c)) =
-            i32x2{pack2<IN>(x[0], x[1]), pack2<IN>(x[2], x[3])};
-      }
-    }
-  }
+  int64_t tile = blockIdx.x / a.k_heads;
+  if (tile < a.k_tiles) return keys_role<IN, DP, true>(a, tile, kh, st);
+  tile -= a.k_tiles;
+  if (tile < a.q_tiles) return rows_role<IN, DP>(a, a.q_tiles - 1 - tile, kh, st);
+  return keys_role<IN, DP, false>(a, tile - a.q_tiles, kh, st);
 }
 
 template <int IN, int DP>
-hipError_t launch_in(const AttnArgs& a, hipStream_t s) {
-  hipError_t e = hipSuccess;
+hipError_t launch_in(AttnArgs a, hipStream_t s) {
   if (a.q_rows > 0) {
     hipLaunchKernelGGL(attention_delta_kernel<IN>, dim3((unsigned)((a.q_rows * a.q_heads + 15) / 16)),
                        dim3(256), 0, s, a);
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    const int64_t tiles = a.q_rows * a.group / kRows + a.batch + 2;
-    hipLaunchKernelGGL((attention_dq_kernel<IN, DP>), dim3((unsigned)(tiles * a.k_heads)), dim3(kThreads),
-                       0, s, a);
-    e = hipGetLastError();
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (a.k_rows > 0) {
-    const int64_t tiles = a.k_rows / kKeys + a.batch + 2;
-    hipLaunchKernelGGL((attention_dkv_kernel<IN, DP>), dim3((unsigned)(tiles * a.k_heads)), dim3(kThreads),
-                       0, s, a);
-    e = hipGetLastError();
-  }
-  return e;
+  a.q_tiles = a.q_rows > 0 ? a.q_rows * a.group / kBlock + a.batch + 2 : 0;
+  a.k_tiles = a.k_rows > 0 ? a.k_rows / kBlock + a.batch + 2 : 0;
+  hipLaunchKernelGGL((attention_backward_kernel<IN, DP>), dim3((unsigned)((a.q_tiles + 2 * a.k_tiles) * a.k_heads)),
+                     dim3(kThreads), 0, s, a);
+  return hipGetLastError();
 }
 
 template <int IN>

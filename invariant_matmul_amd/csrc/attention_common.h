@@ -105,6 +105,44 @@ struct TileOf {
   }
 };
 
+// Workgroups of the kernels that walk through a sequence: four waves with 32 rows or keys
+// each, two workgroups on a compute unit.
+constexpr int kWaves = 4, kThreads = 64 * kWaves;
+
+// Moves a tile of keys or values to LDS; what lies past its `left` rows or past the
+// dimension is zeros.  A wave fills 1 KB at a time, lane l the 16 bytes at 16 l: each
+// lane fetches what belongs in its fixed slot.  The workgroup's next rows have a buffer of
+// their own, so that one offset serves all.
+template <int DP>
+struct Mover {
+  static constexpr int N = kTile * TileOf<DP>::SLOTS / kThreads, ROWS = kThreads / TileOf<DP>::SLOTS;
+  static_assert(ROWS % TileOf<DP>::SLOTS == 0, "the rows of a thread have the same slot");
+  unsigned off;  // of the thread's first row
+  __device__ __forceinline__ Mover(int64_t row_bytes, int dim) {
+    const int row = threadIdx.x / TileOf<DP>::SLOTS;
+    const int slot = (threadIdx.x % TileOf<DP>::SLOTS) ^ (row & (TileOf<DP>::SLOTS - 1));
+    off = slot * 8 < dim ? (unsigned)(row * (int)row_bytes + slot * 16) : OOB;
+  }
+  __device__ __forceinline__ void move(const char* from, char* to, int64_t left, int64_t row_bytes, int dim) const {
+    // (rows behind the last: past the buffer's end, or, where rows overlap, values that no row sees)
+    const int rows = (int)(left < kTile ? left : kTile);
+    char* const mine = to + __builtin_amdgcn_readfirstlane(threadIdx.x & ~63) * 16;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int last = rows - 1 - i * ROWS;
+      const auto buf = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(from) + i * ROWS * row_bytes, 0,
+                                                         last < 0 ? 0 : last * (int)row_bytes + 2 * dim, 0x00020000);
+      dma16(buf, mine + i * kThreads * 16, off, 0);
+    }
+  }
+};
+
+// This wave's transfers have landed, and everyone's; and everyone has read what it read before.
+__device__ __forceinline__ void landed() {
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+}
+
 // Where a lane's pieces of a tile lie.  Slots are XORed, so a piece's place is that of the
 // first one XOR a constant: `again` keeps the compiler from holding all of them in
 // registers over a loop.

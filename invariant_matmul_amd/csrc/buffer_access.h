@@ -24,5 +24,12 @@ __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t buf, char* dst, uns
 #endif
 }
 
+// ... 4 bytes per lane (lane l to dst + 4 l).
+__device__ __forceinline__ void dma4(__amdgpu_buffer_rsrc_t buf, char* dst, unsigned off) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, IMM_LDS(dst), 4, off, 0, 0, 0);
+#endif
+}
+
 }  // namespace dev
 }  // namespace imm

@@ -203,7 +203,7 @@ gemm_status attention_plan(int64_t q_rows, int64_t k_rows, int64_t batch, int q_
   // fewer than 2^32 threads
   if (q_rows > INT_MAX / q_heads || k_rows > (int64_t)1 << 30 || batch > 1 << 20 ||
       (q_rows * group / 128 + batch + 2) * k_heads >= (int64_t)1 << 23 ||
-      (k_rows / 128 + batch + 2) * k_heads >= (int64_t)1 << 23)
+      (k_rows / 128 + batch + 2) * k_heads >= (int64_t)1 << 22)
     return GEMM_ERR_UNSUPPORTED;
   attention_plan_s p{q_rows, k_rows, max_q, (int)batch, q_heads, k_heads, dim, dtype, causal != 0, false, scale};
   if (p.max_q == 0 || p.max_q > q_rows) p.max_q = q_rows;
@@ -219,7 +219,7 @@ size_t attention_workspace_size(attention_plan_t p) {
 }
 
 size_t attention_backward_workspace_size(attention_plan_t p) {
-  return p ? (size_t)p->q_rows * (size_t)p->q_heads * sizeof(float) : 0;
+  return p ? 2 * (size_t)p->q_rows * (size_t)p->q_heads * sizeof(float) : 0;
 }
 
 static gemm_status attention_args(attention_plan_t p, const void* q, int64_t q_token,
@@ -305,6 +305,11 @@ gemm_status attention_backward(attention_plan_t p, const void* d_o, const void* 
                                   cu_k, k_lens, &a);
   if (st != GEMM_OK) return st;
   const bool rows = p->q_rows > 0, keys = p->k_rows > 0;
+  // 64 packed rows of q, and of the contiguous gradient, within 31 bits
+  const int64_t reach = ((int64_t)1 << 30) - kAttnMaxDim;
+  if (rows && (q_token > reach / 128 || (a.group > 1 && q_head > reach / 2 / (a.group - 1)) ||
+               (int64_t)p->q_heads * p->dim > reach / 128))
+    return GEMM_ERR_UNSUPPORTED;
   const size_t need = attention_backward_workspace_size(p);
   if (rows && (!good(d_o, 16) || !good(o, 16) || !aligned(o_low, 16) || !good(lse, 4) || !good(dq, 16))) return GEMM_ERR_INVALID_VALUE;
   if (keys && (!good(dk, 16) || !good(dv, 16))) return GEMM_ERR_INVALID_VALUE;
@@ -333,7 +338,7 @@ gemm_status attention_backward(attention_plan_t p, const void* d_o, const void* 
   a.o = const_cast<void*>(o);
   a.o_low = const_cast<void*>(o_low);
   a.lse = const_cast<float*>(lse);
-  a.delta = static_cast<float*>(workspace);
+  a.stats = static_cast<float*>(workspace);
   a.dq = dq, a.dk = dk, a.dv = dv;
   return status_of(launch_attention_backward(p->dtype, a, static_cast<hipStream_t>(stream)));
 }

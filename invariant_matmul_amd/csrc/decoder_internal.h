@@ -62,7 +62,8 @@ struct AttnArgs {
   int part_rows;           // rows a chunk slot holds: max_q group
   // backward
   const void* d_o;         // [q_rows, q_heads, dim]
-  float* delta;            // [q_rows, q_heads]
+  float* stats;            // -lse log2(e) and delta, [2, k_heads, q_rows, group]
+  int64_t q_tiles, k_tiles;
   void *dq, *dk, *dv;      // contiguous
 };
 bool attention_few_rows(int64_t max_q, int group);

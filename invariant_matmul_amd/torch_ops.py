@@ -864,6 +864,8 @@ def attention_backward(do, q, k, v, o, saved, cu_q=None, cu_k=None, *, k_lens=No
     Tk, hk, _ = k.shape
     plan = _attention_plan(Tq, Tk, batch, hq, hk, D, q.dtype, causal, scale, 0)
     q, q_token, q_head = _in_place(q)
+    if (hq // hk - 1) * q_head > 1 << 28:  # a group's heads within 31 bits of each other
+        q, q_token, q_head = _in_place(q.contiguous())
     k, k_token, k_head = _in_place(k)
     v, v_token, v_head = _in_place(v)
     do, o, o_low, lse = _dense(do), _dense(o), _dense(o_low), lse.contiguous()

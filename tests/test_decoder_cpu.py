@@ -116,18 +116,18 @@ def test_attention_refusals():
     assert run(kt=1 << 23) == UNSUPPORTED and run(vt=1 << 23) == UNSUPPORTED  # 256 rows past 31 bits
     many = imm.attention_plan(1000, 600, 2, 8, 2, 128, "bf16")
     assert imm.attention_workspace_size(many) == 0
-    assert imm.attention_backward_workspace_size(many) == 1000 * 8 * 4
+    assert imm.attention_backward_workspace_size(many) == 2 * 1000 * 8 * 4
     # (the group decides with max_q: 64 rows of a key head at most)
     assert imm.attention_workspace_size(imm.attention_plan(64, 600, 1, 2, 2, 64, "bf16")) > 0
     assert imm.attention_workspace_size(imm.attention_plan(65, 600, 1, 2, 2, 64, "bf16")) == 0
 
-    def back(do=P, o=P, low=P, lse=P, dq=P, dk=P, dv=P, ws=P, n=1000 * 8 * 4):
+    def back(do=P, o=P, low=P, lse=P, dq=P, dk=P, dv=P, ws=P, n=2 * 1000 * 8 * 4):
         return L.attention_backward(many.handle, do, P, 1024, 128, P, 256, 128, P, 256, 128, o, low, lse, P, P, 0, dq, dk, dv, ws,
                                     n, None)
 
     for name in ("do", "o", "lse", "dq", "dk", "dv"):
         assert back(**{name: 0}) == INVALID and back(**{name: P + 2}) == INVALID, name
-    assert back(low=P + 2) == INVALID and back(ws=0) == WORKSPACE and back(n=1000 * 8 * 4 - 1) == WORKSPACE
+    assert back(low=P + 2) == INVALID and back(ws=0) == WORKSPACE and back(n=2 * 1000 * 8 * 4 - 1) == WORKSPACE
     empty = imm.attention_plan(0, 600, 2, 8, 2, 128, "bf16")
     assert run(plan=empty, q=0, o=0, n=0) == OK
 
