@@ -60,7 +60,8 @@ __device__ __forceinline__ void load8(const void* x, int64_t i, int64_t end, flo
         f[4 + e] = b[e];
       }
     } else {
-      widen8<IN>(*reinterpret_cast<const u32x4_any*>(static_cast<const char*>(x) + 2 * i), f);
+      const u32x4_t v = *reinterpret_cast<const u32x4_any*>(static_cast<const char*>(x) + 2 * i);
+      widen8<IN>(v, f);
     }
   } else {
 #pragma unroll
@@ -87,10 +88,28 @@ __device__ __forceinline__ uint64_t lane_of(uint64_t v, int lane) {
          (unsigned)__builtin_amdgcn_readlane((int)v, lane);
 }
 
-// A wave's best keys, sorted: lane i holds the i-th (0: none yet).  `last` is entry top - 1.
+__device__ __forceinline__ uint64_t larger(uint64_t a, uint64_t b) { return a > b ? a : b; }
+__device__ __forceinline__ uint64_t smaller(uint64_t a, uint64_t b) { return a < b ? a : b; }
+// A step of a bitonic network over the lanes: the larger of two keys that are `d` lanes
+// apart goes to the lower lane, or to the higher one.
+__device__ __forceinline__ uint64_t exchange(uint64_t key, int d, bool falling) {
+  const uint64_t other = __shfl_xor(key, d);
+  return ((threadIdx.x & d) == 0) == falling ? larger(key, other) : smaller(key, other);
+}
+// Keys of a wave in falling order (a bitonic sort).
+__device__ __forceinline__ uint64_t sorted(uint64_t key) {
+#pragma unroll
+  for (int k = 2; k <= 64; k <<= 1)
+#pragma unroll
+    for (int d = k >> 1; d > 0; d >>= 1) key = exchange(key, d, (threadIdx.x & 63 & k) == 0);
+  return key;
+}
+
+// A wave's 64 best keys, in falling order over its lanes (0: none); `last` is entry top - 1.
 struct Best {
   uint64_t mine, last;
   int top;
+  uint64_t* room;  // LDS for 128 keys
   __device__ __forceinline__ void insert(uint64_t key) {  // uniform, > last
     const uint64_t up = __shfl_up(mine, 1);
     const int lane = threadIdx.x & 63;
@@ -98,16 +117,67 @@ struct Best {
     mine = lane < at ? mine : lane == at ? key : up;
     last = lane_of(mine, top - 1);
   }
-  // every lane's key that is among the best so far
-  __device__ __forceinline__ void offer(uint64_t key) {
-    uint64_t todo = __ballot(key > last);
-    while (todo) {
-      const int l = __ffsll((unsigned long long)todo) - 1;
-      const uint64_t k = lane_of(key, l);
-      todo &= todo - 1;
+  // 64 keys in falling order: the larger of each and of the opposite place are the best 64, in
+  // bitonic order.
+  __device__ __forceinline__ void join(uint64_t key) {
+    mine = larger(mine, __shfl(key, 63 - (threadIdx.x & 63)));
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) mine = exchange(mine, d, true);
+    last = lane_of(mine, top - 1);
+  }
+  // The first `n` keys of the room (n <= 64): by insertion where they are few.
+  __device__ __forceinline__ void take(int n) {
+    const int lane = threadIdx.x & 63;
+    const uint64_t key = lane < n ? room[lane] : 0;
+    if (n > 8) {
+      join(sorted(key));
+      return;
+    }
+    for (int i = 0; i < n; ++i) {
+      const uint64_t k = lane_of(key, i);
       if (k > last) insert(k);
     }
   }
+  // E keys of every lane, the largest of which is `largest`.  Keys that cannot be among
+  // the best are passed by: those below `last`, and, of the first keys, those whose value is
+  // below the top-th largest of the lanes' own largest.  The others are gathered in LDS.
+  template <int E, class KEY>
+  __device__ __forceinline__ void offer(uint64_t largest, KEY&& key) {
+    if (!__any(largest > last)) return;
+    uint64_t least = last;
+    if (last == 0) {
+      unsigned value = 0;
+      for (unsigned bit = 1u << 31; bit; bit >>= 1)
+        if (__popcll(__ballot((unsigned)(largest >> 32) >= (value | bit))) >= top) value |= bit;
+      least = value ? ((uint64_t)value << 32) - 1 : 0;
+    }
+    const int lane = threadIdx.x & 63;
+    int n = 0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const uint64_t k = key(e);
+      const uint64_t found = __ballot(k > least);
+      if (!found) continue;
+      if (k > least) room[n + __popcll(found & ((1ull << lane) - 1))] = k;
+      n += __popcll(found);
+      if (n >= 64) {
+        wait_lds();
+        take(64);
+        least = larger(least, last);
+        n -= 64;
+        const uint64_t rest = room[64 + lane];
+        wait_lds();
+        if (lane < n) room[lane] = rest;
+      }
+    }
+    if (n) {
+      wait_lds();
+      take(n);
+      wait_lds();  // before the room is used again
+    }
+  }
+  // (the room is one wave's: its own LDS operations are in order)
+  __device__ __forceinline__ static void wait_lds() { __builtin_amdgcn_wave_barrier(); }
 };
 
 struct Sums {
@@ -163,17 +233,18 @@ __device__ __forceinline__ Sums take_unit(const void* row, int64_t v0, int64_t v
     }
   const Sums all = join_lanes(Sums{m, s, t});
   if (top) {
-    // a NaN takes no part in m, but is in s
-    const bool some = order(m) > (unsigned)(best.last >> 32) || s != s || best.last == 0;
-    if (__any(some)) {
+    unsigned highest = order(m);
+    if (__any(s != s)) {  // a NaN, which takes no part in m, or an infinity
 #pragma unroll
       for (int i = 0; i < kVecs; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int64_t v = v0 + 512 * i + 8 * lane + e;
-          best.offer(v < vocab ? key_of(x[i][e], v) : 0);
-        }
+        for (int e = 0; e < 8; ++e) highest = max(highest, order(x[i][e]));
     }
+    const uint64_t largest = (uint64_t)highest << 32 | 0xffffffffu;
+    best.offer<8 * kVecs>(largest, [&](int e) {
+      const int64_t v = v0 + 512 * (e / 8) + 8 * lane + e % 8;
+      return v < vocab ? key_of(x[e / 8][e % 8], v) : 0ull;
+    });
   }
   return all;
 }
@@ -181,7 +252,7 @@ __device__ __forceinline__ Sums take_unit(const void* row, int64_t v0, int64_t v
 // The row's results from its units' sums and the waves' lists, by one wave.
 template <int IN>
 __device__ __forceinline__ void finish(const LogprobsArgs& g, int64_t row, const float* sums,
-                                       const uint64_t* lists, int nlists) {
+                                       const uint64_t* lists, int nlists, uint64_t* room) {
   const int lane = threadIdx.x & 63;
   Sums a{kNone, 0.0f, 0.0f};
   for (int u = lane; u < g.units; u += 64)
@@ -204,8 +275,18 @@ __device__ __forceinline__ void finish(const LogprobsArgs& g, int64_t row, const
     g.logprob[row * g.n + i] = lp;
   }
   if (g.top) {
-    Best best{0, 0, g.top};
-    for (int i = 0; i < nlists; ++i) best.offer(lane < g.top ? lists[(int64_t)i * g.top + lane] : 0);
+    Best best{0, 0, g.top, room};
+    // a list a lane, 16 entries at a time (they fall: the first is the largest)
+    for (int l0 = 0; l0 < nlists; l0 += 64) {
+      const uint64_t* const list = lists + (int64_t)(l0 + lane) * g.top;
+      const bool mine = l0 + lane < nlists;
+      for (int e0 = 0; e0 < g.top; e0 += 16) {
+        uint64_t k[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) k[e] = mine && e0 + e < g.top ? list[e0 + e] : 0;
+        best.offer<16>(k[0], [&](int e) { return k[e]; });
+      }
+    }
     if (lane < g.top) {
       g.top_logprob[row * g.top + lane] = (value_of((unsigned)(best.mine >> 32)) - a.m) - ln_s;
       g.top_token[row * g.top + lane] = 0xffffffffu - (unsigned)best.mine;
@@ -217,13 +298,13 @@ __device__ __forceinline__ void finish(const LogprobsArgs& g, int64_t row, const
 template <int IN, bool PARTS>
 __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobsArgs g) {
   extern __shared__ float shared[];  // sums [units, 3] of a whole row
-  __shared__ uint64_t lists[kWaves][kLogprobsMaxTop];
+  __shared__ uint64_t lists[kWaves][kLogprobsMaxTop], room[kWaves][128];
   const int wave = threadIdx.x / 64, lane = threadIdx.x & 63;
   const int64_t row = PARTS ? blockIdx.x / g.parts : blockIdx.x;
   const int part = PARTS ? (int)(blockIdx.x % g.parts) : 0;
   const char* const x = static_cast<const char*>(g.x) + row * g.row_stride * Size<IN>::value;
   float* const sums = PARTS ? g.sums + row * g.units * 3 : shared;
-  Best best{0, 0, g.top ? g.top : 1};
+  Best best{0, 0, g.top ? g.top : 1, room[wave]};
   const int step = PARTS ? kWaves * g.parts : kWaves;
   for (int u = part * kWaves + wave; u < g.units; u += step) {
     const Sums a = take_unit<IN>(x, (int64_t)u * kUnit, g.vocab, best, g.top > 0);
@@ -239,15 +320,16 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobsArgs g) {
   } else {
     if (lane < g.top) lists[0][wave * g.top + lane] = best.mine;
     __syncthreads();
-    if (wave == 0) finish<IN>(g, row, sums, lists[0], kWaves);
+    if (wave == 0) finish<IN>(g, row, sums, lists[0], kWaves, room[0]);
   }
 }
 
 template <int IN>
 __global__ __launch_bounds__(64) void logprobs_join_kernel(LogprobsArgs g) {
   const int64_t row = blockIdx.x;
+  __shared__ uint64_t room[128];
   const int lists = g.parts * kWaves;
-  finish<IN>(g, row, g.sums + row * g.units * 3, g.best + row * lists * g.top, lists);
+  finish<IN>(g, row, g.sums + row * g.units * 3, g.best + row * lists * g.top, lists, room);
 }
 
 // The gradient of the logits: a workgroup takes 2048 logits of a row.
