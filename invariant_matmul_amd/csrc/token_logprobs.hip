@@ -88,20 +88,60 @@ __device__ __forceinline__ uint64_t lane_of(uint64_t v, int lane) {
          (unsigned)__builtin_amdgcn_readlane((int)v, lane);
 }
 
+// The value of the lane D lanes apart (lane ^ D), by moves within the vector unit: a
+// shuffle through LDS takes ten times as long, and a join of 64 lanes is 6 to 21 of them, each
+// waiting for the last.
+template <int D>
+__device__ __forceinline__ unsigned lane_xor(unsigned v) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  constexpr int ALL = 0xf;
+  if constexpr (D == 1) return __builtin_amdgcn_mov_dpp(v, 0xb1, ALL, ALL, true);        // within four: 1 0 3 2
+  else if constexpr (D == 2) return __builtin_amdgcn_mov_dpp(v, 0x4e, ALL, ALL, true);   // 2 3 0 1
+  else if constexpr (D == 4)                                                             // eight mirrored, fours mirrored
+    return __builtin_amdgcn_mov_dpp(__builtin_amdgcn_mov_dpp(v, 0x141, ALL, ALL, true), 0x1b, ALL, ALL, true);
+  else if constexpr (D == 8) return __builtin_amdgcn_mov_dpp(v, 0x128, ALL, ALL, true);  // sixteen turned by 8
+  else {
+    const auto r = D == 16 ? __builtin_amdgcn_permlane16_swap(v, v, false, false)
+                           : __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return threadIdx.x & D ? r[0] : r[1];
+  }
+#else
+  return v;
+#endif
+}
+template <int D>
+__device__ __forceinline__ float lane_xor(float v) { return __uint_as_float(lane_xor<D>(__float_as_uint(v))); }
+template <int D>
+__device__ __forceinline__ uint64_t lane_xor(uint64_t v) {
+  return (uint64_t)lane_xor<D>((unsigned)(v >> 32)) << 32 | lane_xor<D>((unsigned)v);
+}
+// f<1>(), f<2>(), f<4>() ... up to f<32>(), or down
+template <int D = 1, class F>
+__device__ __forceinline__ void each_up(F&& f) {
+  f(std::integral_constant<int, D>{});
+  if constexpr (D < 32) each_up<2 * D>(f);
+}
+template <int D, class F>
+__device__ __forceinline__ void each_down(F&& f) {
+  f(std::integral_constant<int, D>{});
+  if constexpr (D > 1) each_down<D / 2>(f);
+}
+
 __device__ __forceinline__ uint64_t larger(uint64_t a, uint64_t b) { return a > b ? a : b; }
 __device__ __forceinline__ uint64_t smaller(uint64_t a, uint64_t b) { return a < b ? a : b; }
-// A step of a bitonic network over the lanes: the larger of two keys that are `d` lanes
+// A step of a bitonic network over the lanes: the larger of two keys that are D lanes
 // apart goes to the lower lane, or to the higher one.
-__device__ __forceinline__ uint64_t exchange(uint64_t key, int d, bool falling) {
-  const uint64_t other = __shfl_xor(key, d);
-  return ((threadIdx.x & d) == 0) == falling ? larger(key, other) : smaller(key, other);
+template <int D>
+__device__ __forceinline__ uint64_t exchange(uint64_t key, bool falling) {
+  const uint64_t other = lane_xor<D>(key);
+  return ((threadIdx.x & D) == 0) == falling ? larger(key, other) : smaller(key, other);
 }
 // Keys of a wave in falling order (a bitonic sort).
 __device__ __forceinline__ uint64_t sorted(uint64_t key) {
-#pragma unroll
-  for (int k = 2; k <= 64; k <<= 1)
-#pragma unroll
-    for (int d = k >> 1; d > 0; d >>= 1) key = exchange(key, d, (threadIdx.x & 63 & k) == 0);
+  each_up([&](auto k) {
+    constexpr int K = decltype(k)::value;
+    each_down<K>([&](auto d) { key = exchange<decltype(d)::value>(key, (threadIdx.x & 63 & (2 * K)) == 0); });
+  });
   return key;
 }
 
@@ -121,8 +161,7 @@ struct Best {
   // bitonic order.
   __device__ __forceinline__ void join(uint64_t key) {
     mine = larger(mine, __shfl(key, 63 - (threadIdx.x & 63)));
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) mine = exchange(mine, d, true);
+    each_down<32>([&](auto d) { mine = exchange<decltype(d)::value>(mine, true); });
     last = lane_of(mine, top - 1);
   }
   // The first `n` keys of the room (n <= 64): by insertion where they are few.
@@ -140,14 +179,15 @@ struct Best {
   }
   // E keys of every lane, the largest of which is `largest`.  Keys that cannot be among
   // the best are passed by: those below `last`, and, of the first keys, those whose value is
-  // below the top-th largest of the lanes' own largest.  The others are gathered in LDS.
+  // below the top-th largest of the lanes' own largest (to 16 bits, which bf16 values have).  The
+  // others are gathered in LDS.
   template <int E, class KEY>
   __device__ __forceinline__ void offer(uint64_t largest, KEY&& key) {
     if (!__any(largest > last)) return;
     uint64_t least = last;
     if (last == 0) {
       unsigned value = 0;
-      for (unsigned bit = 1u << 31; bit; bit >>= 1)
+      for (unsigned bit = 1u << 31; bit >= 1u << 16; bit >>= 1)
         if (__popcll(__ballot((unsigned)(largest >> 32) >= (value | bit))) >= top) value |= bit;
       least = value ? ((uint64_t)value << 32) - 1 : 0;
     }
@@ -202,16 +242,16 @@ __device__ __forceinline__ Sums join(Sums a, Sums b) {
   return Sums{m, a.s + b.s, a.t + b.t};
 }
 __device__ __forceinline__ Sums join_lanes(Sums a) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1)
-    a = join(a, Sums{__shfl_xor(a.m, d), __shfl_xor(a.s, d), __shfl_xor(a.t, d)});
+  each_up([&](auto d) {
+    constexpr int D = decltype(d)::value;
+    a = join(a, Sums{lane_xor<D>(a.m), lane_xor<D>(a.s), lane_xor<D>(a.t)});
+  });
   return a;
 }
 
 // One unit: its sums (in every lane), and its logits offered to `best`.
-template <int IN>
-__device__ __forceinline__ Sums take_unit(const void* row, int64_t v0, int64_t vocab, Best& best,
-                                          bool top) {
+template <int IN, bool TOP>
+__device__ __forceinline__ Sums take_unit(const void* row, int64_t v0, int64_t vocab, Best& best) {
   const int lane = threadIdx.x & 63;
   float x[kVecs][8];
 #pragma unroll
@@ -232,7 +272,7 @@ __device__ __forceinline__ Sums take_unit(const void* row, int64_t v0, int64_t v
       t = fmaf(p, fmaxf(d, kLeast), t);
     }
   const Sums all = join_lanes(Sums{m, s, t});
-  if (top) {
+  if constexpr (TOP) {
     unsigned highest = order(m);
     if (__any(s != s)) {  // a NaN, which takes no part in m, or an infinity
 #pragma unroll
@@ -295,7 +335,7 @@ __device__ __forceinline__ void finish(const LogprobsArgs& g, int64_t row, const
 }
 
 // PARTS: the workgroup's part of a row, to the workspace; otherwise a whole row.
-template <int IN, bool PARTS>
+template <int IN, bool PARTS, bool TOP>
 __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobsArgs g) {
   extern __shared__ float shared[];  // sums [units, 3] of a whole row
   __shared__ uint64_t lists[kWaves][kLogprobsMaxTop], room[kWaves][128];
@@ -307,7 +347,7 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobsArgs g) {
   Best best{0, 0, g.top ? g.top : 1, room[wave]};
   const int step = PARTS ? kWaves * g.parts : kWaves;
   for (int u = part * kWaves + wave; u < g.units; u += step) {
-    const Sums a = take_unit<IN>(x, (int64_t)u * kUnit, g.vocab, best, g.top > 0);
+    const Sums a = take_unit<IN, TOP>(x, (int64_t)u * kUnit, g.vocab, best);
     if (lane == 0) {
       sums[3 * u] = a.m;
       sums[3 * u + 1] = a.s;
@@ -413,19 +453,19 @@ hipError_t launch_logprobs(int in, const LogprobsArgs& a, hipStream_t s) {
   with_type(in, [&](auto dt) {
     constexpr int IN = decltype(dt)::value;
     if (a.parts > 1) {
-      hipLaunchKernelGGL((logprobs_kernel<IN, true>), dim3((unsigned)(a.rows * a.parts)),
-                         dim3(kThreads), 0, s, a);
+      const auto kernel = a.top ? logprobs_kernel<IN, true, true> : logprobs_kernel<IN, true, false>;
+      hipLaunchKernelGGL(kernel, dim3((unsigned)(a.rows * a.parts)), dim3(kThreads), 0, s, a);
       e = hipGetLastError();
       if (e != hipSuccess) return;
       hipLaunchKernelGGL(logprobs_join_kernel<IN>, dim3((unsigned)a.rows), dim3(64), 0, s, a);
       e = hipGetLastError();
       return;
     }
+    const auto kernel = a.top ? logprobs_kernel<IN, false, true> : logprobs_kernel<IN, false, false>;
     const int64_t most = (int64_t)1 << 23;  // (a launch holds fewer than 2^32 threads)
     for (int64_t r = 0; r < a.rows && e == hipSuccess; r += most) {
       const int64_t rows = a.rows - r < most ? a.rows - r : most;
-      hipLaunchKernelGGL((logprobs_kernel<IN, false>), dim3((unsigned)rows), dim3(kThreads),
-                         a.units * 3 * sizeof(float), s, from_row(a, in, r, rows));
+      hipLaunchKernelGGL(kernel, dim3((unsigned)rows), dim3(kThreads), a.units * 3 * sizeof(float), s, from_row(a, in, r, rows));
       e = hipGetLastError();
     }
   });
