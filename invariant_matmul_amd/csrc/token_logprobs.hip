@@ -336,7 +336,7 @@ __device__ __forceinline__ void finish(const LogprobsArgs& g, int64_t row, const
 
 // PARTS: the workgroup's part of a row, to the workspace; otherwise a whole row.
 template <int IN, bool PARTS, bool TOP>
-__global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobsArgs g) {
+__global__ __launch_bounds__(kThreads, PARTS ? 5 : 6) void logprobs_kernel(LogprobsArgs g) {
   extern __shared__ float shared[];  // sums [units, 3] of a whole row
   __shared__ uint64_t lists[kWaves][kLogprobsMaxTop], room[kWaves][128];
   const int wave = threadIdx.x / 64, lane = threadIdx.x & 63;
