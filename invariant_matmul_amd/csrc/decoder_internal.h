@@ -11,8 +11,8 @@ namespace imm {
 constexpr int kRopeMaxDim = 512;     // 64 lanes of 8 elements
 constexpr int kRopeMaxAxes = 4;
 // Workgroups of the backward pass with weights (each leaves its parts of the
-// weights' gradients): two per compute unit of a 256-CU MI355X.
-constexpr int64_t kRopeBwdGroups = 512;
+// weights' gradients): four per compute unit of a 256-CU MI355X.
+constexpr int64_t kRopeBwdGroups = 1024;
 struct HeadRopeArgs {
   // [0] queries, [1] keys: x[t * token_stride + h * head_stride + d]
   const void* x[2];
@@ -29,7 +29,7 @@ struct HeadRopeArgs {
   int axes, section_end[kRopeMaxAxes];
   int norm, interleaved;
   float eps;
-  int tokens_per_group;
+  int share;                 // 2^share waves take a token
 };
 int64_t head_rope_groups(int64_t tokens, int heads, int dim);
 hipError_t launch_head_rope(int in, HeadRopeArgs a, hipStream_t s);
