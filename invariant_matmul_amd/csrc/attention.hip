@@ -191,9 +191,9 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttnArgs a) {
   const int64_t tiles = gridDim.x / a.k_heads;
   const int kh = blockIdx.x % a.k_heads;
   const int64_t tile = tiles - 1 - blockIdx.x / a.k_heads;
-  const int seg = segment_of_tile(a, tile, kRows);
-  const Sequence s = segment(a, seg);
-  const int64_t r0 = (tile - (s.q0 * a.group / kRows + seg)) * kRows;
+  const Found found = segment_of_tile(a, tile, kRows);
+  const Sequence s = found.s;
+  const int64_t r0 = (tile - (s.q0 * a.group / kRows + found.segment)) * kRows;
   const int64_t rows = s.n * a.group;
   if (r0 >= rows) return;
 
@@ -315,14 +315,12 @@ __global__ __launch_bounds__(kFewThreads, 2) void attention_few_kernel(AttnArgs 
   const int quad = lane / 16, col = lane % 16;
   const int kh = blockIdx.x % a.k_heads;
   const int64_t slot = blockIdx.x / a.k_heads;
-  // the sequence of this chunk slot: sequence b's begin at k_start(b) / 256 + b
-  int lo = 0, hi = a.batch - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) / 2;
-    if (k_start(a, mid) / kAttnChunk + mid <= slot) lo = mid;
-    else hi = mid - 1;
-  }
-  const Sequence s = segment(a, lo + 1);
+  // the sequence of this chunk slot: sequence b's begin at its first key / 256 + b
+  const Found found = find_segment(a, [&](int i, int64_t, int64_t k) {
+    return i == 0 || (i <= a.batch && k / kAttnChunk + (i - 1) <= slot);
+  });
+  const Sequence s = found.s;
+  if (found.segment == 0) return;
   const int64_t c0 = (slot - s.slot0) * kAttnChunk;
   if (c0 < 0 || c0 >= s.m || s.n == 0) return;
   const int64_t queries = s.n < a.max_q ? s.n : a.max_q;
@@ -450,18 +448,20 @@ __global__ __launch_bounds__(kFewThreads, 2) void attention_few_kernel(AttnArgs 
 }
 
 // The chunks of a row, joined in ascending order: a wave per query and head, two
-// dimensions a lane.
+// dimensions a lane.  Latency bounds it: the references and factors of 64 chunks are made by a lane
+// each, and 32 chunks' results are in flight at a time.
 template <int IN>
 __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
+  constexpr int U = 32;
   const int lane = threadIdx.x & 63;
-  const int64_t at = (int64_t)blockIdx.x * 4 + threadIdx.x / 64;
+  const int64_t at = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   if (at >= a.q_rows * a.q_heads) return;
   const int64_t q = at / a.q_heads;
   const int head = (int)(at - q * a.q_heads), kh = head / a.group;
-  const int seg = segment_of_row(a, q);
-  const Sequence s = segment(a, seg);
+  const Found found = find_segment(a, [&](int, int64_t first, int64_t) { return first <= q; });
+  const Sequence s = found.s;
   const int64_t t = q - s.q0;
-  const bool said = t < a.max_q || seg == 0 || seg > a.batch;  // (rows in no sequence have no keys)
+  const bool said = t < a.max_q || found.segment == 0 || found.segment > a.batch;  // (rows in no sequence have no keys)
   const int64_t seen = keys_seen(a, s, t);
   const int64_t row = t * a.group + (head - kh * a.group);
   float M = kNegInf, L = 0.0f, O0 = 0.0f, O1 = 0.0f;
@@ -469,28 +469,52 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
   if (said) {
     const int64_t first = (s.slot0 * a.k_heads + kh) * a.part_rows + row;
     const int64_t step = (int64_t)a.k_heads * a.part_rows;
-    const int chunks = (int)((seen + kAttnChunk - 1) / kAttnChunk);
-    constexpr int U = 8;
-    for (int c0 = 0; c0 < chunks; c0 += U) {
-      float2 ml[U], o[U];
+    const int chunks = __builtin_amdgcn_readfirstlane((int)((seen + kAttnChunk - 1) / kAttnChunk));
+    for (int c0 = 0; c0 < chunks; c0 += 64) {
+      const int n = chunks - c0 < 64 ? chunks - c0 : 64;
+      float2 o[U];
+      auto load = [&](int u0) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t i = first + (c0 + u) * step;
-        ml[u] = float2{0, 0};
-        o[u] = float2{0, 0};
-        if (c0 + u < chunks) {
-          ml[u] = reinterpret_cast<const float2*>(a.part_ml)[i];
-          if (mine) o[u] = *reinterpret_cast<const float2*>(a.part_o + i * a.dim + 2 * lane);
+        for (int u = 0; u < U; ++u) {
+          o[u] = float2{0, 0};
+          if (u0 + u < n && mine)
+            o[u] = *reinterpret_cast<const float2*>(a.part_o + (first + (c0 + u0 + u) * step) * a.dim + 2 * lane);
         }
+      };
+      float2 ml{kNegInf, 0.0f};
+      if (lane < n) ml = reinterpret_cast<const float2*>(a.part_ml)[first + (c0 + lane) * step];
+      load(0);
+      // the reference after each chunk: it is set again at few of them
+      float before = M, after = M;
+      for (int from = 0;;) {
+        const uint64_t set = __ballot(lane >= from && reference(M, ml.x) != M);
+        if (!set) break;
+        const int l = __ffsll((unsigned long long)set) - 1;
+        const float to = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ml.x), l));
+        if (lane > l) before = to;
+        if (lane >= l) after = to;
+        M = to;
+        from = l + 1;
       }
+      const float fa = shrink(before, after);
+      const float fb = ml.x == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(ml.x - after);
+      const bool ones = __all(fa == 1.0f);
+      for (int u0 = 0; u0 < n; u0 += U) {
+        if (u0) load(u0);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (c0 + u < chunks) {
-          const Join j = join_chunk(M, ml[u].x);
-          M = j.m;
-          L = joined(L, ml[u].y, j);
-          O0 = joined(O0, o[u].x, j);
-          O1 = joined(O1, o[u].y, j);
+        for (int u = 0; u < U; ++u) {
+          if (u0 + u >= n) break;
+          const float b = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(fb), u0 + u));
+          const float l = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ml.y), u0 + u));
+          if (!ones) {  // (a product with 1 changes nothing)
+            const float f = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(fa), u0 + u));
+            L *= f;
+            O0 *= f;
+            O1 *= f;
+          }
+          L = fmaf(l, b, L);
+          O0 = fmaf(o[u].x, b, O0);
+          O1 = fmaf(o[u].y, b, O1);
         }
       }
     }

@@ -93,9 +93,9 @@ __device__ __forceinline__ void rows_role(const AttnArgs& a, int64_t tile, int k
   using T = TileOf<DP>;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int quad = lane / 16, col = lane % 16;
-  const int seg = segment_of_tile(a, tile, kBlock);
-  const Sequence s = segment(a, seg);
-  const int64_t r0 = (tile - (s.q0 * a.group / kBlock + seg)) * kBlock;
+  const Found found = segment_of_tile(a, tile, kBlock);
+  const Sequence s = found.s;
+  const int64_t r0 = (tile - (s.q0 * a.group / kBlock + found.segment)) * kBlock;
   const int64_t rows = s.n * a.group;
   if (r0 >= rows) return;
 
@@ -195,11 +195,6 @@ __device__ __forceinline__ void rows_role(const AttnArgs& a, int64_t tile, int k
   }
 }
 
-// Segment i of the keys: as for the queries, with the rows before and behind the sequences.
-__device__ __forceinline__ int64_t key_start(const AttnArgs& a, int i) {
-  return i <= 0 ? 0 : i > a.batch + 1 ? a.k_rows : k_start(a, i - 1);
-}
-
 // Moves 64 packed rows of a sequence's q or do to LDS (rows past the last: zeros).  The rows of
 // a thread keep their query and head as counts that advance by 64 rows.
 template <int DP>
@@ -254,17 +249,11 @@ __device__ __forceinline__ void keys_role(const AttnArgs& a, int64_t tile, int k
   using T = TileOf<DP>;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int quad = lane / 16, col = lane % 16;
-  int lo = 0, hi = a.batch + 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) / 2;
-    if (key_start(a, mid) / kBlock + mid <= tile) lo = mid;
-    else hi = mid - 1;
-  }
-  const int64_t k_first = key_start(a, lo);
-  const int64_t k_end = lo == a.batch + 1 ? a.k_rows : key_start(a, lo + 1);
-  const int64_t c0 = (tile - (k_first / kBlock + lo)) * kBlock;  // of the segment
+  const Found found = find_segment(a, [&](int i, int64_t, int64_t k) { return k / kBlock + i <= tile; });
+  const Sequence s = found.s;
+  const int64_t k_first = s.k0, k_end = found.k_end;
+  const int64_t c0 = (tile - (k_first / kBlock + found.segment)) * kBlock;  // of the segment
   if (c0 >= k_end - k_first) return;
-  const Sequence s = segment(a, lo);
   const int rows = (int)(s.n * a.group);
   const int64_t w0 = c0 + 32 * wave;
   // the first row that sees a key

@@ -47,40 +47,55 @@ __device__ __forceinline__ int64_t k_start(const AttnArgs& a, int b) {
   if (!a.cu_k) return b == 0 ? 0 : a.k_rows;
   return clamp64(a.cu_k[b], 0, a.k_rows);
 }
-__device__ __forceinline__ Sequence segment(const AttnArgs& a, int i) {
-  Sequence s{};
-  s.q0 = q_start(a, i);
-  const int64_t end = i == a.batch + 1 ? a.q_rows : q_start(a, i + 1);
-  s.n = end > s.q0 ? end - s.q0 : 0;
-  if (i >= 1 && i <= a.batch) {
-    s.k0 = k_start(a, i - 1);
-    const int64_t ke = k_start(a, i);
-    s.m = ke > s.k0 ? ke - s.k0 : 0;
-    if (a.k_lens) s.m = clamp64(a.k_lens[i - 1], 0, s.m);
-    s.slot0 = s.k0 / kAttnChunk + (i - 1);
+// Segment i of the keys (with the rows before the first and behind the last sequence).
+__device__ __forceinline__ int64_t key_start(const AttnArgs& a, int i) {
+  return i <= 0 ? 0 : i > a.batch + 1 ? a.k_rows : k_start(a, i - 1);
+}
+
+// The last segment for which begins(i, its first query, its first key) holds, and
+// what it is.  A lane looks at a segment: a call waits for memory once (and once more for each
+// factor of 64 in the number of sequences), where a binary search waits at every step.
+struct Found {
+  int segment;
+  int64_t k_end;  // of its room
+  Sequence s;
+};
+template <class F>
+__device__ __forceinline__ Found find_segment(const AttnArgs& a, F&& begins) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0, n = a.batch + 2;
+  while (n > 63) {
+    const int step = (n + 63) / 64, i = lo + lane * step;
+    const bool ok = i < lo + n && begins(i, q_start(a, i), key_start(a, i));
+    const int c = __popcll(__ballot(ok));
+    const int skip = (c > 0 ? c - 1 : 0) * step;
+    lo += skip;
+    n = n - skip < step ? n - skip : step;
   }
-  return s;
+  const int i = lo + lane;
+  const int64_t q = q_start(a, i), k = key_start(a, i);
+  int len = 0x7fffffff;
+  if (a.k_lens && i >= 1 && i <= a.batch) len = a.k_lens[i - 1];
+  const int c = __popcll(__ballot(lane < n && begins(i, q, k)));
+  const int l = c > 0 ? c - 1 : 0;
+  // (rows and keys are counted in 31 bits)
+  auto of = [](int64_t v, int lane_of) { return (int64_t)__builtin_amdgcn_readlane((int)v, lane_of); };
+  Found f{};
+  f.segment = lo + l;
+  f.s.q0 = of(q, l);
+  f.s.k0 = of(k, l);
+  f.k_end = clamp64(of(k, l + 1), f.s.k0, a.k_rows);
+  f.s.n = clamp64(of(q, l + 1) - f.s.q0, 0, a.q_rows);
+  if (f.segment >= 1 && f.segment <= a.batch) {
+    f.s.m = clamp64(of(len, l), 0, f.k_end - f.s.k0);
+    f.s.slot0 = f.s.k0 / kAttnChunk + (f.segment - 1);
+  }
+  return f;
 }
 // Tiles of `rows` packed rows: segment i begins at tile start(i) group / rows + i,
 // so that every segment has the tiles it needs and no sum over segments is taken.
-// The last segment that begins at or before tile t:
-__device__ __forceinline__ int segment_of_tile(const AttnArgs& a, int64_t t, int rows) {
-  int lo = 0, hi = a.batch + 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) / 2;
-    if (q_start(a, mid) * a.group / rows + mid <= t) lo = mid;
-    else hi = mid - 1;
-  }
-  return lo;
-}
-__device__ __forceinline__ int segment_of_row(const AttnArgs& a, int64_t row) {
-  int lo = 0, hi = a.batch + 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) / 2;
-    if (q_start(a, mid) <= row) lo = mid;
-    else hi = mid - 1;
-  }
-  return lo;
+__device__ __forceinline__ Found segment_of_tile(const AttnArgs& a, int64_t t, int rows) {
+  return find_segment(a, [&](int i, int64_t q, int64_t) { return q * a.group / rows + i <= t; });
 }
 
 // 16 bytes of a buffer; zeros past its end.
