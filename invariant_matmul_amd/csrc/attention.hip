@@ -188,13 +188,13 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttnArgs a) {
   const int quad = lane / 16, col = lane % 16;
   // heads vary fastest: neighbouring workgroups go to different XCDs, so a key
   // head's workgroups meet in few of the L2s.  The last rows (the most keys) first.
-  const int64_t tiles = gridDim.x / a.k_heads;
-  const int kh = blockIdx.x % a.k_heads;
-  const int64_t tile = tiles - 1 - blockIdx.x / a.k_heads;
-  const Found found = segment_of_tile(a, tile, kRows);
+  const int tiles = gridDim.x / (unsigned)a.k_heads;
+  const int kh = blockIdx.x % (unsigned)a.k_heads;
+  const int tile = tiles - 1 - (int)(blockIdx.x / (unsigned)a.k_heads);
+  const Found found = segment_of_tile<kRows>(a, tile);
   const Sequence s = found.s;
-  const int64_t r0 = (tile - (s.q0 * a.group / kRows + found.segment)) * kRows;
-  const int64_t rows = s.n * a.group;
+  const int r0 = (tile - (s.q0 * a.group / kRows + found.segment)) * kRows;
+  const int rows = s.n * a.group;
   if (r0 >= rows) return;
 
   // this lane's rows: column `col` of the two blocks of 16 of its wave
@@ -202,9 +202,9 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttnArgs a) {
   w.scale_log2 = a.scale_log2;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int64_t row = r0 + 32 * wave + 16 * i + col, t = row / a.group;
-    const int h = (int)(row - t * a.group);
-    w.seen[i] = (int)keys_seen(a, s, t);
+    const int row = r0 + 32 * wave + 16 * i + col, t = row / a.group;
+    const int h = row - t * a.group;
+    w.seen[i] = keys_seen(a, s, t);
     const char* const q = static_cast<const char*>(a.q) + 2 * ((s.q0 + t) * a.q_token + (kh * a.group + h) * a.q_head);
 #pragma unroll
     for (int ks = 0; ks < T::KS; ++ks) {
@@ -215,10 +215,10 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttnArgs a) {
   }
   // keys that any row of the workgroup, and of the wave, sees, and those that all of
   // them see (rows past the end see none, which needs no mask)
-  auto seen_of = [&](int64_t r) { return (int)keys_seen(a, s, (r < rows ? r : rows - 1) / a.group); };
+  auto seen_of = [&](int r) { return keys_seen(a, s, (r < rows ? r : rows - 1) / a.group); };
   const int need = __builtin_amdgcn_readfirstlane(seen_of(r0 + kRows - 1));
   const int all_see = __builtin_amdgcn_readfirstlane(seen_of(r0));
-  const int64_t w0 = r0 + 32 * wave;
+  const int w0 = r0 + 32 * wave;
   const int wave_need = __builtin_amdgcn_readfirstlane(w0 < rows ? seen_of(w0 + 31) : 0);
   const int wave_all = __builtin_amdgcn_readfirstlane(w0 < rows ? seen_of(w0) : 0);
   w.clear_all();
@@ -255,7 +255,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttnArgs a) {
     const bool poison = k0 + kTile > all_see && clean(vt);
     if (k0 < wave_need) {
       w.template step<decltype(first)::value>(kt, vt, k0, k0 + kTile > wave_all);
-      if (poison) w.add_not_finite(vp, v_bytes, k0, (int)s.m, a.dim);
+      if (poison) w.add_not_finite(vp, v_bytes, k0, s.m, a.dim);
     }
   };
   const std::true_type first;
@@ -272,9 +272,9 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttnArgs a) {
 
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int64_t row = r0 + 32 * wave + 16 * i + col;
+    const int row = r0 + 32 * wave + 16 * i + col;
     if (row >= rows) continue;
-    const int64_t t = row / a.group;
+    const int t = row / a.group;
     const int64_t at = (s.q0 + t) * a.q_heads + kh * a.group + (row - t * a.group);
     // a row without keys is zero; one whose keys are all -infinity is 0 / 0
     const float inv = w.seen[i] == 0 ? 0.0f : 1.0f / w.L[i];
@@ -305,6 +305,9 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttnArgs a) {
 // all four steps.
 constexpr int kFewWaves = 4, kFewThreads = 64 * kFewWaves;
 
+// The first chunk slot of a sequence: every sequence has the slots that it needs.
+__device__ __forceinline__ int first_slot(const Found& f) { return f.s.k0 / kAttnChunk + f.segment - 1; }
+
 template <int IN, int DP>
 __global__ __launch_bounds__(kFewThreads, 2) void attention_few_kernel(AttnArgs a) {
   using T = TileOf<DP>;
@@ -313,19 +316,19 @@ __global__ __launch_bounds__(kFewThreads, 2) void attention_few_kernel(AttnArgs 
   __shared__ float ml[kFewWaves][16], sl[kFewWaves][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int quad = lane / 16, col = lane % 16;
-  const int kh = blockIdx.x % a.k_heads;
-  const int64_t slot = blockIdx.x / a.k_heads;
+  const int kh = blockIdx.x % (unsigned)a.k_heads;
+  const int slot = blockIdx.x / (unsigned)a.k_heads;
   // the sequence of this chunk slot: sequence b's begin at its first key / 256 + b
-  const Found found = find_segment(a, [&](int i, int64_t, int64_t k) {
+  const Found found = find_segment(a, [&](int i, int, int k) {
     return i == 0 || (i <= a.batch && k / kAttnChunk + (i - 1) <= slot);
   });
   const Sequence s = found.s;
   if (found.segment == 0) return;
-  const int64_t c0 = (slot - s.slot0) * kAttnChunk;
+  const int c0 = (slot - first_slot(found)) * kAttnChunk;
   if (c0 < 0 || c0 >= s.m || s.n == 0) return;
-  const int64_t queries = s.n < a.max_q ? s.n : a.max_q;
+  const int queries = s.n < a.max_q ? s.n : (int)a.max_q;
   if (c0 >= keys_seen(a, s, queries - 1)) return;
-  const int left = (int)(s.m - c0 < kAttnChunk ? s.m - c0 : kAttnChunk);
+  const int left = s.m - c0 < kAttnChunk ? s.m - c0 : kAttnChunk;
 
   const auto kb = buffer_at(static_cast<const char*>(a.k) + 2 * ((s.k0 + c0) * a.k_token + kh * a.k_head));
   const auto vb = buffer_at(static_cast<const char*>(a.v) + 2 * ((s.k0 + c0) * a.v_token + kh * a.v_head));
@@ -365,12 +368,12 @@ __global__ __launch_bounds__(kFewThreads, 2) void attention_few_kernel(AttnArgs 
     __syncthreads();
   }
 
-  const int64_t rows = queries * a.group;
+  const int rows = queries * a.group;
   const Lanes<DP> lanes;
-  for (int64_t r0 = 0; r0 < rows; r0 += 16) {
-    const int64_t row = r0 + col, t = row / a.group;
-    const int h = (int)(row - t * a.group);
-    const int seen = (int)clamp64((row < rows ? keys_seen(a, s, t) : 0) - c0, 0, kAttnChunk);
+  for (int r0 = 0; r0 < rows; r0 += 16) {
+    const int row = r0 + col, t = row / a.group;
+    const int h = row - t * a.group;
+    const int seen = clamped((row < rows ? keys_seen(a, s, t) : 0) - c0, 0, kAttnChunk);
     f32x4 sc[4];
     {
       const char* const q = static_cast<const char*>(a.q) + 2 * ((s.q0 + t) * a.q_token + (kh * a.group + h) * a.q_head);
@@ -424,7 +427,7 @@ __global__ __launch_bounds__(kFewThreads, 2) void attention_few_kernel(AttnArgs 
       }
     }
     l = row_sum(l);
-    const int64_t at = (slot * a.k_heads + kh) * a.part_rows + row;
+    const int64_t at = ((int64_t)slot * a.k_heads + kh) * a.part_rows + row;
     if (row < rows) {
       if (wave == 0 && quad == 0) {
         a.part_ml[2 * at] = m[kFewWaves - 1];
@@ -448,42 +451,47 @@ __global__ __launch_bounds__(kFewThreads, 2) void attention_few_kernel(AttnArgs 
 }
 
 // The chunks of a row, joined in ascending order: a wave per query and head, two
-// dimensions a lane.  Latency bounds it: the references and factors of 64 chunks are made by a lane
-// each, and 32 chunks' results are in flight at a time.
+// dimensions a lane.  Latency bounds it, that of the code too (each of its lines is
+// fetched for one pass): the references and factors of 64 chunks are made by a lane
+// each, and two groups of 8 chunks' results are in flight in a short loop.
 template <int IN>
 __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
-  constexpr int U = 32;
+  constexpr int U = 8;
   const int lane = threadIdx.x & 63;
-  const int64_t at = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-  if (at >= a.q_rows * a.q_heads) return;
-  const int64_t q = at / a.q_heads;
-  const int head = (int)(at - q * a.q_heads), kh = head / a.group;
-  const Found found = find_segment(a, [&](int, int64_t first, int64_t) { return first <= q; });
+  const unsigned at = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  if (at >= (unsigned)a.q_rows * a.q_heads) return;
+  const int q = at / (unsigned)a.q_heads, head = at - q * a.q_heads;
+  const int kh = head / (unsigned)a.group;
+  const Found found = find_segment(a, [&](int, int first, int) { return first <= q; });
   const Sequence s = found.s;
-  const int64_t t = q - s.q0;
+  const int t = q - s.q0;
   const bool said = t < a.max_q || found.segment == 0 || found.segment > a.batch;  // (rows in no sequence have no keys)
-  const int64_t seen = keys_seen(a, s, t);
-  const int64_t row = t * a.group + (head - kh * a.group);
+  const int seen = keys_seen(a, s, t);
   float M = kNegInf, L = 0.0f, O0 = 0.0f, O1 = 0.0f;
   const bool mine = 2 * lane < a.dim;
-  if (said) {
-    const int64_t first = (s.slot0 * a.k_heads + kh) * a.part_rows + row;
+  if (said && seen > 0) {
     const int64_t step = (int64_t)a.k_heads * a.part_rows;
-    const int chunks = __builtin_amdgcn_readfirstlane((int)((seen + kAttnChunk - 1) / kAttnChunk));
+    const int64_t first = (int64_t)first_slot(found) * step + kh * a.part_rows + t * a.group + (head - kh * a.group);
+    const int chunks = (seen + kAttnChunk - 1) / kAttnChunk;
+    const float2* ml_at = reinterpret_cast<const float2*>(a.part_ml) + first + lane * step;
+    const char* o_at = reinterpret_cast<const char*>(a.part_o + first * a.dim + 2 * lane);
+    const int64_t o_step = step * a.dim * 4;
+    // (rows past the last chunk are loaded as the last once more)
+    float2 o[U], next[U];
+    int asked = 0;
+    auto load = [&](float2(&to)[U]) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (mine) to[u] = *reinterpret_cast<const float2*>(o_at);
+        o_at += ++asked < chunks ? o_step : 0;
+      }
+    };
+    load(next);
     for (int c0 = 0; c0 < chunks; c0 += 64) {
       const int n = chunks - c0 < 64 ? chunks - c0 : 64;
-      float2 o[U];
-      auto load = [&](int u0) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          o[u] = float2{0, 0};
-          if (u0 + u < n && mine)
-            o[u] = *reinterpret_cast<const float2*>(a.part_o + (first + (c0 + u0 + u) * step) * a.dim + 2 * lane);
-        }
-      };
       float2 ml{kNegInf, 0.0f};
-      if (lane < n) ml = reinterpret_cast<const float2*>(a.part_ml)[first + (c0 + lane) * step];
-      load(0);
+      if (lane < n) ml = *ml_at;
+      ml_at += 64 * step;
       // the reference after each chunk: it is set again at few of them
       float before = M, after = M;
       for (int from = 0;;) {
@@ -500,10 +508,11 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
       const float fb = ml.x == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(ml.x - after);
       const bool ones = __all(fa == 1.0f);
       for (int u0 = 0; u0 < n; u0 += U) {
-        if (u0) load(u0);
+#pragma unroll
+        for (int u = 0; u < U; ++u) o[u] = next[u];
+        if (c0 + u0 + U < chunks) load(next);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          if (u0 + u >= n) break;
           const float b = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(fb), u0 + u));
           const float l = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ml.y), u0 + u));
           if (!ones) {  // (a product with 1 changes nothing)
@@ -512,20 +521,21 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
             O0 *= f;
             O1 *= f;
           }
-          L = fmaf(l, b, L);
-          O0 = fmaf(o[u].x, b, O0);
-          O1 = fmaf(o[u].y, b, O1);
+          if (u0 + u < n) {
+            L = fmaf(l, b, L);
+            O0 = fmaf(o[u].x, b, O0);
+            O1 = fmaf(o[u].y, b, O1);
+          }
         }
       }
     }
-  } else {
-    L = O0 = O1 = __builtin_nanf("");  // a sequence longer than the call said
   }
+  if (!said) L = O0 = O1 = __builtin_nanf("");  // a sequence longer than the call said
   const bool empty = seen == 0 && said;
   const float inv = empty ? 0.0f : 1.0f / L;
   if (mine) {
     const int y = pack2<IN>(O0 * inv, O1 * inv);
-    const int64_t to = (at * a.dim) / 2 + lane;
+    const int64_t to = (int64_t)at * a.dim / 2 + lane;
     static_cast<int*>(a.o)[to] = y;
     if (a.o_low) static_cast<int*>(a.o_low)[to] = pack2_rest<IN>(O0 * inv, O1 * inv, y);
   }

@@ -49,8 +49,8 @@ __global__ __launch_bounds__(256) void attention_delta_kernel(AttnArgs a) {
 #pragma unroll
   for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
   if (c == 0 && at < a.q_rows * a.q_heads) {
-    const int64_t q = at / a.q_heads;
-    const int head = (int)(at - q * a.q_heads), kh = head / a.group;
+    const int q = (unsigned)at / (unsigned)a.q_heads;
+    const int head = (int)at - q * a.q_heads, kh = head / a.group;
     const int64_t to = ((int64_t)kh * a.q_rows + q) * a.group + (head - kh * a.group);
     a.stats[to] = -a.lse[at] * kLog2e;
     a.stats[a.q_rows * a.q_heads + to] = sum;
@@ -89,36 +89,36 @@ struct Stages {  // (arrays of their own, as in the forward kernel)
 
 // dq of the rows from r0 on.
 template <int IN, int DP>
-__device__ __forceinline__ void rows_role(const AttnArgs& a, int64_t tile, int kh, const Stages<DP>& st) {
+__device__ __forceinline__ void rows_role(const AttnArgs& a, int tile, int kh, const Stages<DP>& st) {
   using T = TileOf<DP>;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int quad = lane / 16, col = lane % 16;
-  const Found found = segment_of_tile(a, tile, kBlock);
+  const Found found = segment_of_tile<kBlock>(a, tile);
   const Sequence s = found.s;
-  const int64_t r0 = (tile - (s.q0 * a.group / kBlock + found.segment)) * kBlock;
-  const int64_t rows = s.n * a.group;
+  const int r0 = (tile - (s.q0 * a.group / kBlock + found.segment)) * kBlock;
+  const int rows = s.n * a.group;
   if (r0 >= rows) return;
 
   int seen[2];
   float nl[2], delta[2];
   i32x4 qf[2][T::KS], gf[2][T::KS];
   f32x4 dq[2][T::DB];
-  const int64_t w0 = r0 + 32 * wave;
+  const int w0 = r0 + 32 * wave;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int64_t row = w0 + 16 * i + col, t = row / a.group;
-    const int64_t h = kh * a.group + (row - t * a.group);
+    const int row = w0 + 16 * i + col, t = row / a.group;
+    const int h = kh * a.group + (row - t * a.group);
     const bool live = row < rows;
-    seen[i] = (int)keys_seen(a, s, t);
+    seen[i] = keys_seen(a, s, t);
     const int64_t at = ((int64_t)kh * a.q_rows + s.q0) * a.group + row;
     nl[i] = live ? a.stats[at] : 0.0f;
     delta[i] = live ? a.stats[a.q_rows * a.q_heads + at] : 0.0f;
     row_operand<DP>(qf[i], static_cast<const char*>(a.q) + 2 * ((s.q0 + t) * a.q_token + h * a.q_head), live, a.dim);
-    row_operand<DP>(gf[i], static_cast<const char*>(a.d_o) + 2 * ((s.q0 + t) * a.q_heads + h) * a.dim, live, a.dim);
+    row_operand<DP>(gf[i], static_cast<const char*>(a.d_o) + 2 * ((int64_t)(s.q0 + t) * a.q_heads + h) * a.dim, live, a.dim);
 #pragma unroll
     for (int d = 0; d < T::DB; ++d) dq[i][d] = f32x4{};
   }
-  auto seen_of = [&](int64_t r) { return (int)keys_seen(a, s, (r < rows ? r : rows - 1) / a.group); };
+  auto seen_of = [&](int r) { return keys_seen(a, s, (r < rows ? r : rows - 1) / a.group); };
   const int need = __builtin_amdgcn_readfirstlane(seen_of(r0 + kBlock - 1));
   const int wave_need = __builtin_amdgcn_readfirstlane(w0 < rows ? seen_of(w0 + 31) : 0);
   const int wave_all = __builtin_amdgcn_readfirstlane(w0 < rows ? seen_of(w0) : 0);
@@ -189,9 +189,9 @@ __device__ __forceinline__ void rows_role(const AttnArgs& a, int64_t tile, int k
   }
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int64_t row = w0 + 16 * i + col, t = row / a.group;
+    const int row = w0 + 16 * i + col, t = row / a.group;
     const int64_t h = kh * a.group + (row - t * a.group);
-    if (row < rows) store_rows<IN, DP>(dq[i], a.scale, a.dq, ((s.q0 + t) * a.q_heads + h) * a.dim, a.dim);
+    if (row < rows) store_rows<IN, DP>(dq[i], a.scale, a.dq, ((int64_t)(s.q0 + t) * a.q_heads + h) * a.dim, a.dim);
   }
 }
 
@@ -245,28 +245,28 @@ struct RowMover {
 
 // dk (DK) or dv of the keys of a tile.
 template <int IN, int DP, bool DK>
-__device__ __forceinline__ void keys_role(const AttnArgs& a, int64_t tile, int kh, const Stages<DP>& st) {
+__device__ __forceinline__ void keys_role(const AttnArgs& a, int tile, int kh, const Stages<DP>& st) {
   using T = TileOf<DP>;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int quad = lane / 16, col = lane % 16;
-  const Found found = find_segment(a, [&](int i, int64_t, int64_t k) { return k / kBlock + i <= tile; });
+  const Found found = find_segment(a, [&](int i, int, int k) { return k / kBlock + i <= tile; });
   const Sequence s = found.s;
-  const int64_t k_first = s.k0, k_end = found.k_end;
-  const int64_t c0 = (tile - (k_first / kBlock + found.segment)) * kBlock;  // of the segment
+  const int k_first = s.k0, k_end = found.k_end;
+  const int c0 = (tile - (k_first / kBlock + found.segment)) * kBlock;  // of the segment
   if (c0 >= k_end - k_first) return;
-  const int rows = (int)(s.n * a.group);
-  const int64_t w0 = c0 + 32 * wave;
+  const int rows = s.n * a.group;
+  const int w0 = c0 + 32 * wave;
   // the first row that sees a key
-  auto first_row = [&](int64_t key) {
+  auto first_row = [&](int key) {
     if (key >= s.m) return rows;
-    return a.causal ? (int)clamp64(key - (s.m - s.n), 0, s.n) * a.group : 0;
+    return a.causal ? clamped(key - (s.m - s.n), 0, s.n) * a.group : 0;
   };
   i32x4 kf[2][T::KS], vf[DK ? 2 : 1][T::KS];
   f32x4 sum[2][T::DB];
   int from_row[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    const int64_t key = w0 + 16 * j + col;
+    const int key = w0 + 16 * j + col;
     row_operand<DP>(kf[j], static_cast<const char*>(a.k) + 2 * ((k_first + key) * a.k_token + kh * a.k_head), key < s.m, a.dim);
     if constexpr (DK)
       row_operand<DP>(vf[j], static_cast<const char*>(a.v) + 2 * ((k_first + key) * a.v_token + kh * a.v_head), key < s.m, a.dim);
@@ -278,7 +278,7 @@ __device__ __forceinline__ void keys_role(const AttnArgs& a, int64_t tile, int k
   const int wave_from = first_row(w0), wave_all = first_row(w0 + 31);
 
   const char* const qp = static_cast<const char*>(a.q) + 2 * (s.q0 * a.q_token + (int64_t)kh * a.group * a.q_head);
-  const char* const gp = static_cast<const char*>(a.d_o) + 2 * (s.q0 * a.q_heads + (int64_t)kh * a.group) * a.dim;
+  const char* const gp = static_cast<const char*>(a.d_o) + 2 * ((int64_t)s.q0 * a.q_heads + kh * a.group) * a.dim;
   const float* const stats = a.stats + ((int64_t)kh * a.q_rows + s.q0) * a.group;
   const int64_t all_rows = a.q_rows * a.q_heads;
   RowMover<DP> rm(from, a.group, a.dim);
@@ -354,9 +354,9 @@ __device__ __forceinline__ void keys_role(const AttnArgs& a, int64_t tile, int k
   }
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    const int64_t key = w0 + 16 * j + col;
+    const int key = w0 + 16 * j + col;
     if (key < k_end - k_first)
-      store_rows<IN, DP>(sum[j], DK ? a.scale : 1.0f, DK ? a.dk : a.dv, ((k_first + key) * a.k_heads + kh) * a.dim, a.dim);
+      store_rows<IN, DP>(sum[j], DK ? a.scale : 1.0f, DK ? a.dk : a.dv, ((int64_t)(k_first + key) * a.k_heads + kh) * a.dim, a.dim);
   }
 }
 
@@ -368,12 +368,12 @@ __global__ __launch_bounds__(kThreads, 2) void attention_backward_kernel(AttnArg
   __shared__ __attribute__((aligned(1024))) char x0[BYTES], y0[BYTES], x1[BYTES], y1[BYTES];
   __shared__ __attribute__((aligned(256))) float n0[kTile], d0[kTile], n1[kTile], d1[kTile];
   const Stages<DP> st{x0, y0, x1, y1, n0, d0, n1, d1};
-  const int kh = blockIdx.x % a.k_heads;
-  int64_t tile = blockIdx.x / a.k_heads;
+  const int kh = blockIdx.x % (unsigned)a.k_heads;
+  int tile = blockIdx.x / (unsigned)a.k_heads;
   if (tile < a.k_tiles) return keys_role<IN, DP, true>(a, tile, kh, st);
   tile -= a.k_tiles;
-  if (tile < a.q_tiles) return rows_role<IN, DP>(a, a.q_tiles - 1 - tile, kh, st);
-  return keys_role<IN, DP, false>(a, tile - a.q_tiles, kh, st);
+  if (tile < a.q_tiles) return rows_role<IN, DP>(a, (int)a.q_tiles - 1 - tile, kh, st);
+  return keys_role<IN, DP, false>(a, tile - (int)a.q_tiles, kh, st);
 }
 
 template <int IN, int DP>

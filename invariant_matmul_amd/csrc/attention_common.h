@@ -26,30 +26,30 @@ constexpr float kNegInf = -__builtin_inff();
 constexpr float kLn2 = 0.693147180559945309417f;
 
 // A sequence of a call: its rows of q and its keys.  What the device's arrays say is
-// clamped to the operands, so that no contents of theirs reach outside.
+// clamped to the operands, so that no contents of theirs reach outside.  (Keys are counted in
+// 30 bits, rows times heads in 31.)
 struct Sequence {
-  int64_t q0, k0;   // first query, first key row
-  int64_t n, m;     // queries, keys
-  int64_t slot0;    // its first chunk slot
+  int q0, k0;   // first query, first key row
+  int n, m;     // queries, keys
 };
 
-__device__ __forceinline__ int64_t clamp64(int64_t v, int64_t lo, int64_t hi) {
-  return v < lo ? lo : v > hi ? hi : v;
-}
-// Segment i of the queries: 0 and batch + 1 are the rows before the first and
-// behind the last sequence (they have no keys).
-__device__ __forceinline__ int64_t q_start(const AttnArgs& a, int i) {
+__device__ __forceinline__ int clamped(int v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : v; }
+
+// Segment i: sequence i - 1, or the rows before the first sequence (0) or behind the last
+// (batch + 1), which have no keys.  Where its queries and keys begin:
+__device__ __forceinline__ int q_start(const AttnArgs& a, int i) {
+  const int rows = (int)a.q_rows;
   if (i <= 0) return 0;
-  if (!a.cu_q) return i == 1 ? 0 : a.q_rows;
-  return i > a.batch + 1 ? a.q_rows : clamp64(a.cu_q[i - 1], 0, a.q_rows);
+  if (i > a.batch + 1) return rows;
+  if (!a.cu_q) return i == 1 ? 0 : rows;
+  return clamped(a.cu_q[i - 1], 0, rows);
 }
-__device__ __forceinline__ int64_t k_start(const AttnArgs& a, int b) {
-  if (!a.cu_k) return b == 0 ? 0 : a.k_rows;
-  return clamp64(a.cu_k[b], 0, a.k_rows);
-}
-// Segment i of the keys (with the rows before the first and behind the last sequence).
-__device__ __forceinline__ int64_t key_start(const AttnArgs& a, int i) {
-  return i <= 0 ? 0 : i > a.batch + 1 ? a.k_rows : k_start(a, i - 1);
+__device__ __forceinline__ int key_start(const AttnArgs& a, int i) {
+  const int rows = (int)a.k_rows;
+  if (i <= 0) return 0;
+  if (i > a.batch + 1) return rows;
+  if (!a.cu_k) return i == 1 ? 0 : rows;
+  return clamped(a.cu_k[i - 1], 0, rows);
 }
 
 // The last segment for which begins(i, its first query, its first key) holds, and
@@ -57,7 +57,7 @@ __device__ __forceinline__ int64_t key_start(const AttnArgs& a, int i) {
 // factor of 64 in the number of sequences), where a binary search waits at every step.
 struct Found {
   int segment;
-  int64_t k_end;  // of its room
+  int k_end;  // of its room
   Sequence s;
 };
 template <class F>
@@ -73,29 +73,26 @@ __device__ __forceinline__ Found find_segment(const AttnArgs& a, F&& begins) {
     n = n - skip < step ? n - skip : step;
   }
   const int i = lo + lane;
-  const int64_t q = q_start(a, i), k = key_start(a, i);
   int len = 0x7fffffff;
   if (a.k_lens && i >= 1 && i <= a.batch) len = a.k_lens[i - 1];
+  const int q = q_start(a, i), k = key_start(a, i);
   const int c = __popcll(__ballot(lane < n && begins(i, q, k)));
   const int l = c > 0 ? c - 1 : 0;
-  // (rows and keys are counted in 31 bits)
-  auto of = [](int64_t v, int lane_of) { return (int64_t)__builtin_amdgcn_readlane((int)v, lane_of); };
   Found f{};
   f.segment = lo + l;
-  f.s.q0 = of(q, l);
-  f.s.k0 = of(k, l);
-  f.k_end = clamp64(of(k, l + 1), f.s.k0, a.k_rows);
-  f.s.n = clamp64(of(q, l + 1) - f.s.q0, 0, a.q_rows);
-  if (f.segment >= 1 && f.segment <= a.batch) {
-    f.s.m = clamp64(of(len, l), 0, f.k_end - f.s.k0);
-    f.s.slot0 = f.s.k0 / kAttnChunk + (f.segment - 1);
-  }
+  f.s.q0 = __builtin_amdgcn_readlane(q, l);
+  f.s.k0 = __builtin_amdgcn_readlane(k, l);
+  const int q_end = __builtin_amdgcn_readlane(q, l + 1), k_end = __builtin_amdgcn_readlane(k, l + 1);
+  f.k_end = k_end > f.s.k0 ? k_end : f.s.k0;
+  f.s.n = q_end > f.s.q0 ? q_end - f.s.q0 : 0;
+  if (f.segment >= 1 && f.segment <= a.batch) f.s.m = clamped(__builtin_amdgcn_readlane(len, l), 0, f.k_end - f.s.k0);
   return f;
 }
-// Tiles of `rows` packed rows: segment i begins at tile start(i) group / rows + i,
+// Tiles of ROWS packed rows: segment i begins at tile start(i) group / ROWS + i,
 // so that every segment has the tiles it needs and no sum over segments is taken.
-__device__ __forceinline__ Found segment_of_tile(const AttnArgs& a, int64_t t, int rows) {
-  return find_segment(a, [&](int i, int64_t q, int64_t) { return q * a.group / rows + i <= t; });
+template <int ROWS>
+__device__ __forceinline__ Found segment_of_tile(const AttnArgs& a, int t) {
+  return find_segment(a, [&](int i, int q, int) { return q * a.group / ROWS + i <= t; });
 }
 
 // 16 bytes of a buffer; zeros past its end.
@@ -306,9 +303,9 @@ __device__ __forceinline__ float joined(float o, float chunk_o, const Join& j) {
 }
 
 // Keys that query t of a sequence sees: [0, seen).
-__device__ __forceinline__ int64_t keys_seen(const AttnArgs& a, const Sequence& s, int64_t t) {
+__device__ __forceinline__ int keys_seen(const AttnArgs& a, const Sequence& s, int t) {
   if (t >= s.n) return 0;
-  return a.causal ? clamp64(s.m - s.n + t + 1, 0, s.m) : s.m;
+  return a.causal ? clamped(s.m - s.n + t + 1, 0, s.m) : s.m;
 }
 
 }  // namespace dev
