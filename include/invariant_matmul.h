@@ -638,9 +638,9 @@ void head_rope_plan_destroy(head_rope_plan_t plan);
  * ------------------------------------------------------------------------- */
 typedef struct attention_plan_s* attention_plan_t;
 
-/* Plan the call.  max_q: no sequence has more queries (0: q_rows).  A small max_q is
- * what selects the kernel of few rows; a sequence with more queries than max_q says
- * then has NaN in the rows past it.  scale > 0.  GEMM_ERR_INVALID_VALUE for a
+/* Plan the call.  max_q: no sequence has more queries (0: q_rows).  Where it is small and caches are
+ * long, a kernel of few rows takes the call (the bits are the same); a sequence with more
+ * queries than max_q says has NaN in the rows past it.  scale > 0.  GEMM_ERR_INVALID_VALUE for a
  * negative size, batch < 1 or a NULL handle, GEMM_ERR_UNSUPPORTED for other types, sizes
  * (k_rows up to 2^30, q_rows q_heads below 2^31) or scales. */
 gemm_status attention_plan(int64_t q_rows, int64_t k_rows, int64_t batch, int q_heads, int k_heads,

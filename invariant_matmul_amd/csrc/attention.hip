@@ -276,7 +276,12 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttnArgs a) {
     if (row >= rows) continue;
     const int t = row / a.group;
     const int64_t at = (s.q0 + t) * a.q_heads + kh * a.group + (row - t * a.group);
-    // a row without keys is zero; one whose keys are all -infinity is 0 / 0
+    // a row without keys is zero; one whose keys are all -infinity is 0 / 0; and NaN is what a
+    // sequence longer than the call said has past that, here as in the kernel of few rows
+    if (t >= a.max_q && found.segment >= 1 && found.segment <= a.batch) {
+      w.L[i] = __builtin_nanf("");
+      w.seen[i] = 1;
+    }
     const float inv = w.seen[i] == 0 ? 0.0f : 1.0f / w.L[i];
 #pragma unroll
     for (int d = 0; d < T::DB; ++d) {
@@ -312,6 +317,7 @@ template <int IN, int DP>
 __global__ __launch_bounds__(kFewThreads, 2) void attention_few_kernel(AttnArgs a) {
   using T = TileOf<DP>;
   __shared__ __attribute__((aligned(16))) char vt[kFewWaves][kTile * T::PITCH];
+  // (with a second set of these, and a barrier less, two workgroups would not fit into the LDS)
   __shared__ i32x4 pl[kFewWaves][2][64];
   __shared__ float ml[kFewWaves][16], sl[kFewWaves][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -332,7 +338,19 @@ __global__ __launch_bounds__(kFewThreads, 2) void attention_few_kernel(AttnArgs 
 
   const auto kb = buffer_at(static_cast<const char*>(a.k) + 2 * ((s.k0 + c0) * a.k_token + kh * a.k_head));
   const auto vb = buffer_at(static_cast<const char*>(a.v) + 2 * ((s.k0 + c0) * a.v_token + kh * a.v_head));
-  i32x4 kf[4][T::KS];
+  const int rows = queries * a.group;
+  i32x4 kf[4][T::KS], qf[T::KS];
+  auto load_rows = [&](int r0) {
+    const int row = r0 + col, t = row / a.group, h = row - t * a.group;
+    const char* const q = static_cast<const char*>(a.q) + 2 * ((s.q0 + t) * a.q_token + (kh * a.group + h) * a.q_head);
+#pragma unroll
+    for (int ks = 0; ks < T::KS; ++ks) {
+      const int d = 32 * ks + 8 * quad;
+      qf[ks] = i32x4{};
+      if (row < rows && d < a.dim) qf[ks] = *reinterpret_cast<const i32x4*>(q + 2 * d);
+    }
+  };
+  load_rows(0);
 #pragma unroll
   for (int b = 0; b < 4; ++b)
 #pragma unroll
@@ -368,29 +386,18 @@ __global__ __launch_bounds__(kFewThreads, 2) void attention_few_kernel(AttnArgs 
     __syncthreads();
   }
 
-  const int rows = queries * a.group;
   const Lanes<DP> lanes;
   for (int r0 = 0; r0 < rows; r0 += 16) {
     const int row = r0 + col, t = row / a.group;
-    const int h = row - t * a.group;
     const int seen = clamped((row < rows ? keys_seen(a, s, t) : 0) - c0, 0, kAttnChunk);
     f32x4 sc[4];
-    {
-      const char* const q = static_cast<const char*>(a.q) + 2 * ((s.q0 + t) * a.q_token + (kh * a.group + h) * a.q_head);
-      i32x4 qf[T::KS];
 #pragma unroll
-      for (int ks = 0; ks < T::KS; ++ks) {
-        const int d = 32 * ks + 8 * quad;
-        qf[ks] = i32x4{};
-        if (row < rows && d < a.dim) qf[ks] = *reinterpret_cast<const i32x4*>(q + 2 * d);
-      }
+    for (int b = 0; b < 4; ++b) {
+      sc[b] = f32x4{};
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        sc[b] = f32x4{};
-#pragma unroll
-        for (int ks = 0; ks < T::KS; ++ks) sc[b] = mfma16_v<IN>(kf[b][ks], qf[ks], sc[b]);
-      }
+      for (int ks = 0; ks < T::KS; ++ks) sc[b] = mfma16_v<IN>(kf[b][ks], qf[ks], sc[b]);
     }
+    if (r0 + 16 < rows) load_rows(r0 + 16);
 #pragma unroll
     for (int b = 0; b < 4; ++b)
 #pragma unroll
@@ -569,7 +576,28 @@ hipError_t launch_dim(const AttnArgs& a, hipStream_t s) {
 
 }  // namespace
 
-bool attention_few_rows(int64_t max_q, int group) { return max_q * group <= kAttnFewRows; }
+// Which kernel takes a call (the bits are the same): the one with the least estimated time, in us,
+// from what the host knows.  Both wait for memory and launch (6, or 8 with the join).  The kernel of
+// many rows takes 1.5 for a step of 64 keys of a workgroup alone on its compute unit (1.0 up
+// to 64 dimensions), 2 where two share it; the kernel of few rows 3 for a chunk's keys and 1.3
+// (1.7 shared) for each 16 rows, and its results go to memory and back at 4.5 TB/s.
+// Measured, few against many rows' kernel, bf16, 8 key heads of 128 with 4 query heads each:
+//   1 sequence of 8192 keys, 32 queries 29 and 194, 100 queries 68 and 196, 500 queries 275 and 198;
+//   4 of 16384 keys, 100 queries 263 and 387; 1 of 16384 keys, 512 queries 442 and 388;
+//   16 of 2048 keys, 100 queries 101 and 66.
+bool attention_few_rows(const AttnArgs& a) {
+  constexpr double kMostBytes = 512e6;  // of workspace
+  const double rows = (double)a.max_q * a.group, keys = (double)a.k_rows / a.batch;
+  const double slots = (double)attention_chunk_slots(a.k_rows, a.batch) * a.k_heads;
+  const double bytes = slots * rows * (a.dim + 2) * 4;
+  if (bytes > kMostBytes || slots >= 1 << 24 || a.k_rows == 0) return false;
+  const double rounds = slots <= 512 ? 1 : slots / 512, tiles = (rows + 15) / 16;
+  const double few = 8 + rounds * (3 + tiles * (slots <= 256 ? 1.3 : 1.7)) + 2 * bytes / 4.5e6;
+  const double groups = ((double)a.q_rows * a.group / kRows + a.batch) * a.k_heads;
+  const double step = a.dim <= 64 ? 0.67 : 1.0;
+  const double many = 6 + (keys / kTile + 1) * step * (groups <= 256 ? 1.5 : groups <= 512 ? 2 : groups / 256);
+  return few < many;
+}
 int64_t attention_chunk_slots(int64_t k_rows, int batch) { return k_rows / kAttnChunk + batch; }
 
 hipError_t launch_attention(int in, const AttnArgs& a, hipStream_t s) {

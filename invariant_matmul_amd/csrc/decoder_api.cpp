@@ -207,7 +207,10 @@ gemm_status attention_plan(int64_t q_rows, int64_t k_rows, int64_t batch, int q_
     return GEMM_ERR_UNSUPPORTED;
   attention_plan_s p{q_rows, k_rows, max_q, (int)batch, q_heads, k_heads, dim, dtype, causal != 0, false, scale};
   if (p.max_q == 0 || p.max_q > q_rows) p.max_q = q_rows;
-  p.few = attention_few_rows(p.max_q, (int)group);
+  AttnArgs sizes{};
+  sizes.q_rows = q_rows, sizes.k_rows = k_rows, sizes.batch = (int)batch, sizes.k_heads = k_heads;
+  sizes.group = (int)group, sizes.dim = dim, sizes.max_q = p.max_q;
+  p.few = q_rows > 0 && attention_few_rows(sizes);
   *plan = new (std::nothrow) attention_plan_s(p);
   return *plan ? GEMM_OK : GEMM_ERR_INVALID_VALUE;
 }

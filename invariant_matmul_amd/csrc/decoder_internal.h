@@ -40,9 +40,6 @@ hipError_t launch_head_rope_backward(int in, HeadRopeArgs a, void* const* dweigh
 constexpr int kAttnMaxDim = 128;
 constexpr int kAttnChunk = 256;  // keys whose products one softmax partial holds
 constexpr int kAttnTile = 64;    // keys of a step
-// Rows (queries of a sequence times heads that share a key head) up to which the
-// few-rows kernel takes a call.
-constexpr int64_t kAttnFewRows = 64;
 struct AttnArgs {
   const void *q, *k, *v;
   void* o;                 // [q_rows, q_heads, dim]
@@ -66,7 +63,7 @@ struct AttnArgs {
   int64_t q_tiles, k_tiles;
   void *dq, *dk, *dv;      // contiguous
 };
-bool attention_few_rows(int64_t max_q, int group);
+bool attention_few_rows(const AttnArgs& a);  // by its sizes
 int64_t attention_chunk_slots(int64_t k_rows, int batch);
 hipError_t launch_attention(int in, const AttnArgs& a, hipStream_t s);
 hipError_t launch_attention_backward(int in, const AttnArgs& a, hipStream_t s);

@@ -117,9 +117,10 @@ def test_attention_refusals():
     many = imm.attention_plan(1000, 600, 2, 8, 2, 128, "bf16")
     assert imm.attention_workspace_size(many) == 0
     assert imm.attention_backward_workspace_size(many) == 2 * 1000 * 8 * 4
-    # (the group decides with max_q: 64 rows of a key head at most)
-    assert imm.attention_workspace_size(imm.attention_plan(64, 600, 1, 2, 2, 64, "bf16")) > 0
-    assert imm.attention_workspace_size(imm.attention_plan(65, 600, 1, 2, 2, 64, "bf16")) == 0
+    # new tokens over long caches go to the kernel of few rows, prompts and long pieces do not
+    few = lambda *args, **kw: imm.attention_workspace_size(imm.attention_plan(*args, "bf16", **kw)) > 0  # noqa: E731
+    assert few(1, 8192, 1, 32, 8, 128) and few(61, 61 * 8192, 61, 32, 4, 128, max_q=1) and few(100, 8192, 1, 32, 8, 128)
+    assert not few(8192, 8192, 1, 32, 8, 128) and not few(512, 16384, 1, 32, 8, 128) and not few(61, 61 * 8192, 61, 32, 4, 128)
 
     def back(do=P, o=P, low=P, lse=P, dq=P, dk=P, dv=P, ws=P, n=2 * 1000 * 8 * 4):
         return L.attention_backward(many.handle, do, P, 1024, 128, P, 256, 128, P, 256, 128, o, low, lse, P, P, 0, dq, dk, dv, ws,

@@ -199,10 +199,11 @@ def test_masked_lowest_values():
 
 
 def test_more_queries_than_said():
-    q, k, v, _ = make(9, 300, 2, 1, 64, "bf16", 12)
-    o = torch_ops.attention(q, k, v, ints([0, 2, 9]), ints([0, 100, 300]), max_q=4)
-    full = torch_ops.attention(q, k, v, ints([0, 2, 9]), ints([0, 100, 300]))
-    assert torch.equal(o[:2], full[:2]) and torch.isnan(o[6:]).all()
+    for keys in (100, 2000):  # either kernel
+        q, k, v, _ = make(9, 3 * keys, 2, 1, 64, "bf16", 12)
+        o = torch_ops.attention(q, k, v, ints([0, 2, 9]), ints([0, keys, 3 * keys]), max_q=4)
+        full = torch_ops.attention(q, k, v, ints([0, 2, 9]), ints([0, keys, 3 * keys]))
+        assert torch.equal(o[:6], full[:6]) and torch.isnan(o[6:]).all() and torch.isfinite(full).all()
 
 
 def test_contents_of_the_arrays_stay_inside():
