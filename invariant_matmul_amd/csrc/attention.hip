@@ -580,7 +580,7 @@ hipError_t launch_dim(const AttnArgs& a, hipStream_t s) {
 // from what the host knows.  Both wait for memory and launch (6, or 8 with the join).  The kernel of
 // many rows takes 1.5 for a step of 64 keys of a workgroup alone on its compute unit (1.0 up
 // to 64 dimensions), 2 where two share it; the kernel of few rows 3 for a chunk's keys and 1.3
-// (1.7 shared) for each 16 rows, and its results go to memory and back at 4.5 TB/s.
+// (1.7 shared) for each 16 rows, and its results go to the caches and back at 6 TB/s.
 // Measured, few against many rows' kernel, bf16, 8 key heads of 128 with 4 query heads each:
 //   1 sequence of 8192 keys, 32 queries 29 and 194, 100 queries 68 and 196, 500 queries 275 and 198;
 //   4 of 16384 keys, 100 queries 263 and 387; 1 of 16384 keys, 512 queries 442 and 388;
@@ -592,7 +592,7 @@ bool attention_few_rows(const AttnArgs& a) {
   const double bytes = slots * rows * (a.dim + 2) * 4;
   if (bytes > kMostBytes || slots >= 1 << 24 || a.k_rows == 0) return false;
   const double rounds = slots <= 512 ? 1 : slots / 512, tiles = (rows + 15) / 16;
-  const double few = 8 + rounds * (3 + tiles * (slots <= 256 ? 1.3 : 1.7)) + 2 * bytes / 4.5e6;
+  const double few = 8 + rounds * (3 + tiles * (slots <= 256 ? 1.3 : 1.7)) + 2 * bytes / 6e6;
   const double groups = ((double)a.q_rows * a.group / kRows + a.batch) * a.k_heads;
   const double step = a.dim <= 64 ? 0.67 : 1.0;
   const double many = 6 + (keys / kTile + 1) * step * (groups <= 256 ? 1.5 : groups <= 512 ? 2 : groups / 256);
