@@ -7,13 +7,20 @@
 // sequences, on the room behind a cache or on which kernel runs.  A prompt
 // taken at once, in pieces or token by token gives the same bits.  For that, every
 // kernel sums in one order.  Keys are cut from the sequence's first one on into
-// chunks of 256 and steps of 64.  Within a chunk the running maximum, sum and
+// chunks of 256 and steps of 64.  Within a chunk a reference of the logits, the sums and the
 // output go from step to step (each step: S on the matrix cores, p about the
-// running maximum, p rounded to the input's type, two steps of 32 keys
+// reference, p rounded to the input's type, two steps of 32 keys
 // into the output's chain); a chunk's results start anew, and chunks are joined
-// in ascending order by fp32 products with powers of two and one fma.  So chunks
+// in ascending order by fp32 products and one fma.  So chunks
 // can be worked on by workgroups of their own (few rows) or one after the other
 // (many rows).
+//
+// Rounding.  p is rounded to 16 bits for the product with v, and o is divided by the sum of
+// the rounded p, in fp32: the weights then add up to 1, and where one key has most of the weight
+// its rounding drops out of o (8195 packed bf16 tokens: o and its gradients off by 0.0019 and
+// 0.0025 of themselves, with the sum of the unrounded p by 0.0020 and 0.0026, at the same time;
+// about the exact maximum by 0.0017 and 0.0024, but 16384 tokens take 2240 us instead of 2108).
+// lse is of the unrounded sum, in fp32 too.
 #include "attention_common.h"
 
 namespace imm {
@@ -59,12 +66,12 @@ __device__ __forceinline__ f32x4 only_not_finite(i32x2 four) {
 }
 
 // The rows of a wave through one step.
-template <int IN, int DP>
+template <int IN, int DP, bool SAVE>
 struct WaveRows {
   using T = TileOf<DP>;
   i32x4 q[2][T::KS];
   f32x4 O[2][T::DB], o[2][T::DB];  // of the chunks so far, of this chunk
-  float M[2], L[2], m[2], l[2];
+  float M[2], L[2], E[2], m[2], l[2], e[2];  // references and sums (E, e: with SAVE)
   int seen[2];                     // keys of this lane's rows
   Lanes<DP> at;
   float scale_log2;
@@ -73,7 +80,7 @@ struct WaveRows {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       M[i] = kNegInf;
-      L[i] = 0.0f;
+      L[i] = E[i] = 0.0f;
 #pragma unroll
       for (int d = 0; d < T::DB; ++d) O[i][d] = f32x4{};
     }
@@ -104,7 +111,7 @@ struct WaveRows {
           for (int r = 0; r < 4; ++r)
             if (k0 + 16 * b + 4 * quad + r >= seen[i]) sc[i][b][r] = kNegInf;
     }
-    constexpr int PRE = 4;
+    constexpr int PRE = 3;
     i32x4 pre[PRE];
 #pragma unroll
     for (int d = 0; d < PRE; ++d) pre[d] = column_fragment<DP>(vt, at, 0, d);
@@ -114,7 +121,7 @@ struct WaveRows {
       const float top = lane_max(sc[i]) * scale_log2;
       if constexpr (FIRST) {
         m[i] = reference(kNegInf, row_max(top));
-        l[i] = probabilities(sc[i], scale_log2, m[i]);
+        l[i] = e[i] = 0.0f;
       } else {
         // (no lane has a logit that sets the reference of its row again: nothing changes)
         if (__any(reference(m[i], top) != m[i])) {
@@ -122,13 +129,16 @@ struct WaveRows {
           const float f = shrink(m[i], to);
           m[i] = to;
           l[i] *= f;
+          if (SAVE) e[i] *= f;
 #pragma unroll
           for (int d = 0; d < T::DB; ++d) o[i][d] *= f;
         }
-        l[i] += probabilities(sc[i], scale_log2, m[i]);
       }
+      probabilities(sc[i], scale_log2, m[i]);
+      if (SAVE) e[i] += sum_of(sc[i]);
       pf[i][0] = pack_blocks<IN>(sc[i][0], sc[i][1]);
       pf[i][1] = pack_blocks<IN>(sc[i][2], sc[i][3]);
+      l[i] = add_pairs<IN>(pf[i][1], add_pairs<IN>(pf[i][0], l[i]));
     }
 #pragma unroll
     for (int p = 0; p < 2; ++p)
@@ -163,6 +173,7 @@ struct WaveRows {
         const Join j = join_chunk(M[i], m[i]);
         M[i] = j.m;
         L[i] = joined(L[i], row_sum(l[i]), j);
+        if (SAVE) E[i] = joined(E[i], row_sum(e[i]), j);
         // (a product with 1 changes nothing)
         if (__any(j.a != 1.0f)) {
 #pragma unroll
@@ -177,7 +188,8 @@ struct WaveRows {
   }
 };
 
-template <int IN, int DP>
+// SAVE: lse and what o's rounding left too, for the backward pass.
+template <int IN, int DP, bool SAVE>
 __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttnArgs a) {
   using T = TileOf<DP>;
   // (arrays of their own: the compiler then knows that a transfer into one stage does not
@@ -198,7 +210,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttnArgs a) {
   if (r0 >= rows) return;
 
   // this lane's rows: column `col` of the two blocks of 16 of its wave
-  WaveRows<IN, DP> w;
+  WaveRows<IN, DP, SAVE> w;
   w.scale_log2 = a.scale_log2;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -279,7 +291,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttnArgs a) {
     // a row without keys is zero; one whose keys are all -infinity is 0 / 0; and NaN is what a
     // sequence longer than the call said has past that, here as in the kernel of few rows
     if (t >= a.max_q && found.segment >= 1 && found.segment <= a.batch) {
-      w.L[i] = __builtin_nanf("");
+      w.L[i] = w.E[i] = __builtin_nanf("");
       w.seen[i] = 1;
     }
     const float inv = w.seen[i] == 0 ? 0.0f : 1.0f / w.L[i];
@@ -291,12 +303,12 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttnArgs a) {
       const i32x2 y{pack2<IN>(x[0], x[1]), pack2<IN>(x[2], x[3])};
       const int64_t to = 2 * (at * a.dim + c);
       *reinterpret_cast<i32x2*>(static_cast<char*>(a.o) + to) = y;
-      if (a.o_low)
+      if (SAVE && a.o_low)
         *reinterpret_cast<i32x2*>(static_cast<char*>(a.o_low) + to) =
             i32x2{pack2_rest<IN>(x[0], x[1], y[0]), pack2_rest<IN>(x[2], x[3], y[1])};
     }
-    if (a.lse && quad == 0)
-      a.lse[at] = w.seen[i] == 0 ? kNegInf : (w.M[i] + __builtin_amdgcn_logf(w.L[i])) * kLn2;
+    if (SAVE && a.lse && quad == 0)
+      a.lse[at] = w.seen[i] == 0 ? kNegInf : (w.M[i] + __builtin_amdgcn_logf(w.E[i])) * kLn2;
   }
 }
 
@@ -319,7 +331,7 @@ __global__ __launch_bounds__(kFewThreads, 2) void attention_few_kernel(AttnArgs 
   __shared__ __attribute__((aligned(16))) char vt[kFewWaves][kTile * T::PITCH];
   // (with a second set of these, and a barrier less, two workgroups would not fit into the LDS)
   __shared__ i32x4 pl[kFewWaves][2][64];
-  __shared__ float ml[kFewWaves][16], sl[kFewWaves][64];
+  __shared__ float ml[kFewWaves][16], se[kFewWaves][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int quad = lane / 16, col = lane % 16;
   const int kh = blockIdx.x % (unsigned)a.k_heads;
@@ -411,18 +423,22 @@ __global__ __launch_bounds__(kFewThreads, 2) void attention_few_kernel(AttnArgs 
 #pragma unroll
     for (int w = 1; w < kFewWaves; ++w) m[w] = reference(m[w - 1], ml[w][col]);
     const float about = wave == 0 ? m[0] : wave == 1 ? m[1] : wave == 2 ? m[2] : m[3];
-    sl[wave][lane] = probabilities(sc, a.scale_log2, about);
+    probabilities(sc, a.scale_log2, about);
+    se[wave][lane] = sum_of(sc);
     pl[wave][0][lane] = pack_blocks<IN>(sc[0], sc[1]);
     pl[wave][1][lane] = pack_blocks<IN>(sc[2], sc[3]);
     __syncthreads();
     f32x4 o[(T::DB + kFewWaves - 1) / kFewWaves];
 #pragma unroll
     for (auto& x : o) x = f32x4{};
-    float l = 0.0f;
+    float l = 0.0f, sum = 0.0f;
 #pragma unroll
     for (int w = 0; w < kFewWaves; ++w) {
       const float f = w == 0 ? shrink(kNegInf, m[0]) : shrink(m[w - 1], m[w]);
-      l = l * f + sl[w][lane];
+      l *= f;
+      sum = sum * f + se[w][lane];
+#pragma unroll
+      for (int p = 0; p < 2; ++p) l = add_pairs<IN>(pl[w][p][lane], l);
 #pragma unroll
       for (int i = 0; i < (T::DB + kFewWaves - 1) / kFewWaves; ++i) {
         const int d = kFewWaves * i + wave;
@@ -434,11 +450,11 @@ __global__ __launch_bounds__(kFewThreads, 2) void attention_few_kernel(AttnArgs 
       }
     }
     l = row_sum(l);
+    sum = row_sum(sum);
     const int64_t at = ((int64_t)slot * a.k_heads + kh) * a.part_rows + row;
     if (row < rows) {
       if (wave == 0 && quad == 0) {
-        a.part_ml[2 * at] = m[kFewWaves - 1];
-        a.part_ml[2 * at + 1] = l;
+        reinterpret_cast<f32x4*>(a.part_ml)[at] = f32x4{m[kFewWaves - 1], l, sum, 0.0f};
       }
 #pragma unroll
       for (int i = 0; i < (T::DB + kFewWaves - 1) / kFewWaves; ++i) {
@@ -453,7 +469,7 @@ __global__ __launch_bounds__(kFewThreads, 2) void attention_few_kernel(AttnArgs 
         }
       }
     }
-    __syncthreads();  // before the next rows use ml, sl and pl
+    __syncthreads();  // before the next rows use ml, se and pl
   }
 }
 
@@ -474,13 +490,13 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
   const int t = q - s.q0;
   const bool said = t < a.max_q || found.segment == 0 || found.segment > a.batch;  // (rows in no sequence have no keys)
   const int seen = keys_seen(a, s, t);
-  float M = kNegInf, L = 0.0f, O0 = 0.0f, O1 = 0.0f;
+  float M = kNegInf, L = 0.0f, E = 0.0f, O0 = 0.0f, O1 = 0.0f;
   const bool mine = 2 * lane < a.dim;
   if (said && seen > 0) {
     const int64_t step = (int64_t)a.k_heads * a.part_rows;
     const int64_t first = (int64_t)first_slot(found) * step + kh * a.part_rows + t * a.group + (head - kh * a.group);
     const int chunks = (seen + kAttnChunk - 1) / kAttnChunk;
-    const float2* ml_at = reinterpret_cast<const float2*>(a.part_ml) + first + lane * step;
+    const f32x4* ml_at = reinterpret_cast<const f32x4*>(a.part_ml) + first + lane * step;
     const char* o_at = reinterpret_cast<const char*>(a.part_o + first * a.dim + 2 * lane);
     const int64_t o_step = step * a.dim * 4;
     // (rows past the last chunk are loaded as the last once more)
@@ -496,23 +512,23 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
     load(next);
     for (int c0 = 0; c0 < chunks; c0 += 64) {
       const int n = chunks - c0 < 64 ? chunks - c0 : 64;
-      float2 ml{kNegInf, 0.0f};
+      f32x4 ml{kNegInf, 0.0f, 0.0f, 0.0f};
       if (lane < n) ml = *ml_at;
       ml_at += 64 * step;
       // the reference after each chunk: it is set again at few of them
       float before = M, after = M;
       for (int from = 0;;) {
-        const uint64_t set = __ballot(lane >= from && reference(M, ml.x) != M);
+        const uint64_t set = __ballot(lane >= from && reference(M, ml[0]) != M);
         if (!set) break;
         const int l = __ffsll((unsigned long long)set) - 1;
-        const float to = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ml.x), l));
+        const float to = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ml[0]), l));
         if (lane > l) before = to;
         if (lane >= l) after = to;
         M = to;
         from = l + 1;
       }
       const float fa = shrink(before, after);
-      const float fb = ml.x == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(ml.x - after);
+      const float fb = ml[0] == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(ml[0] - after);
       const bool ones = __all(fa == 1.0f);
       for (int u0 = 0; u0 < n; u0 += U) {
 #pragma unroll
@@ -521,15 +537,18 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const float b = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(fb), u0 + u));
-          const float l = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ml.y), u0 + u));
+          const float l = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ml[1]), u0 + u));
+          const float e = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ml[2]), u0 + u));
           if (!ones) {  // (a product with 1 changes nothing)
             const float f = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(fa), u0 + u));
             L *= f;
+            E *= f;
             O0 *= f;
             O1 *= f;
           }
           if (u0 + u < n) {
             L = fmaf(l, b, L);
+            E = fmaf(e, b, E);
             O0 = fmaf(o[u].x, b, O0);
             O1 = fmaf(o[u].y, b, O1);
           }
@@ -537,7 +556,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
       }
     }
   }
-  if (!said) L = O0 = O1 = __builtin_nanf("");  // a sequence longer than the call said
+  if (!said) L = E = O0 = O1 = __builtin_nanf("");  // a sequence longer than the call said
   const bool empty = seen == 0 && said;
   const float inv = empty ? 0.0f : 1.0f / L;
   if (mine) {
@@ -546,7 +565,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
     static_cast<int*>(a.o)[to] = y;
     if (a.o_low) static_cast<int*>(a.o_low)[to] = pack2_rest<IN>(O0 * inv, O1 * inv, y);
   }
-  if (a.lse && lane == 0) a.lse[at] = empty ? kNegInf : (M + __builtin_amdgcn_logf(L)) * kLn2;
+  if (a.lse && lane == 0) a.lse[at] = empty ? kNegInf : (M + __builtin_amdgcn_logf(E)) * kLn2;
 }
 
 template <int IN, int DP>
@@ -562,8 +581,8 @@ hipError_t launch_in(const AttnArgs& a, hipStream_t s) {
     return hipGetLastError();
   }
   const int64_t tiles = a.q_rows * a.group / kRows + a.batch + 2;
-  hipLaunchKernelGGL((attention_kernel<IN, DP>), dim3((unsigned)(tiles * a.k_heads)), dim3(kThreads), 0,
-                     s, a);
+  const auto kernel = a.lse || a.o_low ? attention_kernel<IN, DP, true> : attention_kernel<IN, DP, false>;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)(tiles * a.k_heads)), dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
 
@@ -589,7 +608,7 @@ bool attention_few_rows(const AttnArgs& a) {
   constexpr double kMostBytes = 512e6;  // of workspace
   const double rows = (double)a.max_q * a.group, keys = (double)a.k_rows / a.batch;
   const double slots = (double)attention_chunk_slots(a.k_rows, a.batch) * a.k_heads;
-  const double bytes = slots * rows * (a.dim + 2) * 4;
+  const double bytes = slots * rows * (a.dim + 4) * 4;
   if (bytes > kMostBytes || slots >= 1 << 24 || a.k_rows == 0) return false;
   const double rounds = slots <= 512 ? 1 : slots / 512, tiles = (rows + 15) / 16;
   const double few = 8 + rounds * (3 + tiles * (slots <= 256 ? 1.3 : 1.7)) + 2 * bytes / 6e6;

@@ -221,6 +221,25 @@ __device__ __forceinline__ i32x4 pack_blocks(const f32x4& a, const f32x4& b) {
                pack2<IN>(b[2], b[3])};
 }
 
+// sum + the four pairs of 16-bit values of a.
+template <int IN>
+__device__ __forceinline__ float add_pairs(const i32x4& a, float sum) {
+#if defined(__HIP_DEVICE_COMPILE__)
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int two = a[e];
+    if constexpr (IN == GEMM_F16) {
+      typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+      sum = __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, two), f16x2{1, 1}, sum, false);
+    } else {
+      typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+      sum = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, two), bf16x2{1, 1}, sum, false);
+    }
+  }
+#endif
+  return sum;
+}
+
 // Over the four lanes of a row.  (The swaps of 16 and 32 lanes hand every lane both values.)
 struct Both {
   float a, b;
@@ -275,22 +294,23 @@ __device__ __forceinline__ float reference(float m, float step_max) {
 __device__ __forceinline__ float shrink(float a, float b) {
   return a == b || a == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(a - b);
 }
-// Probabilities about the reference m (of a row without any, 0), in place;
-// their sum in the lane.
-__device__ __forceinline__ float probabilities(f32x4 (&s)[4], float scale_log2, float m) {
+// Probabilities about the reference m (of a row without any, 0), in place.
+__device__ __forceinline__ void probabilities(f32x4 (&s)[4], float scale_log2, float m) {
   const float about = m == kNegInf ? 0.0f : m;
-  float sum = 0.0f;
 #pragma unroll
-  for (int b = 0; b < 4; ++b) {
+  for (int b = 0; b < 4; ++b)
 #pragma unroll
     for (int r = 0; r < 4; ++r) s[b][r] = __builtin_amdgcn_exp2f(fmaf(s[b][r], scale_log2, -about));
-    sum += (s[b][0] + s[b][1]) + (s[b][2] + s[b][3]);
-  }
+}
+__device__ __forceinline__ float sum_of(const f32x4 (&s)[4]) {
+  float sum = 0.0f;
+#pragma unroll
+  for (int b = 0; b < 4; ++b) sum += (s[b][0] + s[b][1]) + (s[b][2] + s[b][3]);
   return sum;
 }
 
 // The result of the keys so far and that of one more chunk, about a reference that follows the
-// chunks' as theirs follow the logits: o = o a + chunk_o b, l = l a + chunk_l b.
+// chunks' as theirs follow the logits: o = o a + chunk_o b, and so the sums.
 struct Join {
   float m, a, b;
 };

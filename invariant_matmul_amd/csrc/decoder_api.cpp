@@ -218,7 +218,7 @@ gemm_status attention_plan(int64_t q_rows, int64_t k_rows, int64_t batch, int q_
 size_t attention_workspace_size(attention_plan_t p) {
   if (!p || !p->few) return 0;
   const size_t slots = (size_t)attention_chunk_slots(p->k_rows, p->batch);
-  return slots * (size_t)(p->q_heads * p->max_q) * (size_t)(p->dim + 2) * sizeof(float);
+  return slots * (size_t)(p->q_heads * p->max_q) * (size_t)(p->dim + 4) * sizeof(float);
 }
 
 size_t attention_backward_workspace_size(attention_plan_t p) {

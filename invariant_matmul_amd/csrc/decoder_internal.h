@@ -53,7 +53,8 @@ struct AttnArgs {
   int64_t max_q;
   float scale, scale_log2;  // scale log2(e)
   int causal;
-  // few rows: partial results per (chunk, key head, row): o [.., dim] and (m, l)
+  // few rows: partial results per (chunk, key head, row): o [.., dim] and
+  // (reference, sum of rounded, sum of unrounded probabilities, 0)
   float *part_o, *part_ml;
   int64_t chunks;          // chunk slots of all sequences
   int part_rows;           // rows a chunk slot holds: max_q group

@@ -105,7 +105,7 @@ def test_attention_refusals():
                                None)
 
     # few rows: a chunk slot per 256 keys and sequence, for 4 queries of 8 heads
-    need = (600 // 256 + 2) * 4 * 8 * (128 + 2) * 4
+    need = (600 // 256 + 2) * 4 * 8 * (128 + 4) * 4
     assert imm.attention_workspace_size(plan) == need
     for bad in ({"q": 0}, {"q": P + 8}, {"k": 0}, {"v": P + 4}, {"qt": 1028}, {"kh": -8}, {"vt": 12}, {"cq": 0}, {"ck": 0},
                 {"cq": 0, "ck": 0}, {"cq": P + 2}, {"lens": P + 1}, {"o": 0}, {"o": P + 8}, {"low": P + 8}, {"lse": P + 2},
