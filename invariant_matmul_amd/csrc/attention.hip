@@ -28,10 +28,9 @@ namespace {
 using namespace dev;
 
 // ---- Many rows -----------------------------------------------------------------
-// A workgroup takes 256 rows of a key head, 32 a wave, and walks through their keys
-// 64 at a time: the next step's keys and values go by DMA into the other half of a
+// A workgroup takes 128 rows of a key head, 32 a wave (or 64, 16 a wave: SETS sets of 16), and
+// walks through their keys 64 at a time: the next step's keys and values go by DMA into the other half of a
 // two-stage LDS buffer while this one's are used.
-constexpr int kRows = 32 * kWaves;
 
 template <int IN>
 __device__ __forceinline__ bool not_finite(unsigned two) {
@@ -66,19 +65,19 @@ __device__ __forceinline__ f32x4 only_not_finite(i32x2 four) {
 }
 
 // The rows of a wave through one step.
-template <int IN, int DP, bool SAVE>
+template <int IN, int DP, bool SAVE, int SETS>
 struct WaveRows {
   using T = TileOf<DP>;
-  i32x4 q[2][T::KS];
-  f32x4 O[2][T::DB], o[2][T::DB];  // of the chunks so far, of this chunk
-  float M[2], L[2], E[2], m[2], l[2], e[2];  // references and sums (E, e: with SAVE)
-  int seen[2];                     // keys of this lane's rows
+  i32x4 q[SETS][T::KS];
+  f32x4 O[SETS][T::DB], o[SETS][T::DB];  // of the chunks so far, of this chunk
+  float M[SETS], L[SETS], E[SETS], m[SETS], l[SETS], e[SETS];  // references and sums (E, e: with SAVE)
+  int seen[SETS];  // keys of this lane's rows
   Lanes<DP> at;
   float scale_log2;
 
   __device__ __forceinline__ void clear_all() {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < SETS; ++i) {
       M[i] = kNegInf;
       L[i] = E[i] = 0.0f;
 #pragma unroll
@@ -91,20 +90,21 @@ struct WaveRows {
   __device__ __forceinline__ void step(const char* kt, const char* vt, int k0, bool masked) {
     const int quad = (threadIdx.x & 63) / 16;
     at.again();
-    f32x4 sc[2][4];
+    f32x4 sc[SETS][4];
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
-      sc[0][b] = sc[1][b] = f32x4{};
+#pragma unroll
+      for (int i = 0; i < SETS; ++i) sc[i][b] = f32x4{};
 #pragma unroll
       for (int ks = 0; ks < T::KS; ++ks) {
         const i32x4 kf = row_fragment<DP>(kt, at, b, ks);
-        sc[0][b] = mfma16_v<IN>(kf, q[0][ks], sc[0][b]);
-        sc[1][b] = mfma16_v<IN>(kf, q[1][ks], sc[1][b]);
+#pragma unroll
+        for (int i = 0; i < SETS; ++i) sc[i][b] = mfma16_v<IN>(kf, q[i][ks], sc[i][b]);
       }
     }
     if (masked) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < SETS; ++i)
 #pragma unroll
         for (int b = 0; b < 4; ++b)
 #pragma unroll
@@ -115,9 +115,9 @@ struct WaveRows {
     i32x4 pre[PRE];
 #pragma unroll
     for (int d = 0; d < PRE; ++d) pre[d] = column_fragment<DP>(vt, at, 0, d);
-    i32x4 pf[2][2];
+    i32x4 pf[SETS][2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < SETS; ++i) {
       const float top = lane_max(sc[i]) * scale_log2;
       if constexpr (FIRST) {
         m[i] = reference(kNegInf, row_max(top));
@@ -145,8 +145,8 @@ struct WaveRows {
 #pragma unroll
       for (int d = 0; d < T::DB; ++d) {
         const i32x4 vf = p == 0 && d < PRE ? pre[d < PRE ? d : 0] : column_fragment<DP>(vt, at, p, d);
-        o[0][d] = mfma16_v<IN>(vf, pf[0][p], FIRST && p == 0 ? f32x4{} : o[0][d]);
-        o[1][d] = mfma16_v<IN>(vf, pf[1][p], FIRST && p == 0 ? f32x4{} : o[1][d]);
+#pragma unroll
+        for (int i = 0; i < SETS; ++i) o[i][d] = mfma16_v<IN>(vf, pf[i][p], FIRST && p == 0 ? f32x4{} : o[i][d]);
       }
   }
   // The values of a step that are not finite, for the rows that see them.
@@ -160,14 +160,14 @@ struct WaveRows {
         if (c < dim) x = *reinterpret_cast<const i32x2*>(v + j * v_bytes + 2 * c);
         const f32x4 bad = only_not_finite<IN>(x);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) o[i][d] += j < seen[i] ? bad : f32x4{};
+        for (int i = 0; i < SETS; ++i) o[i][d] += j < seen[i] ? bad : f32x4{};
       }
     }
   }
   // The end of the chunk that begins at c0.
   __device__ __forceinline__ void join(int c0) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < SETS; ++i) {
       // (a chunk that the row does not see leaves it as it is, to the sign of a zero)
       if (c0 < seen[i]) {
         const Join j = join_chunk(M[i], m[i]);
@@ -189,8 +189,9 @@ struct WaveRows {
 };
 
 // SAVE: lse and what o's rounding left too, for the backward pass.
-template <int IN, int DP, bool SAVE>
+template <int IN, int DP, bool SAVE, int SETS>
 __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttnArgs a) {
+  constexpr int kRows = 16 * SETS * kWaves;
   using T = TileOf<DP>;
   // (arrays of their own: the compiler then knows that a transfer into one stage does not
   // touch the other, and lets the reads of that go on)
@@ -202,19 +203,27 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttnArgs a) {
   // head's workgroups meet in few of the L2s.  The last rows (the most keys) first.
   const int tiles = gridDim.x / (unsigned)a.k_heads;
   const int kh = blockIdx.x % (unsigned)a.k_heads;
-  const int tile = tiles - 1 - (int)(blockIdx.x / (unsigned)a.k_heads);
-  const Found found = segment_of_tile<kRows>(a, tile);
+  const int tile = blockIdx.x / (unsigned)a.k_heads;
+  FoundTile f;
+  if (a.sorted) {
+    f = longest_first<kRows>(a, tile);
+  } else {
+    f.found = segment_of_tile<kRows>(a, tiles - 1 - tile);
+    f.first = (tiles - 1 - tile - (f.found.s.q0 * a.group / kRows + f.found.segment)) * kRows;
+  }
+  const Found found = f.found;
   const Sequence s = found.s;
-  const int r0 = (tile - (s.q0 * a.group / kRows + found.segment)) * kRows;
+  const int r0 = f.first;
   const int rows = s.n * a.group;
   if (r0 >= rows) return;
 
   // this lane's rows: column `col` of the two blocks of 16 of its wave
-  WaveRows<IN, DP, SAVE> w;
+  const int w0 = r0 + 16 * SETS * wave;
+  WaveRows<IN, DP, SAVE, SETS> w;
   w.scale_log2 = a.scale_log2;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int row = r0 + 32 * wave + 16 * i + col, t = row / a.group;
+  for (int i = 0; i < SETS; ++i) {
+    const int row = w0 + 16 * i + col, t = row / a.group;
     const int h = row - t * a.group;
     w.seen[i] = keys_seen(a, s, t);
     const char* const q = static_cast<const char*>(a.q) + 2 * ((s.q0 + t) * a.q_token + (kh * a.group + h) * a.q_head);
@@ -230,8 +239,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttnArgs a) {
   auto seen_of = [&](int r) { return keys_seen(a, s, (r < rows ? r : rows - 1) / a.group); };
   const int need = __builtin_amdgcn_readfirstlane(seen_of(r0 + kRows - 1));
   const int all_see = __builtin_amdgcn_readfirstlane(seen_of(r0));
-  const int w0 = r0 + 32 * wave;
-  const int wave_need = __builtin_amdgcn_readfirstlane(w0 < rows ? seen_of(w0 + 31) : 0);
+  const int wave_need = __builtin_amdgcn_readfirstlane(w0 < rows ? seen_of(w0 + 16 * SETS - 1) : 0);
   const int wave_all = __builtin_amdgcn_readfirstlane(w0 < rows ? seen_of(w0) : 0);
   w.clear_all();
 
@@ -283,8 +291,8 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttnArgs a) {
   }
 
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int row = r0 + 32 * wave + 16 * i + col;
+  for (int i = 0; i < SETS; ++i) {
+    const int row = w0 + 16 * i + col;
     if (row >= rows) continue;
     const int t = row / a.group;
     const int64_t at = (s.q0 + t) * a.q_heads + kh * a.group + (row - t * a.group);
@@ -568,6 +576,27 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
   if (a.lse && lane == 0) a.lse[at] = empty ? kNegInf : (M + __builtin_amdgcn_logf(E)) * kLn2;
 }
 
+// Workgroups of 128 rows.
+int64_t groups_of(const AttnArgs& a) { return (a.q_rows * a.group / (32 * kWaves) + a.batch) * a.k_heads; }
+// Up to two of them a compute unit, what one takes for its keys alone is what the call takes:
+// waves then take 16 rows instead of 32, which halves a step's products and exponentials, not its reads
+// (8 key heads of 128, 4 query heads each: 1000 tokens 30 -> 23 us, 2000 56 -> 54, but 4000, with
+// 1024 workgroups, 155 -> 184).
+constexpr int64_t kSmallGroups = 512;
+// While they are few rounds of what the compute units hold, those with the most keys go first: 13
+// sequences of 169 to 1340 tokens, 2 key heads of 64, 16 query heads, 38 -> 34 us; 5 of 183 to
+// 3544, 8 key heads of 128, 142 -> 133.  (Equal sequences lose up to 2 us by it, and with
+// 4096 workgroups it gives nothing.)
+constexpr int64_t kSortedGroups = 2048;
+
+template <int IN, int DP, int SETS>
+void launch_rows(AttnArgs a, hipStream_t s) {
+  const int64_t tiles = a.q_rows * a.group / (16 * SETS * kWaves) + a.batch + 2;
+  a.sorted = a.batch > 1 && a.batch + 2 <= kSortedSegments && groups_of(a) <= kSortedGroups;
+  const auto kernel = a.lse || a.o_low ? attention_kernel<IN, DP, true, SETS> : attention_kernel<IN, DP, false, SETS>;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)(tiles * a.k_heads)), dim3(kThreads), 0, s, a);
+}
+
 template <int IN, int DP>
 hipError_t launch_in(const AttnArgs& a, hipStream_t s) {
   if (a.part_o) {
@@ -580,9 +609,8 @@ hipError_t launch_in(const AttnArgs& a, hipStream_t s) {
                        dim3(256), 0, s, a);
     return hipGetLastError();
   }
-  const int64_t tiles = a.q_rows * a.group / kRows + a.batch + 2;
-  const auto kernel = a.lse || a.o_low ? attention_kernel<IN, DP, true> : attention_kernel<IN, DP, false>;
-  hipLaunchKernelGGL(kernel, dim3((unsigned)(tiles * a.k_heads)), dim3(kThreads), 0, s, a);
+  if (groups_of(a) <= kSmallGroups) launch_rows<IN, DP, 1>(a, s);
+  else launch_rows<IN, DP, 2>(a, s);
   return hipGetLastError();
 }
 
@@ -597,13 +625,13 @@ hipError_t launch_dim(const AttnArgs& a, hipStream_t s) {
 
 // Which kernel takes a call (the bits are the same): the one with the least estimated time, in us,
 // from what the host knows.  Both wait for memory and launch (6, or 8 with the join).  The kernel of
-// many rows takes 1.5 for a step of 64 keys of a workgroup alone on its compute unit (1.0 up
-// to 64 dimensions), 2 where two share it; the kernel of few rows 3 for a chunk's keys and 1.3
-// (1.7 shared) for each 16 rows, and its results go to the caches and back at 6 TB/s.
-// Measured, few against many rows' kernel, bf16, 8 key heads of 128 with 4 query heads each:
-//   1 sequence of 8192 keys, 32 queries 29 and 194, 100 queries 68 and 196, 500 queries 275 and 198;
-//   4 of 16384 keys, 100 queries 263 and 387; 1 of 16384 keys, 512 queries 442 and 388;
-//   16 of 2048 keys, 100 queries 101 and 66.
+// many rows takes 1.02 for a step of 64 keys (0.6 up to 64 dimensions), and as much for each
+// 256 workgroups where these fill the compute units; the kernel of few rows 3 for a chunk's
+// keys and 1.3 (1.7 shared) for each 16 rows, and its results go to the caches and back at
+// 6 TB/s.  Measured, few against many rows' kernel, bf16, 8 key heads of 128 with 4 query heads each:
+//   1 sequence of 8192 keys, 32 queries 31 and 133, 100 queries 71 and 135, 500 queries 290 and 136;
+//   4 of 16384 keys, 100 queries 273 and 265; 1 of 16384 keys, 300 queries 276 and 265;
+//   4 of 4096 keys, 64 queries 59 and 71; 16 of 2048 keys, 100 queries 106 and 58.
 bool attention_few_rows(const AttnArgs& a) {
   constexpr double kMostBytes = 512e6;  // of workspace
   const double rows = (double)a.max_q * a.group, keys = (double)a.k_rows / a.batch;
@@ -612,9 +640,9 @@ bool attention_few_rows(const AttnArgs& a) {
   if (bytes > kMostBytes || slots >= 1 << 24 || a.k_rows == 0) return false;
   const double rounds = slots <= 512 ? 1 : slots / 512, tiles = (rows + 15) / 16;
   const double few = 8 + rounds * (3 + tiles * (slots <= 256 ? 1.3 : 1.7)) + 2 * bytes / 6e6;
-  const double groups = ((double)a.q_rows * a.group / kRows + a.batch) * a.k_heads;
-  const double step = a.dim <= 64 ? 0.67 : 1.0;
-  const double many = 6 + (keys / kTile + 1) * step * (groups <= 256 ? 1.5 : groups <= 512 ? 2 : groups / 256);
+  const double groups = (double)groups_of(a);
+  const double step = a.dim <= 64 ? 0.6 : 1.02;
+  const double many = 6 + (keys / kTile + 1) * step * (groups <= kSmallGroups ? 1 : groups / 256);
   return few < many;
 }
 int64_t attention_chunk_slots(int64_t k_rows, int batch) { return k_rows / kAttnChunk + batch; }

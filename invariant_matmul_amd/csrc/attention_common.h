@@ -95,6 +95,42 @@ __device__ __forceinline__ Found segment_of_tile(const AttnArgs& a, int t) {
   return find_segment(a, [&](int i, int q, int) { return q * a.group / ROWS + i <= t; });
 }
 
+// The same tiles, none empty, with the longest sequence's first and each sequence's last rows first
+// (up to kSortedSegments segments, a lane each).
+constexpr int kSortedSegments = 32;
+struct FoundTile {
+  Found found;
+  int first;  // row of the tile; past the rows if there is no such tile
+};
+template <int ROWS>
+__device__ __forceinline__ FoundTile longest_first(const AttnArgs& a, int t) {
+  const int lane = threadIdx.x & 63, segments = a.batch + 2;
+  int len = 0x7fffffff;
+  if (a.k_lens && lane >= 1 && lane <= a.batch) len = a.k_lens[lane - 1];
+  const int q = q_start(a, lane), k = key_start(a, lane);
+  const int q_end = q_start(a, lane + 1), k_end = key_start(a, lane + 1);
+  const int n = q_end > q ? q_end - q : 0, room = k_end > k ? k_end - k : 0;
+  const int m = lane >= 1 && lane <= a.batch ? clamped(len, 0, room) : 0;
+  const int tiles = lane < segments ? (n * a.group + ROWS - 1) / ROWS : 0;
+  int before = 0;
+  for (int j = 0; j < segments; ++j) {
+    const int mj = __builtin_amdgcn_readlane(m, j), tj = __builtin_amdgcn_readlane(tiles, j);
+    before += mj > m || (mj == m && j < lane) ? tj : 0;
+  }
+  const uint64_t in = __ballot(t >= before && t - before < tiles);
+  FoundTile f{};
+  if (in == 0) return f;
+  const int l = __builtin_ctzll(in);
+  f.found.segment = l;
+  f.found.s.q0 = __builtin_amdgcn_readlane(q, l);
+  f.found.s.k0 = __builtin_amdgcn_readlane(k, l);
+  f.found.s.n = __builtin_amdgcn_readlane(n, l);
+  f.found.s.m = __builtin_amdgcn_readlane(m, l);
+  f.found.k_end = f.found.s.k0 + __builtin_amdgcn_readlane(room, l);
+  f.first = (__builtin_amdgcn_readlane(tiles, l) - 1 - (t - __builtin_amdgcn_readlane(before, l))) * ROWS;
+  return f;
+}
+
 // 16 bytes of a buffer; zeros past its end.
 __device__ __forceinline__ u32x4 load_b128(__amdgpu_buffer_rsrc_t buf, unsigned off) {
 #if defined(__HIP_DEVICE_COMPILE__)

@@ -53,6 +53,7 @@ struct AttnArgs {
   int64_t max_q;
   float scale, scale_log2;  // scale log2(e)
   int causal;
+  int sorted;              // many rows: the longest sequences first
   // few rows: partial results per (chunk, key head, row): o [.., dim] and
   // (reference, sum of rounded, sum of unrounded probabilities, 0)
   float *part_o, *part_ml;

@@ -96,7 +96,7 @@ def test_attention_plan_arguments(args, kw, want):
 
 def test_attention_refusals():
     L = imm.lib()
-    plan = imm.attention_plan(10, 600, 2, 8, 2, 128, "bf16", max_q=4)
+    plan = imm.attention_plan(10, 6000, 2, 8, 2, 128, "bf16", max_q=4)
 
     def run(q=P, qt=1024, qh=128, k=P, kt=256, kh=128, v=P, vt=256, vh=128, cq=P, ck=P, lens=0, o=P, low=0, lse=0, ws=P,
             n=None, plan=plan):
@@ -105,7 +105,7 @@ def test_attention_refusals():
                                None)
 
     # few rows: a chunk slot per 256 keys and sequence, for 4 queries of 8 heads
-    need = (600 // 256 + 2) * 4 * 8 * (128 + 4) * 4
+    need = (6000 // 256 + 2) * 4 * 8 * (128 + 4) * 4
     assert imm.attention_workspace_size(plan) == need
     for bad in ({"q": 0}, {"q": P + 8}, {"k": 0}, {"v": P + 4}, {"qt": 1028}, {"kh": -8}, {"vt": 12}, {"cq": 0}, {"ck": 0},
                 {"cq": 0, "ck": 0}, {"cq": P + 2}, {"lens": P + 1}, {"o": 0}, {"o": P + 8}, {"low": P + 8}, {"lse": P + 2},
