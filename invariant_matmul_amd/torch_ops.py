@@ -649,12 +649,19 @@ def _needs_grad(*tensors) -> bool:
     return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
 
 
+def _refuse_second(where: str):
+    """At the head of a backward pass: with create_graph=True autograd is on there, and would take
+    the gradients for constants."""
+    if torch.is_grad_enabled():
+        raise RuntimeError(f"{where} is differentiable once: its gradients have none (create_graph=True)")
+
+
 def _check_rope(where, q, k, positions, inv_freq, q_weight, k_weight, norm, sections):
     """(device, tokens, dim, plan-ready sections)"""
-    dtype, device = q.dtype, q.device
-    if not (q.is_cuda and dtype in _DT and q.dim() == 3 and k.dim() == 3 and k.dtype == dtype
-            and k.device == device and k.shape[0] == q.shape[0] and k.shape[2] == q.shape[2]
-            and q.shape[2] > 0 and q.shape[2] % 8 == 0):
+    dtype, device, size, k_size = q.dtype, q.device, q.shape, k.shape
+    if not (q.is_cuda and dtype in _DT and len(size) == 3 and len(k_size) == 3 and k.dtype == dtype
+            and k.device == device and k_size[0] == size[0] and k_size[2] == size[2]
+            and size[2] > 0 and size[2] % 8 == 0):
         raise ValueError(f"{where}: needs fp16/bf16 CUDA tensors q [T, q_heads, D] and k [T, k_heads, D] of one "
                          f"type, D a multiple of 8; got {tuple(q.shape)} {q.dtype} on {q.device} and "
                          f"{tuple(k.shape)} {k.dtype} on {k.device}")
@@ -664,12 +671,12 @@ def _check_rope(where, q, k, positions, inv_freq, q_weight, k_weight, norm, sect
         sections = tuple(int(n) for n in sections)
         if not sections or min(sections) < 0 or sum(sections) != inv_freq.shape[0]:
             raise ValueError(f"{where}: sections {sections} must add up to the {inv_freq.shape[0]} frequencies")
-    want = (q.shape[0],) if sections is None else (len(sections), q.shape[0])
+    want = size[:1] if sections is None else (len(sections), size[0])
     if positions.dtype != torch.int64 or positions.shape != want or positions.device != device:
-        raise ValueError(f"{where}: positions must be int64 {want} on {device}, got {positions.dtype} "
+        raise ValueError(f"{where}: positions must be int64 {tuple(want)} on {device}, got {positions.dtype} "
                          f"{tuple(positions.shape)} on {positions.device}")
     for w in (q_weight, k_weight):
-        if w is not None and (not norm or w.dtype != dtype or w.device != device or w.shape != q.shape[2:]):
+        if w is not None and (not norm or w.dtype != dtype or w.device != device or w.shape != size[2:]):
             raise ValueError(f"{where}: a weight must hold {q.shape[2]} values of {dtype} on {device} (and needs "
                              "norm=True)")
     return sections
@@ -746,8 +753,8 @@ class _QkNormRope(torch.autograd.Function):
                              sections)
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
     def backward(ctx, dq_out, dk_out):
+        _refuse_second("qk_norm_rope")
         q, k, q_weight, k_weight, positions, inv_freq = ctx.saved_tensors
         eps, norm, interleaved, sections = ctx.options
         need = ctx.needs_input_grad
@@ -781,11 +788,11 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, inv_
 
 def _check_attention(where, q, k, v, cu_q, cu_k, k_lens):
     """(cu_k, batch)"""
-    dtype, device = q.dtype, q.device
-    if not (q.is_cuda and dtype in _DT and q.dim() == 3 and k.dim() == 3 and v.shape == k.shape
-            and k.dtype == v.dtype == dtype and k.device == v.device == device and k.shape[2] == q.shape[2]
-            and 0 < q.shape[2] <= 128 and q.shape[2] % 8 == 0 and k.shape[1] > 0 and q.shape[1] > 0
-            and q.shape[1] % k.shape[1] == 0):
+    dtype, device, size, k_size = q.dtype, q.device, q.shape, k.shape
+    if not (q.is_cuda and dtype in _DT and len(size) == 3 and len(k_size) == 3 and v.shape == k_size
+            and k.dtype == v.dtype == dtype and k.device == v.device == device and k_size[2] == size[2]
+            and 0 < size[2] <= 128 and size[2] % 8 == 0 and k_size[1] > 0 and size[1] > 0
+            and size[1] % k_size[1] == 0):
         raise ValueError(f"{where}: needs fp16/bf16 CUDA tensors of one type, q [Tq, q_heads, D], k and v [Tk, k_heads, "
                          f"D], D a multiple of 8 up to 128 and q_heads a multiple of k_heads; got {tuple(q.shape)} "
                          f"{q.dtype} on {q.device}, {tuple(k.shape)} {k.dtype} on {k.device} and {tuple(v.shape)} "
@@ -795,9 +802,10 @@ def _check_attention(where, q, k, v, cu_q, cu_k, k_lens):
             raise ValueError(f"{where}: cu_k needs cu_q")
         batch = 1
     else:
-        cu_k = cu_q if cu_k is None else cu_k
         batch = cu_q.numel() - 1
-        for t in (cu_q, cu_k):
+        both = (cu_q,) if cu_k is None or cu_k is cu_q else (cu_q, cu_k)
+        cu_k = both[-1]
+        for t in both:
             if t.dtype != torch.int32 or t.shape != (batch + 1,) or batch < 1 or t.device != device:
                 raise ValueError(f"{where}: cu_q and cu_k must be int32 vectors of sequences + 1 values on {device}")
     if k_lens is not None and (k_lens.dtype != torch.int32 or k_lens.shape != (batch,) or k_lens.device != device):
@@ -894,8 +902,8 @@ class _Attention(torch.autograd.Function):
         return o
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
     def backward(ctx, do):
+        _refuse_second("attention")
         q, k, v, o, lse, o_low, cu_q, cu_k, k_lens = ctx.saved_tensors
         causal, scale = ctx.options
         grads = attention_backward(do, q, k, v, o, AttentionSaved(lse, o_low), cu_q, cu_k, k_lens=k_lens, causal=causal, scale=scale)
@@ -932,15 +940,16 @@ _LOGITS = (torch.float32, torch.float16, torch.bfloat16)
 
 def _check_logits(where, logits, tokens):
     """(rows, vocabulary, tokens of a row)"""
-    if not (logits.is_cuda and logits.dtype in _LOGITS and logits.dim() >= 1 and logits.shape[-1] > 0):
+    size, shape, device = logits.shape, tokens.shape, logits.device
+    if not (logits.is_cuda and logits.dtype in _LOGITS and size and size[-1] > 0):
         raise ValueError(f"{where}: needs fp32/fp16/bf16 CUDA logits [..., V], got {tuple(logits.shape)} {logits.dtype} "
                          f"on {logits.device}")
-    lead = logits.shape[:-1]
-    if tokens.dtype != torch.int64 or tokens.device != logits.device or not (
-            tokens.shape == lead or tokens.shape[:-1] == lead and tokens.dim() == logits.dim()):
+    lead = size[:-1]
+    if tokens.dtype != torch.int64 or tokens.device != device or not (
+            shape == lead or shape[:-1] == lead and len(shape) == len(size)):
         raise ValueError(f"{where}: tokens must be int64 {tuple(lead)} or {tuple(lead)} + (n,) on {logits.device}, got "
                          f"{tokens.dtype} {tuple(tokens.shape)} on {tokens.device}")
-    return math.prod(lead), logits.shape[-1], 1 if tokens.shape == lead else tokens.shape[-1]
+    return math.prod(lead), size[-1], 1 if shape == lead else shape[-1]
 
 
 def _rows_of(logits: torch.Tensor):
@@ -1021,8 +1030,8 @@ class _TokenLogprobs(torch.autograd.Function):
         return lp, ent, top_lp, top_tok
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
     def backward(ctx, dlogprob, dentropy, *_):
+        _refuse_second("token_logprobs")
         logits, tokens, norm, ent = ctx.saved_tensors
         if dlogprob is None and dentropy is None:
             return None, None, None
