@@ -360,8 +360,11 @@ __device__ __forceinline__ void keys_role(const AttnArgs& a, int tile, int kh, c
   }
 }
 
-// Workgroups: the tiles of keys for dk, of rows for dq, of keys for dv; a key head's tiles in
-// descending order of work.
+// Workgroups: the tiles of keys, 8 for dk and the same 8 for dv in turn, which then read the same
+// rows at the same time, and the tiles of rows for dq; a sequence's tiles in descending order of work.
+// (All of dk, then dq, then all of dv: 2380 us instead of 1981 for 8192 tokens of 8 key heads and 32
+// query heads of 128, 453 instead of 390 for 5 sequences of 183 to 3544 tokens, 16 query heads.)
+constexpr int kTurn = 8;
 template <int IN, int DP>
 __global__ __launch_bounds__(kThreads, 2) void attention_backward_kernel(AttnArgs a) {
   constexpr int BYTES = kTile * TileOf<DP>::PITCH;
@@ -370,10 +373,13 @@ __global__ __launch_bounds__(kThreads, 2) void attention_backward_kernel(AttnArg
   const Stages<DP> st{x0, y0, x1, y1, n0, d0, n1, d1};
   const int kh = blockIdx.x % (unsigned)a.k_heads;
   int tile = blockIdx.x / (unsigned)a.k_heads;
-  if (tile < a.k_tiles) return keys_role<IN, DP, true>(a, tile, kh, st);
-  tile -= a.k_tiles;
-  if (tile < a.q_tiles) return rows_role<IN, DP>(a, (int)a.q_tiles - 1 - tile, kh, st);
-  return keys_role<IN, DP, false>(a, tile - (int)a.q_tiles, kh, st);
+  const int turns = a.k_turns * 2 * kTurn;
+  if (tile >= turns) return rows_role<IN, DP>(a, (int)a.q_tiles - 1 - (tile - turns), kh, st);
+  const bool dk = tile / kTurn % 2 == 0;
+  tile = tile / (2 * kTurn) * kTurn + tile % kTurn;
+  if (tile >= a.k_tiles) return;
+  if (dk) keys_role<IN, DP, true>(a, tile, kh, st);
+  else keys_role<IN, DP, false>(a, tile, kh, st);
 }
 
 template <int IN, int DP>
@@ -386,7 +392,8 @@ hipError_t launch_in(AttnArgs a, hipStream_t s) {
   }
   a.q_tiles = a.q_rows > 0 ? a.q_rows * a.group / kBlock + a.batch + 2 : 0;
   a.k_tiles = a.k_rows > 0 ? a.k_rows / kBlock + a.batch + 2 : 0;
-  hipLaunchKernelGGL((attention_backward_kernel<IN, DP>), dim3((unsigned)((a.q_tiles + 2 * a.k_tiles) * a.k_heads)),
+  a.k_turns = (int)((a.k_tiles + kTurn - 1) / kTurn);
+  hipLaunchKernelGGL((attention_backward_kernel<IN, DP>), dim3((unsigned)((a.q_tiles + 2 * kTurn * a.k_turns) * a.k_heads)),
                      dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }

@@ -63,6 +63,7 @@ struct AttnArgs {
   const void* d_o;         // [q_rows, q_heads, dim]
   float* stats;            // -lse log2(e) and delta, [2, k_heads, q_rows, group]
   int64_t q_tiles, k_tiles;
+  int k_turns;
   void *dq, *dk, *dv;      // contiguous
 };
 bool attention_few_rows(const AttnArgs& a);  // by its sizes
