@@ -489,7 +489,7 @@ template <int IN>
 __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
   constexpr int U = 8;
   const int lane = threadIdx.x & 63;
-  const unsigned at = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const unsigned at = (blockIdx.y * gridDim.x + blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   if (at >= (unsigned)a.q_rows * a.q_heads) return;
   const int q = at / (unsigned)a.q_heads, head = at - q * a.q_heads;
   const int kh = head / (unsigned)a.group;
@@ -605,8 +605,7 @@ hipError_t launch_in(const AttnArgs& a, hipStream_t s) {
                          dim3(kFewThreads), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(attention_join_kernel<IN>, dim3((unsigned)((a.q_rows * a.q_heads + 3) / 4)),
-                       dim3(256), 0, s, a);
+    hipLaunchKernelGGL(attention_join_kernel<IN>, grid_of((a.q_rows * a.q_heads + 3) / 4), dim3(256), 0, s, a);
     return hipGetLastError();
   }
   if (groups_of(a) <= kSmallGroups) launch_rows<IN, DP, 1>(a, s);

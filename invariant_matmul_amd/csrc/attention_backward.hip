@@ -30,7 +30,7 @@ constexpr float kLog2e = 1.44269504088896340736f;
 // rounding makes 0.00166).
 template <int IN>
 __global__ __launch_bounds__(256) void attention_delta_kernel(AttnArgs a) {
-  const int64_t at = (int64_t)blockIdx.x * 16 + threadIdx.x / 16;
+  const int64_t at = (int64_t)(blockIdx.y * gridDim.x + blockIdx.x) * 16 + threadIdx.x / 16;
   const int c = threadIdx.x % 16 * 8;
   const bool in = at < a.q_rows * a.q_heads && c < a.dim;
   float sum = 0.0f;
@@ -385,8 +385,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_backward_kernel(AttnArg
 template <int IN, int DP>
 hipError_t launch_in(AttnArgs a, hipStream_t s) {
   if (a.q_rows > 0) {
-    hipLaunchKernelGGL(attention_delta_kernel<IN>, dim3((unsigned)((a.q_rows * a.q_heads + 15) / 16)),
-                       dim3(256), 0, s, a);
+    hipLaunchKernelGGL(attention_delta_kernel<IN>, grid_of((a.q_rows * a.q_heads + 15) / 16), dim3(256), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }

@@ -52,6 +52,12 @@ __device__ __forceinline__ int key_start(const AttnArgs& a, int i) {
   return clamped(a.cu_k[i - 1], 0, rows);
 }
 
+// Workgroups in two axes: a launch holds fewer than 2^32 threads along one.  (Those past the last do nothing.)
+inline dim3 grid_of(int64_t groups) {
+  const int64_t x = groups < 1 << 20 ? groups : 1 << 20;
+  return dim3((unsigned)x, (unsigned)((groups + x - 1) / x));
+}
+
 // The last segment for which begins(i, its first query, its first key) holds, and
 // what it is.  A lane looks at a segment: a call waits for memory once (and once more for each
 // factor of 64 in the number of sequences), where a binary search waits at every step.

@@ -203,7 +203,7 @@ gemm_status attention_plan(int64_t q_rows, int64_t k_rows, int64_t batch, int q_
   // fewer than 2^32 threads
   if (q_rows > INT_MAX / q_heads || k_rows > (int64_t)1 << 30 || batch > 1 << 20 ||
       (q_rows * group / 128 + batch + 2) * k_heads >= (int64_t)1 << 23 ||
-      (k_rows / 128 + batch + 2) * k_heads >= (int64_t)1 << 22)
+      (k_rows / 128 + batch + 10) * k_heads >= (int64_t)1 << 22)
     return GEMM_ERR_UNSUPPORTED;
   attention_plan_s p{q_rows, k_rows, max_q, (int)batch, q_heads, k_heads, dim, dtype, causal != 0, false, scale};
   if (p.max_q == 0 || p.max_q > q_rows) p.max_q = q_rows;

@@ -192,3 +192,22 @@ def test_heads_4_gb_apart():
     got = torch_ops.attention_backward(do[:, ::2].contiguous(), view, k, v, o, saved)
     same = torch_ops.attention_backward(do[:, ::2].contiguous(), q[:, ::2].contiguous(), k, v, o, saved)
     assert all(torch.equal(a, b) for a, b in zip(got, same))
+
+
+def test_more_rows_than_a_launch_has_threads():
+    # 2^28 rows and heads: 16 lanes each for delta, and a wave each where results are joined
+    T, hq, D = (1 << 24) + 5, 16, 8
+    g = torch.Generator(device=dev()).manual_seed(36)
+    q, do = (torch.empty(T, hq, D, dtype=torch.bfloat16, device=dev()).normal_(generator=g) for _ in range(2))
+    k, v = (torch.empty(9, 1, D, dtype=torch.bfloat16, device=dev()).normal_(generator=g) for _ in range(2))
+    o, saved = torch_ops.attention_forward(q, k, v, causal=False)
+    dq, _, _ = torch_ops.attention_backward(do, q, k, v, o, saved, causal=False)
+    for lo in (0, T // 2, T - 50):
+        part = slice(lo, lo + 50)
+        o1, s1 = torch_ops.attention_forward(q[part], k, v, causal=False)
+        assert torch.equal(o[part], o1) and torch.equal(saved.lse[part], s1.lse)
+        assert torch.equal(dq[part], torch_ops.attention_backward(do[part], q[part], k, v, o1, s1, causal=False)[0])
+    assert takes_few(q, k, 2, 1)
+    few = torch_ops.attention(q, k, v, ints([T - 3, T - 2, T - 1]), ints([0, 4, 9]), max_q=1)
+    assert (few[:T - 3] == 0).all() and (few[T - 1] == 0).all()
+    assert torch.equal(few[T - 2], torch_ops.attention(q[T - 2:T - 1], k[4:], v[4:])[0])
