@@ -621,9 +621,9 @@ void head_rope_plan_destroy(head_rope_plan_t plan);
  *
  * q [q_rows, q_heads, dim], k and v [k_rows, k_heads, dim] are fp16 or bf16 with
  * strides as above; dim a multiple of 8 up to 128.  o is contiguous, lse fp32
- * [q_rows, q_heads].  Logits, statistics and sums are fp32; probabilities (about
- * the running maximum, so at most 1) are rounded to the input's type for their product
- * with v.
+ * [q_rows, q_heads].  Logits, statistics and sums are fp32; probabilities (about a
+ * reference of the row's own logits, at most 2^8) are rounded to the input's type for
+ * their product with v and for the sum that o is divided by, not for lse.
  *
  * A row of o is a bitwise function of its query and of the keys and values it sees,
  * in their order (and of dim and scale): not of the number of queries of the call or
@@ -641,8 +641,9 @@ typedef struct attention_plan_s* attention_plan_t;
 /* Plan the call.  max_q: no sequence has more queries (0: q_rows).  Where it is small and caches are
  * long, a kernel of few rows takes the call (the bits are the same); a sequence with more
  * queries than max_q says has NaN in the rows past it.  scale > 0.  GEMM_ERR_INVALID_VALUE for a
- * negative size, batch < 1 or a NULL handle, GEMM_ERR_UNSUPPORTED for other types, sizes
- * (k_rows up to 2^30, q_rows q_heads below 2^31) or scales. */
+ * negative size, batch < 1 or a NULL handle, GEMM_ERR_UNSUPPORTED for other types, scales or sizes
+ * (batch up to 2^20, k_rows up to 2^30, fewer than 2^23 tiles of 128 rows of the key
+ * heads and 2^22 of 128 keys). */
 gemm_status attention_plan(int64_t q_rows, int64_t k_rows, int64_t batch, int q_heads, int k_heads,
                            int dim, gemm_dtype dtype, int causal, float scale, int64_t max_q,
                            attention_plan_t* plan);
@@ -651,8 +652,9 @@ gemm_status attention_plan(int64_t q_rows, int64_t k_rows, int64_t batch, int q_
 size_t attention_workspace_size(attention_plan_t plan);
 
 /* o, and for the backward pass lse and o_low, on `stream`.  o_low has the form of o and
- * receives what the rounding of o left, rounded to the type; each may be NULL.  cu_q and cu_k may both be NULL for one sequence of all
- * rows.  q, k, v and o are 16-byte aligned, strides multiples of 8 elements. */
+ * receives what the rounding of o left, rounded to the type; each may be NULL.  cu_q and cu_k
+ * may both be NULL for one sequence of all rows.  q, k, v and o are 16-byte aligned,
+ * strides multiples of 8 elements. */
 gemm_status attention_run(attention_plan_t plan, const void* q, int64_t q_token_stride,
                           int64_t q_head_stride, const void* k, int64_t k_token_stride,
                           int64_t k_head_stride, const void* v, int64_t v_token_stride,
@@ -670,7 +672,9 @@ size_t attention_backward_workspace_size(attention_plan_t plan);
  * p and ds rounded to the input's type for their products (fp16: a ds below 2^-25 is
  * lost, so gradients need the scaling of the loss that fp16 training has).  Rows in no
  * sequence and keys past k_lens have zero gradients.  Sums in a fixed order, without
- * atomics: the gradients of a sequence are a bitwise function of it alone. */
+ * atomics: the gradients of a sequence are a bitwise function of it alone.  A NaN or infinity
+ * in q, k, v or d_o stays in its sequence; there it may reach, beyond the formula's
+ * gradients, those of queries and keys up to 64 places away that do not see each other. */
 gemm_status attention_backward(attention_plan_t plan, const void* d_o, const void* q,
                                int64_t q_token_stride, int64_t q_head_stride, const void* k,
                                int64_t k_token_stride, int64_t k_head_stride, const void* v,

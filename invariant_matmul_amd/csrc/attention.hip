@@ -6,20 +6,19 @@
 // their order, alone: they do not depend on how many queries the call holds, on the other
 // sequences, on the room behind a cache or on which kernel runs.  A prompt
 // taken at once, in pieces or token by token gives the same bits.  For that, every
-// kernel sums in one order.  Keys are cut from the sequence's first one on into
-// chunks of 256 and steps of 64.  Within a chunk a reference of the logits, the sums and the
-// output go from step to step (each step: S on the matrix cores, p about the
-// reference, p rounded to the input's type, two steps of 32 keys
-// into the output's chain); a chunk's results start anew, and chunks are joined
-// in ascending order by fp32 products and one fma.  So chunks
-// can be worked on by workgroups of their own (few rows) or one after the other
-// (many rows).
+// kernel sums in one order.  Keys are cut from the sequence's first one on into chunks of 256
+// and steps of 64.  Within a chunk a reference of the logits, the sums and the output go from
+// step to step (each step: S on the matrix cores, p about the reference, p rounded to the
+// input's type, two steps of 32 keys into the output's chain); a chunk's results start anew,
+// and chunks are joined in ascending order by fp32 products and one fma.  So chunks can be
+// worked on by workgroups of their own (few rows) or one after the other (many rows).
 //
 // Rounding.  p is rounded to 16 bits for the product with v, and o is divided by the sum of
 // the rounded p, in fp32: the weights then add up to 1, and where one key has most of the weight
-// its rounding drops out of o (8195 packed bf16 tokens: o and its gradients off by 0.0019 and
-// 0.0025 of themselves, with the sum of the unrounded p by 0.0020 and 0.0026, at the same time;
-// about the exact maximum by 0.0017 and 0.0024, but 16384 tokens take 2240 us instead of 2108).
+// its rounding drops out of o (packed bf16 tokens: o and its gradients off by 0.0019 and 0.0025
+// of themselves, with the sum of the unrounded p by 0.0020 and 0.0026, in the same time; about
+// the exact maximum by 0.0017 and 0.0024, but 6 % slower.  The outputs' own rounding makes
+// 0.0017, and that of ds, which has no way around it, as much again of the gradients).
 // lse is of the unrounded sum, in fp32 too.
 #include "attention_common.h"
 
@@ -29,8 +28,13 @@ using namespace dev;
 
 // ---- Many rows -----------------------------------------------------------------
 // A workgroup takes 128 rows of a key head, 32 a wave (or 64, 16 a wave: SETS sets of 16), and
-// walks through their keys 64 at a time: the next step's keys and values go by DMA into the other half of a
-// two-stage LDS buffer while this one's are used.
+// walks through their keys 64 at a time: the next step's keys and values go by DMA into the
+// other half of a two-stage LDS buffer while this one's are used.  Two workgroups share a compute
+// unit, so that one's exponentials run beside the other's products: 16384 causal tokens, 32
+// query and 8 key heads of 128 in bf16, take 2080 us (1057 TFLOP/s; matrix units busy 42 %,
+// then exponentials and packing, waits 30 %).  With one workgroup of 8 waves a unit that took
+// 2407, with every new maximum as the reference 2240, with a step's first values read
+// after the softmax 2156.
 
 template <int IN>
 __device__ __forceinline__ bool not_finite(unsigned two) {
@@ -325,9 +329,12 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttnArgs a) {
 // at once: the keys as fragments in registers (each of the four waves its step of 64), the
 // values through registers to LDS.  Each wave makes its step's logits and their
 // maximum; with the maxima of the steps before, which LDS holds, every wave has the
-// running maximum that one wave alone would have had, so the probabilities are
+// reference that one wave alone would have had, so the probabilities are
 // those of the chain; then each wave takes a quarter of the output's dimensions through
 // all four steps.
+// Memory bounds it where there are many chunks (61 caches of up to 8192 keys, 32 query and 4
+// key heads of 128: 126 us, 4.4 TB/s, and the join 8), latency where there are few (8192 keys
+// of 8 heads: 11 us and the join 6, most of them launches and trips to memory).
 constexpr int kFewWaves = 4, kFewThreads = 64 * kFewWaves;
 
 // The first chunk slot of a sequence: every sequence has the slots that it needs.
