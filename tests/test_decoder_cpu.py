@@ -172,7 +172,7 @@ def test_host_pointers_are_refused():
     buf = ctypes.create_string_buffer(1 << 16)
     at = (ctypes.addressof(buf) + 63) & ~63
     plan = imm.logprobs_plan(2, 16, "f32", 1, 0)
-    assert imm.lib().logprobs_run(plan.handle, at, 16, at + 1024, at + 2048, at + 3072, 0, 0, 0, 0, 0, None) in (INVALID, 4)
+    assert imm.lib().logprobs_run(plan.handle, at, 16, at + 1024, at + 2048, at + 4096, 0, 0, 0, 0, 0, None) in (INVALID, 4)
     rope = imm.head_rope_plan(1, 1, 1, 16, 16, "bf16")
     assert imm.lib().head_rope_run(rope.handle, at, 16, 16, at, 16, 16, at, at, 0, 0, at, at, None) in (INVALID, 4)
     att = imm.attention_plan(100, 2, 1, 1, 1, 16, "bf16")
