@@ -193,6 +193,41 @@ def test_captured_and_replayed():
         assert all(same(out, want) for _, out in graphs), i
 
 
+def test_a_captured_backward_pass():
+    # forward and backward by autograd in one graph, of leaves that no graph made outside holds
+    g = torch.Generator().manual_seed(8)
+    q, k, v, wq = (torch.randn(*n, generator=g).bfloat16().to(dev()) for n in ((70, HQ, D), (70, HK, D), (70, HK, D), (D,)))
+    at, tok, cu, freq = torch.arange(70, device=dev()), torch.arange(70, device=dev()), ints([0, 30, 70]), FREQ.to(dev())
+
+    def step(leaves):
+        q, k, v, wq = leaves
+        a, b = torch_ops.qk_norm_rope(q, k, at, freq, wq, wq)
+        lp, ent = torch_ops.token_logprobs(torch_ops.attention(a, b, v, cu).flatten(1), tok)
+        return torch.autograd.grad(-lp.sum() - 0.1 * ent.sum(), leaves)
+
+    def eager():
+        return step([t.clone().requires_grad_() for t in (q, k, v, wq)])
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        eager()
+    torch.cuda.synchronize()
+    leaves = [t.clone().requires_grad_() for t in (q, k, v, wq)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        grads = step(leaves)
+    for i in range(4):
+        with torch.no_grad():
+            for t, leaf in zip((q, k, v, wq), leaves):
+                t.mul_(-0.75)
+                leaf.copy_(t)
+        graph.replay()
+        torch.ones(3000, device=dev()).sum().item()
+        want = eager()
+        torch.cuda.synchronize()
+        assert same(grads, want), i
+
+
 def test_on_other_streams_at_once():
     runs = [calls(5 + i)[0] for i in range(3)]
     want = [run() for run in runs]
