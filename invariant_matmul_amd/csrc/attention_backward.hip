@@ -6,12 +6,13 @@
 //
 // One kernel makes lse and delta of every row ready, one makes the gradients: its workgroups
 // have a role each, dq of 128 rows, which walk through their keys, and dk or dv of 128
-// keys, which walk through the rows that see them.  p is made by all three and ds by two,
-// so that every sum is one chain in one workgroup: no atomics, and the gradients of a
-// sequence depend on that sequence alone.  dk and dv apart cost one product more (q k twice)
-// than together, but fit a wave into half of a SIMD's registers: with both at once
-// (254 + 256 registers, one wave a SIMD) that kernel took 3180 us for 8192 keys of 8 heads
-// and 32 query heads of 128.
+// keys, which walk through the rows that see them (64 of each in small calls).  p is made by
+// all three and ds by two, so that every sum is one chain in one workgroup: no atomics, and
+// the gradients of a sequence depend on that sequence alone.  dk and dv apart cost one product
+// more (q k twice) than together, but fit a wave into half of a SIMD's registers: with both at
+// once (254 + 256 registers, one wave a SIMD) that kernel took 3180 us for 8192 tokens of 8 key
+// heads and 32 query heads of 128 where now all three take 1900 (matrix units busy 41 %,
+// then exponentials, differences and packing, waits 28 %).
 // p and ds are rounded to the input's type for their products, all else is fp32.
 #include "attention_common.h"
 #include "rows16.h"
@@ -20,7 +21,8 @@ namespace imm {
 namespace {
 using namespace dev;
 
-constexpr int kBlock = 32 * kWaves;  // rows (dq) or keys (dk, dv) of a workgroup
+template <int SETS>
+constexpr int kBlock = 16 * SETS * kWaves;  // rows (dq) or keys (dk, dv) of a workgroup
 constexpr float kLog2e = 1.44269504088896340736f;
 
 // -lse log2(e) and delta of every row in the order of the packed rows, [key head][query][head
@@ -88,24 +90,24 @@ struct Stages {  // (arrays of their own, as in the forward kernel)
 };
 
 // dq of the rows from r0 on.
-template <int IN, int DP>
+template <int IN, int DP, int SETS>
 __device__ __forceinline__ void rows_role(const AttnArgs& a, int tile, int kh, const Stages<DP>& st) {
   using T = TileOf<DP>;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int quad = lane / 16, col = lane % 16;
-  const Found found = segment_of_tile<kBlock>(a, tile);
+  const Found found = segment_of_tile<kBlock<SETS>>(a, tile);
   const Sequence s = found.s;
-  const int r0 = (tile - (s.q0 * a.group / kBlock + found.segment)) * kBlock;
+  const int r0 = (tile - (s.q0 * a.group / kBlock<SETS> + found.segment)) * kBlock<SETS>;
   const int rows = s.n * a.group;
   if (r0 >= rows) return;
 
-  int seen[2];
-  float nl[2], delta[2];
-  i32x4 qf[2][T::KS], gf[2][T::KS];
-  f32x4 dq[2][T::DB];
-  const int w0 = r0 + 32 * wave;
+  int seen[SETS];
+  float nl[SETS], delta[SETS];
+  i32x4 qf[SETS][T::KS], gf[SETS][T::KS];
+  f32x4 dq[SETS][T::DB];
+  const int w0 = r0 + 16 * SETS * wave;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < SETS; ++i) {
     const int row = w0 + 16 * i + col, t = row / a.group;
     const int h = kh * a.group + (row - t * a.group);
     const bool live = row < rows;
@@ -119,8 +121,8 @@ __device__ __forceinline__ void rows_role(const AttnArgs& a, int tile, int kh, c
     for (int d = 0; d < T::DB; ++d) dq[i][d] = f32x4{};
   }
   auto seen_of = [&](int r) { return keys_seen(a, s, (r < rows ? r : rows - 1) / a.group); };
-  const int need = __builtin_amdgcn_readfirstlane(seen_of(r0 + kBlock - 1));
-  const int wave_need = __builtin_amdgcn_readfirstlane(w0 < rows ? seen_of(w0 + 31) : 0);
+  const int need = __builtin_amdgcn_readfirstlane(seen_of(r0 + kBlock<SETS> - 1));
+  const int wave_need = __builtin_amdgcn_readfirstlane(w0 < rows ? seen_of(w0 + 16 * SETS - 1) : 0);
   const int wave_all = __builtin_amdgcn_readfirstlane(w0 < rows ? seen_of(w0) : 0);
 
   const int64_t k_bytes = 2 * a.k_token, v_bytes = 2 * a.v_token;
@@ -140,24 +142,25 @@ __device__ __forceinline__ void rows_role(const AttnArgs& a, int tile, int kh, c
     lanes.again();
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      f32x4 sc[2][2], dp[2][2];  // [row set][block of keys]
+      f32x4 sc[SETS][2], dp[SETS][2];  // [row set][block of keys]
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
-        sc[0][b] = sc[1][b] = dp[0][b] = dp[1][b] = f32x4{};
+#pragma unroll
+        for (int i = 0; i < SETS; ++i) sc[i][b] = dp[i][b] = f32x4{};
 #pragma unroll
         for (int ks = 0; ks < T::KS; ++ks) {
           const i32x4 kf = row_fragment<DP>(kt, lanes, 2 * half + b, ks);
           const i32x4 vf = row_fragment<DP>(vt, lanes, 2 * half + b, ks);
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
+          for (int i = 0; i < SETS; ++i) {
             sc[i][b] = mfma16_v<IN>(kf, qf[i][ks], sc[i][b]);
             dp[i][b] = mfma16_v<IN>(vf, gf[i][ks], dp[i][b]);
           }
         }
       }
-      i32x4 sf[2];
+      i32x4 sf[SETS];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < SETS; ++i) {
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -177,8 +180,8 @@ __device__ __forceinline__ void rows_role(const AttnArgs& a, int tile, int kh, c
 #pragma unroll
       for (int d = 0; d < T::DB; ++d) {
         const i32x4 kf = column_fragment<DP>(kt, lanes, half, d);
-        dq[0][d] = mfma16_v<IN>(kf, sf[0], dq[0][d]);
-        dq[1][d] = mfma16_v<IN>(kf, sf[1], dq[1][d]);
+#pragma unroll
+        for (int i = 0; i < SETS; ++i) dq[i][d] = mfma16_v<IN>(kf, sf[i], dq[i][d]);
       }
     }
   };
@@ -188,7 +191,7 @@ __device__ __forceinline__ void rows_role(const AttnArgs& a, int tile, int kh, c
     if (k0 + kTile < need) one(k0 + kTile, st.x1, st.y1, st.x0, st.y0);
   }
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < SETS; ++i) {
     const int row = w0 + 16 * i + col, t = row / a.group;
     const int64_t h = kh * a.group + (row - t * a.group);
     if (row < rows) store_rows<IN, DP>(dq[i], a.scale, a.dq, ((int64_t)(s.q0 + t) * a.q_heads + h) * a.dim, a.dim);
@@ -244,28 +247,28 @@ struct RowMover {
 };
 
 // dk (DK) or dv of the keys of a tile.
-template <int IN, int DP, bool DK>
+template <int IN, int DP, bool DK, int SETS>
 __device__ __forceinline__ void keys_role(const AttnArgs& a, int tile, int kh, const Stages<DP>& st) {
   using T = TileOf<DP>;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int quad = lane / 16, col = lane % 16;
-  const Found found = find_segment(a, [&](int i, int, int k) { return k / kBlock + i <= tile; });
+  const Found found = find_segment(a, [&](int i, int, int k) { return k / kBlock<SETS> + i <= tile; });
   const Sequence s = found.s;
   const int k_first = s.k0, k_end = found.k_end;
-  const int c0 = (tile - (k_first / kBlock + found.segment)) * kBlock;  // of the segment
+  const int c0 = (tile - (k_first / kBlock<SETS> + found.segment)) * kBlock<SETS>;  // of the segment
   if (c0 >= k_end - k_first) return;
   const int rows = s.n * a.group;
-  const int w0 = c0 + 32 * wave;
+  const int w0 = c0 + 16 * SETS * wave;
   // the first row that sees a key
   auto first_row = [&](int key) {
     if (key >= s.m) return rows;
     return a.causal ? clamped(key - (s.m - s.n), 0, s.n) * a.group : 0;
   };
-  i32x4 kf[2][T::KS], vf[DK ? 2 : 1][T::KS];
-  f32x4 sum[2][T::DB];
-  int from_row[2];
+  i32x4 kf[SETS][T::KS], vf[DK ? SETS : 1][T::KS];
+  f32x4 sum[SETS][T::DB];
+  int from_row[SETS];
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
+  for (int j = 0; j < SETS; ++j) {
     const int key = w0 + 16 * j + col;
     row_operand<DP>(kf[j], static_cast<const char*>(a.k) + 2 * ((k_first + key) * a.k_token + kh * a.k_head), key < s.m, a.dim);
     if constexpr (DK)
@@ -275,7 +278,7 @@ __device__ __forceinline__ void keys_role(const AttnArgs& a, int tile, int kh, c
     for (int d = 0; d < T::DB; ++d) sum[j][d] = f32x4{};
   }
   const int from = first_row(c0) / kTile * kTile;
-  const int wave_from = first_row(w0), wave_all = first_row(w0 + 31);
+  const int wave_from = first_row(w0), wave_all = first_row(w0 + 16 * SETS - 1);
 
   const char* const qp = static_cast<const char*>(a.q) + 2 * (s.q0 * a.q_token + (int64_t)kh * a.group * a.q_head);
   const char* const gp = static_cast<const char*>(a.d_o) + 2 * ((int64_t)s.q0 * a.q_heads + kh * a.group) * a.dim;
@@ -302,19 +305,20 @@ __device__ __forceinline__ void keys_role(const AttnArgs& a, int tile, int kh, c
     lanes.again();
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      f32x4 sc[2][2], dp[2][2];  // [block of rows][block of keys]
+      f32x4 sc[2][SETS], dp[2][SETS];  // [block of rows][block of keys]
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
-        sc[b][0] = sc[b][1] = dp[b][0] = dp[b][1] = f32x4{};
+#pragma unroll
+        for (int j = 0; j < SETS; ++j) sc[b][j] = dp[b][j] = f32x4{};
 #pragma unroll
         for (int ks = 0; ks < T::KS; ++ks) {
           const i32x4 qf = row_fragment<DP>(qt, lanes, 2 * half + b, ks);
 #pragma unroll
-          for (int j = 0; j < 2; ++j) sc[b][j] = mfma16_v<IN>(qf, kf[j][ks], sc[b][j]);
+          for (int j = 0; j < SETS; ++j) sc[b][j] = mfma16_v<IN>(qf, kf[j][ks], sc[b][j]);
           if constexpr (DK) {
             const i32x4 gf = row_fragment<DP>(gt, lanes, 2 * half + b, ks);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) dp[b][j] = mfma16_v<IN>(gf, vf[j][ks], dp[b][j]);
+            for (int j = 0; j < SETS; ++j) dp[b][j] = mfma16_v<IN>(gf, vf[j][ks], dp[b][j]);
           }
         }
       }
@@ -325,7 +329,7 @@ __device__ __forceinline__ void keys_role(const AttnArgs& a, int tile, int kh, c
         f32x4 delta{};
         if constexpr (DK) delta = *reinterpret_cast<const f32x4*>(deltas + at);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < SETS; ++j) {
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const float p = __builtin_amdgcn_exp2f(fmaf(sc[b][j][r], a.scale_log2, nl[r]));
@@ -338,12 +342,14 @@ __device__ __forceinline__ void keys_role(const AttnArgs& a, int tile, int kh, c
           }
         }
       }
-      const i32x4 f0 = pack_blocks<IN>(sc[0][0], sc[1][0]), f1 = pack_blocks<IN>(sc[0][1], sc[1][1]);
+      i32x4 f[SETS];
+#pragma unroll
+      for (int j = 0; j < SETS; ++j) f[j] = pack_blocks<IN>(sc[0][j], sc[1][j]);
 #pragma unroll
       for (int d = 0; d < T::DB; ++d) {
         const i32x4 x = column_fragment<DP>(DK ? qt : gt, lanes, half, d);
-        sum[0][d] = mfma16_v<IN>(x, f0, sum[0][d]);
-        sum[1][d] = mfma16_v<IN>(x, f1, sum[1][d]);
+#pragma unroll
+        for (int j = 0; j < SETS; ++j) sum[j][d] = mfma16_v<IN>(x, f[j], sum[j][d]);
       }
     }
   };
@@ -353,7 +359,7 @@ __device__ __forceinline__ void keys_role(const AttnArgs& a, int tile, int kh, c
     if (r0 + kTile < rows) one(r0 + kTile, st.x1, st.y1, st.n1, st.d1, st.x0, st.y0, st.n0, st.d0);
   }
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
+  for (int j = 0; j < SETS; ++j) {
     const int key = w0 + 16 * j + col;
     if (key < k_end - k_first)
       store_rows<IN, DP>(sum[j], DK ? a.scale : 1.0f, DK ? a.dk : a.dv, ((int64_t)(k_first + key) * a.k_heads + kh) * a.dim, a.dim);
@@ -365,7 +371,7 @@ __device__ __forceinline__ void keys_role(const AttnArgs& a, int tile, int kh, c
 // (All of dk, then dq, then all of dv: 2380 us instead of 1981 for 8192 tokens of 8 key heads and 32
 // query heads of 128, 453 instead of 390 for 5 sequences of 183 to 3544 tokens, 16 query heads.)
 constexpr int kTurn = 8;
-template <int IN, int DP>
+template <int IN, int DP, int SETS>
 __global__ __launch_bounds__(kThreads, 2) void attention_backward_kernel(AttnArgs a) {
   constexpr int BYTES = kTile * TileOf<DP>::PITCH;
   __shared__ __attribute__((aligned(1024))) char x0[BYTES], y0[BYTES], x1[BYTES], y1[BYTES];
@@ -374,12 +380,27 @@ __global__ __launch_bounds__(kThreads, 2) void attention_backward_kernel(AttnArg
   const int kh = blockIdx.x % (unsigned)a.k_heads;
   int tile = blockIdx.x / (unsigned)a.k_heads;
   const int turns = a.k_turns * 2 * kTurn;
-  if (tile >= turns) return rows_role<IN, DP>(a, (int)a.q_tiles - 1 - (tile - turns), kh, st);
+  if (tile >= turns) return rows_role<IN, DP, SETS>(a, (int)a.q_tiles - 1 - (tile - turns), kh, st);
   const bool dk = tile / kTurn % 2 == 0;
   tile = tile / (2 * kTurn) * kTurn + tile % kTurn;
   if (tile >= a.k_tiles) return;
-  if (dk) keys_role<IN, DP, true>(a, tile, kh, st);
-  else keys_role<IN, DP, false>(a, tile, kh, st);
+  if (dk) keys_role<IN, DP, true, SETS>(a, tile, kh, st);
+  else keys_role<IN, DP, false, SETS>(a, tile, kh, st);
+}
+
+// Up to three workgroups of 128 rows or keys a compute unit, the longest chain of steps is what
+// the call takes: waves then take 16 rows or keys instead of 32 (8 key heads of 128: 2000 tokens
+// with 4 query heads each, 770 workgroups, 266 -> 205 us; 900 with 2 each, 250 workgroups, 67 ->
+// 51; 3544 with 2 each, 900 workgroups, 252 -> 259).  The bits are the same.
+constexpr int64_t kSmallGroups = 800;
+
+template <int IN, int DP, int SETS>
+void launch_roles(AttnArgs a, hipStream_t s) {
+  a.q_tiles = a.q_rows > 0 ? a.q_rows * a.group / kBlock<SETS> + a.batch + 2 : 0;
+  a.k_tiles = a.k_rows > 0 ? a.k_rows / kBlock<SETS> + a.batch + 2 : 0;
+  a.k_turns = (int)((a.k_tiles + kTurn - 1) / kTurn);
+  const int64_t grid = (a.q_tiles + 2 * kTurn * a.k_turns) * a.k_heads;
+  hipLaunchKernelGGL((attention_backward_kernel<IN, DP, SETS>), dim3((unsigned)grid), dim3(kThreads), 0, s, a);
 }
 
 template <int IN, int DP>
@@ -389,11 +410,9 @@ hipError_t launch_in(AttnArgs a, hipStream_t s) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  a.q_tiles = a.q_rows > 0 ? a.q_rows * a.group / kBlock + a.batch + 2 : 0;
-  a.k_tiles = a.k_rows > 0 ? a.k_rows / kBlock + a.batch + 2 : 0;
-  a.k_turns = (int)((a.k_tiles + kTurn - 1) / kTurn);
-  hipLaunchKernelGGL((attention_backward_kernel<IN, DP>), dim3((unsigned)((a.q_tiles + 2 * kTurn * a.k_turns) * a.k_heads)),
-                     dim3(kThreads), 0, s, a);
+  const int64_t groups = (a.q_rows * a.group / kBlock<2> + 2 * (a.k_rows / kBlock<2>) + 3 * a.batch) * a.k_heads;
+  if (groups <= kSmallGroups) launch_roles<IN, DP, 1>(a, s);
+  else launch_roles<IN, DP, 2>(a, s);
   return hipGetLastError();
 }
 

@@ -35,7 +35,8 @@ def test_32_rows_a_wave(lengths, heads, causal, dt):
     q, k, v, do = make(sum(nq), sum(nk), hq, hk, D, dt, sum(nq) + hq)
     assert groups(q, k, len(nq)) > 512 and not takes_few(q, k, len(nq), None)
     o, saved = check(q, k, v, do, nq, nk, causal)
-    # without what the backward pass takes, and a few key heads alone (16 rows a wave)
+    grads = torch_ops.attention_backward(do, q, k, v, o, saved, starts(nq), starts(nk), causal=causal)
+    # without what the backward pass takes, and a few key heads alone (16 rows or keys a wave)
     assert torch.equal(torch_ops.attention(q, k, v, starts(nq), starts(nk), causal=causal), o)
     g = hq // hk
     for lo in (0, hk - 3):
@@ -44,6 +45,9 @@ def test_32_rows_a_wave(lengths, heads, causal, dt):
         o1, s1 = torch_ops.attention_forward(*part, starts(nq), starts(nk), causal=causal)
         assert torch.equal(o1, o[:, lo * g:(lo + 3) * g]) and torch.equal(s1.lse, saved.lse[:, lo * g:(lo + 3) * g])
         assert torch.equal(s1.o_low, saved.o_low[:, lo * g:(lo + 3) * g])
+        alone = torch_ops.attention_backward(do[:, lo * g:(lo + 3) * g], *part, o1, s1, starts(nq), starts(nk), causal=causal)
+        for one, all_, h in zip(alone, grads, (g, 1, 1)):
+            assert torch.equal(one, all_[:, lo * h:(lo + 3) * h])
 
 
 def test_32_rows_a_wave_and_bad_values():
