@@ -11,9 +11,10 @@
 // the gradients of a sequence depend on that sequence alone.  dk and dv apart cost one product
 // more (q k twice) than together, but fit a wave into half of a SIMD's registers: with both at
 // once (254 + 256 registers, one wave a SIMD) that kernel took 3180 us for 8192 tokens of 8 key
-// heads and 32 query heads of 128 where now all three take 1900 (matrix units busy 41 %,
+// heads and 32 query heads of 128 where now all three take 2000 (matrix units busy 41 %,
 // then exponentials, differences and packing, waits 28 %).
-// p and ds are rounded to the input's type for their products, all else is fp32.
+// p and ds are rounded to the input's type for their products (the rest of large ds follows),
+// all else is fp32.
 #include "attention_common.h"
 #include "rows16.h"
 
@@ -81,6 +82,27 @@ __device__ __forceinline__ void store_rows(const f32x4 (&x)[TileOf<DP>::DB], flo
     if (c < dim)
       *reinterpret_cast<i32x2*>(static_cast<char*>(to) + 2 * (at + c)) = i32x2{pack2<IN>(y[0], y[1]), pack2<IN>(y[2], y[3])};
   }
+}
+
+// What the rounding of two blocks of ds left, where p is large.  The rounding of ds is the
+// largest error of dq and dk, and the few large p of a row make much of it: their rest goes
+// through the product too, in the steps that have one.  (Packed bf16 documents of 200 to 3500
+// tokens: dq is off by 0.0023 of itself instead of 0.0025, with the rests of all p by 0.0018,
+// and its own rounding makes 0.0017.  It costs 5 to 8 % of the kernel's time, as much by the
+// branch as by the products.)  A rule of the element alone: zeros add nothing.
+constexpr float kLarge = 0.25f;
+template <int IN>
+__device__ __forceinline__ i32x4 rest_of(const f32x4& a, const f32x4& b, const f32x4& pa, const f32x4& pb,
+                                         const i32x4& rounded) {
+  i32x4 rest;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const f32x4 &x = e < 2 ? a : b, &p = e < 2 ? pa : pb;
+    const int i = 2 * (e % 2);
+    const int kept = (p[i] >= kLarge ? 0xffff : 0) | (p[i + 1] >= kLarge ? (int)0xffff0000 : 0);
+    rest[e] = pack2_rest<IN>(x[i], x[i + 1], rounded[e]) & kept;
+  }
+  return rest;
 }
 
 template <int DP>
@@ -159,14 +181,16 @@ __device__ __forceinline__ void rows_role(const AttnArgs& a, int tile, int kh, c
         }
       }
       i32x4 sf[SETS];
+      float largest = 0.0f;
 #pragma unroll
       for (int i = 0; i < SETS; ++i) {
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const float p = __builtin_amdgcn_exp2f(fmaf(sc[i][b][r], a.scale_log2, nl[i]));
-            dp[i][b][r] = p * (dp[i][b][r] - delta[i]);
+            sc[i][b][r] = __builtin_amdgcn_exp2f(fmaf(sc[i][b][r], a.scale_log2, nl[i]));
+            dp[i][b][r] = sc[i][b][r] * (dp[i][b][r] - delta[i]);
+            largest = fmaxf(largest, sc[i][b][r]);
           }
         if (!all) {
 #pragma unroll
@@ -182,6 +206,16 @@ __device__ __forceinline__ void rows_role(const AttnArgs& a, int tile, int kh, c
         const i32x4 kf = column_fragment<DP>(kt, lanes, half, d);
 #pragma unroll
         for (int i = 0; i < SETS; ++i) dq[i][d] = mfma16_v<IN>(kf, sf[i], dq[i][d]);
+      }
+      if (__any(largest >= kLarge)) {
+#pragma unroll
+        for (int i = 0; i < SETS; ++i) sf[i] = rest_of<IN>(dp[i][0], dp[i][1], sc[i][0], sc[i][1], sf[i]);
+#pragma unroll
+        for (int d = 0; d < T::DB; ++d) {
+          const i32x4 kf = column_fragment<DP>(kt, lanes, half, d);
+#pragma unroll
+          for (int i = 0; i < SETS; ++i) dq[i][d] = mfma16_v<IN>(kf, sf[i], dq[i][d]);
+        }
       }
     }
   };
@@ -305,6 +339,7 @@ __device__ __forceinline__ void keys_role(const AttnArgs& a, int tile, int kh, c
     lanes.again();
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
+      float largest = 0.0f;
       f32x4 sc[2][SETS], dp[2][SETS];  // [block of rows][block of keys]
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
@@ -332,24 +367,37 @@ __device__ __forceinline__ void keys_role(const AttnArgs& a, int tile, int kh, c
         for (int j = 0; j < SETS; ++j) {
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const float p = __builtin_amdgcn_exp2f(fmaf(sc[b][j][r], a.scale_log2, nl[r]));
-            sc[b][j][r] = DK ? p * (dp[b][j][r] - delta[r]) : p;
+            sc[b][j][r] = __builtin_amdgcn_exp2f(fmaf(sc[b][j][r], a.scale_log2, nl[r]));
+            if constexpr (DK) {
+              dp[b][j][r] = sc[b][j][r] * (dp[b][j][r] - delta[r]);
+              largest = fmaxf(largest, sc[b][j][r]);
+            }
           }
           if (!all) {
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-              if (r0 + at + r < from_row[j]) sc[b][j][r] = 0.0f;
+              if (r0 + at + r < from_row[j]) (DK ? dp : sc)[b][j][r] = 0.0f;
           }
         }
       }
       i32x4 f[SETS];
 #pragma unroll
-      for (int j = 0; j < SETS; ++j) f[j] = pack_blocks<IN>(sc[0][j], sc[1][j]);
+      for (int j = 0; j < SETS; ++j) f[j] = pack_blocks<IN>((DK ? dp : sc)[0][j], (DK ? dp : sc)[1][j]);
 #pragma unroll
       for (int d = 0; d < T::DB; ++d) {
         const i32x4 x = column_fragment<DP>(DK ? qt : gt, lanes, half, d);
 #pragma unroll
         for (int j = 0; j < SETS; ++j) sum[j][d] = mfma16_v<IN>(x, f[j], sum[j][d]);
+      }
+      if (DK && __any(largest >= kLarge)) {
+#pragma unroll
+        for (int j = 0; j < SETS; ++j) f[j] = rest_of<IN>(dp[0][j], dp[1][j], sc[0][j], sc[1][j], f[j]);
+#pragma unroll
+        for (int d = 0; d < T::DB; ++d) {
+          const i32x4 x = column_fragment<DP>(qt, lanes, half, d);
+#pragma unroll
+          for (int j = 0; j < SETS; ++j) sum[j][d] = mfma16_v<IN>(x, f[j], sum[j][d]);
+        }
       }
     }
   };
