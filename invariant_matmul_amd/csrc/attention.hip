@@ -15,10 +15,9 @@
 //
 // Rounding.  p is rounded to 16 bits for the product with v, and o is divided by the sum of
 // the rounded p, in fp32: the weights then add up to 1, and where one key has most of the weight
-// its rounding drops out of o (packed bf16 tokens: o and its gradients off by 0.0019 and 0.0025
-// of themselves, with the sum of the unrounded p by 0.0020 and 0.0026, in the same time; about
-// the exact maximum by 0.0017 and 0.0024, but 6 % slower.  The outputs' own rounding makes
-// 0.0017, and that of ds, which has no way around it, as much again of the gradients).
+// its rounding drops out of o (packed bf16 tokens: o is off by 0.0019 of itself, with the sum of
+// the unrounded p by 0.0020, in the same time; about the exact maximum by 0.0017, but 6 %
+// slower.  Its own rounding makes 0.0017).
 // lse is of the unrounded sum, in fp32 too.
 #include "attention_common.h"
 
@@ -31,7 +30,7 @@ using namespace dev;
 // walks through their keys 64 at a time: the next step's keys and values go by DMA into the
 // other half of a two-stage LDS buffer while this one's are used.  Two workgroups share a compute
 // unit, so that one's exponentials run beside the other's products: 16384 causal tokens, 32
-// query and 8 key heads of 128 in bf16, take 2080 us (1057 TFLOP/s; matrix units busy 42 %,
+// query and 8 key heads of 128 in bf16, take 2060 to 2120 us (1040 to 1070 TFLOP/s; matrix units busy 42 %,
 // then exponentials and packing, waits 30 %).  With one workgroup of 8 waves a unit that took
 // 2407, with every new maximum as the reference 2240, with a step's first values read
 // after the softmax 2156.

@@ -11,7 +11,7 @@
 // the gradients of a sequence depend on that sequence alone.  dk and dv apart cost one product
 // more (q k twice) than together, but fit a wave into half of a SIMD's registers: with both at
 // once (254 + 256 registers, one wave a SIMD) that kernel took 3180 us for 8192 tokens of 8 key
-// heads and 32 query heads of 128 where now all three take 2000 (matrix units busy 41 %,
+// heads and 32 query heads of 128 where now all three take 2000 (matrix units busy 39 %,
 // then exponentials, differences and packing, waits 28 %).
 // p and ds are rounded to the input's type for their products (the rest of large ds follows),
 // all else is fp32.
