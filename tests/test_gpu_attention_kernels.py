@@ -215,3 +215,21 @@ def test_more_rows_than_a_launch_has_threads():
     few = torch_ops.attention(q, k, v, ints([T - 3, T - 2, T - 1]), ints([0, 4, 9]), max_q=1)
     assert (few[:T - 3] == 0).all() and (few[T - 1] == 0).all()
     assert torch.equal(few[T - 2], torch_ops.attention(q[T - 2:T - 1], k[4:], v[4:])[0])
+
+
+@pytest.mark.parametrize("nq,nk", [([5], [3000]), ([1, 3, 2], [2500, 2900, 2100])], ids=str)
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_gradients_of_few_rows(nq, nk, dt):
+    q, k, v, do = make(sum(nq), sum(nk), 8, 2, 128, dt, 37)
+    assert takes_few(q, k, len(nq), max(nq))
+    check(q, k, v, do, nq, nk, True, max_q=max(nq))
+
+
+@pytest.mark.parametrize("heads", [(64, 1, 64), (100, 1, 128), (129, 1, 8), (146, 2, 40)])
+def test_many_heads_of_a_group(heads):
+    # more heads of a group than a step has rows
+    hq, hk, D = heads
+    nq, nk = [70, 1, 33], [70, 5, 90]
+    q, k, v, do = make(sum(nq), sum(nk), hq, hk, D, "bf16", hq)
+    for causal in (True, False):
+        check(q, k, v, do, nq, nk, causal)
