@@ -207,13 +207,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttnArgs a) {
   const int tiles = gridDim.x / (unsigned)a.k_heads;
   const int kh = blockIdx.x % (unsigned)a.k_heads;
   const int tile = blockIdx.x / (unsigned)a.k_heads;
-  FoundTile f;
-  if (a.sorted) {
-    f = longest_first<kRows>(a, tile);
-  } else {
-    f.found = segment_of_tile<kRows>(a, tiles - 1 - tile);
-    f.first = (tiles - 1 - tile - (f.found.s.q0 * a.group / kRows + f.found.segment)) * kRows;
-  }
+  const FoundTile f = a.sorted ? longest_first<kRows>(a, tile) : tile_of_rows<kRows>(a, tiles - 1 - tile);
   const Found found = f.found;
   const Sequence s = found.s;
   const int r0 = f.first;
@@ -336,9 +330,6 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttnArgs a) {
 // of 8 heads: 11 us and the join 6, most of them launches and trips to memory).
 constexpr int kFewWaves = 4, kFewThreads = 64 * kFewWaves;
 
-// The first chunk slot of a sequence: every sequence has the slots that it needs.
-__device__ __forceinline__ int first_slot(const Found& f) { return f.s.k0 / kAttnChunk + f.segment - 1; }
-
 template <int IN, int DP>
 __global__ __launch_bounds__(kFewThreads, 2) void attention_few_kernel(AttnArgs a) {
   using T = TileOf<DP>;
@@ -350,14 +341,10 @@ __global__ __launch_bounds__(kFewThreads, 2) void attention_few_kernel(AttnArgs 
   const int quad = lane / 16, col = lane % 16;
   const int kh = blockIdx.x % (unsigned)a.k_heads;
   const int slot = blockIdx.x / (unsigned)a.k_heads;
-  // the sequence of this chunk slot: sequence b's begin at its first key / 256 + b
-  const Found found = find_segment(a, [&](int i, int, int k) {
-    return i == 0 || (i <= a.batch && k / kAttnChunk + (i - 1) <= slot);
-  });
-  const Sequence s = found.s;
-  if (found.segment == 0) return;
-  const int c0 = (slot - first_slot(found)) * kAttnChunk;
-  if (c0 < 0 || c0 >= s.m || s.n == 0) return;
+  const FoundTile chunk = chunk_of_slot(a, slot);
+  const Sequence s = chunk.found.s;
+  const int c0 = chunk.first;
+  if (c0 >= s.m || s.n == 0) return;  // (a segment that is no sequence has no keys)
   const int queries = s.n < a.max_q ? s.n : (int)a.max_q;
   if (c0 >= keys_seen(a, s, queries - 1)) return;
   const int left = s.m - c0 < kAttnChunk ? s.m - c0 : kAttnChunk;
@@ -499,7 +486,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
   if (at >= (unsigned)a.q_rows * a.q_heads) return;
   const int q = at / (unsigned)a.q_heads, head = at - q * a.q_heads;
   const int kh = head / (unsigned)a.group;
-  const Found found = find_segment(a, [&](int, int first, int) { return first <= q; });
+  const Found found = segment_of_query(a, q);
   const Sequence s = found.s;
   const int t = q - s.q0;
   const bool said = t < a.max_q || found.segment == 0 || found.segment > a.batch;  // (rows in no sequence have no keys)

@@ -117,9 +117,9 @@ __device__ __forceinline__ void rows_role(const AttnArgs& a, int tile, int kh, c
   using T = TileOf<DP>;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int quad = lane / 16, col = lane % 16;
-  const Found found = segment_of_tile<kBlock<SETS>>(a, tile);
-  const Sequence s = found.s;
-  const int r0 = (tile - (s.q0 * a.group / kBlock<SETS> + found.segment)) * kBlock<SETS>;
+  const FoundTile f = tile_of_rows<kBlock<SETS>>(a, tile);
+  const Sequence s = f.found.s;
+  const int r0 = f.first;
   const int rows = s.n * a.group;
   if (r0 >= rows) return;
 
@@ -286,10 +286,10 @@ __device__ __forceinline__ void keys_role(const AttnArgs& a, int tile, int kh, c
   using T = TileOf<DP>;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int quad = lane / 16, col = lane % 16;
-  const Found found = find_segment(a, [&](int i, int, int k) { return k / kBlock<SETS> + i <= tile; });
-  const Sequence s = found.s;
-  const int k_first = s.k0, k_end = found.k_end;
-  const int c0 = (tile - (k_first / kBlock<SETS> + found.segment)) * kBlock<SETS>;  // of the segment
+  const FoundTile t = tile_of_keys<kBlock<SETS>>(a, tile);
+  const Sequence s = t.found.s;
+  const int k_first = s.k0, k_end = t.found.k_end;
+  const int c0 = t.first;
   if (c0 >= k_end - k_first) return;
   const int rows = s.n * a.group;
   const int w0 = c0 + 16 * SETS * wave;
