@@ -629,7 +629,9 @@ void head_rope_plan_destroy(head_rope_plan_t plan);
  * in their order (and of dim and scale): not of the number of queries of the call or
  * of its sequence, other sequences, room in a cache, or max_q.  A prompt taken at
  * once, in pieces or token by token over a cache has the same bits.  What lies in k and
- * v where a row does not see it does not reach the row, NaN included.
+ * v where a row does not see it does not reach the row, NaN included.  A value of v that is not
+ * finite and that the row sees is added to the row's result as it is, whatever its weight: o is
+ * that infinity there, or NaN (a NaN, or infinities of both signs).
  *
  * cu_q, cu_k (int32 [batch + 1]) and k_lens (int32 [batch]) are device memory, read by the
  * kernels: values that ascend, from 0 to the rows.  Others are clamped to the operands:

@@ -19,6 +19,12 @@
 // the unrounded p by 0.0020, in the same time; about the exact maximum by 0.0017, but 6 %
 // slower.  Its own rounding makes 0.0017).
 // lse is of the unrounded sum, in fp32 too.
+//
+// Values that are not finite.  In the products they would reach rows that do not see them (0
+// times infinity), and be NaN in the rows that see them with a probability that rounds to 0, as
+// in any row whose factors later fall to 0.  So the sums are of the finite values, and the row's
+// others are added to the quotient at the end: o is infinite or NaN where the row
+// sees such a value, whatever its weight.  Only calls that hold some pay for it.
 #include "attention_common.h"
 
 namespace imm {
@@ -52,19 +58,14 @@ __device__ __forceinline__ u32x4 only_finite(u32x4 v) {
   return v;
 }
 
-// ... and the others' values, zeros in the place of the finite ones.
-template <int IN>
-__device__ __forceinline__ f32x4 only_not_finite(i32x2 four) {
-  f32x4 f;
-#pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const unsigned bits = ((unsigned)four[r / 2] >> (16 * (r % 2))) & 0xffffu;
-    constexpr unsigned E = IN == GEMM_F16 ? 0x7c00u : 0x7f80u;
-    // (infinity or NaN in fp32: an fp16 fraction moves up with its sign)
-    const unsigned wide = IN == GEMM_F16 ? (bits & 0x8000u) << 16 | 0x7f800000u | (bits & 0x3ffu) << 13 : bits << 16;
-    f[r] = (bits & E) == E ? __uint_as_float(wide) : 0.0f;
-  }
-  return f;
+// x + value R of a pair if that is not finite, otherwise x as it is.
+template <int IN, int R>
+__device__ __forceinline__ float plus_not_finite(float x, unsigned two) {
+  constexpr unsigned E = IN == GEMM_F16 ? 0x7c00u : 0x7f80u;
+  const unsigned bits = R ? two >> 16 : two & 0xffffu;
+  // (infinity or NaN in fp32: an fp16 fraction moves up with its sign)
+  const unsigned wide = IN == GEMM_F16 ? (bits & 0x8000u) << 16 | 0x7f800000u | (bits & 0x3ffu) << 13 : bits << 16;
+  return (bits & E) == E ? x + __uint_as_float(wide) : x;
 }
 
 // The rows of a wave through one step.
@@ -152,7 +153,7 @@ struct WaveRows {
         for (int i = 0; i < SETS; ++i) o[i][d] = mfma16_v<IN>(vf, pf[i][p], FIRST && p == 0 ? f32x4{} : o[i][d]);
       }
   }
-  // The values of a step that are not finite, for the rows that see them.
+  // O + the values of a step that are not finite, for the rows that see them.
   __device__ __forceinline__ void add_not_finite(const char* v, int64_t v_bytes, int k0, int end, int dim) {
     const int quad = (threadIdx.x & 63) / 16;
     for (int j = k0; j < k0 + kTile && j < end; ++j) {
@@ -161,9 +162,14 @@ struct WaveRows {
         const int c = 16 * d + 4 * quad;
         i32x2 x{};
         if (c < dim) x = *reinterpret_cast<const i32x2*>(v + j * v_bytes + 2 * c);
-        const f32x4 bad = only_not_finite<IN>(x);
 #pragma unroll
-        for (int i = 0; i < SETS; ++i) o[i][d] += j < seen[i] ? bad : f32x4{};
+        for (int i = 0; i < SETS; ++i)
+          if (j < seen[i]) {
+            O[i][d][0] = plus_not_finite<IN, 0>(O[i][d][0], x[0]);
+            O[i][d][1] = plus_not_finite<IN, 1>(O[i][d][1], x[0]);
+            O[i][d][2] = plus_not_finite<IN, 0>(O[i][d][2], x[1]);
+            O[i][d][3] = plus_not_finite<IN, 1>(O[i][d][3], x[1]);
+          }
       }
     }
   }
@@ -231,14 +237,12 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttnArgs a) {
       if (row < rows && d < a.dim) w.q[i][ks] = *reinterpret_cast<const i32x4*>(q + 2 * d);
     }
   }
-  // keys that any row of the workgroup, and of the wave, sees, and those that all of
-  // them see (rows past the end see none, which needs no mask)
+  // keys that any row of the workgroup, and of the wave, sees, and those that all of the
+  // wave's see (rows past the end see none, which needs no mask)
   auto seen_of = [&](int r) { return keys_seen(a, s, (r < rows ? r : rows - 1) / a.group); };
   const int need = __builtin_amdgcn_readfirstlane(seen_of(r0 + kRows - 1));
-  const int all_see = __builtin_amdgcn_readfirstlane(seen_of(r0));
   const int wave_need = __builtin_amdgcn_readfirstlane(w0 < rows ? seen_of(w0 + 16 * SETS - 1) : 0);
   const int wave_all = __builtin_amdgcn_readfirstlane(w0 < rows ? seen_of(w0) : 0);
-  w.clear_all();
 
   const int64_t k_bytes = 2 * a.k_token, v_bytes = 2 * a.v_token;
   const char* const kp = static_cast<const char*>(a.k) + 2 * (s.k0 * a.k_token + kh * a.k_head);
@@ -248,63 +252,85 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttnArgs a) {
     km.move(kp + k0 * k_bytes, kt, s.m - k0, k_bytes, a.dim);
     vm.move(vp + k0 * v_bytes, vt, s.m - k0, v_bytes, a.dim);
   };
-  // A step that some rows do not see all of: values that are not finite are taken out of it (0
-  // times a NaN would reach the rows that do not see it) and added for the rows that do.
+  // Zeros in the place of a tile's values that are not finite.
   auto clean = [&](char* vt) {
-    bool bad = false;
     u32x4* const mine = reinterpret_cast<u32x4*>(vt) + threadIdx.x;
-    constexpr int N = Mover<DP>::N;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const u32x4 v = mine[i * kThreads];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) bad |= not_finite<IN>(v[e]);
-    }
-    if (!__syncthreads_or(bad)) return false;
-#pragma unroll
-    for (int i = 0; i < N; ++i) mine[i * kThreads] = only_finite<IN>(mine[i * kThreads]);
+    for (int i = 0; i < Mover<DP>::N; ++i) mine[i * kThreads] = only_finite<IN>(mine[i * kThreads]);
     __syncthreads();
-    return true;
   };
+  bool careful = false;
   auto one = [&](auto first, int k0, char* kt, char* vt, char* next_k, char* next_v) {
     landed();  // this step's tiles are there, and the other stage has been read
     if (k0 + kTile < need) fetch(k0 + kTile, next_k, next_v);
-    const bool poison = k0 + kTile > all_see && clean(vt);
-    if (k0 < wave_need) {
-      w.template step<decltype(first)::value>(kt, vt, k0, k0 + kTile > wave_all);
-      if (poison) w.add_not_finite(vp, v_bytes, k0, s.m, a.dim);
-    }
+    if (careful) clean(vt);
+    if (k0 < wave_need) w.template step<decltype(first)::value>(kt, vt, k0, k0 + kTile > wave_all);
   };
   const std::true_type first;
   const std::false_type further;
-  if (need > 0) fetch(0, k_a, v_a);
-  for (int c0 = 0; c0 < need; c0 += kAttnChunk) {
-    one(first, c0, k_a, v_a, k_b, v_b);
-    for (int k0 = c0 + kTile; k0 < c0 + kAttnChunk && k0 < need; k0 += 2 * kTile) {
-      one(further, k0, k_b, v_b, k_a, v_a);
-      if (k0 + kTile < c0 + kAttnChunk && k0 + kTile < need) one(further, k0 + kTile, k_a, v_a, k_b, v_b);
+  for (;;) {
+    w.clear_all();
+    if (need > 0) fetch(0, k_a, v_a);
+    for (int c0 = 0; c0 < need; c0 += kAttnChunk) {
+      one(first, c0, k_a, v_a, k_b, v_b);
+      for (int k0 = c0 + kTile; k0 < c0 + kAttnChunk && k0 < need; k0 += 2 * kTile) {
+        one(further, k0, k_b, v_b, k_a, v_a);
+        if (k0 + kTile < c0 + kAttnChunk && k0 + kTile < need) one(further, k0 + kTile, k_a, v_a, k_b, v_b);
+      }
+      if (c0 < wave_need) w.join(c0);
     }
-    if (c0 < wave_need) w.join(c0);
+    // A value that is not finite, seen or not, has left a result that is not finite in every row whose
+    // steps held it; if there are such, all steps once more without those values.  (The
+    // barrier is also the one before the stages are filled again.)
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < SETS; ++i)
+#pragma unroll
+      for (int d = 0; d < T::DB; ++d)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) bad |= !(fabsf(w.O[i][d][r]) < __builtin_inff());
+    if (careful || !__syncthreads_or(bad)) break;
+    careful = true;
   }
 
+  // (rows that are past the call's are not stored)
+#pragma unroll
+  for (int i = 0; i < SETS; ++i) {
+    const int t = (w0 + 16 * i + col) / a.group;
+    // a row without keys is zero; one whose keys are all -infinity is 0 / 0; and NaN is what a
+    // sequence longer than the call said has past that, here as in the kernel of few rows
+    const bool unsaid = t >= a.max_q && found.segment >= 1 && found.segment <= a.batch;
+    if (unsaid) w.L[i] = w.E[i] = __builtin_nanf("");
+    const float inv = w.seen[i] == 0 && !unsaid ? 0.0f : 1.0f / w.L[i];
+    if (unsaid) w.seen[i] = 1;
+#pragma unroll
+    for (int d = 0; d < T::DB; ++d) w.O[i][d] *= inv;
+  }
+  if (careful) {
+    for (int k0 = 0; k0 < need; k0 += kTile) {
+      bool bad = false;
+#pragma unroll
+      for (int i = 0; i < Mover<DP>::N; ++i) {
+        const int at = threadIdx.x + i * kThreads, key = k0 + at / T::SLOTS, c = at % T::SLOTS * 8;
+        if (key >= s.m || c >= a.dim) continue;
+        const u32x4 v = *reinterpret_cast<const u32x4*>(vp + key * v_bytes + 2 * c);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) bad |= not_finite<IN>(v[e]);
+      }
+      if (__syncthreads_or(bad) && k0 < wave_need) w.add_not_finite(vp, v_bytes, k0, s.m, a.dim);
+    }
+  }
 #pragma unroll
   for (int i = 0; i < SETS; ++i) {
     const int row = w0 + 16 * i + col;
     if (row >= rows) continue;
     const int t = row / a.group;
     const int64_t at = (s.q0 + t) * a.q_heads + kh * a.group + (row - t * a.group);
-    // a row without keys is zero; one whose keys are all -infinity is 0 / 0; and NaN is what a
-    // sequence longer than the call said has past that, here as in the kernel of few rows
-    if (t >= a.max_q && found.segment >= 1 && found.segment <= a.batch) {
-      w.L[i] = w.E[i] = __builtin_nanf("");
-      w.seen[i] = 1;
-    }
-    const float inv = w.seen[i] == 0 ? 0.0f : 1.0f / w.L[i];
 #pragma unroll
     for (int d = 0; d < T::DB; ++d) {
       const int c = 16 * d + 4 * quad;
       if (c >= a.dim) continue;
-      const f32x4 x = w.O[i][d] * inv;
+      const f32x4 x = w.O[i][d];
       const i32x2 y{pack2<IN>(x[0], x[1]), pack2<IN>(x[2], x[3])};
       const int64_t to = 2 * (at * a.dim + c);
       *reinterpret_cast<i32x2*>(static_cast<char*>(a.o) + to) = y;
@@ -387,10 +413,9 @@ __global__ __launch_bounds__(kFewThreads, 2) void attention_few_kernel(AttnArgs 
 #pragma unroll
     for (int e = 0; e < 4; ++e) bad |= not_finite<IN>(vv[i][e]);
   }
-  // rows that do not see all of the chunk: values that are not finite are taken out of it,
-  // and added for the rows that see them
-  const bool poison = __syncthreads_or(bad) && c0 + left > keys_seen(a, s, 0);
-  if (poison) {
+  // values that are not finite are taken out of the chunk, and told of: the join adds them
+  const bool told = __syncthreads_or(bad);
+  if (told) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int at = threadIdx.x + i * kFewThreads, key = at / T::SLOTS, c = at % T::SLOTS;
@@ -455,19 +480,12 @@ __global__ __launch_bounds__(kFewThreads, 2) void attention_few_kernel(AttnArgs 
     const int64_t at = ((int64_t)slot * a.k_heads + kh) * a.part_rows + row;
     if (row < rows) {
       if (wave == 0 && quad == 0) {
-        reinterpret_cast<f32x4*>(a.part_ml)[at] = f32x4{m[kFewWaves - 1], l, sum, 0.0f};
+        reinterpret_cast<f32x4*>(a.part_ml)[at] = f32x4{m[kFewWaves - 1], l, sum, told ? 1.0f : 0.0f};
       }
 #pragma unroll
       for (int i = 0; i < (T::DB + kFewWaves - 1) / kFewWaves; ++i) {
         const int d = 16 * (kFewWaves * i + wave) + 4 * quad;
-        if (d < a.dim && d < DP) {
-          if (poison) {
-            const char* v = static_cast<const char*>(a.v) + 2 * ((s.k0 + c0) * a.v_token + kh * a.v_head + d);
-            for (int j = 0; j < seen; ++j, v += 2 * a.v_token)
-              o[i] += only_not_finite<IN>(*reinterpret_cast<const i32x2*>(v));
-          }
-          *reinterpret_cast<f32x4*>(a.part_o + at * a.dim + d) = o[i];
-        }
+        if (d < a.dim && d < DP) *reinterpret_cast<f32x4*>(a.part_o + at * a.dim + d) = o[i];
       }
     }
     __syncthreads();  // before the next rows use ml, se and pl
@@ -493,8 +511,9 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
   const int seen = keys_seen(a, s, t);
   float M = kNegInf, L = 0.0f, E = 0.0f, O0 = 0.0f, O1 = 0.0f;
   const bool mine = 2 * lane < a.dim;
+  const int64_t step = (int64_t)a.k_heads * a.part_rows;
+  bool told = false;  // of values that are not finite
   if (said && seen > 0) {
-    const int64_t step = (int64_t)a.k_heads * a.part_rows;
     const int64_t first = (int64_t)first_slot(found) * step + kh * a.part_rows + t * a.group + (head - kh * a.group);
     const int chunks = (seen + kAttnChunk - 1) / kAttnChunk;
     const f32x4* ml_at = reinterpret_cast<const f32x4*>(a.part_ml) + first + lane * step;
@@ -516,6 +535,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
       f32x4 ml{kNegInf, 0.0f, 0.0f, 0.0f};
       if (lane < n) ml = *ml_at;
       ml_at += 64 * step;
+      told |= __any(ml[3] != 0.0f);
       // the reference after each chunk: it is set again at few of them
       float before = M, after = M;
       for (int from = 0;;) {
@@ -560,11 +580,25 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
   if (!said) L = E = O0 = O1 = __builtin_nanf("");  // a sequence longer than the call said
   const bool empty = seen == 0 && said;
   const float inv = empty ? 0.0f : 1.0f / L;
+  O0 *= inv;
+  O1 *= inv;
+  if (told && mine) {
+    const float* ml = a.part_ml + 4 * ((int64_t)first_slot(found) * step + kh * a.part_rows + t * a.group + (head - kh * a.group));
+    const char* v = static_cast<const char*>(a.v) + 2 * (s.k0 * a.v_token + kh * a.v_head) + 4 * lane;
+    for (int c0 = 0; c0 < seen; c0 += kAttnChunk, ml += 4 * step) {
+      if (ml[3] == 0.0f) continue;
+      for (int j = c0; j < c0 + kAttnChunk && j < seen; ++j) {
+        const unsigned two = *reinterpret_cast<const unsigned*>(v + 2 * j * a.v_token);
+        O0 = plus_not_finite<IN, 0>(O0, two);
+        O1 = plus_not_finite<IN, 1>(O1, two);
+      }
+    }
+  }
   if (mine) {
-    const int y = pack2<IN>(O0 * inv, O1 * inv);
+    const int y = pack2<IN>(O0, O1);
     const int64_t to = (int64_t)at * a.dim / 2 + lane;
     static_cast<int*>(a.o)[to] = y;
-    if (a.o_low) static_cast<int*>(a.o_low)[to] = pack2_rest<IN>(O0 * inv, O1 * inv, y);
+    if (a.o_low) static_cast<int*>(a.o_low)[to] = pack2_rest<IN>(O0, O1, y);
   }
   if (a.lse && lane == 0) a.lse[at] = empty ? kNegInf : (M + __builtin_amdgcn_logf(E)) * kLn2;
 }
