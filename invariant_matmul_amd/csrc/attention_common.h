@@ -19,6 +19,10 @@
 #include "decoder_internal.h"
 #include "kernel_common.h"
 
+// From here on a product and a sum are fused where the code says fmaf and nowhere else: the kernels
+// that a call may be given to have to round alike.
+#pragma clang fp contract(off)
+
 namespace imm {
 namespace dev {
 
