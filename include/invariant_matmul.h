@@ -671,8 +671,8 @@ size_t attention_backward_workspace_size(attention_plan_t plan);
  * then the rounding of o is in the gradients) and lse:
  *   ds_ij = p_ij (do_i v_j - sum_d do_id (o + o_low)_id), dv_j = sum_i p_ij do_i,
  *   dq_i = scale sum_j ds_ij k_j, dk_j = scale sum_i ds_ij q_i,
- * p and ds rounded to the input's type for their products (fp16: a ds below 2^-25 is
- * lost, so gradients need the scaling of the loss that fp16 training has).  Rows in no
+ * p and ds rounded to the input's type for their products (fp16: p is raised by 2^14 for
+ * dv's; a ds below 2^-25 is lost, so gradients need the scaling of the loss that fp16 training has).  Rows in no
  * sequence and keys past k_lens have zero gradients.  Sums in a fixed order, without
  * atomics: the gradients of a sequence are a bitwise function of it alone.  A NaN or infinity
  * in q, k, v or d_o stays in its sequence; there it may reach, beyond the formula's

@@ -280,6 +280,13 @@ struct RowMover {
   }
 };
 
+// Binary places by which p is raised for dv's products, and the sums lowered: in fp16 a p below 2^-14 would
+// lose bits, one below 2^-25 all of them, as the p of ten thousand keys that a row sees do (65536 keys: dv
+// off by 0.00077 of itself instead of 0.00021).  p is at most 1 and fp16 reaches 2^15.  (bf16 needs none, and its
+// values times 2^14 may leave fp32's range.)
+template <int IN>
+constexpr int kRaised = IN == GEMM_F16 ? 14 : 0;
+
 // dk (DK) or dv of the keys of a tile.
 template <int IN, int DP, bool DK, int SETS>
 __device__ __forceinline__ void keys_role(const AttnArgs& a, int tile, int kh, const Stages<DP>& st) {
@@ -360,7 +367,8 @@ __device__ __forceinline__ void keys_role(const AttnArgs& a, int tile, int kh, c
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
         const int at = 32 * half + 16 * b + 4 * quad;
-        const f32x4 nl = *reinterpret_cast<const f32x4*>(nls + at);
+        f32x4 nl = *reinterpret_cast<const f32x4*>(nls + at);
+        if constexpr (!DK && kRaised<IN> != 0) nl += (float)kRaised<IN>;
         f32x4 delta{};
         if constexpr (DK) delta = *reinterpret_cast<const f32x4*>(deltas + at);
 #pragma unroll
@@ -410,7 +418,7 @@ __device__ __forceinline__ void keys_role(const AttnArgs& a, int tile, int kh, c
   for (int j = 0; j < SETS; ++j) {
     const int key = w0 + 16 * j + col;
     if (key < k_end - k_first)
-      store_rows<IN, DP>(sum[j], DK ? a.scale : 1.0f, DK ? a.dk : a.dv, ((int64_t)(k_first + key) * a.k_heads + kh) * a.dim, a.dim);
+      store_rows<IN, DP>(sum[j], DK ? a.scale : 1.0f / (1 << kRaised<IN>), DK ? a.dk : a.dv, ((int64_t)(k_first + key) * a.k_heads + kh) * a.dim, a.dim);
   }
 }
 
