@@ -227,6 +227,10 @@ __device__ __forceinline__ void rows_role(const AttnArgs& a, int tile, int kh, c
 #pragma unroll
   for (int i = 0; i < SETS; ++i) {
     const int row = w0 + 16 * i + col, t = row / a.group;
+    if (seen[i] == 0) {  // (whatever the wave's other rows see)
+#pragma unroll
+      for (int d = 0; d < T::DB; ++d) dq[i][d] = f32x4{};
+    }
     const int64_t h = kh * a.group + (row - t * a.group);
     if (row < rows) store_rows<IN, DP>(dq[i], a.scale, a.dq, ((int64_t)(s.q0 + t) * a.q_heads + h) * a.dim, a.dim);
   }
@@ -417,6 +421,10 @@ __device__ __forceinline__ void keys_role(const AttnArgs& a, int tile, int kh, c
 #pragma unroll
   for (int j = 0; j < SETS; ++j) {
     const int key = w0 + 16 * j + col;
+    if (key >= s.m) {  // (the room of a cache)
+#pragma unroll
+      for (int d = 0; d < T::DB; ++d) sum[j][d] = f32x4{};
+    }
     if (key < k_end - k_first)
       store_rows<IN, DP>(sum[j], DK ? a.scale : 1.0f / (1 << kRaised<IN>), DK ? a.dk : a.dv, ((int64_t)(k_first + key) * a.k_heads + kh) * a.dim, a.dim);
   }
