@@ -676,7 +676,8 @@ size_t attention_backward_workspace_size(attention_plan_t plan);
  * sequence and keys past k_lens have zero gradients.  Sums in a fixed order, without
  * atomics: the gradients of a sequence are a bitwise function of it alone.  A NaN or infinity
  * in q, k, v or d_o stays in its sequence; there it may reach, beyond the formula's
- * gradients, those of queries and keys up to 64 places away that do not see each other. */
+ * gradients, those of queries and keys up to 78 places away that do not see each other (a wave
+ * works on 16 rows or keys in steps of 64), and an infinite gradient may be NaN. */
 gemm_status attention_backward(attention_plan_t plan, const void* d_o, const void* q,
                                int64_t q_token_stride, int64_t q_head_stride, const void* k,
                                int64_t k_token_stride, int64_t k_head_stride, const void* v,

@@ -105,21 +105,55 @@ __device__ __forceinline__ i32x4 rest_of(const f32x4& a, const f32x4& b, const f
   return rest;
 }
 
+// Results that are not finite.  A step multiplies by 0 what a row or key does not see, and 0 times an infinity or a
+// NaN is a NaN: how far one reaches beyond what the formula gives follows from the steps that a wave
+// walks, and so from the number of its rows or keys.  A workgroup of two sets a wave that finds such
+// results therefore makes them again with one set a wave, as all smaller calls do: the reach, at most 15 + 63
+// places, and every bit are then the sequence's own.
+template <int SETS, int DB>
+__device__ __forceinline__ bool not_finite(const f32x4 (&x)[SETS][DB]) {
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < SETS; ++i)
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) bad |= !(fabsf(x[i][d][r]) < __builtin_inff());
+  return bad;
+}
+// The kernel's argument from memory once more.  (The compiler would otherwise hold what the rare second
+// pass needs through the loops ahead: 145 scalar registers spilled, the training case 577 us instead of 556, with no
+// second pass at all 553.)
+__device__ __forceinline__ const AttnArgs& again(const AttnArgs& a) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  auto p = (const __attribute__((address_space(4))) AttnArgs*)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return *(const AttnArgs*)p;
+#else
+  return a;
+#endif
+}
+// f(first) of the two halves of a tile, once every wave is done with the stages.
+template <class F>
+__device__ __forceinline__ void by_halves(int first, F&& f) {
+  for (int half = 0; half < 2; ++half) {
+    __syncthreads();
+    f(first + half * kBlock<1>);
+  }
+}
+
 template <int DP>
 struct Stages {  // (arrays of their own, as in the forward kernel)
   char *x0, *y0, *x1, *y1;
   float *n0, *d0, *n1, *d1;
 };
 
-// dq of the rows from r0 on.
+// dq of a sequence's rows from r0 on.
 template <int IN, int DP, int SETS>
-__device__ __forceinline__ void rows_role(const AttnArgs& a, int tile, int kh, const Stages<DP>& st) {
+__device__ __forceinline__ void rows_role(const AttnArgs& a, const Sequence& s, int r0, int kh, const Stages<DP>& st) {
   using T = TileOf<DP>;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int quad = lane / 16, col = lane % 16;
-  const FoundTile f = tile_of_rows<kBlock<SETS>>(a, tile);
-  const Sequence s = f.found.s;
-  const int r0 = f.first;
   const int rows = s.n * a.group;
   if (r0 >= rows) return;
 
@@ -224,6 +258,10 @@ __device__ __forceinline__ void rows_role(const AttnArgs& a, int tile, int kh, c
     one(k0, st.x0, st.y0, st.x1, st.y1);
     if (k0 + kTile < need) one(k0 + kTile, st.x1, st.y1, st.x0, st.y0);
   }
+  if constexpr (SETS == 2) {
+    if (__syncthreads_or(not_finite(dq)))
+      return by_halves(r0, [&](int first) { rows_role<IN, DP, 1>(again(a), s, first, kh, st); });
+  }
 #pragma unroll
   for (int i = 0; i < SETS; ++i) {
     const int row = w0 + 16 * i + col, t = row / a.group;
@@ -291,16 +329,14 @@ struct RowMover {
 template <int IN>
 constexpr int kRaised = IN == GEMM_F16 ? 14 : 0;
 
-// dk (DK) or dv of the keys of a tile.
+// dk (DK) or dv of a segment's keys from c0 on.
 template <int IN, int DP, bool DK, int SETS>
-__device__ __forceinline__ void keys_role(const AttnArgs& a, int tile, int kh, const Stages<DP>& st) {
+__device__ __forceinline__ void keys_role(const AttnArgs& a, const Found& found, int c0, int kh, const Stages<DP>& st) {
   using T = TileOf<DP>;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int quad = lane / 16, col = lane % 16;
-  const FoundTile t = tile_of_keys<kBlock<SETS>>(a, tile);
-  const Sequence s = t.found.s;
-  const int k_first = s.k0, k_end = t.found.k_end;
-  const int c0 = t.first;
+  const Sequence s = found.s;
+  const int k_first = s.k0, k_end = found.k_end;
   if (c0 >= k_end - k_first) return;
   const int rows = s.n * a.group;
   const int w0 = c0 + 16 * SETS * wave;
@@ -418,6 +454,10 @@ __device__ __forceinline__ void keys_role(const AttnArgs& a, int tile, int kh, c
     one(r0, st.x0, st.y0, st.n0, st.d0, st.x1, st.y1, st.n1, st.d1);
     if (r0 + kTile < rows) one(r0 + kTile, st.x1, st.y1, st.n1, st.d1, st.x0, st.y0, st.n0, st.d0);
   }
+  if constexpr (SETS == 2) {
+    if (__syncthreads_or(not_finite(sum)))
+      return by_halves(c0, [&](int first) { keys_role<IN, DP, DK, 1>(again(a), found, first, kh, st); });
+  }
 #pragma unroll
   for (int j = 0; j < SETS; ++j) {
     const int key = w0 + 16 * j + col;
@@ -444,12 +484,16 @@ __global__ __launch_bounds__(kThreads, 2) void attention_backward_kernel(AttnArg
   const int kh = blockIdx.x % (unsigned)a.k_heads;
   int tile = blockIdx.x / (unsigned)a.k_heads;
   const int turns = a.k_turns * 2 * kTurn;
-  if (tile >= turns) return rows_role<IN, DP, SETS>(a, (int)a.q_tiles - 1 - (tile - turns), kh, st);
+  if (tile >= turns) {
+    const FoundTile f = tile_of_rows<kBlock<SETS>>(a, (int)a.q_tiles - 1 - (tile - turns));
+    return rows_role<IN, DP, SETS>(a, f.found.s, f.first, kh, st);
+  }
   const bool dk = tile / kTurn % 2 == 0;
   tile = tile / (2 * kTurn) * kTurn + tile % kTurn;
   if (tile >= a.k_tiles) return;
-  if (dk) keys_role<IN, DP, true, SETS>(a, tile, kh, st);
-  else keys_role<IN, DP, false, SETS>(a, tile, kh, st);
+  const FoundTile f = tile_of_keys<kBlock<SETS>>(a, tile);
+  if (dk) keys_role<IN, DP, true, SETS>(a, f.found, f.first, kh, st);
+  else keys_role<IN, DP, false, SETS>(a, f.found, f.first, kh, st);
 }
 
 // Up to three workgroups of 128 rows or keys a compute unit, the longest chain of steps is what
