@@ -28,6 +28,10 @@
 #include "lanes.h"
 #include "rows16.h"
 
+// A product and a sum are fused where the code says fmaf and nowhere else: the kernels of whole rows and of parts
+// round alike.
+#pragma clang fp contract(off)
+
 namespace imm {
 namespace {
 using namespace dev;
@@ -193,20 +197,15 @@ struct Sums {
 __device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
 // Below this e^d is 0 in fp32; d stays finite, so that 0 d is 0.
 constexpr float kLeast = -1000.0f;
-// The sums about a larger maximum.
-__device__ __forceinline__ void move(Sums& a, float to) {
-  const float d = fmaxf(a.m - to, kLeast), e = exp_of(d);
-  a.t = (a.t + a.s * d) * e;
-  a.s *= e;
-  a.m = to;
-}
+// The sums of both, about the larger maximum.  The first's products are fused with the second's, so that two lanes
+// that join each other's sums may differ in the last bit: lane 0's are the result.  (Without the
+// fused sums they agree, and 4093 rows of 100003 fp32 logits take 311 us instead of 307.)
 __device__ __forceinline__ Sums join(Sums a, Sums b) {
   // (NaN maxima do not occur: a NaN among the logits is in s and t)
   const float m = fmaxf(a.m, b.m);
   if (m == kNone) return Sums{m, a.s + b.s, a.t + b.t};
-  move(a, m);
-  move(b, m);
-  return Sums{m, a.s + b.s, a.t + b.t};
+  const float da = fmaxf(a.m - m, kLeast), ea = exp_of(da), db = fmaxf(b.m - m, kLeast), eb = exp_of(db);
+  return Sums{m, fmaf(a.s, ea, b.s * eb), fmaf(fmaf(a.s, da, a.t), ea, fmaf(b.s, db, b.t) * eb)};
 }
 __device__ __forceinline__ Sums join_lanes(Sums a) {
   each_up([&](auto d) {
@@ -215,8 +214,11 @@ __device__ __forceinline__ Sums join_lanes(Sums a) {
   });
   return a;
 }
+__device__ __forceinline__ float of_lane_0(float v) {
+  return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(v)));
+}
 
-// One unit: its sums (in every lane), and its logits offered to `best`.
+// One unit: its sums (lane 0's), and its logits offered to `best`.
 template <int IN, bool TOP>
 __device__ __forceinline__ Sums take_unit(const void* row, int64_t v0, int64_t vocab, Best& best) {
   const int lane = threadIdx.x & 63;
@@ -265,6 +267,7 @@ __device__ __forceinline__ void finish(const LogprobsArgs& g, int64_t row, const
   for (int u = lane; u < g.units; u += 64)
     a = join(a, Sums{sums[3 * u], sums[3 * u + 1], sums[3 * u + 2]});
   a = join_lanes(a);
+  a = Sums{of_lane_0(a.m), of_lane_0(a.s), of_lane_0(a.t)};  // every column's and every alternative's
   const float ln_s = logf(a.s);
   if (lane == 0) {
     g.entropy[row] = ln_s - a.t / a.s;
@@ -363,7 +366,7 @@ __global__ __launch_bounds__(kThreads) void logprobs_backward_kernel(LogprobsArg
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const float logp = (f[e] - m) - ln_s, p = exp_of(logp);
-    f[e] = mine[e] - p * fmaf(h, fmaxf(logp, kLeast) + ent, all);
+    f[e] = fmaf(-p, fmaf(h, fmaxf(logp, kLeast) + ent, all), mine[e]);
   }
   char* const out = static_cast<char*>(g.dx) + row * g.vocab * Size<IN>::value;
   if (v0 + 8 <= g.vocab) {
