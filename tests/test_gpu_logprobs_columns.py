@@ -4,8 +4,9 @@ import pytest
 import torch
 
 from invariant_matmul_amd import torch_ops
+from tests import decoder_oracle as ref
 from tests.helpers import dev
-from tests.test_gpu_token_logprobs import make
+from tests.test_gpu_token_logprobs import DT, gradient_bound, make
 
 pytestmark = pytest.mark.gpu
 
@@ -36,3 +37,17 @@ def test_columns_and_alternatives(rows, V, dt):
     again = torch_ops.token_logprobs(x, top, 0)[0]
     assert torch.equal(again, top_lp), int((again != top_lp).sum())
     assert (top_lp[:, 1:] <= top_lp[:, :-1]).all()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_gradient_of_a_thousand_tokens_a_row(dt):
+    x, t, g, h = make(2, 3001, dt, 90, n=1024)
+    t[0, 5:900] = -1
+    t[1, ::3] = 17
+    lp, ent, norm = torch_ops.token_logprobs_forward(x, t)
+    dx = torch_ops.token_logprobs_backward(g, h, x, t, norm, ent)
+    want = ref.logprobs_gradient(x, t, g, h)
+    gm = torch.where(t >= 0, g, torch.zeros_like(g)).double().abs()
+    # the sums of g, over a row's tokens and over those that are the same logit: 1024 roundings of 2^-24 at most
+    tol = gradient_bound(x, t, gm, h) + want.abs() * (ref.half(DT[dt]) + 2.0 ** -22) + gm.sum(1, keepdim=True) * 1024 * ref.U
+    ref.close(dx, want, tol + ref.tiny(DT[dt]), "dx")
