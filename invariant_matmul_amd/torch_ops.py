@@ -954,10 +954,19 @@ def _check_logits(where, logits, tokens):
 
 
 def _rows_of(logits: torch.Tensor):
-    """(logits or a copy, row stride) with contiguous rows a stride apart."""
+    """(logits or a copy of its shape, row stride) with contiguous rows a stride apart."""
     V = logits.shape[-1]
-    if logits.dim() == 2 and (logits.stride(1) == 1 or V == 1) and logits.stride(0) >= 0:
-        return logits, logits.stride(0)
+    if logits.stride(-1) == 1 or V == 1:
+        rows, stride = 1, V  # of the dimensions so far, from the last one on
+        for n, s in zip(logits.shape[-2::-1], logits.stride()[-2::-1]):
+            if n != 1:
+                if rows == 1:
+                    stride = s
+                elif s != rows * stride:
+                    break
+                rows *= n
+        else:
+            return logits, stride
     return logits.contiguous(), V
 
 
@@ -982,7 +991,7 @@ def _token_logprobs(where, logits, tokens, top, want_norm):
     ws = torch.empty(nws, dtype=torch.uint8, device=device) if nws else None
     _done(lib().logprobs_run(plan.handle, logits.data_ptr(), stride, tokens.data_ptr(), lp.data_ptr(), ent.data_ptr(),
                              _ptr(norm), _ptr(top_lp), _ptr(top_tok), _ptr(ws), nws, stream), where)
-    return lp, ent, norm, top_lp, top_tok
+    return lp, ent, norm, top_lp, top_tok, logits
 
 
 def token_logprobs_forward(logits, tokens):
@@ -1022,8 +1031,8 @@ def token_logprobs_backward(dlogprob, dentropy, logits, tokens, norm, entropy):
 class _TokenLogprobs(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, tokens, top):
-        lp, ent, norm, top_lp, top_tok = _token_logprobs("token_logprobs", logits, tokens, top, True)
-        ctx.save_for_backward(logits, tokens, norm, ent)
+        lp, ent, norm, top_lp, top_tok, rows = _token_logprobs("token_logprobs", logits, tokens, top, True)
+        ctx.save_for_backward(rows, tokens, norm, ent)  # (where the rows had to be copied, the copy)
         ctx.set_materialize_grads(False)
         if not top:
             return lp, ent
@@ -1047,13 +1056,15 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, top: int = 0):
     gradient flows through these).
 
     A token below 0 is padding (logprob 0, no gradient), one from V on gives NaN.  A logit
-    of -infinity has probability 0.  The logits are read once; rows may be strided.
+    of -infinity has probability 0.  The logits are read once, in place where their rows are contiguous
+    and one stride apart through all leading dimensions; others (logits[:, :-1] of [B, T, V]) are copied first,
+    once for both directions.
     Row i of the results depends on row i alone.  Differentiable once in reverse mode."""
     where = "token_logprobs"
     _refuse_tangent(where, logits)
     if _needs_grad(logits):
         return _TokenLogprobs.apply(logits, tokens, top)
-    lp, ent, _, top_lp, top_tok = _token_logprobs(where, logits, tokens, top, False)
+    lp, ent, _, top_lp, top_tok, _ = _token_logprobs(where, logits, tokens, top, False)
     return (lp, ent, top_lp, top_tok) if top else (lp, ent)
 
 
