@@ -624,6 +624,8 @@ void head_rope_plan_destroy(head_rope_plan_t plan);
  * [q_rows, q_heads].  Logits, statistics and sums are fp32; probabilities (about a
  * reference of the row's own logits, at most 2^8) are rounded to the input's type for
  * their product with v and for the sum that o is divided by, not for lse.
+ * (Sums of probabilities times v that pass fp32's range are infinite, as bf16 values above
+ * 2^120 divided by the number of keys can make them.)
  *
  * A row of o is a bitwise function of its query and of the keys and values it sees,
  * in their order (and of dim and scale): not of the number of queries of the call or

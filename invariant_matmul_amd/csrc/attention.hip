@@ -36,8 +36,8 @@ using namespace dev;
 // walks through their keys 64 at a time: the next step's keys and values go by DMA into the
 // other half of a two-stage LDS buffer while this one's are used.  Two workgroups share a compute
 // unit, so that one's exponentials run beside the other's products: 16384 causal tokens, 32
-// query and 8 key heads of 128 in bf16, take 2060 to 2120 us (1040 to 1070 TFLOP/s; matrix units busy 42 %,
-// then exponentials and packing, waits 30 %).  With one workgroup of 8 waves a unit that took
+// query and 8 key heads of 128 in bf16, take 2040 to 2150 us (1020 to 1080 TFLOP/s; matrix units busy 46 %,
+// vector units, with exponentials and packing, 50 %, waves waiting 21 %), of 64 1180 to 1240 (41 %, 72 % and 19 %).  With one workgroup of 8 waves a unit that took
 // 2407, with every new maximum as the reference 2240, with a step's first values read
 // after the softmax 2156.
 
@@ -352,8 +352,9 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttnArgs a) {
 // those of the chain; then each wave takes a quarter of the output's dimensions through
 // all four steps.
 // Memory bounds it where there are many chunks (61 caches of up to 8192 keys, 32 query and 4
-// key heads of 128: 126 us, 4.4 TB/s, and the join 8), latency where there are few (8192 keys
-// of 8 heads: 11 us and the join 6, most of them launches and trips to memory).
+// key heads of 128: 125 us, 4.4 TB/s, and the join 8), latency where there are few (8192 keys
+// of 8 heads: 12 us and the join 6, most of them launches and trips to memory).  The launch has a workgroup
+// for every 256 rows of room: 61 caches of 900 to 1000 keys take 29 us in 1024 rows of room each, 40 in 8192, 122 in 65536.
 constexpr int kFewWaves = 4, kFewThreads = 64 * kFewWaves;
 
 template <int IN, int DP>

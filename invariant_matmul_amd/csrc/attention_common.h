@@ -1,5 +1,5 @@
-// Parts that the attention kernels share: sequences, tiles in LDS, matrix steps
-// and the softmax of a step.
+// Parts that the attention kernels share: tiles in LDS, matrix steps and the softmax of a
+// step.  (Sequences: attention_sequences.h.)
 //
 // Layout.  The rows of a sequence that share a key head are one matrix: row
 // r = t group + h is query t of the sequence and query head h of the key

@@ -55,7 +55,8 @@ struct AttnArgs {
   int causal;
   int sorted;              // many rows: the longest sequences first
   // few rows: partial results per (chunk, key head, row): o [.., dim] and
-  // (reference, sum of rounded, sum of unrounded probabilities, 0)
+  // (reference, sum of rounded, sum of unrounded probabilities, whether the chunk holds values that
+  // are not finite)
   float *part_o, *part_ml;
   int64_t chunks;          // chunk slots of all sequences
   int part_rows;           // rows a chunk slot holds: max_q group

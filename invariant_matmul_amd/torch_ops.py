@@ -926,7 +926,8 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q=None, cu_k
 
     The bits of a row depend on its query and the keys and values it sees alone: a prompt
     taken at once, in pieces over a cache or token by token gives the same, whatever else shares
-    the call.  Differentiable once in reverse mode (a NaN in a sequence may reach more of that
+    the call.  An infinity or NaN in v is in every row that sees it, whatever its weight, and in
+    no other.  Differentiable once in reverse mode (a NaN in a sequence may reach more of that
     sequence's gradients than the formula's)."""
     where = "attention"
     cu_k, batch = _check_attention(where, q, k, v, cu_q, cu_k, k_lens)
