@@ -323,8 +323,8 @@ struct RowMover {
 };
 
 // Binary places by which p is raised for dv's products, and the sums lowered: in fp16 a p below 2^-14 would
-// lose bits, one below 2^-25 all of them, as the p of ten thousand keys that a row sees do (65536 keys: dv
-// off by 0.00077 of itself instead of 0.00021).  p is at most 1 and fp16 reaches 2^15.  (bf16 needs none, and its
+// lose bits, one below 2^-25 all of them, as the p of ten thousand keys that a row sees do (64 queries over 65536 keys
+// of 64, logits of standard deviation 1: dv would be off by 0.00072 of itself, it is by 0.00030).  p is at most 1 and fp16 reaches 2^15.  (bf16 needs none, and its
 // values times 2^14 may leave fp32's range.)
 template <int IN>
 constexpr int kRaised = IN == GEMM_F16 ? 14 : 0;
